@@ -395,6 +395,154 @@ medusa_status medusa_head_loss(const void* logits, const int32_t* tokens, int K,
                                medusa_dtype dt, void* dlogits, float* loss, float* row_loss, void* ws,
                                size_t ws_bytes, int32_t* d_status, medusa_stream_t stream);
 
+/* ---------------------------------------------------------- (j) paged cache
+ * The verify step's cache kept in pages, and what fills and reads it (guide,
+ * "树形验证": past_key_values; paper review, "局限性": the cache's memory grows
+ * with batch and length).  Sequences of any length share one pool; prompts
+ * enter it in chunks, single tokens decode from it, and the tree is verified
+ * against it.
+ *   k_pages, v_pages [n_layers][n_pages][page_size][Hkv][d] (dtype dt)
+ *   page_table [B][max_pages] int32: row r of sequence b is row r % page_size
+ *   of page page_table[b][r / page_size], the same in every layer
+ *   prefix_len [B] int32: rows sequence b holds before this call's tokens
+ *   q_start [B+1] int32: a chunk call has T tokens, sequence b's are
+ *   q_start[b] .. q_start[b+1]-1 (none, one or many; q_start[0] = 0 and the
+ *   last entry at most T; tokens at and past it are left alone)
+ * Lengths, starts and pages are read on the device only.  A sequence whose
+ * starts decrease or leave [0, T], or whose prefix_len is outside
+ * [0, max_pages * page_size], sets BAD_LENGTH and nothing of it is written.
+ * Entries of page_table behind a sequence's last row are never read.  Pools,
+ * outputs and inputs must not overlap one another (ALIAS), except where a call
+ * says so.  page_size >= 1, max_pages >= 1, n_layers * n_pages * page_size
+ * and n_layers * T < 2^31, max_pages * page_size < 2^31 - 2^16.
+ *
+ * medusa_rope_plan: how a rotary embedding turns.  The leading rotary_dim
+ * elements of a head are pairs (i, i + rotary_dim/2), or (2i, 2i+1) when
+ * interleaved; pair i turns by pos * f_i and is multiplied by `magnitude`, the
+ * other elements pass unchanged.  f_i = base^(-2i / rotary_dim), scaled for
+ * contexts longer than the original one:
+ *   MEDUSA_ROPE_PLAIN   as it is (factor, low, high, original_len ignored)
+ *   MEDUSA_ROPE_LINEAR  f / factor
+ *   MEDUSA_ROPE_BANDS   t f + (1 - t) f / factor, t = (turns - low) / (high - low)
+ *                       clamped to [0, 1], turns = original_len f / 2 pi
+ *   MEDUSA_ROPE_RAMP    the same with t falling linearly over the pair index, from 1
+ *                       at a to 0 at b: with r(n) = rotary_dim ln(original_len /
+ *                       (2 pi n)) / (2 ln base), a = max(floor r(high), 0) and
+ *                       b = min(ceil r(low), rotary_dim - 1)
+ * medusa_rope_plan_init fills a plan on the host (frequencies in double, kept
+ * as 64-bit fractions of a turn, so an angle is exact modulo one turn at any
+ * int32 position).  rotary_dim even, 2..MEDUSA_MAX_HEAD_DIM; base > 0 (> 1 for
+ * RAMP); factor > 0; 0 < low < high; original_len >= 1; magnitude finite. */
+#define MEDUSA_MAX_HEAD_DIM 256
+typedef enum medusa_rope_scaling {
+  MEDUSA_ROPE_PLAIN = 0,
+  MEDUSA_ROPE_LINEAR = 1,
+  MEDUSA_ROPE_BANDS = 2,
+  MEDUSA_ROPE_RAMP = 3
+} medusa_rope_scaling;
+
+typedef struct medusa_rope_plan {
+  int32_t rotary_dim, interleaved;
+  float magnitude;
+  int32_t reserved;
+  uint64_t turn[MEDUSA_MAX_HEAD_DIM / 2]; /* f_i / 2 pi modulo 1, times 2^64 */
+} medusa_rope_plan;
+
+medusa_status medusa_rope_plan_init(int rotary_dim, int interleaved, double base, medusa_rope_scaling scaling,
+                                    double factor, double low, double high, int original_len,
+                                    double magnitude, medusa_rope_plan* out);
+
+/* medusa_rope: q [n_layers][T][Hq][d] and k [n_layers][T][Hkv][d] (or NULL,
+ * with k_out) rotated at pos [T] into q_out / k_out (dense).  ldq and ldk are
+ * the elements from one token to the next in q and k (>= Hq*d, Hkv*d: slices
+ * of one fused projection; a layer is T * ld elements).  q_out may be q and
+ * k_out may be k when dense (in place); they must not overlap otherwise.
+ * inverse != 0 turns by the opposite angle: the gradient of the rotation,
+ * from the gradients of its outputs to those of its inputs.  rotary_dim <= d
+ * <= MEDUSA_MAX_HEAD_DIM; fp32 arithmetic, one rounding to dt.  pos may be any
+ * int32.  Pointers are aligned to their element size. */
+medusa_status medusa_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, const int32_t* pos,
+                          const medusa_rope_plan* plan, int inverse, int n_layers, int T, int Hq, int Hkv, int d,
+                          medusa_dtype dt, void* q_out, void* k_out, medusa_stream_t stream);
+
+/* medusa_paged_append: the chunk's keys and values enter the cache: token i of
+ * sequence b becomes row prefix_len[b] + i, its key rotated (plan NULL: as it
+ * is) at pos[q_start[b] + i], or at its row number when pos is NULL; q, when
+ * not NULL, is rotated into q_out on the way (q_out may be q when dense).
+ *   q [n_layers][T][Hq][d], k, v [n_layers][T][Hkv][d] with ldq, ldk, ldv as in
+ *   medusa_rope.
+ * A sequence that would pass max_pages * page_size rows sets CACHE_OVERFLOW
+ * and enters no row (its q_out is still written); a page outside [0, n_pages)
+ * sets BAD_INDEX and the tokens on it are not entered.  Two sequences that
+ * share a page they both write race on it. */
+medusa_status medusa_paged_append(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                  const int32_t* pos, const medusa_rope_plan* plan, const int32_t* page_table,
+                                  const int32_t* q_start, const int32_t* prefix_len, int n_layers, int T, int B,
+                                  int Hq, int Hkv, int d, int n_pages, int page_size, int max_pages,
+                                  medusa_dtype dt, void* q_out, void* k_pages, void* v_pages, int32_t* d_status,
+                                  medusa_stream_t stream);
+
+/* medusa_paged_attention: causal attention of the chunk over the cache, the
+ * chunk's own rows included (enter them first): token i of sequence b sees rows
+ * 0 .. prefix_len[b] + i.  For q head h and kv head h / G, G = Hq / Hkv:
+ *   out = softmax(scale q K^T) V   (fp32 scores, softmax and accumulation)
+ *   q   [n_layers][T][Hq][d] with ldq as in medusa_rope
+ *   out [n_layers][T][Hq][d] dt;  lse [n_layers][T][Hq] fp32 or NULL: the natural
+ *   logarithm of the sum of exp(scale q.k) over the visible keys.
+ * One token per sequence is a decoding step, a whole prompt a prefill, any mix
+ * of lengths one call.  Rows behind a sequence's last one are never part of a
+ * result, whatever they hold; rows it has must be finite.  A page outside
+ * [0, n_pages) among a sequence's rows sets BAD_INDEX and counts as zero rows;
+ * prefix_len + chunk past max_pages * page_size sets BAD_LENGTH (unwritten).
+ * bf16 with d <= 128 a multiple of 8, page_size a multiple of 8, G <= 128 and
+ * ldq a multiple of 8 runs on tcgen05 tensor cores; everything else on CUDA
+ * cores (fp32 never uses TF32).  d a multiple of 4 up to MEDUSA_MAX_HEAD_DIM,
+ * q, pools and out 16-byte aligned, ldq a multiple of 4, scale > 0.
+ * The key tiles of all (layer, kv head, sequence, row block) items are laid end
+ * to end and divided evenly over the SMs; an item shared by several CTAs leaves
+ * partial results in the workspace, added in a fixed order by a second kernel
+ * (deterministic on a given device).  Workspace: medusa_paged_attention_
+ * workspace_size() bytes, 16-byte aligned, its contents before the call do not
+ * matter; calls that may run at the same time need one each. */
+size_t medusa_paged_attention_workspace_size(int n_layers, int T, int B, int Hq, int Hkv, int d, int page_size,
+                                             medusa_dtype dt);
+medusa_status medusa_paged_attention(const void* q, int64_t ldq, const void* k_pages, const void* v_pages,
+                                     const int32_t* page_table, const int32_t* q_start, const int32_t* prefix_len,
+                                     int n_layers, int T, int B, int Hq, int Hkv, int d, int n_pages,
+                                     int page_size, int max_pages, float scale, medusa_dtype dt, void* out,
+                                     float* lse, void* ws, size_t ws_bytes, int32_t* d_status,
+                                     medusa_stream_t stream);
+
+/* medusa_paged_tree_attention: medusa_tree_attention over a paged prefix:
+ * node i of row b sees cache rows 0 .. prefix_len[b] - 1 and the tree rows j
+ * with mask bit (i, j) set.
+ *   q, out [n_layers][B][N][Hq][d]; kt, vt [n_layers][B][N][Hkv][d];
+ *   mask [N][ceil(N/32)]; lse [n_layers][B][N][Hq] or NULL.
+ * A node that sees nothing gets zeros, and -inf as lse.  N <= MEDUSA_MAX_NODES;
+ * other limits, kernels and errors as in medusa_paged_attention (kt and vt
+ * 16-byte aligned); the workspace is medusa_paged_attention_workspace_size(
+ * n_layers, B * N, B, ...) bytes. */
+medusa_status medusa_paged_tree_attention(const void* q, const void* k_pages, const void* v_pages,
+                                          const int32_t* page_table, const void* kt, const void* vt,
+                                          const uint32_t* mask, const int32_t* prefix_len, int n_layers, int B,
+                                          int N, int Hq, int Hkv, int d, int n_pages, int page_size,
+                                          int max_pages, float scale, medusa_dtype dt, void* out, float* lse,
+                                          void* ws, size_t ws_bytes, int32_t* d_status, medusa_stream_t stream);
+
+/* medusa_paged_compact: medusa_kv_compact into pages: row prefix_len[b] + i of
+ * the cache takes kt / vt[l][b][path_nodes[b][i]] for i < accept_len[b], and
+ * new_len[b] = prefix_len[b] + accept_len[b] (new_len may be prefix_len).  A
+ * row past max_pages * page_size sets CACHE_OVERFLOW; an accept_len outside
+ * 1..Dmax+1, a path node outside [0, N) or a page outside [0, n_pages) sets
+ * BAD_INDEX, a negative prefix_len BAD_LENGTH: that row writes nothing and
+ * keeps new_len = prefix_len.  Rows are moved as 16-byte words when Hkv * d and
+ * the pointers allow it, else 4 or 2 bytes at a time. */
+medusa_status medusa_paged_compact(void* k_pages, void* v_pages, const int32_t* page_table, const void* kt,
+                                   const void* vt, const int32_t* path_nodes, const int32_t* accept_len,
+                                   const int32_t* prefix_len, int32_t* new_len, int n_layers, int B, int N,
+                                   int Hkv, int d, int n_pages, int page_size, int max_pages, int Dmax,
+                                   medusa_dtype dt, int32_t* d_status, medusa_stream_t stream);
+
 /* ------------------------------------------------------------------ status
  * Synchronises `stream`, copies the device status word to *host_code and
  * resets it to 0.  Returns CUDA_ERROR if the stream holds a failed launch. */

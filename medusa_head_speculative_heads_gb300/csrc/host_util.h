@@ -21,6 +21,14 @@ inline bool dtype_ok(int dt) { return dt == MEDUSA_F32 || dt == MEDUSA_BF16; }
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// Sizes of a paged cache: pool rows and a sequence's rows stay inside int32,
+// with room for a tile behind the last row.
+inline bool cache_sizes_ok(int n_layers, int n_pages, int page_size, int max_pages) {
+  if (n_pages < 1 || page_size < 1 || max_pages < 1) return false;
+  const long long pool = (long long)n_pages * page_size;
+  return pool <= 0x7fffffffll / n_layers && (long long)max_pages * page_size < 0x7fffffffll - 65536;
+}
+
 // Bump allocator over a caller-provided workspace (256-byte aligned slices).
 struct WsCarver {
   char* base;

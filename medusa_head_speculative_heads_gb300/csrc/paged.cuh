@@ -1,0 +1,203 @@
+// Shared parts of the paged-cache calls: the cache's addressing, the tokens of
+// a chunk, and how attention work is laid out and divided.
+#pragma once
+
+#include "common.cuh"
+
+namespace medusa {
+namespace paged {
+
+struct Cache {
+  const int32_t* page_table;  // [B][max_pages]
+  int n_pages, page_size, max_pages;
+  // Rows a sequence can hold (host-checked: < 2^31 - 2^16).
+  __host__ __device__ int rows() const { return max_pages * page_size; }
+};
+
+// Pool row (within one layer) of row r of sequence b, or -1 for a page outside
+// the pool.  0 <= r < rows().
+__device__ __forceinline__ int pool_row(const Cache& c, int b, int r) {
+  const int pg = r / c.page_size;
+  const int id = __ldg(c.page_table + (size_t)b * c.max_pages + pg);
+  return id >= 0 && id < c.n_pages ? id * c.page_size + (r - pg * c.page_size) : -1;
+}
+
+// ------------------------------------------------------------------ attention work
+//
+// An item is (layer, head group, sequence, block of `ctok` tokens); its cost is
+// its number of KT-key tiles.  All items' tiles are laid end to end, layer and
+// head group outermost (CTAs that run together then read the same head's rows),
+// and CTA c of C takes tiles [c Q, (c + 1) Q), Q = max(ceil(U / C), min_tiles).
+// Each CTA has at most two items that it shares with others: the one its range
+// starts inside (partial slot 0) and the one its range ends inside (slot 1).
+struct Work {
+  const int32_t* q_start;     // [B + 1], or NULL: N tokens each (tree)
+  const int32_t* prefix_len;  // [B]
+  int B, T, N;                // N: tree nodes, 0 for a causal chunk
+  int nl, nh, cap;            // nh: head groups per layer; cap: rows a sequence can hold
+  int ctok, KT;               // tokens per block and keys per tile (powers of two)
+  int ctas, min_tiles;
+};
+
+struct Seq {
+  int q0, len, L;  // first token, tokens, rows before them
+  bool ok;
+};
+
+__device__ __forceinline__ Seq seq_of(const Work& w, int b) {
+  Seq s;
+  s.L = __ldg(w.prefix_len + b);
+  if (w.q_start) {
+    const int a = __ldg(w.q_start + b), e = __ldg(w.q_start + b + 1);
+    s.q0 = a;
+    s.ok = a >= 0 && e >= a && e <= w.T && (e == a || (s.L >= 0 && s.L <= w.cap - (e - a)));
+    s.len = s.ok ? e - a : 0;
+  } else {
+    s.q0 = b * w.N;
+    s.ok = s.L >= 0 && s.L <= w.cap;
+    s.len = s.ok ? w.N : 0;
+  }
+  return s;
+}
+
+__device__ __forceinline__ int n_blocks(const Work& w, const Seq& s) { return (s.len + w.ctok - 1) / w.ctok; }
+
+// Key tiles of block i of a sequence.  Causal: the rows up to the block's last
+// token.  Tree: the prefix tiles, then the tree tiles.
+__device__ __forceinline__ int block_tiles(const Work& w, const Seq& s, int i) {
+  if (w.N) return (s.L + w.KT - 1) / w.KT + (w.N + w.KT - 1) / w.KT;
+  const int last = min(s.len, (i + 1) * w.ctok);
+  return (s.L + last + w.KT - 1) / w.KT;
+}
+
+// Tiles of the sequence's first i blocks, i <= n_blocks, in closed form.  With
+// L = a KT + r, a block's count is a + ceil((r + k ctok) / KT), k = 1, 2, ...:
+// when ctok is m tiles, ceil(r / KT) + m k; when a tile is m blocks,
+// ceil((ceil(r / ctok) + k) / m), summed by h(n) = sum_{j <= n} ceil(j / m).
+__device__ __forceinline__ long long tiles_before(const Work& w, const Seq& s, int i) {
+  if (i == 0) return 0;
+  if (w.N) return (long long)i * block_tiles(w, s, 0);
+  const int nb = n_blocks(w, s);
+  const bool all = i == nb;  // the last block may be short: added on its own
+  const long long n = all ? i - 1 : i;
+  const long long a = s.L / w.KT;
+  const int r = s.L % w.KT;
+  long long t = n * a;
+  if (w.ctok >= w.KT) {
+    const long long m = w.ctok / w.KT;
+    t += n * (r > 0) + m * n * (n + 1) / 2;
+  } else {
+    const long long m = w.KT / w.ctok;
+    const long long r1 = (r + w.ctok - 1) / w.ctok;
+    auto h = [m](long long x) {
+      const long long q = x / m, e = x % m;
+      return m * q * (q + 1) / 2 + e * (q + 1);
+    };
+    t += h(r1 + n) - h(r1);
+  }
+  return all ? t + block_tiles(w, s, nb - 1) : t;
+}
+
+__device__ __forceinline__ long long seq_tiles(const Work& w, const Seq& s) {
+  return s.len > 0 ? tiles_before(w, s, n_blocks(w, s)) : 0;
+}
+
+// The item that holds a tile: block i of sequence b for layer-head lg, the
+// global index of its first tile and its tile count.
+struct Item {
+  int lg, b, i, tiles;
+  long long first;
+  Seq s;
+};
+
+// Block-wide set-up: every thread of the CTA calls plan_find() once.  It sums the
+// tiles per layer-head over the sequences and, for the tile `want(U, Q)` picks,
+// finds the item that holds it.  sh: 2 * 32 + 4 long longs of shared memory.
+// Returns false when that tile does not exist.
+struct Plan {
+  long long per, U, Q;  // tiles per layer-head, in all, per CTA
+};
+
+template <typename Want>
+__device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, long long* sh, Want want) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wp = tid >> 5, nw = (nt + 31) >> 5;
+  long long mine = 0;
+  for (int b = tid; b < w.B; b += nt) mine += seq_tiles(w, seq_of(w, b));
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) sh[wp] = mine;
+  __syncthreads();
+  long long per = 0;
+  for (int j = 0; j < nw; ++j) per += sh[j];
+  pl.per = per;
+  pl.U = per * ((long long)w.nl * w.nh);
+  pl.Q = (pl.U + w.ctas - 1) / w.ctas;
+  if (pl.Q < w.min_tiles) pl.Q = w.min_tiles;
+  const long long u = want(pl);
+  if (u < 0 || u >= pl.U) return false;
+  const long long off = u % per;
+  // The sequence whose tiles hold `off`: block-wide scan, blockDim sequences at a time.
+  long long base = 0;
+  for (int b0 = 0; b0 < w.B; b0 += nt) {
+    const int b = b0 + tid;
+    Seq s;
+    long long v = 0;
+    if (b < w.B) {
+      s = seq_of(w, b);
+      v = seq_tiles(w, s);
+    }
+    long long inc = v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    __syncthreads();  // the last use of sh is over
+    if (lane == 31) sh[32 + wp] = inc;
+    __syncthreads();
+    long long before = base, total = 0;
+    for (int j = 0; j < nw; ++j) {
+      if (j < wp) before += sh[32 + j];
+      total += sh[32 + j];
+    }
+    const long long lo = before + inc - v;
+    if (b < w.B && off >= lo && off < lo + v) {  // one thread
+      int i0 = 0, i1 = n_blocks(w, s);
+      while (i1 - i0 > 1) {
+        const int m = (i0 + i1) >> 1;
+        if (tiles_before(w, s, m) <= off - lo) i0 = m;
+        else i1 = m;
+      }
+      sh[64] = b;
+      sh[65] = i0;
+      sh[66] = lo + tiles_before(w, s, i0);
+    }
+    base += total;
+    if (base > off) break;  // the same in every thread
+  }
+  __syncthreads();
+  it.lg = (int)(u / per);
+  it.b = (int)sh[64];
+  it.i = (int)sh[65];
+  it.s = seq_of(w, it.b);
+  it.first = (long long)it.lg * per + sh[66];
+  it.tiles = block_tiles(w, it.s, it.i);
+  return true;
+}
+
+// The next item in order; false behind the last one.
+__device__ __forceinline__ bool next_item(const Work& w, Item& it) {
+  it.first += it.tiles;
+  ++it.i;
+  while (it.s.len == 0 || it.i >= n_blocks(w, it.s)) {
+    it.i = 0;
+    if (++it.b == w.B) {
+      it.b = 0;
+      if (++it.lg == w.nl * w.nh) return false;
+    }
+    it.s = seq_of(w, it.b);
+  }
+  it.tiles = block_tiles(w, it.s, it.i);
+  return true;
+}
+
+}  // namespace paged
+}  // namespace medusa

@@ -1,0 +1,478 @@
+// medusa_paged_attention and medusa_paged_tree_attention: entry points, the
+// CUDA-core kernel (fp32, and what the tensor-core kernel does not take) and
+// the merge of items that several CTAs share.
+//
+// Paper review ("Medusa: Simple LLM Inference Acceleration Framework with
+// Multiple Decoding Heads"), section "Medusa 的三个核心组件": each token attends
+// to its own predecessors; "局限性": the cache grows with batch and length, so
+// it is kept in pages here.
+//
+// One pass over the keys with a running maximum m and sum l per row:
+//   m' = max(m, max s), f = 2^(m - m'), l' = f l + sum 2^(s - m'),
+//   O' = f O + sum 2^(s - m') v,
+// s in the log2 domain (scale log2 e folded in); at the end O / l.  Two parts
+// of a row combine the same way.
+#include "host_util.h"
+#include "paged_attn.cuh"
+
+namespace medusa {
+namespace paged {
+
+constexpr int kSimtThreads = 256;
+constexpr int kSimtKeys = 64;
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const uint16_t* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(uint16_t* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2_rn(v.x, v.y), bf16x2_rn(v.z, v.w));
+}
+
+// A tile is 16 RM rows x 64 keys; thread (ty, tx) of 16 x 16 holds rows
+// ty RM .. + RM - 1: their scores of keys tx + 16 j and their columns
+// 4 tx + 64 j .. + 3 of O, in registers.  Operands are fp32 in shared memory,
+// rows padded by 16 bytes, so the sixteen rows a quarter warp reads lie in
+// different banks.  Probabilities pass through shared memory between threads
+// of one half warp.
+template <int DC>
+__host__ __device__ constexpr int simt_pitch() { return 16 * DC + 4; }
+template <int DC, int RM>
+constexpr size_t simt_smem() {
+  return ((size_t)(16 * RM + 2 * kSimtKeys) * simt_pitch<DC>() + (size_t)16 * RM * (kSimtKeys + 4)) * sizeof(float);
+}
+
+template <typename T, int DC, int RM>
+__global__ void __launch_bounds__(kSimtThreads) paged_attn_simt_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int R = 16 * RM, DP = simt_pitch<DC>(), PP = kSimtKeys + 4;
+  extern __shared__ float4 smem4[];
+  float* Qs = reinterpret_cast<float*>(smem4);
+  float* Ks = Qs + R * DP;
+  float* Vs = Ks + kSimtKeys * DP;
+  float* Ps = Vs + kSimtKeys * DP;
+  __shared__ long long sh[68];
+  __shared__ const T *s_k[2][kSimtKeys], *s_v[2][kSimtKeys];  // row starts of a tile's keys (NULL: zeros)
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  if (blockIdx.x == 0)
+    for (int b = tid; b < a.w.B; b += kSimtThreads)
+      if (!seq_of(a.w, b).ok) set_status(a.d_status, MEDUSA_DEV_BAD_LENGTH);
+  Plan pl;
+  Item it;
+  if (!plan_find(a.w, pl, it, sh, [](const Plan& p) { return p.Q * blockIdx.x; })) return;
+  const long long u0 = pl.Q * blockIdx.x, u1 = u0 + pl.Q < pl.U ? u0 + pl.Q : pl.U;
+  const int dv = a.d / 4;
+
+  for (long long u = u0; u < u1;) {
+    const long long end = it.first + it.tiles < u1 ? it.first + it.tiles : u1;
+    const int t0 = (int)(u - it.first), t1 = (int)(end - it.first);
+    const int l = it.lg / a.w.nh, kvh = it.lg % a.w.nh / a.nsub;
+    const int pre = a.w.N ? (it.s.L + kSimtKeys - 1) / kSimtKeys : it.tiles;  // tiles of cache rows
+    const int rows_end = a.w.N ? it.s.L : it.s.L + min(it.s.len, (it.i + 1) * a.w.ctok);
+    // Where the keys of tile t lie.
+    auto find_rows = [&](int t) {
+      if (tid >= kSimtKeys) return;
+      const T *k = nullptr, *v = nullptr;
+      if (t < pre) {
+        const int j = t * kSimtKeys + tid;
+        if (j < rows_end) {
+          const int slot = pool_row(a.cache, it.b, j);
+          if (slot >= 0) {
+            const size_t at = (((size_t)l * a.cache.n_pages * a.cache.page_size + slot) * a.Hkv + kvh) * a.d;
+            k = static_cast<const T*>(a.k_pages) + at;
+            v = static_cast<const T*>(a.v_pages) + at;
+          } else {
+            set_status(a.d_status, MEDUSA_DEV_BAD_INDEX);
+          }
+        }
+      } else {
+        const int j = (t - pre) * kSimtKeys + tid;
+        if (j < a.w.N) {
+          const size_t at = (((size_t)l * a.w.T + it.s.q0 + j) * a.Hkv + kvh) * a.d;
+          k = static_cast<const T*>(a.kt) + at;
+          v = static_cast<const T*>(a.vt) + at;
+        }
+      }
+      s_k[t & 1][tid] = k;
+      s_v[t & 1][tid] = v;
+    };
+    find_rows(t0);
+    __syncthreads();  // Qs, Ks, Vs of the item before are no longer read
+    for (int idx = tid; idx < R * 4 * DC; idx += kSimtThreads) {
+      const int r = idx / (4 * DC), c = idx - r * (4 * DC);
+      const Row x = row_of(a, it, r);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (x.ok && c < dv)
+        v = load4(static_cast<const T*>(a.q) + ((long long)l * a.w.T + it.s.q0 + x.tok) * a.ldq + (long long)x.h * a.d + 4 * c);
+      store4(Qs + r * DP + 4 * c, v);
+    }
+    Row row[RM];
+    float m[RM], sum[RM];
+    float4 o[RM][DC / 4];
+#pragma unroll
+    for (int i = 0; i < RM; ++i) {
+      row[i] = row_of(a, it, ty * RM + i);
+      m[i] = -INFINITY;
+      sum[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < DC / 4; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+
+    for (int t = t0; t < t1; ++t) {
+      if (t > t0) __syncthreads();  // the tile before is no longer read; s_k of this one is written
+      for (int idx = tid; idx < kSimtKeys * 4 * DC; idx += kSimtThreads) {
+        const int r = idx / (4 * DC), c = idx - r * (4 * DC);
+        const T *k = s_k[t & 1][r], *v = s_v[t & 1][r];
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (k && c < dv) {
+          x = load4(k + 4 * c);
+          y = load4(v + 4 * c);
+        }
+        store4(Ks + r * DP + 4 * c, x);
+        store4(Vs + r * DP + 4 * c, y);
+      }
+      if (t + 1 < t1) find_rows(t + 1);
+      __syncthreads();
+
+      float s[RM][4];
+#pragma unroll
+      for (int i = 0; i < RM; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+      for (int c = 0; c < dv; ++c) {
+        float4 kk[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kk[j] = load4(Ks + (tx + 16 * j) * DP + 4 * c);
+#pragma unroll
+        for (int i = 0; i < RM; ++i) {
+          const float4 qq = load4(Qs + (ty * RM + i) * DP + 4 * c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            s[i][j] = fmaf(qq.w, kk[j].w, fmaf(qq.z, kk[j].z, fmaf(qq.y, kk[j].y, fmaf(qq.x, kk[j].x, s[i][j]))));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < RM; ++i) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int key = (t < pre ? t : t - pre) * kSimtKeys + tx + 16 * j;
+          bool see;
+          if (t >= pre) see = row[i].ok && key < a.w.N && ((__ldg(a.mask + (size_t)row[i].tok * a.W + (key >> 5)) >> (key & 31)) & 1u);
+          else see = row[i].ok && key < (a.w.N ? it.s.L : it.s.L + row[i].tok + 1);
+          s[i][j] = see ? s[i][j] * a.scale_log2 : -INFINITY;
+          mx = fmaxf(mx, s[i][j]);
+        }
+#pragma unroll
+        for (int e = 8; e; e >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, e));
+        const float mn = fmaxf(m[i], mx), off = mn == -INFINITY ? 0.f : mn;
+        const float f = exp2f(m[i] - off);  // 0 for the first keys seen
+        m[i] = mn;
+        float rs = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = exp2f(s[i][j] - off);
+          rs += p;
+          Ps[(ty * RM + i) * PP + tx + 16 * j] = p;
+        }
+        sum[i] = fmaf(sum[i], f, rs);  // this thread's share; its sixteen are added at the end
+#pragma unroll
+        for (int c = 0; c < DC / 4; ++c) {
+          o[i][c].x *= f;
+          o[i][c].y *= f;
+          o[i][c].z *= f;
+          o[i][c].w *= f;
+        }
+      }
+      __syncwarp();  // a row's probabilities are written and read by one half warp
+#pragma unroll 2
+      for (int j = 0; j < kSimtKeys; j += 4) {
+        float4 p[RM];
+#pragma unroll
+        for (int i = 0; i < RM; ++i) p[i] = load4(Ps + (ty * RM + i) * PP + j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+          for (int c = 0; c < DC / 4; ++c) {
+            const float4 v = load4(Vs + (j + e) * DP + 4 * tx + 64 * c);
+#pragma unroll
+            for (int i = 0; i < RM; ++i) {
+              const float pe = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
+              o[i][c].x = fmaf(pe, v.x, o[i][c].x);
+              o[i][c].y = fmaf(pe, v.y, o[i][c].y);
+              o[i][c].z = fmaf(pe, v.z, o[i][c].z);
+              o[i][c].w = fmaf(pe, v.w, o[i][c].w);
+            }
+          }
+        }
+      }
+      __syncwarp();
+    }
+
+    const bool whole = t0 == 0 && t1 == it.tiles;
+    const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
+#pragma unroll
+    for (int i = 0; i < RM; ++i) {
+      float ls = sum[i];
+#pragma unroll
+      for (int e = 8; e; e >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, e);
+      if (!row[i].ok) continue;
+      const size_t at = whole ? out_row(a, it, row[i]) : (size_t)slot * a.R + ty * RM + i;
+      const float f = !whole ? 1.f : ls > 0.f ? 1.f / ls : 0.f;
+#pragma unroll
+      for (int c = 0; c < DC / 4; ++c) {
+        const int col = 4 * tx + 64 * c;
+        if (col >= a.d) continue;
+        const float4 v = make_float4(o[i][c].x * f, o[i][c].y * f, o[i][c].z * f, o[i][c].w * f);
+        if (whole) store4(static_cast<T*>(a.out) + at * a.d + col, v);
+        else store4(a.part_o + at * a.d + col, v);
+      }
+      if (tx == 0) {
+        if (!whole) a.part_ml[at] = make_float2(m[i], ls);
+        else if (a.lse) a.lse[at] = lse_of(m[i], ls);
+      }
+    }
+    u = end;
+    if (u < u1 && !next_item(a.w, it)) break;
+  }
+}
+
+// Adds the parts of every item that several CTAs share.  CTA boundary c (tile
+// c Q, c = 1 .. C - 1) belongs to the item it falls inside; the first boundary
+// inside an item merges all of its parts, in the order of the CTAs:
+// O = sum 2^(m_p - M) O_p, l = sum 2^(m_p - M) l_p, M = max m_p.  One warp per
+// row (its lanes share the columns); blockIdx.y takes every gridDim.y-th group
+// of eight rows.
+template <typename T>
+__global__ void __launch_bounds__(256) paged_attn_merge_kernel(const __grid_constant__ AttnArgs a) {
+  __shared__ long long sh[68];
+  pdl_wait();
+  pdl_trigger();
+  const long long c = blockIdx.x + 1;
+  Plan pl;
+  Item it;
+  if (!plan_find(a.w, pl, it, sh, [c](const Plan& p) { return p.Q * c; })) return;
+  if (it.first >= c * pl.Q || it.first < (c - 1) * pl.Q) return;  // no shared item, or not its first boundary
+  const int first = (int)(c - 1), last = (int)((it.first + it.tiles - 1) / pl.Q);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r = blockIdx.y * 8 + warp; r < a.R; r += gridDim.y * 8) {
+    const Row x = row_of(a, it, r);
+    if (!x.ok) continue;
+    // CTA p's part: slot 1 of the CTA the item starts in, slot 0 of the others.
+    auto at = [&](int p) { return (size_t)(2 * p + (p == first ? 1 : 0)) * a.R + r; };
+    float M = -INFINITY;
+    for (int p = first + lane; p <= last; p += 32) M = fmaxf(M, a.part_ml[at(p)].x);
+    M = warp_max(M);
+    const float off = M == -INFINITY ? 0.f : M;
+    float l = 0.f;
+    for (int p = first + lane; p <= last; p += 32) {
+      const float2 q = a.part_ml[at(p)];
+      l = fmaf(exp2f(q.x - off), q.y, l);
+    }
+    l = warp_sum(l);
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const size_t to = out_row(a, it, x);
+    for (int col = 4 * lane; col < a.d; col += 128) {
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int p = first; p <= last; ++p) {
+        const size_t w = at(p);
+        const float2 ml = a.part_ml[w];
+        const float f = ml.y > 0.f ? exp2f(ml.x - off) : 0.f;
+        const float4 v = *reinterpret_cast<const float4*>(a.part_o + w * a.d + col);
+        if (f > 0.f) {  // a part that saw no key may hold anything
+          o.x = fmaf(f, v.x, o.x);
+          o.y = fmaf(f, v.y, o.y);
+          o.z = fmaf(f, v.z, o.z);
+          o.w = fmaf(f, v.w, o.w);
+        }
+      }
+      store4(static_cast<T*>(a.out) + to * a.d + col, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    }
+    if (a.lse && lane == 0) a.lse[to] = lse_of(M, l);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+// How a call is divided: which kernel, its block of rows and its CTAs.
+struct Division {
+  int R, ctas, KT, min_tiles, sub, nsub, tile_rows, tile_tok, ctok;
+};
+
+static int pow2_at_most(int x) {
+  int p = 1;
+  while (2 * p <= x) p *= 2;
+  return p;
+}
+
+static Division divide(int T, int B, int Hq, int Hkv, int d, int page_size, medusa_dtype dt) {
+  Division v{};
+  const int G = Hq / Hkv, sms = device_sm_count();
+  (void)page_size;
+  (void)dt;
+  // Rows of a tile: 16 when a sequence has at most 16 on average (decoding), else 64.
+  v.R = (long long)T * G <= 16ll * B || d > 128 ? 16 : 64;
+  v.tile_rows = v.R;
+  // CTAs that fit an SM (registers and shared memory).
+  v.ctas = sms * (v.R == 16 ? (d <= 64 ? 3 : d <= 128 ? 2 : 1) : (d <= 64 ? 2 : 1));
+  v.KT = kSimtKeys;
+  v.min_tiles = 2;
+  v.nsub = (G + v.R - 1) / v.R;
+  v.sub = (G + v.nsub - 1) / v.nsub;
+  v.tile_tok = v.ctok = pow2_at_most(v.R / v.sub);
+  return v;
+}
+
+static size_t ws_bytes_of(const Division& v, int d) { return (size_t)v.ctas * 2 * v.R * (d + 2) * sizeof(float); }
+
+template <typename T, int DC, int RM>
+static medusa_status simt_go(const AttnArgs& a, cudaStream_t s) {
+  constexpr size_t smem = simt_smem<DC, RM>();
+  auto kern = paged_attn_simt_kernel<T, DC, RM>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return MEDUSA_ERR_CUDA;
+  launch_pdl(kern, dim3(a.w.ctas), dim3(kSimtThreads), smem, s, a);
+  return MEDUSA_OK;
+}
+
+template <typename T>
+static medusa_status simt_launch(const AttnArgs& a, cudaStream_t s) {
+  if (a.R == 16) return a.d <= 64 ? simt_go<T, 4, 1>(a, s) : a.d <= 128 ? simt_go<T, 8, 1>(a, s) : simt_go<T, 16, 1>(a, s);
+  return a.d <= 64 ? simt_go<T, 4, 4>(a, s) : simt_go<T, 8, 4>(a, s);
+}
+
+// Arguments that both entry points check and fill alike.
+static medusa_status attend(AttnArgs& a, int n_layers, int T, int B, int Hq, int Hkv, int d, int n_pages, int page_size,
+                            int max_pages, int64_t ldq, float scale, medusa_dtype dt, void* ws, size_t ws_bytes,
+                            cudaStream_t s) {
+  const Division v = divide(T, B, Hq, Hkv, d, page_size, dt);
+  a.cache.n_pages = n_pages;
+  a.cache.page_size = page_size;
+  a.cache.max_pages = max_pages;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.G = Hq / Hkv;
+  a.ldq = ldq;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  if (!ws || !aligned16(ws) || ws_bytes < ws_bytes_of(v, d)) return MEDUSA_ERR_WORKSPACE;
+  a.part_o = static_cast<float*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)v.ctas * 2 * v.R * d);
+  a.R = v.R;
+  a.tile_rows = v.tile_rows;
+  a.tile_tok = v.tile_tok;
+  a.sub = v.sub;
+  a.nsub = v.nsub;
+  a.w.nl = n_layers;
+  a.w.nh = Hkv * v.nsub;
+  a.w.cap = max_pages * page_size;
+  a.w.ctok = v.ctok;
+  a.w.KT = v.KT;
+  a.w.ctas = v.ctas;
+  a.w.min_tiles = v.min_tiles;
+  a.w.B = B;
+  a.w.T = T;
+  const medusa_status st = dt == MEDUSA_BF16 ? simt_launch<uint16_t>(a, s) : simt_launch<float>(a, s);
+  if (st != MEDUSA_OK) return st;
+  const dim3 grid(v.ctas - 1, v.R > 64 ? 4 : 1);
+  if (dt == MEDUSA_BF16) launch_pdl(paged_attn_merge_kernel<uint16_t>, grid, dim3(256), 0, s, a);
+  else launch_pdl(paged_attn_merge_kernel<float>, grid, dim3(256), 0, s, a);
+  return launch_status();
+}
+
+static bool sizes_ok(int n_layers, int T, int B, int Hq, int Hkv, int d, int n_pages, int page_size, int max_pages,
+                     float scale, int dt) {
+  if (n_layers < 1 || T < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq > 65535) return false;
+  if (d < 4 || d % 4 || d > MEDUSA_MAX_HEAD_DIM || !(scale > 0.f) || !(scale < INFINITY) || !dtype_ok(dt)) return false;
+  if ((long long)n_layers * T > 0x7fffffffll || (long long)n_layers * Hq > 0x7fffffffll) return false;
+  return cache_sizes_ok(n_layers, n_pages, page_size, max_pages);
+}
+
+}  // namespace paged
+}  // namespace medusa
+
+using namespace medusa;
+using namespace medusa::paged;
+
+extern "C" size_t medusa_paged_attention_workspace_size(int n_layers, int T, int B, int Hq, int Hkv, int d, int page_size,
+                                                        medusa_dtype dt) {
+  if (n_layers < 1 || T < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || d < 4 || d > MEDUSA_MAX_HEAD_DIM || page_size < 1 || !dtype_ok(dt))
+    return 0;
+  return ws_bytes_of(divide(T, B, Hq, Hkv, d, page_size, dt), d);
+}
+
+extern "C" medusa_status medusa_paged_attention(const void* q, int64_t ldq, const void* k_pages, const void* v_pages,
+                                                const int32_t* page_table, const int32_t* q_start,
+                                                const int32_t* prefix_len, int n_layers, int T, int B, int Hq, int Hkv,
+                                                int d, int n_pages, int page_size, int max_pages, float scale,
+                                                medusa_dtype dt, void* out, float* lse, void* ws, size_t ws_bytes,
+                                                int32_t* d_status, medusa_stream_t stream) {
+  if (!q || !k_pages || !v_pages || !page_table || !q_start || !prefix_len || !out) return MEDUSA_ERR_INVALID_ARG;
+  if (!sizes_ok(n_layers, T, B, Hq, Hkv, d, n_pages, page_size, max_pages, scale, dt)) return MEDUSA_ERR_INVALID_ARG;
+  if (ldq < (int64_t)Hq * d || ldq % 4 || !aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
+    return MEDUSA_ERR_INVALID_ARG;
+  const uintptr_t words = (uintptr_t)page_table | (uintptr_t)q_start | (uintptr_t)prefix_len | (uintptr_t)lse;
+  if (words & 3) return MEDUSA_ERR_INVALID_ARG;
+  const size_t es = dtype_bytes(dt), tokens = (size_t)n_layers * T;
+  const size_t nq = ((tokens - 1) * (size_t)ldq + (size_t)Hq * d) * es, no = tokens * Hq * d * es;
+  const size_t np = (size_t)n_layers * n_pages * page_size * Hkv * d * es, nl = tokens * Hq * 4;
+  if (overlaps(out, no, q, nq) || overlaps(out, no, k_pages, np) || overlaps(out, no, v_pages, np)) return MEDUSA_ERR_ALIAS;
+  if (lse && (overlaps(lse, nl, out, no) || overlaps(lse, nl, q, nq) || overlaps(lse, nl, k_pages, np) || overlaps(lse, nl, v_pages, np)))
+    return MEDUSA_ERR_ALIAS;
+  AttnArgs a{};
+  a.q = q;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.out = out;
+  a.lse = lse;
+  a.d_status = d_status;
+  a.cache.page_table = page_table;
+  a.w.q_start = q_start;
+  a.w.prefix_len = prefix_len;
+  return attend(a, n_layers, T, B, Hq, Hkv, d, n_pages, page_size, max_pages, ldq, scale, dt, ws, ws_bytes,
+                reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" medusa_status medusa_paged_tree_attention(const void* q, const void* k_pages, const void* v_pages,
+                                                     const int32_t* page_table, const void* kt, const void* vt,
+                                                     const uint32_t* mask, const int32_t* prefix_len, int n_layers, int B,
+                                                     int N, int Hq, int Hkv, int d, int n_pages, int page_size,
+                                                     int max_pages, float scale, medusa_dtype dt, void* out, float* lse,
+                                                     void* ws, size_t ws_bytes, int32_t* d_status, medusa_stream_t stream) {
+  if (!q || !k_pages || !v_pages || !page_table || !kt || !vt || !mask || !prefix_len || !out) return MEDUSA_ERR_INVALID_ARG;
+  if (B < 1 || N < 1 || N > MEDUSA_MAX_NODES || (long long)B * N > 0x7fffffffll) return MEDUSA_ERR_INVALID_ARG;
+  if (!sizes_ok(n_layers, B * N, B, Hq, Hkv, d, n_pages, page_size, max_pages, scale, dt)) return MEDUSA_ERR_INVALID_ARG;
+  const void* rows[] = {q, k_pages, v_pages, kt, vt, out};
+  for (const void* p : rows)
+    if (!aligned16(p)) return MEDUSA_ERR_INVALID_ARG;
+  const uintptr_t words = (uintptr_t)page_table | (uintptr_t)mask | (uintptr_t)prefix_len | (uintptr_t)lse;
+  if (words & 3) return MEDUSA_ERR_INVALID_ARG;
+  const size_t es = dtype_bytes(dt), tokens = (size_t)n_layers * B * N;
+  const size_t no = tokens * Hq * d * es, nt = tokens * Hkv * d * es, nl = tokens * Hq * 4;
+  const size_t np = (size_t)n_layers * n_pages * page_size * Hkv * d * es;
+  const void* in[] = {q, k_pages, v_pages, kt, vt};
+  const size_t size[] = {no, np, np, nt, nt};
+  for (int i = 0; i < 5; ++i)
+    if (overlaps(out, no, in[i], size[i]) || (lse && overlaps(lse, nl, in[i], size[i]))) return MEDUSA_ERR_ALIAS;
+  if (lse && overlaps(lse, nl, out, no)) return MEDUSA_ERR_ALIAS;
+  AttnArgs a{};
+  a.q = q;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.kt = kt;
+  a.vt = vt;
+  a.mask = mask;
+  a.W = (N + 31) / 32;
+  a.out = out;
+  a.lse = lse;
+  a.d_status = d_status;
+  a.cache.page_table = page_table;
+  a.w.prefix_len = prefix_len;
+  a.w.N = N;
+  return attend(a, n_layers, B * N, B, Hq, Hkv, d, n_pages, page_size, max_pages, (int64_t)Hq * d, scale, dt, ws, ws_bytes,
+                reinterpret_cast<cudaStream_t>(stream));
+}

@@ -1,0 +1,58 @@
+// What the two paged-attention kernels (CUDA cores and tensor cores) and the
+// merge of their partial results share.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "medusa.h"
+#include "paged.cuh"
+
+namespace medusa {
+namespace paged {
+
+struct AttnArgs {
+  Work w;
+  Cache cache;
+  const void *q, *k_pages, *v_pages, *kt, *vt;
+  const uint32_t* mask;  // [N][W]
+  void* out;
+  float* lse;
+  float* part_o;    // [slot][R][d] unnormalised sums of shared items
+  float2* part_ml;  // [slot][R] their row maxima (log2 domain) and row sums
+  int32_t* d_status;
+  long long ldq;
+  int Hq, Hkv, d, G;
+  int sub, nsub;  // q heads per head group, groups per kv head
+  int R;          // rows of a partial slot
+  int tile_rows, tile_tok;  // a block is tiles of tile_rows rows: tile_tok tokens x sub heads each
+  int W;
+  float scale_log2;
+};
+
+// Row r of item it's block: its token within the sequence and its q head.
+struct Row {
+  int tok, h;
+  bool ok;
+};
+__device__ __forceinline__ Row row_of(const AttnArgs& a, const Item& it, int r) {
+  Row x;
+  const int tile = r / a.tile_rows, m = r - tile * a.tile_rows;
+  const int t = m / a.sub, g = m - t * a.sub;
+  const int hg = it.lg % a.w.nh, part = hg % a.nsub;
+  x.tok = it.i * a.w.ctok + tile * a.tile_tok + t;
+  x.h = hg / a.nsub * a.G + part * a.sub + g;
+  x.ok = t < a.tile_tok && x.tok < it.s.len && part * a.sub + g < a.G;
+  return x;
+}
+// Index of the row in q, out ([nl * T] tokens, Hq heads) and lse.
+__device__ __forceinline__ size_t out_row(const AttnArgs& a, const Item& it, const Row& x) {
+  return ((size_t)(it.lg / a.w.nh) * a.w.T + it.s.q0 + x.tok) * a.Hq + x.h;
+}
+
+// Natural logarithm of the softmax's sum from its maximum (log2 domain) and scaled sum.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+}  // namespace paged
+}  // namespace medusa

@@ -1,0 +1,439 @@
+// medusa_rope and medusa_paged_append: the rotary embedding in the forms
+// backbones use, and the entry of a chunk's keys and values into the paged
+// cache with the rotation on the way.
+//
+// Pair (x0, x1) of a head at position p turns by a = p f_i:
+//   y0 = m (x0 cos a - x1 sin a),  y1 = m (x1 cos a + x0 sin a).
+// The gradient of the inputs is the same turn by -a.
+//
+// The angle is formed in whole numbers: f_i / 2 pi modulo 1 as a 64-bit
+// fraction (host, from double), times the int32 position modulo 2^64, is the
+// angle in turns with an error of at most |p| 2^-64 turns beyond that of the
+// double frequency.  The nearest quarter turn is split off in the integer, so
+// sincospif sees at most an eighth of a turn, rounded to 24 bits.
+//
+// Bandwidth bounds both calls (each element is read and written once, about 20
+// operations a pair).  A CTA takes one to eight tokens so that a thread has about four
+// 32-byte tasks (two vectors, a pair's halves): their angles are formed once,
+// by all threads, while the first tasks' loads are in flight, and kept in
+// shared memory for every head.
+#include <cmath>
+
+#include "host_util.h"
+#include "paged.cuh"
+
+namespace medusa {
+namespace paged {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxTokens = 8;  // tokens per CTA
+constexpr int kRopeUnroll = 4;     // tasks in flight per thread
+
+struct RopeArgs {
+  const void *q, *k, *v;  // q, k, v may be NULL
+  long long ldq, ldk, ldv;
+  void *q_out, *k_out;  // dense; k_out NULL when keys enter the cache
+  void *k_pages, *v_pages;
+  const int32_t *pos, *q_start, *prefix_len;
+  int32_t* d_status;
+  Cache cache;
+  int nl, T, B, Hq, Hkv, d, rotary, inverse;
+  int tokens;  // per CTA
+  float magnitude;
+  unsigned long long turn[MEDUSA_MAX_HEAD_DIM / 2];
+};
+
+template <int BYTES>
+struct Vec;
+template <>
+struct Vec<16> { using type = uint4; };
+template <>
+struct Vec<8> { using type = uint2; };
+template <>
+struct Vec<4> { using type = uint32_t; };
+template <>
+struct Vec<2> { using type = uint16_t; };
+
+template <typename T, int W>
+union Chunk {  // W elements as one load or store
+  typename Vec<W * sizeof(T)>::type v;
+  T e[W];
+};
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(uint16_t x) { return bf16_bits_to_f32(x); }
+__device__ __forceinline__ void put(float& d, float x) { d = x; }
+__device__ __forceinline__ void put(uint16_t& d, float x) { d = (uint16_t)f32_to_bf16_bits(x); }
+
+// (cos, sin) of p turns of `turn` 2^-64, times m.
+__device__ __forceinline__ float2 turn_of(int p, unsigned long long turn, int inverse, float m) {
+  unsigned long long v = (unsigned long long)(long long)p * turn;
+  if (inverse) v = 0ull - v;
+  const unsigned quarter = (unsigned)((v + (1ull << 61)) >> 62);           // nearest quarter turn, modulo 4
+  const long long rest = (long long)(v - ((unsigned long long)quarter << 62));  // [-2^61, 2^61)
+  float s, c;
+  sincospif((float)(int)(rest >> 31) * 2.3283064365386963e-10f, &s, &c);  // rest 2^-63 half turns, in units of 2^-32
+  float cc = (quarter & 1) ? -s : c, ss = (quarter & 1) ? c : s;
+  if (quarter & 2) {
+    cc = -cc;
+    ss = -ss;
+  }
+  return make_float2(cc * m, ss * m);
+}
+
+template <typename T, int W, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+  using C = Chunk<T, W>;
+  using V = typename Vec<W * sizeof(T)>::type;
+  __shared__ float2 cs[kRopeMaxTokens][MEDUSA_MAX_HEAD_DIM / 2];
+  __shared__ int s_slot[kRopeMaxTokens];  // pool row, -1: not entered, -2: nothing of the token is written
+  __shared__ int s_pos[kRopeMaxTokens];
+  pdl_wait();
+  pdl_trigger();
+  const unsigned per_head = a.d / (2 * W), turned = a.rotary / (2 * W), half = a.rotary / 2;
+  const unsigned hq = a.q ? a.Hq : 0, hk = a.k ? a.Hkv : 0, hv = a.v ? a.Hkv : 0;
+  const unsigned per_tok = (hq + hk + hv) * per_head;
+  const long long tok0 = (long long)blockIdx.x * a.tokens, all = (long long)a.nl * a.T;
+  const int n_tok = (int)(all - tok0 < a.tokens ? all - tok0 : a.tokens);
+  const unsigned tasks = per_tok * (unsigned)n_tok;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // One task: 2 W elements of one head, the two members of W pairs or a plain copy.
+  struct Task {
+    const T *s0, *s1;
+    unsigned tok, head, c;
+  };
+  auto find = [&](unsigned id) {
+    Task t;
+    t.tok = id / per_tok;
+    const unsigned r = id - t.tok * per_tok;
+    t.head = r / per_head;
+    t.c = r - t.head * per_head;
+    const long long at = tok0 + t.tok;
+    const T* base;
+    const bool value = t.head >= hq + hk;
+    if (t.head < hq) base = static_cast<const T*>(a.q) + at * a.ldq + (long long)t.head * a.d;
+    else if (!value) base = static_cast<const T*>(a.k) + at * a.ldk + (long long)(t.head - hq) * a.d;
+    else base = static_cast<const T*>(a.v) + at * a.ldv + (long long)(t.head - hq - hk) * a.d;
+    const bool split = !INTER && !value && t.c < turned;
+    t.s0 = base + (split ? t.c * W : !INTER && !value && t.c >= turned ? a.rotary + (t.c - turned) * 2 * W : t.c * 2 * W);
+    t.s1 = split ? t.s0 + half : t.s0 + W;
+    return t;
+  };
+
+  Task task[kRopeUnroll];
+  C x0[kRopeUnroll], x1[kRopeUnroll];
+  auto load = [&](unsigned first) {
+#pragma unroll
+    for (int u = 0; u < kRopeUnroll; ++u) {
+      const unsigned id = first + u * kRopeThreads;
+      if (id < tasks) {
+        task[u] = find(id);
+        x0[u].v = *reinterpret_cast<const V*>(task[u].s0);
+        x1[u].v = *reinterpret_cast<const V*>(task[u].s1);
+      }
+    }
+  };
+  load(threadIdx.x);
+
+  if (a.k_pages) {
+    // Token tok: its sequence is the number of starts q_start[1 .. B] at or before it.
+    for (int tk = warp; tk < n_tok; tk += kRopeThreads / 32) {
+      const int t = (int)((tok0 + tk) % a.T);
+      int b = 0;
+      for (int j = lane; j < a.B; j += 32) b += __ldg(a.q_start + 1 + j) <= t;
+      b = __reduce_add_sync(0xffffffffu, b);
+      int slot = -2, p = 0;
+      if (b < a.B) {
+        const int q0 = __ldg(a.q_start + b), q1 = __ldg(a.q_start + b + 1), L = __ldg(a.prefix_len + b);
+        int err = MEDUSA_DEV_OK;
+        if (q0 < 0 || q0 > t || q1 > a.T || L < 0 || L > a.cache.rows()) {
+          err = MEDUSA_DEV_BAD_LENGTH;
+        } else {
+          const int row = L + (t - q0);
+          p = row;
+          slot = -1;
+          if (L > a.cache.rows() - (q1 - q0)) err = MEDUSA_DEV_CACHE_OVERFLOW;
+          else if ((slot = pool_row(a.cache, b, row)) < 0) err = MEDUSA_DEV_BAD_INDEX;
+        }
+        if (err && lane == 0) set_status(a.d_status, err);
+      }
+      if (lane == 0) {
+        s_slot[tk] = slot;
+        s_pos[tk] = a.pos ? __ldg(a.pos + t) : p;
+      }
+    }
+    __syncthreads();
+  }
+  for (unsigned j = threadIdx.x; j < half * n_tok; j += kRopeThreads) {
+    const unsigned tk = j / half, i = j - tk * half;
+    const int p = a.k_pages ? s_pos[tk] : __ldg(a.pos + (tok0 + tk) % a.T);
+    cs[tk][i] = turn_of(p, a.turn[i], a.inverse, a.magnitude);
+  }
+  __syncthreads();
+
+  for (unsigned first = threadIdx.x; first < tasks; first += kRopeUnroll * kRopeThreads) {
+    if (first != threadIdx.x) load(first);
+#pragma unroll
+    for (int u = 0; u < kRopeUnroll; ++u) {
+      if (first + u * kRopeThreads >= tasks) break;
+      const Task& t = task[u];
+      const long long at = tok0 + t.tok;
+      const int slot = a.k_pages ? s_slot[t.tok] : 0;
+      if (slot == -2) continue;
+      T* dst;
+      if (t.head < hq) {
+        dst = static_cast<T*>(a.q_out) + (at * a.Hq + t.head) * a.d;
+      } else {
+        const bool value = t.head >= hq + hk;
+        const unsigned h = t.head - hq - (value ? hk : 0u);
+        if (a.k_pages) {
+          if (slot < 0) continue;
+          const long long row = (at / a.T) * ((long long)a.cache.n_pages * a.cache.page_size) + slot;
+          dst = static_cast<T*>(value ? a.v_pages : a.k_pages) + (row * a.Hkv + h) * a.d;
+        } else {
+          dst = static_cast<T*>(a.k_out) + (at * a.Hkv + h) * a.d;
+        }
+        if (value) {
+          dst += t.c * 2 * W;
+          *reinterpret_cast<V*>(dst) = x0[u].v;
+          *reinterpret_cast<V*>(dst + W) = x1[u].v;
+          continue;
+        }
+      }
+      if (t.c >= turned) {  // behind the turned part
+        dst += a.rotary + (t.c - turned) * 2 * W;
+        *reinterpret_cast<V*>(dst) = x0[u].v;
+        *reinterpret_cast<V*>(dst + W) = x1[u].v;
+        continue;
+      }
+      const float2* f = cs[t.tok] + t.c * W;
+      C y0, y1;
+      if constexpr (INTER) {  // pairs follow one another through both vectors
+        T xs[2 * W], ys[2 * W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          xs[e] = x0[u].e[e];
+          xs[W + e] = x1[u].e[e];
+        }
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const float p0 = to_f32(xs[2 * e]), p1 = to_f32(xs[2 * e + 1]);
+          put(ys[2 * e], p0 * f[e].x - p1 * f[e].y);
+          put(ys[2 * e + 1], p1 * f[e].x + p0 * f[e].y);
+        }
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          y0.e[e] = ys[e];
+          y1.e[e] = ys[W + e];
+        }
+        dst += t.c * 2 * W;
+        *reinterpret_cast<V*>(dst) = y0.v;
+        *reinterpret_cast<V*>(dst + W) = y1.v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const float p0 = to_f32(x0[u].e[e]), p1 = to_f32(x1[u].e[e]);
+          put(y0.e[e], p0 * f[e].x - p1 * f[e].y);
+          put(y1.e[e], p1 * f[e].x + p0 * f[e].y);
+        }
+        dst += t.c * W;
+        *reinterpret_cast<V*>(dst) = y0.v;
+        *reinterpret_cast<V*>(dst + half) = y1.v;
+      }
+    }
+  }
+}
+
+// Elements per vector: the widest of 16 bytes and below that divides every
+// offset the kernel forms.
+static int rope_width(const RopeArgs& a, size_t es) {
+  for (int w = (int)(16 / es); w > 1; w /= 2) {
+    auto fits = [&](const void* p) { return (reinterpret_cast<uintptr_t>(p) & (w * es - 1)) == 0; };
+    if (a.d % (2 * w) || a.rotary % (2 * w)) continue;
+    if (!fits(a.q) || !fits(a.k) || !fits(a.v) || !fits(a.q_out) || !fits(a.k_out) || !fits(a.k_pages) || !fits(a.v_pages))
+      continue;
+    if ((a.q && a.ldq % w) || (a.k && a.ldk % w) || (a.v && a.ldv % w)) continue;
+    return w;
+  }
+  return 1;
+}
+
+template <typename T, int W>
+static void rope_go(const RopeArgs& a, bool inter, unsigned grid, cudaStream_t s) {
+  if (inter) launch_pdl(rope_kernel<T, W, true>, dim3(grid), dim3(kRopeThreads), 0, s, a);
+  else launch_pdl(rope_kernel<T, W, false>, dim3(grid), dim3(kRopeThreads), 0, s, a);
+}
+
+static medusa_status rope_launch(RopeArgs& a, const medusa_rope_plan* plan, medusa_dtype dt, cudaStream_t s) {
+  if (plan) {
+    a.rotary = plan->rotary_dim;
+    a.magnitude = plan->magnitude;
+    for (int i = 0; i < a.rotary / 2; ++i) a.turn[i] = plan->turn[i];
+  }
+  const int w = rope_width(a, dtype_bytes(dt));
+  const long long all = (long long)a.nl * a.T;
+  const long long per_tok = (long long)((a.q ? a.Hq : 0) + (a.k ? a.Hkv : 0) + (a.v ? a.Hkv : 0)) * (a.d / (2 * w));
+  // Tokens per CTA: enough for a thread's tasks in flight, but first one CTA per SM.
+  long long n = (kRopeThreads * kRopeUnroll + per_tok - 1) / per_tok;
+  const long long spread = all / (2 * device_sm_count());
+  if (n > spread) n = spread;
+  a.tokens = n < 1 ? 1 : n > kRopeMaxTokens ? kRopeMaxTokens : (int)n;
+  const unsigned grid = (unsigned)((all + a.tokens - 1) / a.tokens);
+  const bool inter = plan && plan->interleaved;
+  if (dt == MEDUSA_BF16) {
+    if (w == 8) rope_go<uint16_t, 8>(a, inter, grid, s);
+    else if (w == 4) rope_go<uint16_t, 4>(a, inter, grid, s);
+    else if (w == 2) rope_go<uint16_t, 2>(a, inter, grid, s);
+    else rope_go<uint16_t, 1>(a, inter, grid, s);
+  } else {
+    if (w == 4) rope_go<float, 4>(a, inter, grid, s);
+    else if (w == 2) rope_go<float, 2>(a, inter, grid, s);
+    else rope_go<float, 1>(a, inter, grid, s);
+  }
+  return launch_status();
+}
+
+// Bytes from the first to behind the last element of [nl][T][H][d] with token stride ld.
+static size_t span(int nl, int T, long long ld, int H, int d, size_t es) {
+  return ((size_t)((long long)nl * T - 1) * (size_t)ld + (size_t)H * d) * es;
+}
+
+static bool plan_ok(const medusa_rope_plan* p, int d) {
+  return p->rotary_dim >= 2 && p->rotary_dim % 2 == 0 && p->rotary_dim <= d && std::isfinite(p->magnitude);
+}
+
+}  // namespace paged
+}  // namespace medusa
+
+using namespace medusa;
+using namespace medusa::paged;
+
+extern "C" medusa_status medusa_rope_plan_init(int rotary_dim, int interleaved, double base, medusa_rope_scaling scaling,
+                                               double factor, double low, double high, int original_len,
+                                               double magnitude, medusa_rope_plan* out) {
+  if (!out || rotary_dim < 2 || rotary_dim % 2 || rotary_dim > MEDUSA_MAX_HEAD_DIM) return MEDUSA_ERR_INVALID_ARG;
+  if (!(base > 0.0) || !std::isfinite(base) || !std::isfinite(magnitude)) return MEDUSA_ERR_INVALID_ARG;
+  const int kind = (int)scaling;
+  if (kind < MEDUSA_ROPE_PLAIN || kind > MEDUSA_ROPE_RAMP) return MEDUSA_ERR_INVALID_ARG;
+  if (kind != MEDUSA_ROPE_PLAIN && !(factor > 0.0 && std::isfinite(factor))) return MEDUSA_ERR_INVALID_ARG;
+  const bool bands = kind == MEDUSA_ROPE_BANDS, ramp = kind == MEDUSA_ROPE_RAMP;
+  if ((bands || ramp) && !(low > 0.0 && high > low && std::isfinite(high) && original_len >= 1)) return MEDUSA_ERR_INVALID_ARG;
+  if (ramp && !(base > 1.0)) return MEDUSA_ERR_INVALID_ARG;
+  const double kTwoPi = 6.283185307179586476925286766559;
+  double from = 0.0, to = 1.0;
+  if (ramp) {
+    auto pair = [&](double turns) { return rotary_dim * std::log(original_len / (kTwoPi * turns)) / (2.0 * std::log(base)); };
+    from = std::fmax(std::floor(pair(high)), 0.0);
+    to = std::fmin(std::ceil(pair(low)), (double)(rotary_dim - 1));
+  }
+  *out = medusa_rope_plan{};
+  out->rotary_dim = rotary_dim;
+  out->interleaved = interleaved ? 1 : 0;
+  out->magnitude = (float)magnitude;
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / rotary_dim);
+    double keep = 1.0, g = f;
+    if (kind == MEDUSA_ROPE_LINEAR) {
+      g = f / factor;
+    } else if (bands || ramp) {
+      keep = bands ? (original_len * f / kTwoPi - low) / (high - low) : 1.0 - (i - from) / std::fmax(to - from, 0.001);
+      keep = std::fmin(std::fmax(keep, 0.0), 1.0);
+      g = keep * f + (1.0 - keep) * f / factor;
+    }
+    const double turns = g / kTwoPi;
+    if (!std::isfinite(turns)) return MEDUSA_ERR_INVALID_ARG;
+    out->turn[i] = (uint64_t)std::ldexp(turns - std::floor(turns), 64);
+  }
+  return MEDUSA_OK;
+}
+
+extern "C" medusa_status medusa_rope(const void* q, int64_t ldq, const void* k, int64_t ldk, const int32_t* pos,
+                                     const medusa_rope_plan* plan, int inverse, int n_layers, int T, int Hq, int Hkv,
+                                     int d, medusa_dtype dt, void* q_out, void* k_out, medusa_stream_t stream) {
+  if (!q || !q_out || !pos || !plan || (k != nullptr) != (k_out != nullptr) || !dtype_ok(dt)) return MEDUSA_ERR_INVALID_ARG;
+  if (n_layers < 1 || T < 1 || Hq < 1 || (k && Hkv < 1) || d < 2 || d % 2 || d > MEDUSA_MAX_HEAD_DIM) return MEDUSA_ERR_INVALID_ARG;
+  if ((long long)n_layers * T > 0x7fffffffll || Hq > 65535 || Hkv > 65535 || !plan_ok(plan, d)) return MEDUSA_ERR_INVALID_ARG;
+  if (ldq < (int64_t)Hq * d || (k && ldk < (int64_t)Hkv * d)) return MEDUSA_ERR_INVALID_ARG;
+  const size_t es = dtype_bytes(dt);
+  const uintptr_t all = (uintptr_t)q | (uintptr_t)k | (uintptr_t)q_out | (uintptr_t)k_out;
+  if ((all & (es - 1)) || ((uintptr_t)pos & 3)) return MEDUSA_ERR_INVALID_ARG;
+  const size_t nq = span(n_layers, T, ldq, Hq, d, es), nk = k ? span(n_layers, T, ldk, Hkv, d, es) : 0;
+  const size_t oq = span(n_layers, T, (long long)Hq * d, Hq, d, es), ok = k ? span(n_layers, T, (long long)Hkv * d, Hkv, d, es) : 0;
+  const size_t np = (size_t)T * 4;
+  if (!(q_out == q && ldq == (int64_t)Hq * d) && overlaps(q, nq, q_out, oq)) return MEDUSA_ERR_ALIAS;
+  if (overlaps(q_out, oq, pos, np)) return MEDUSA_ERR_ALIAS;
+  if (k) {
+    if (!(k_out == k && ldk == (int64_t)Hkv * d) && overlaps(k, nk, k_out, ok)) return MEDUSA_ERR_ALIAS;
+    if (overlaps(q_out, oq, k, nk) || overlaps(q_out, oq, k_out, ok) || overlaps(k_out, ok, q, nq) || overlaps(k_out, ok, pos, np))
+      return MEDUSA_ERR_ALIAS;
+  }
+  RopeArgs a{};
+  a.q = q;
+  a.k = k;
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.pos = pos;
+  a.nl = n_layers;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.inverse = inverse ? 1 : 0;
+  return rope_launch(a, plan, dt, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" medusa_status medusa_paged_append(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                                             int64_t ldv, const int32_t* pos, const medusa_rope_plan* plan,
+                                             const int32_t* page_table, const int32_t* q_start, const int32_t* prefix_len,
+                                             int n_layers, int T, int B, int Hq, int Hkv, int d, int n_pages,
+                                             int page_size, int max_pages, medusa_dtype dt, void* q_out, void* k_pages,
+                                             void* v_pages, int32_t* d_status, medusa_stream_t stream) {
+  if (!k || !v || !page_table || !q_start || !prefix_len || !k_pages || !v_pages || (q != nullptr) != (q_out != nullptr))
+    return MEDUSA_ERR_INVALID_ARG;
+  if (!dtype_ok(dt) || n_layers < 1 || T < 1 || B < 1 || (q && Hq < 1) || Hkv < 1 || d < 2 || d % 2 || d > MEDUSA_MAX_HEAD_DIM)
+    return MEDUSA_ERR_INVALID_ARG;
+  if (!cache_sizes_ok(n_layers, n_pages, page_size, max_pages) || (long long)n_layers * T > 0x7fffffffll) return MEDUSA_ERR_INVALID_ARG;
+  if (Hq > 65535 || Hkv > 65535 || (plan && !plan_ok(plan, d))) return MEDUSA_ERR_INVALID_ARG;
+  if ((q && ldq < (int64_t)Hq * d) || ldk < (int64_t)Hkv * d || ldv < (int64_t)Hkv * d) return MEDUSA_ERR_INVALID_ARG;
+  const size_t es = dtype_bytes(dt);
+  const uintptr_t all = (uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out | (uintptr_t)k_pages | (uintptr_t)v_pages;
+  const uintptr_t words = (uintptr_t)pos | (uintptr_t)page_table | (uintptr_t)q_start | (uintptr_t)prefix_len;
+  if ((all & (es - 1)) || (words & 3)) return MEDUSA_ERR_INVALID_ARG;
+  const size_t np = (size_t)n_layers * n_pages * page_size * Hkv * d * es;
+  const size_t nk = span(n_layers, T, ldk, Hkv, d, es), nv = span(n_layers, T, ldv, Hkv, d, es);
+  const size_t nq = q ? span(n_layers, T, ldq, Hq, d, es) : 0, oq = q ? span(n_layers, T, (long long)Hq * d, Hq, d, es) : 0;
+  if (overlaps(k_pages, np, v_pages, np)) return MEDUSA_ERR_ALIAS;
+  for (const void* pool : {(const void*)k_pages, (const void*)v_pages})
+    if (overlaps(pool, np, k, nk) || overlaps(pool, np, v, nv) || (q && (overlaps(pool, np, q, nq) || overlaps(pool, np, q_out, oq))))
+      return MEDUSA_ERR_ALIAS;
+  if (q) {
+    if (!(q_out == q && ldq == (int64_t)Hq * d) && overlaps(q, nq, q_out, oq)) return MEDUSA_ERR_ALIAS;
+    if (overlaps(q_out, oq, k, nk) || overlaps(q_out, oq, v, nv)) return MEDUSA_ERR_ALIAS;
+  }
+  RopeArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.q_out = q_out;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.pos = pos;
+  a.q_start = q_start;
+  a.prefix_len = prefix_len;
+  a.d_status = d_status;
+  a.cache = Cache{page_table, n_pages, page_size, max_pages};
+  a.nl = n_layers;
+  a.T = T;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.magnitude = 1.f;
+  return rope_launch(a, plan, dt, reinterpret_cast<cudaStream_t>(stream));
+}
