@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(256) paged_attn_merge_kernel(const __grid_cons
 
 // How a call is divided: which kernel, its block of rows and its CTAs.
 struct Division {
+  bool tc;
   int R, ctas, KT, min_tiles, sub, nsub, tile_rows, tile_tok, ctok;
 };
 
@@ -310,11 +311,26 @@ static int pow2_at_most(int x) {
   return p;
 }
 
+static bool tc_shape(int G, int d, int page_size, medusa_dtype dt) {
+  return dt == MEDUSA_BF16 && d >= 8 && d <= 128 && d % 8 == 0 && page_size % 8 == 0 && G <= 128;
+}
+
 static Division divide(int T, int B, int Hq, int Hkv, int d, int page_size, medusa_dtype dt) {
   Division v{};
   const int G = Hq / Hkv, sms = device_sm_count();
-  (void)page_size;
-  (void)dt;
+  v.tc = tc_shape(G, d, page_size, dt);
+  if (v.tc) {
+    v.R = 256;
+    v.tile_rows = 128;
+    v.ctas = sms;
+    v.KT = 128;
+    v.min_tiles = 2;
+    v.sub = G;
+    v.nsub = 1;
+    v.tile_tok = pow2_at_most(128 / G);
+    v.ctok = 2 * v.tile_tok;
+    return v;
+  }
   // Rows of a tile: 16 when a sequence has at most 16 on average (decoding), else 64.
   v.R = (long long)T * G <= 16ll * B || d > 128 ? 16 : 64;
   v.tile_rows = v.R;
@@ -376,7 +392,7 @@ static medusa_status attend(AttnArgs& a, int n_layers, int T, int B, int Hq, int
   a.w.min_tiles = v.min_tiles;
   a.w.B = B;
   a.w.T = T;
-  const medusa_status st = dt == MEDUSA_BF16 ? simt_launch<uint16_t>(a, s) : simt_launch<float>(a, s);
+  const medusa_status st = v.tc ? paged_attention_tc(a, s) : dt == MEDUSA_BF16 ? simt_launch<uint16_t>(a, s) : simt_launch<float>(a, s);
   if (st != MEDUSA_OK) return st;
   const dim3 grid(v.ctas - 1, v.R > 64 ? 4 : 1);
   if (dt == MEDUSA_BF16) launch_pdl(paged_attn_merge_kernel<uint16_t>, grid, dim3(256), 0, s, a);
@@ -417,6 +433,7 @@ extern "C" medusa_status medusa_paged_attention(const void* q, int64_t ldq, cons
     return MEDUSA_ERR_INVALID_ARG;
   const uintptr_t words = (uintptr_t)page_table | (uintptr_t)q_start | (uintptr_t)prefix_len | (uintptr_t)lse;
   if (words & 3) return MEDUSA_ERR_INVALID_ARG;
+  if (tc_shape(Hq / Hkv, d, page_size, dt) && ldq % 8) return MEDUSA_ERR_INVALID_ARG;
   const size_t es = dtype_bytes(dt), tokens = (size_t)n_layers * T;
   const size_t nq = ((tokens - 1) * (size_t)ldq + (size_t)Hq * d) * es, no = tokens * Hq * d * es;
   const size_t np = (size_t)n_layers * n_pages * page_size * Hkv * d * es, nl = tokens * Hq * 4;

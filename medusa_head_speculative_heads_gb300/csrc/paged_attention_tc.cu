@@ -1,0 +1,597 @@
+// Paged attention on tcgen05 tensor cores: bf16, head dims up to 128 (computed
+// as 64 or 128 columns, the rest zeros), fp32 scores and sums in tensor memory.
+//
+// The mathematics is that of paged_attention.cu: one pass over the key tiles
+// with a running maximum and sum per row.  An item is a block of up to 2 x 128
+// query rows (token, q head of the group) of one sequence and kv head; a key
+// tile is 128 rows of the cache (or of the tree).
+//
+// Two streams run side by side in a CTA, each with its own scores S and sums O
+// in tensor memory (4 x 128 columns, all of it), its own MMA-issuing warp and
+// its own four softmax warps (a thread holds one query row), so that one's
+// softmax runs under the other's products:
+//  - a block of more than 128 rows: stream s has rows 128 s .. 128 s + 127, and
+//    both use every K and V tile, read from global memory once;
+//  - a block of at most 128 rows (decoding, small trees): both streams have the
+//    same rows, stream s the key tiles t0 + s, t0 + s + 2, ...; their two
+//    results are added as two parts of a row are.
+// Within a stream S = Q K^T, softmax, O += P V follow one another; P (bf16)
+// overwrites S, and the next tile's S is issued by the same thread behind the
+// P V that reads P, which orders the two.  A completed S therefore also says
+// that the P V before it is done, and O may be rescaled; that happens only when
+// a row's maximum has grown by more than 2^8 (the stale maximum is exact
+// arithmetic: the same power of two scales P and the sum).
+//
+// Warp 0 brings Q and the K and V tiles by TMA into a ring of 128-row slots.
+// A tile is copied in boxes of gcd(page_size, 128) rows, one lane each looking
+// its page up; a page that does not exist is read as rows behind the pool,
+// which arrive as zeros.  Rows behind the last one are masked in S; the rows
+// of V up to the next multiple of 16 are zeroed before P V reads them (0 times
+// what a stale row holds could be NaN), and the products stop there.
+//
+// Every wait is bounded: a timeout sets MEDUSA_DEV_TIMEOUT, all roles stop,
+// copies and MMAs in flight are waited for and tensor memory is freed.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "host_util.h"
+#include "paged_attn.cuh"
+#include "sm100.cuh"
+
+namespace medusa {
+namespace paged {
+using namespace sm100;
+
+namespace tc {
+
+constexpr int kThreads = 384;          // TMA, two MMA issuers, one idle; 2 x 4 softmax warps
+constexpr int kKeys = 128;             // keys of a tile
+constexpr uint32_t kHalf = 16384;      // 128 rows x 128 bytes (64 columns)
+constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr uint64_t kDrainNs = 100000000ull;
+constexpr uint32_t kTmemCols = 512;    // S0, S1, O0, O1
+constexpr int kMaxSlots = 10;
+
+// DH: columns computed, 64 or 128.
+template <int DH>
+struct Cfg {
+  static constexpr int halves = DH / 64;
+  static constexpr uint32_t slot = halves * kHalf;  // K or V of one tile; also Q of one stream
+  static constexpr int slots = DH == 128 ? 5 : 10;
+  static constexpr uint32_t off_ring = 2 * slot;
+  static constexpr uint32_t off_bar = off_ring + slots * slot;
+  static constexpr uint32_t smem = off_bar + 512 + 1024;  // barriers, alignment
+  static constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false, false);
+  static constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DH, false, true);
+};
+
+struct Bars {
+  uint64_t full[kMaxSlots], empty[kMaxSlots];  // empty: two releases (a sole user's two)
+  uint64_t q_full[2], q_empty[2];              // likewise
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2], ml_full, drain[2];
+};
+
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// All lanes wait; true when all saw the phase end (the tcgen05 operations that
+// follow are warp-collective).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const bool ok = mbar_wait_bounded(bar, parity, abort, kWaitNs);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// 2^x on the SFU: relative error about 2^-22, far below P's rounding to bf16.
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void st_v8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+               "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+// The part of an item that a CTA works on, and how its two streams share it.
+struct Unit {
+  int t0, t1;       // key tiles
+  bool two;         // two row tiles; else one, its key tiles taken in turn
+  int pre;          // the item's tiles of cache rows (the rest are tree tiles)
+  int rows_end;     // cache rows the block may see
+  int l, kvh;
+};
+__device__ __forceinline__ Unit unit_of(const AttnArgs& a, const Item& it, long long u, long long u1) {
+  Unit x;
+  x.t0 = (int)(u - it.first);
+  x.t1 = (int)((it.first + it.tiles < u1 ? it.first + it.tiles : u1) - it.first);
+  const int tok0 = it.i * a.w.ctok;
+  x.two = it.s.len - tok0 > a.tile_tok;
+  x.rows_end = a.w.N ? it.s.L : it.s.L + min(it.s.len, tok0 + a.w.ctok);
+  x.pre = a.w.N ? (it.s.L + kKeys - 1) / kKeys : it.tiles;
+  x.l = it.lg / a.w.nh;
+  x.kvh = it.lg - x.l * a.w.nh;
+  return x;
+}
+// Key tiles [t0, end) that stream s of a two-tile block uses: a causal first
+// half does not see the tiles only the second one does.
+__device__ __forceinline__ int stream_end(const AttnArgs& a, const Item& it, const Unit& x, int s) {
+  if (!x.two || s == 1 || a.w.N) return x.t1;
+  const int seen = (it.s.L + it.i * a.w.ctok + a.tile_tok + kKeys - 1) / kKeys;
+  return min(x.t1, seen);
+}
+// Keys of tile t that rows of stream s may see, at most 128.
+__device__ __forceinline__ int tile_keys(const AttnArgs& a, const Item& it, const Unit& x, int s, int t) {
+  if (t >= x.pre) return min(kKeys, a.w.N - (t - x.pre) * kKeys);
+  int end = x.rows_end;
+  if (x.two && s == 0 && !a.w.N) end = it.s.L + it.i * a.w.ctok + a.tile_tok;
+  return min(kKeys, end - t * kKeys);
+}
+// Rows of tile t that were copied and may be read as they are.
+__device__ __forceinline__ int tile_rows_loaded(const AttnArgs& a, const Unit& x, int t) {
+  return t >= x.pre ? min(kKeys, a.w.N - (t - x.pre) * kKeys) : min(kKeys, x.rows_end - t * kKeys);
+}
+
+}  // namespace tc
+
+template <int DH>
+__global__ void __launch_bounds__(tc::kThreads, 1)
+paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kt,
+                     const __grid_constant__ CUtensorMap tm_vt, const __grid_constant__ AttnArgs a, const int box_rows) {
+  using namespace tc;
+  using C = Cfg<DH>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  static_assert(sizeof(Bars) <= 512, "barrier area");
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::off_bar);
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  __shared__ union {
+    long long plan[68];  // set-up only
+    float2 ml[128];      // stream 1's row maxima and sums, for stream 0 to add
+  } sh;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    for (int i = 0; i < C::slots; ++i) {
+      mbar_init(&bars->full[i], 1);
+      mbar_init(&bars->empty[i], 2);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->q_full[s], 1);
+      mbar_init(&bars->q_empty[s], 2);
+      mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->p_full[s], 128);
+      mbar_init(&bars->o_full[s], 1);
+      mbar_init(&bars->o_free[s], 128);
+      mbar_init(&bars->drain[s], 1);
+    }
+    mbar_init(&bars->ml_full, 128);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&s_tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch(&tm_q);
+    tma_prefetch(&tm_k);
+    tma_prefetch(&tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // Nothing above reads memory an earlier kernel may write.
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t tmem = s_tmem;
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < a.w.B; b += kThreads)
+      if (!seq_of(a.w, b).ok) set_status(a.d_status, MEDUSA_DEV_BAD_LENGTH);
+  Plan pl;
+  Item it;
+  const bool any = plan_find(a.w, pl, it, sh.plan, [](const Plan& p) { return p.Q * blockIdx.x; });
+  const long long u0 = pl.Q * blockIdx.x, u1 = any ? (u0 + pl.Q < pl.U ? u0 + pl.Q : pl.U) : u0;
+  __syncthreads();  // sh.plan is no longer read
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    int c = 0, issued = 0;  // slots used
+    int qn0 = 0, qn1 = 0, qsel = 0;  // loads into the two Q buffers
+    bool alive = true;
+    const int box = lane & 15, half = lane >> 4;
+    const long long pool_rows = (long long)a.cache.n_pages * a.cache.page_size;
+    for (long long u = u0; u < u1 && alive;) {
+      const Unit x = unit_of(a, it, u, u1);
+      const int row0 = x.l * a.w.T + it.s.q0 + it.i * a.w.ctok;
+      for (int k = 0; k < (x.two ? 2 : 1) && alive; ++k) {
+        const int qb = x.two ? k : qsel, used = qb ? qn1 : qn0;
+        if (used > 0 && !(alive = warp_wait(&bars->q_empty[qb], (used - 1) & 1, &s_abort))) break;
+        if (lane == 0) {
+          mbar_expect_tx(&bars->q_full[qb], (uint32_t)(C::halves * a.tile_tok * a.G * 128));
+          for (int h = 0; h < C::halves; ++h)
+            tma_load_3d(smem + qb * C::slot + h * kHalf, &tm_q, &bars->q_full[qb], 64 * h, x.kvh * a.G, row0 + k * a.tile_tok);
+        }
+        qn0 += qb == 0;
+        qn1 += qb == 1;
+      }
+      if (!x.two) qsel ^= 1;
+      // The pool row of this lane's box of tile t (behind the pool: zeros).
+      auto box_row = [&](int t) {
+        const int r = t * kKeys + box * box_rows;
+        int row = (int)(pool_rows * a.w.nl);
+        if (t < x.pre && box < kKeys / box_rows && r < x.rows_end) {
+          const int in = pool_row(a.cache, it.b, r);
+          if (in >= 0) row = (int)(pool_rows * x.l) + in;
+          else if (half == 0) set_status(a.d_status, MEDUSA_DEV_BAD_INDEX);
+        }
+        return row;
+      };
+      int row = box_row(x.t0);
+      for (int t = x.t0; t < x.t1 && alive; ++t) {
+        const bool tree = t >= x.pre;
+        const int step = tree ? 64 : box_rows;
+        const int boxes = (tile_rows_loaded(a, x, t) + step - 1) / step;
+        const int at = tree ? x.l * a.w.T + it.s.q0 + (t - x.pre) * kKeys + box * 64 : row;
+        if (t + 1 < x.t1) row = box_row(t + 1);  // its latency passes under this tile's waits
+        for (int kv = 0; kv < 2; ++kv, ++c) {
+          const int sl = c % C::slots;
+          if (c >= C::slots && !(alive = warp_wait(&bars->empty[sl], (uint32_t)(c / C::slots - 1) & 1u, &s_abort))) break;
+          if (lane == 0) mbar_expect_tx(&bars->full[sl], (uint32_t)(boxes * step * 128 * C::halves));
+          __syncwarp();
+          issued = c + 1;
+          if (box < boxes && half < C::halves)
+            tma_load_3d(smem + C::off_ring + sl * C::slot + half * kHalf + box * step * 128,
+                        kv ? (tree ? &tm_vt : &tm_v) : (tree ? &tm_kt : &tm_k), &bars->full[sl], 64 * half, x.kvh, at);
+        }
+      }
+      u = it.first + x.t1;
+      if (u < u1 && !next_item(a.w, it)) break;
+    }
+    if (!alive) {
+      // No copy may land after exit: wait (bounded) for the last phase of every load barrier.
+      if (qn0 > 0) mbar_wait_bounded(&bars->q_full[0], (qn0 - 1) & 1, nullptr, kDrainNs);
+      if (qn1 > 0) mbar_wait_bounded(&bars->q_full[1], (qn1 - 1) & 1, nullptr, kDrainNs);
+      for (int i = issued - 1; i >= 0 && i >= issued - C::slots; --i)
+        mbar_wait_bounded(&bars->full[i % C::slots], (uint32_t)(i / C::slots) & 1u, nullptr, kDrainNs);
+    }
+  } else if (warp == 1 || warp == 2) {
+    // ------------------------------------------------------------ MMA issuer of stream s
+    const int s = warp - 1;
+    const uint32_t ts = tmem + 128 * s, to = tmem + 256 + 128 * s;
+    int g = 0;                       // tiles of earlier units (two ring slots each)
+    int qn0 = 0, qn1 = 0, qsel = 0, n = 0, np = 0;  // n: units, np: tiles of this stream
+    bool alive = true;
+    for (long long u = u0; u < u1 && alive;) {
+      const Unit x = unit_of(a, it, u, u1);
+      const int qb = x.two ? s : qsel, end = stream_end(a, it, x, s);
+      const int other_end = stream_end(a, it, x, 1 - s);
+      if (!(alive = warp_wait(&bars->q_full[qb], (qb ? qn1 : qn0) & 1, &s_abort))) break;
+      // The other stream's rows too: every phase of a buffer is seen before a later one is waited for.
+      if (x.two && !(alive = warp_wait(&bars->q_full[1 - qb], (qb ? qn0 : qn1) & 1, &s_abort))) break;
+      const int first = x.two ? x.t0 : x.t0 + s, step = x.two ? 1 : 2;
+      bool freed = false;  // O read out by the unit before
+      const uint32_t qa = smem_u32(smem + qb * C::slot);
+      for (int t = first; t < end; t += step, ++np) {
+        const int ck = 2 * (g + t - x.t0), cv = ck + 1;
+        const int releases = x.two && t < other_end ? 1 : 2;
+        uint64_t* ek = &bars->empty[ck % C::slots];
+        uint64_t* ev = &bars->empty[cv % C::slots];
+        if (!(alive = warp_wait(&bars->full[ck % C::slots], (uint32_t)(ck / C::slots) & 1u, &s_abort))) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t ka = smem_u32(smem + C::off_ring + (ck % C::slots) * C::slot);
+#pragma unroll
+          for (int kk = 0; kk < DH / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+            mma_bf16(ts, smem_desc_sw128(qa + off, 16, 1024), smem_desc_sw128(ka + off, 16, 1024), C::idesc_qk, kk > 0);
+          }
+          for (int r = 0; r < releases; ++r) mma_commit(ek);
+          if (t + step >= end)
+            for (int r = 0; r < (x.two ? 2 : 1); ++r) mma_commit(&bars->q_empty[qb]);
+          mma_commit(&bars->s_full[s]);
+        }
+        __syncwarp();
+        if (!freed) {
+          if (n > 0 && !(alive = warp_wait(&bars->o_free[s], (n - 1) & 1, &s_abort))) break;
+          freed = true;
+        }
+        if (!(alive = warp_wait(&bars->full[cv % C::slots], (uint32_t)(cv / C::slots) & 1u, &s_abort))) break;
+        const int keys = tile_keys(a, it, x, s, t), steps = (keys + 15) >> 4, have = tile_rows_loaded(a, x, t);
+        uint8_t* vb = smem + C::off_ring + (cv % C::slots) * C::slot;
+        if (have < steps * 16) {
+          for (int i = lane; i < (steps * 16 - have) * 8 * C::halves; i += 32) {
+            const int r = have + i / (8 * C::halves), cc = i % (8 * C::halves);
+            *reinterpret_cast<uint4*>(vb + (cc >> 3) * kHalf + r * 128 + (cc & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (!(alive = warp_wait(&bars->p_full[s], np & 1, &s_abort))) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t va = smem_u32(vb);
+          for (int kk = 0; kk < steps; ++kk)
+            mma_bf16_ts(to, ts + 8 * kk, smem_desc_sw128(va + kk * 2048, kHalf, 1024), C::idesc_pv, kk > 0 || t > first);
+          for (int r = 0; r < releases; ++r) mma_commit(ev);
+          if (t + step >= end) mma_commit(&bars->o_full[s]);
+        }
+        __syncwarp();
+      }
+      if (!alive) break;
+      if (first >= end) {  // no tile of this unit is this stream's
+        if (lane == 0)
+          for (int r = 0; r < (x.two ? 2 : 1); ++r) mbar_arrive(&bars->q_empty[qb]);
+        __syncwarp();
+      }
+      if (!freed && n > 0 && !(alive = warp_wait(&bars->o_free[s], (n - 1) & 1, &s_abort))) break;
+      qn0 += x.two || qsel == 0;
+      qn1 += x.two || qsel == 1;
+      if (!x.two) qsel ^= 1;
+      g += x.t1 - x.t0;
+      ++n;
+      u = it.first + x.t1;
+      if (u < u1 && !next_item(a.w, it)) break;
+    }
+    if (lane == 0) {
+      // This warp's MMAs and the arrives they signal, before TMEM and shared memory go away.
+      mma_commit(&bars->drain[s]);
+      mbar_wait_bounded(&bars->drain[s], 0, nullptr, kDrainNs);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax and output of stream s
+    const int s = (warp - 4) >> 2, q4 = warp & 3;
+    const int m = 32 * q4 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16);
+    const uint32_t ts = lanes + 128 * s, to = lanes + 256;
+    const float sc = a.scale_log2;
+    int n = 0, ns = 0, nb = 0;       // units, tiles, units of one row tile
+    int no = 0, no1 = 0;             // accumulators finished: this stream's, and stream 1's as stream 0 counts them
+    bool alive = true;
+    for (long long u = u0; u < u1 && alive;) {
+      const Unit x = unit_of(a, it, u, u1);
+      const int rt = x.two ? s : 0, end = stream_end(a, it, x, s);
+      const Row row = row_of(a, it, rt * 128 + m);
+      const bool busy = __any_sync(0xffffffffu, row.ok);  // some row of this warp exists
+      const int first = x.two ? x.t0 : x.t0 + s, step = x.two ? 1 : 2;
+      const int tok_first = it.i * a.w.ctok + rt * a.tile_tok;
+      const int sees = a.w.N ? it.s.L : it.s.L + row.tok + 1;                 // cache rows this row sees
+      const int all_see = a.w.N ? it.s.L : it.s.L + tok_first + 1;            // that every row sees
+      float mu = -INFINITY, sum = 0.f;
+      for (int t = first; t < end; t += step, ++ns) {
+        if (!(alive = warp_wait(&bars->s_full[s], ns & 1, &s_abort))) break;
+        if (busy) {
+          tc_fence_after();
+          // Two passes over S in halves of 64 columns (the second one reads tensor memory
+          // again: holding 128 scores took more registers than a thread has).
+          const int keys = tile_keys(a, it, x, s, t), hs = (keys + 63) >> 6;
+          const bool tree = t >= x.pre;
+          const bool masked = tree || keys < kKeys || t * kKeys + kKeys > all_see;
+          uint32_t w[4] = {0u, 0u, 0u, 0u};  // keys this row sees
+          if (masked) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int j = (tree ? t - x.pre : t) * kKeys + 32 * q;  // first key of the word
+              const int lim = (tree ? a.w.N : sees) - j;
+              if (row.ok && lim > 0) {
+                w[q] = lim >= 32 ? 0xffffffffu : (1u << lim) - 1u;
+                if (tree) w[q] &= __ldg(a.mask + (size_t)row.tok * a.W + (j >> 5));
+              }
+            }
+          }
+          float v[64];
+          auto load = [&](int h) {
+            tmem_ld32(ts + 64 * h, v);
+            tmem_ld32(ts + 64 * h + 32, v + 32);
+            tmem_wait_ld();
+            if (masked) {
+              const uint32_t wa = h ? w[2] : w[0], wb = h ? w[3] : w[1];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                v[i] = (wa >> i) & 1u ? v[i] : -INFINITY;
+                v[32 + i] = (wb >> i) & 1u ? v[32 + i] : -INFINITY;
+              }
+            }
+          };
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int h = 0; h < hs; ++h) {
+            load(h);
+#pragma unroll
+            for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], v[i]);
+          }
+          const float mn = fmaxf(mu, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc);
+          const bool need = row.ok && mn > mu + 8.f;
+          const float f = need ? fast_exp2(mu - mn) : 1.f;  // 0 for the first keys seen
+          if (need) mu = mn;
+          const float off = mu == -INFINITY ? 0.f : -mu;  // nothing seen: every 2^x is of -inf
+          float r4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+          for (int h = 0; h < hs; ++h) {
+            load(h);
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float e0 = fast_exp2(fmaf(v[2 * i], sc, off)), e1 = fast_exp2(fmaf(v[2 * i + 1], sc, off));
+              r4[i & 3] += e0 + e1;
+              pk[i] = bf16x2_rn(e0, e1);
+            }
+            tmem_st32u(ts + 32 * h, pk);  // over columns that are read
+          }
+          sum = fmaf(sum, f, (r4[0] + r4[1]) + (r4[2] + r4[3]));
+          if (t > first && __any_sync(0xffffffffu, need)) {
+#pragma unroll
+            for (int q = 0; q < DH / 32; ++q) {
+              float o[32];
+              tmem_ld32(to + 128 * s + 32 * q, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= f;
+              tmem_st32(to + 128 * s + 32 * q, o);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        mbar_arrive(&bars->p_full[s]);
+      }
+      if (!alive) break;
+
+      // The unit's result: O / sum, or a part of it for the merge.
+      const bool whole = x.t0 == 0 && x.t1 == it.tiles;
+      const int slot = 2 * blockIdx.x + (x.t0 == 0 ? 1 : 0);
+      bool o1 = false;
+      float w0 = 1.f, w1 = 0.f;
+      if (s == 1 && n > 0 && !(alive = warp_wait(&bars->o_free[1], (n - 1) & 1, &s_abort))) break;
+      if (!x.two) {
+        if (s == 1) {
+          sh.ml[m] = make_float2(mu, sum);
+          mbar_arrive(&bars->ml_full);
+        } else {
+          if (!(alive = warp_wait(&bars->ml_full, nb & 1, &s_abort))) break;
+          const float2 q = sh.ml[m];
+          o1 = x.t1 - x.t0 > 1;  // stream 1 had a tile
+          const float mm = fmaxf(mu, q.x), off = mm == -INFINITY ? 0.f : mm;
+          w0 = fast_exp2(mu - off);
+          w1 = fast_exp2(q.x - off);
+          sum = fmaf(sum, w0, q.y * w1);
+          mu = mm;
+        }
+        ++nb;
+      }
+      if (x.two || s == 0) {
+        const bool has = first < end;
+        if (has && !(alive = warp_wait(&bars->o_full[s], no & 1, &s_abort))) break;
+        if (o1 && !(alive = warp_wait(&bars->o_full[1], no1 & 1, &s_abort))) break;
+        if (busy) {
+          tc_fence_after();
+          const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+          w0 *= inv;
+          w1 *= inv;
+          const size_t orow = out_row(a, it, row), prow = (size_t)slot * a.R + rt * 128 + m;
+#pragma unroll
+          for (int q = 0; q < DH / 32; ++q) {
+            float o[32];
+            if (has) {
+              tmem_ld32(to + 128 * s + 32 * q, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = w0 > 0.f ? o[i] * w0 : 0.f;
+              if (o1) {
+                float p[32];
+                tmem_ld32(to + 128 + 32 * q, p);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = w1 > 0.f ? fmaf(p[i], w1, o[i]) : o[i];
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            }
+            if (!row.ok) continue;
+            if (whole) {
+              uint16_t* dst = static_cast<uint16_t*>(a.out) + orow * a.d + 32 * q;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (32 * q + 8 * i < a.d)
+                  *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(bf16x2_rn(o[8 * i], o[8 * i + 1]), bf16x2_rn(o[8 * i + 2], o[8 * i + 3]),
+                                                                      bf16x2_rn(o[8 * i + 4], o[8 * i + 5]), bf16x2_rn(o[8 * i + 6], o[8 * i + 7]));
+            } else {
+              float* dst = a.part_o + prow * a.d + 32 * q;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (32 * q + 8 * i < a.d) st_v8(dst + 8 * i, o + 8 * i);
+            }
+          }
+          if (row.ok) {
+            if (!whole) a.part_ml[prow] = make_float2(mu, sum);
+            else if (a.lse) a.lse[orow] = lse_of(mu, sum);
+          }
+          tc_fence_before();
+        }
+        if (x.two) {
+          mbar_arrive(&bars->o_free[s]);
+        } else {
+          mbar_arrive(&bars->o_free[0]);
+          mbar_arrive(&bars->o_free[1]);
+        }
+      }
+      no += first < end;
+      no1 += x.two || x.t1 - x.t0 > 1;  // stream 1 sees every tile of a two-tile block
+      ++n;
+      u = it.first + x.t1;
+      if (u < u1 && !next_item(a.w, it)) break;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (threadIdx.x == 0 && s_abort) set_status(a.d_status, MEDUSA_DEV_TIMEOUT);
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+// ------------------------------------------------------------------ host side
+
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    cudaGetLastError();
+    return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+  }();
+  return fn;
+}
+
+// [rows][heads][d] bf16 with `pitch` elements between rows; boxes of 64 columns x bh heads x br rows.
+static bool make_map(CUtensorMap* m, const void* base, int d, int heads, long long rows, long long pitch, int bh, int br) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)pitch * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)bh, (cuuint32_t)br}, es[3] = {1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DH>
+static medusa_status go(const AttnArgs& a, const CUtensorMap* m, int box_rows, cudaStream_t s) {
+  auto kern = paged_attn_tc_kernel<DH>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tc::Cfg<DH>::smem) != cudaSuccess)
+    return MEDUSA_ERR_CUDA;
+  launch_pdl(kern, dim3(a.w.ctas), dim3(tc::kThreads), tc::Cfg<DH>::smem, s, m[0], m[1], m[2], m[3], m[4], a, box_rows);
+  return MEDUSA_OK;
+}
+
+medusa_status paged_attention_tc(const AttnArgs& a, cudaStream_t s) {
+  if (!encode_fn()) return MEDUSA_ERR_CUDA;
+  int box_rows = 128;
+  while (a.cache.page_size % box_rows) box_rows /= 2;
+  const long long tokens = (long long)a.w.nl * a.w.T, rows = (long long)a.w.nl * a.cache.n_pages * a.cache.page_size;
+  CUtensorMap m[5];
+  if (!make_map(&m[0], a.q, a.d, a.Hq, tokens, a.ldq, a.G, a.tile_tok)) return MEDUSA_ERR_CUDA;
+  if (!make_map(&m[1], a.k_pages, a.d, a.Hkv, rows, (long long)a.Hkv * a.d, 1, box_rows)) return MEDUSA_ERR_CUDA;
+  if (!make_map(&m[2], a.v_pages, a.d, a.Hkv, rows, (long long)a.Hkv * a.d, 1, box_rows)) return MEDUSA_ERR_CUDA;
+  if (a.w.N) {
+    if (!make_map(&m[3], a.kt, a.d, a.Hkv, tokens, (long long)a.Hkv * a.d, 1, 64)) return MEDUSA_ERR_CUDA;
+    if (!make_map(&m[4], a.vt, a.d, a.Hkv, tokens, (long long)a.Hkv * a.d, 1, 64)) return MEDUSA_ERR_CUDA;
+  } else {
+    m[3] = m[1];
+    m[4] = m[2];
+  }
+  return a.d <= 64 ? go<64>(a, m, box_rows, s) : go<128>(a, m, box_rows, s);
+}
+
+}  // namespace paged
+}  // namespace medusa

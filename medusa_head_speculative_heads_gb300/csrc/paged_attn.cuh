@@ -54,5 +54,9 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
+// Tensor-core kernel (paged_attention_tc.cu): bf16, d <= 128 a multiple of 8,
+// page_size a multiple of 8, at most 128 q heads per kv head.
+medusa_status paged_attention_tc(const AttnArgs& a, cudaStream_t s);
+
 }  // namespace paged
 }  // namespace medusa
