@@ -35,7 +35,8 @@ struct Work {
   const int32_t* prefix_len;  // [B]
   int B, T, N;                // N: tree nodes, 0 for a causal chunk
   int nl, nh, cap;            // nh: head groups per layer; cap: rows a sequence can hold
-  int ctok, KT;               // tokens per block and keys per tile (powers of two)
+  int ctok, KT;               // tokens per block and keys per tile
+  int ctok_log2, KT_log2;     // both are powers of two
   int ctas, min_tiles;
 };
 
@@ -60,14 +61,14 @@ __device__ __forceinline__ Seq seq_of(const Work& w, int b) {
   return s;
 }
 
-__device__ __forceinline__ int n_blocks(const Work& w, const Seq& s) { return (s.len + w.ctok - 1) / w.ctok; }
+__device__ __forceinline__ int n_blocks(const Work& w, const Seq& s) { return (s.len + w.ctok - 1) >> w.ctok_log2; }
 
 // Key tiles of block i of a sequence.  Causal: the rows up to the block's last
 // token.  Tree: the prefix tiles, then the tree tiles.
 __device__ __forceinline__ int block_tiles(const Work& w, const Seq& s, int i) {
-  if (w.N) return (s.L + w.KT - 1) / w.KT + (w.N + w.KT - 1) / w.KT;
+  if (w.N) return ((s.L + w.KT - 1) >> w.KT_log2) + ((w.N + w.KT - 1) >> w.KT_log2);
   const int last = min(s.len, (i + 1) * w.ctok);
-  return (s.L + last + w.KT - 1) / w.KT;
+  return (s.L + last + w.KT - 1) >> w.KT_log2;
 }
 
 // Tiles of the sequence's first i blocks, i <= n_blocks, in closed form.  With
@@ -80,18 +81,16 @@ __device__ __forceinline__ long long tiles_before(const Work& w, const Seq& s, i
   const int nb = n_blocks(w, s);
   const bool all = i == nb;  // the last block may be short: added on its own
   const long long n = all ? i - 1 : i;
-  const long long a = s.L / w.KT;
-  const int r = s.L % w.KT;
-  long long t = n * a;
+  const int r = s.L & (w.KT - 1);
+  long long t = n * (s.L >> w.KT_log2);
   if (w.ctok >= w.KT) {
-    const long long m = w.ctok / w.KT;
-    t += n * (r > 0) + m * n * (n + 1) / 2;
+    t += n * (r > 0) + ((n * (n + 1) / 2) << (w.ctok_log2 - w.KT_log2));
   } else {
-    const long long m = w.KT / w.ctok;
-    const long long r1 = (r + w.ctok - 1) / w.ctok;
+    const int m = w.KT_log2 - w.ctok_log2;
+    const long long r1 = (r + w.ctok - 1) >> w.ctok_log2;
     auto h = [m](long long x) {
-      const long long q = x / m, e = x % m;
-      return m * q * (q + 1) / 2 + e * (q + 1);
+      const long long q = x >> m, e = x & ((1ll << m) - 1);
+      return ((q * (q + 1) / 2) << m) + e * (q + 1);
     };
     t += h(r1 + n) - h(r1);
   }
@@ -111,74 +110,101 @@ struct Item {
 };
 
 // Block-wide set-up: every thread of the CTA calls plan_find() once.  It sums the
-// tiles per layer-head over the sequences and, for the tile `want(U, Q)` picks,
-// finds the item that holds it.  sh: 2 * 32 + 4 long longs of shared memory.
-// Returns false when that tile does not exist.
+// tiles per layer-head over the sequences and, for the tile `want(plan)` picks,
+// finds the item that holds it; false when that tile does not exist.  sh: 70 long
+// longs of shared memory.  Up to blockDim sequences take one round of loads and
+// two barriers.
 struct Plan {
   long long per, U, Q;  // tiles per layer-head, in all, per CTA
 };
 
+__device__ __forceinline__ long long divided(long long a, long long b) {  // a, b >= 0; most fit 32 bits
+  return (a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+
 template <typename Want>
 __device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, long long* sh, Want want) {
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wp = tid >> 5, nw = (nt + 31) >> 5;
-  long long mine = 0;
-  for (int b = tid; b < w.B; b += nt) mine += seq_tiles(w, seq_of(w, b));
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sh[wp] = mine;
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wp = tid >> 5, nw = nt >> 5;
+  // Inclusive sums over the warp, the first blockDim sequences' kept for the search.
+  Seq s{};
+  long long v = 0, rest = 0;
+  if (tid < w.B) {
+    s = seq_of(w, tid);
+    v = seq_tiles(w, s);
+  }
+  for (int b = tid + nt; b < w.B; b += nt) rest += seq_tiles(w, seq_of(w, b));
+  long long inc = v;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  for (int o = 16; o; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+  if (lane == 31) {
+    sh[wp] = inc;
+    sh[32 + wp] = rest;
+  }
   __syncthreads();
-  long long per = 0;
-  for (int j = 0; j < nw; ++j) per += sh[j];
+  long long before = 0, total = 0, per = 0;
+  for (int j = 0; j < nw; ++j) {
+    if (j < wp) before += sh[j];
+    total += sh[j];
+    per += sh[32 + j];
+  }
+  per += total;
   pl.per = per;
   pl.U = per * ((long long)w.nl * w.nh);
-  pl.Q = (pl.U + w.ctas - 1) / w.ctas;
+  pl.Q = divided(pl.U + w.ctas - 1, w.ctas);
   if (pl.Q < w.min_tiles) pl.Q = w.min_tiles;
   const long long u = want(pl);
   if (u < 0 || u >= pl.U) return false;
-  const long long off = u % per;
-  // The sequence whose tiles hold `off`: block-wide scan, blockDim sequences at a time.
+  const long long lg = divided(u, per), off = u - lg * per;
+  // The sequence whose tiles hold `off`, blockDim sequences at a time.
   long long base = 0;
-  for (int b0 = 0; b0 < w.B; b0 += nt) {
-    const int b = b0 + tid;
-    Seq s;
-    long long v = 0;
-    if (b < w.B) {
-      s = seq_of(w, b);
-      v = seq_tiles(w, s);
-    }
-    long long inc = v;
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    __syncthreads();  // the last use of sh is over
-    if (lane == 31) sh[32 + wp] = inc;
-    __syncthreads();
-    long long before = base, total = 0;
-    for (int j = 0; j < nw; ++j) {
-      if (j < wp) before += sh[32 + j];
-      total += sh[32 + j];
-    }
-    const long long lo = before + inc - v;
-    if (b < w.B && off >= lo && off < lo + v) {  // one thread
+  for (int b0 = 0;;) {
+    const long long lo = base + before + inc - v;
+    if (v > 0 && off >= lo && off < lo + v) {  // one thread
       int i0 = 0, i1 = n_blocks(w, s);
       while (i1 - i0 > 1) {
         const int m = (i0 + i1) >> 1;
         if (tiles_before(w, s, m) <= off - lo) i0 = m;
         else i1 = m;
       }
-      sh[64] = b;
+      sh[64] = b0 + tid;
       sh[65] = i0;
       sh[66] = lo + tiles_before(w, s, i0);
+      sh[67] = s.q0;
+      sh[68] = s.len;
+      sh[69] = s.L;
     }
     base += total;
-    if (base > off) break;  // the same in every thread
+    b0 += nt;
+    if (base > off || b0 >= w.B) break;  // the same in every thread
+    const int b = b0 + tid;
+    v = 0;
+    if (b < w.B) {
+      s = seq_of(w, b);
+      v = seq_tiles(w, s);
+    }
+    inc = v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    __syncthreads();  // the last use of sh[0 .. 31] is over
+    if (lane == 31) sh[wp] = inc;
+    __syncthreads();
+    before = total = 0;
+    for (int j = 0; j < nw; ++j) {
+      if (j < wp) before += sh[j];
+      total += sh[j];
+    }
   }
   __syncthreads();
-  it.lg = (int)(u / per);
+  it.lg = (int)lg;
   it.b = (int)sh[64];
   it.i = (int)sh[65];
-  it.s = seq_of(w, it.b);
-  it.first = (long long)it.lg * per + sh[66];
+  it.s = Seq{(int)sh[67], (int)sh[68], (int)sh[69], true};
+  it.first = lg * per + sh[66];
   it.tiles = block_tiles(w, it.s, it.i);
   return true;
 }

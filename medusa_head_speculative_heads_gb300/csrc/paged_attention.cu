@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt_kernel(const __g
   float* Ks = Qs + R * DP;
   float* Vs = Ks + kSimtKeys * DP;
   float* Ps = Vs + kSimtKeys * DP;
-  __shared__ long long sh[68];
+  __shared__ long long sh[70];
   __shared__ const T *s_k[2][kSimtKeys], *s_v[2][kSimtKeys];  // row starts of a tile's keys (NULL: zeros)
   pdl_wait();
   pdl_trigger();
@@ -63,7 +63,9 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt_kernel(const __g
       if (!seq_of(a.w, b).ok) set_status(a.d_status, MEDUSA_DEV_BAD_LENGTH);
   Plan pl;
   Item it;
-  if (!plan_find(a.w, pl, it, sh, [](const Plan& p) { return p.Q * blockIdx.x; })) return;
+  const bool any = plan_find(a.w, pl, it, sh, [](const Plan& p) { return p.Q * blockIdx.x; });
+  if (tid == 0) note_shared(a, pl, it, any);
+  if (!any) return;
   const long long u0 = pl.Q * blockIdx.x, u1 = u0 + pl.Q < pl.U ? u0 + pl.Q : pl.U;
   const int dv = a.d / 4;
 
@@ -241,23 +243,20 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt_kernel(const __g
   }
 }
 
-// Adds the parts of every item that several CTAs share.  CTA boundary c (tile
-// c Q, c = 1 .. C - 1) belongs to the item it falls inside; the first boundary
-// inside an item merges all of its parts, in the order of the CTAs:
+// Adds the parts of every item that several CTAs share.  The CTA boundary c
+// (tile c Q, c = 1 .. C - 1) belongs to the item it falls inside; the first
+// boundary inside an item merges all of its parts, in the order of the CTAs:
 // O = sum 2^(m_p - M) O_p, l = sum 2^(m_p - M) l_p, M = max m_p.  One warp per
 // row (its lanes share the columns); blockIdx.y takes every gridDim.y-th group
-// of eight rows.
+// of eight rows.  The attention kernel's CTAs have left the items they found.
 template <typename T>
 __global__ void __launch_bounds__(256) paged_attn_merge_kernel(const __grid_constant__ AttnArgs a) {
-  __shared__ long long sh[68];
   pdl_wait();
   pdl_trigger();
-  const long long c = blockIdx.x + 1;
-  Plan pl;
-  Item it;
-  if (!plan_find(a.w, pl, it, sh, [c](const Plan& p) { return p.Q * c; })) return;
-  if (it.first >= c * pl.Q || it.first < (c - 1) * pl.Q) return;  // no shared item, or not its first boundary
-  const int first = (int)(c - 1), last = (int)((it.first + it.tiles - 1) / pl.Q);
+  const Shared sd = a.shared[blockIdx.x + 1];
+  if (sd.first < 0) return;
+  const Item& it = sd.it;
+  const int first = sd.first, last = sd.last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int r = blockIdx.y * 8 + warp; r < a.R; r += gridDim.y * 8) {
     const Row x = row_of(a, it, r);
@@ -305,6 +304,12 @@ struct Division {
   int R, ctas, KT, min_tiles, sub, nsub, tile_rows, tile_tok, ctok;
 };
 
+static int log2_of(int p) {
+  int n = 0;
+  while (p >> (n + 1)) ++n;
+  return n;
+}
+
 static int pow2_at_most(int x) {
   int p = 1;
   while (2 * p <= x) p *= 2;
@@ -344,7 +349,9 @@ static Division divide(int T, int B, int Hq, int Hkv, int d, int page_size, medu
   return v;
 }
 
-static size_t ws_bytes_of(const Division& v, int d) { return (size_t)v.ctas * 2 * v.R * (d + 2) * sizeof(float); }
+static size_t ws_bytes_of(const Division& v, int d) {
+  return (size_t)v.ctas * (2 * v.R * (d + 2) * sizeof(float) + sizeof(Shared));
+}
 
 template <typename T, int DC, int RM>
 static medusa_status simt_go(const AttnArgs& a, cudaStream_t s) {
@@ -378,7 +385,9 @@ static medusa_status attend(AttnArgs& a, int n_layers, int T, int B, int Hq, int
   if (!ws || !aligned16(ws) || ws_bytes < ws_bytes_of(v, d)) return MEDUSA_ERR_WORKSPACE;
   a.part_o = static_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)v.ctas * 2 * v.R * d);
+  a.shared = reinterpret_cast<Shared*>(a.part_ml + (size_t)v.ctas * 2 * v.R);
   a.R = v.R;
+  a.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && d % 16 == 0;
   a.tile_rows = v.tile_rows;
   a.tile_tok = v.tile_tok;
   a.sub = v.sub;
@@ -388,6 +397,8 @@ static medusa_status attend(AttnArgs& a, int n_layers, int T, int B, int Hq, int
   a.w.cap = max_pages * page_size;
   a.w.ctok = v.ctok;
   a.w.KT = v.KT;
+  a.w.ctok_log2 = log2_of(v.ctok);
+  a.w.KT_log2 = log2_of(v.KT);
   a.w.ctas = v.ctas;
   a.w.min_tiles = v.min_tiles;
   a.w.B = B;

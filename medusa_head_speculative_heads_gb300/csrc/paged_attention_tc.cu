@@ -8,21 +8,23 @@
 //
 // Two streams run side by side in a CTA, each with its own scores S and sums O
 // in tensor memory (4 x 128 columns, all of it), its own MMA-issuing warp and
-// its own four softmax warps (a thread holds one query row), so that one's
-// softmax runs under the other's products:
+// its own four softmax warps (a thread holds one query row's 128 scores), so
+// that one's softmax runs under the other's products:
 //  - a block of more than 128 rows: stream s has rows 128 s .. 128 s + 127, and
 //    both use every K and V tile, read from global memory once;
 //  - a block of at most 128 rows (decoding, small trees): both streams have the
 //    same rows, stream s the key tiles t0 + s, t0 + s + 2, ...; their two
 //    results are added as two parts of a row are.
 // Within a stream S = Q K^T, softmax, O += P V follow one another; P (bf16)
-// overwrites S, and the next tile's S is issued by the same thread behind the
+// overwrites S (its first 64 keys are handed over before the last 64 are
+// computed), and the next tile's S is issued by the same thread behind the
 // P V that reads P, which orders the two.  A completed S therefore also says
 // that the P V before it is done, and O may be rescaled; that happens only when
 // a row's maximum has grown by more than 2^8 (the stale maximum is exact
 // arithmetic: the same power of two scales P and the sum).
 //
-// Warp 0 brings Q and the K and V tiles by TMA into a ring of 128-row slots.
+// Warp 3 walks through the CTA's items and describes each one to the others in
+// shared memory.  Warp 0 brings Q and the K and V tiles by TMA into a ring of 128-row slots.
 // A tile is copied in boxes of gcd(page_size, 128) rows, one lane each looking
 // its page up; a page that does not exist is read as rows behind the pool,
 // which arrive as zeros.  Rows behind the last one are masked in S; the rows
@@ -44,13 +46,52 @@ using namespace sm100;
 
 namespace tc {
 
-constexpr int kThreads = 384;          // TMA, two MMA issuers, one idle; 2 x 4 softmax warps
+constexpr int kThreads = 384;          // TMA, two MMA issuers, planner; 2 x 4 softmax warps
 constexpr int kKeys = 128;             // keys of a tile
 constexpr uint32_t kHalf = 16384;      // 128 rows x 128 bytes (64 columns)
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainNs = 100000000ull;
 constexpr uint32_t kTmemCols = 512;    // S0, S1, O0, O1
 constexpr int kMaxSlots = 10;
+constexpr int kUnits = 4;              // described units in flight
+constexpr int kUnitReaders = 11;       // warps that read a description
+
+struct Bars {
+  uint64_t full[kMaxSlots], empty[kMaxSlots];  // empty: two releases (a sole user's two)
+  uint64_t q_full[2], q_empty[2];              // likewise
+  uint64_t s_full[2], p_full[2][2];            // p_full: stream, half of the keys
+  uint64_t o_full[2], o_free[2], ml_full, drain[2];
+  uint64_t u_full[kUnits], u_free[kUnits];
+};
+
+// The part of an item that a CTA works on, and how its two streams share it.
+struct Unit {
+  int t0, t1;      // key tiles; t1 <= 0: no more units
+  int tiles;       // of the whole item
+  int two;         // two row tiles; else one, its key tiles taken in turn
+  int pre;         // tiles of cache rows (the rest are tree tiles)
+  int rows_end;    // cache rows the block may see
+  int end0;        // tiles [t0, end0) are stream 0's when there are two row tiles
+  int b, kvh;
+  int L;           // rows before the sequence's tokens
+  int tok0, ntok;  // the block's tokens within the sequence
+  int row0;        // its first token among all layers' tokens
+  int tree0;       // the sequence's first token there
+  int pool0;       // the layer's first pool row
+};
+
+// Behind the ring.  All shared memory is dynamic, so that it starts on the 1024
+// bytes the swizzled tiles need (checked).
+struct Tail {
+  Bars bars;
+  Unit units[kUnits];
+  union {
+    long long plan[70];  // set-up only
+    float2 ml[128];      // stream 1's row maxima and sums, for stream 0 to add
+  };
+  uint32_t tmem;
+  volatile int abort;
+};
 
 // DH: columns computed, 64 or 128.
 template <int DH>
@@ -60,17 +101,10 @@ struct Cfg {
   static constexpr int slots = DH == 128 ? 5 : 10;
   static constexpr uint32_t off_ring = 2 * slot;
   static constexpr uint32_t off_bar = off_ring + slots * slot;
-  static constexpr uint32_t smem = off_bar + 512 + 1024;  // barriers, alignment
+  static constexpr uint32_t smem = off_bar + sizeof(Tail);
   static constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false, false);
   static constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DH, false, true);
 };
-
-struct Bars {
-  uint64_t full[kMaxSlots], empty[kMaxSlots];  // empty: two releases (a sole user's two)
-  uint64_t q_full[2], q_empty[2];              // likewise
-  uint64_t s_full[2], p_full[2], o_full[2], o_free[2], ml_full, drain[2];
-};
-
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2) {
   asm volatile(
@@ -94,49 +128,87 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// Two fp32 operations at once.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ void st_v8u(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ void st_v8(float* p, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
                "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
 }
 
-// The part of an item that a CTA works on, and how its two streams share it.
-struct Unit {
-  int t0, t1;       // key tiles
-  bool two;         // two row tiles; else one, its key tiles taken in turn
-  int pre;          // the item's tiles of cache rows (the rest are tree tiles)
-  int rows_end;     // cache rows the block may see
-  int l, kvh;
-};
-__device__ __forceinline__ Unit unit_of(const AttnArgs& a, const Item& it, long long u, long long u1) {
+// `left`: the tiles of the CTA's range from tile t0 of the item on.
+__device__ __forceinline__ Unit unit_of(const AttnArgs& a, const Item& it, int t0, long long left) {
   Unit x;
-  x.t0 = (int)(u - it.first);
-  x.t1 = (int)((it.first + it.tiles < u1 ? it.first + it.tiles : u1) - it.first);
-  const int tok0 = it.i * a.w.ctok;
-  x.two = it.s.len - tok0 > a.tile_tok;
-  x.rows_end = a.w.N ? it.s.L : it.s.L + min(it.s.len, tok0 + a.w.ctok);
+  x.t0 = t0;
+  x.t1 = it.tiles - t0 < left ? it.tiles : t0 + (int)left;
+  x.tiles = it.tiles;
+  x.tok0 = it.i << a.w.ctok_log2;
+  x.ntok = min(it.s.len - x.tok0, a.w.ctok);
+  x.two = x.ntok > a.tile_tok;
+  x.rows_end = a.w.N ? it.s.L : it.s.L + x.tok0 + x.ntok;
   x.pre = a.w.N ? (it.s.L + kKeys - 1) / kKeys : it.tiles;
-  x.l = it.lg / a.w.nh;
-  x.kvh = it.lg - x.l * a.w.nh;
+  // A causal first row tile does not see the key tiles that only the second one does.
+  x.end0 = x.two && !a.w.N ? min(x.t1, (it.s.L + x.tok0 + a.tile_tok + kKeys - 1) / kKeys) : x.t1;
+  const int l = it.lg / a.w.nh;
+  x.kvh = it.lg - l * a.w.nh;
+  x.b = it.b;
+  x.L = it.s.L;
+  x.tree0 = l * a.w.T + it.s.q0;
+  x.row0 = x.tree0 + x.tok0;
+  x.pool0 = l * (a.cache.n_pages * a.cache.page_size);
   return x;
 }
-// Key tiles [t0, end) that stream s of a two-tile block uses: a causal first
-// half does not see the tiles only the second one does.
-__device__ __forceinline__ int stream_end(const AttnArgs& a, const Item& it, const Unit& x, int s) {
-  if (!x.two || s == 1 || a.w.N) return x.t1;
-  const int seen = (it.s.L + it.i * a.w.ctok + a.tile_tok + kKeys - 1) / kKeys;
-  return min(x.t1, seen);
-}
+__device__ __forceinline__ int stream_end(const Unit& x, int s) { return x.two && s == 0 ? x.end0 : x.t1; }
 // Keys of tile t that rows of stream s may see, at most 128.
-__device__ __forceinline__ int tile_keys(const AttnArgs& a, const Item& it, const Unit& x, int s, int t) {
+__device__ __forceinline__ int tile_keys(const AttnArgs& a, const Unit& x, int s, int t) {
   if (t >= x.pre) return min(kKeys, a.w.N - (t - x.pre) * kKeys);
-  int end = x.rows_end;
-  if (x.two && s == 0 && !a.w.N) end = it.s.L + it.i * a.w.ctok + a.tile_tok;
+  const int end = x.two && s == 0 && !a.w.N ? x.L + x.tok0 + a.tile_tok : x.rows_end;
   return min(kKeys, end - t * kKeys);
 }
 // Rows of tile t that were copied and may be read as they are.
 __device__ __forceinline__ int tile_rows_loaded(const AttnArgs& a, const Unit& x, int t) {
   return t >= x.pre ? min(kKeys, a.w.N - (t - x.pre) * kKeys) : min(kKeys, x.rows_end - t * kKeys);
+}
+
+// Registers move from the four issuing warps to the softmax warps, which hold
+// 128 scores a thread: 128 x 80 + 256 x 208 of the 384 x 168 that the CTA is
+// launched with.
+__device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
+__device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+
+// The next description, `n` units after the first: false on a timeout.
+__device__ __forceinline__ bool read_unit(Tail* tail, int n, Unit& x, volatile int* abort) {
+  const int k = n % kUnits;
+  if (!warp_wait(&tail->bars.u_full[k], (uint32_t)(n / kUnits) & 1u, abort)) return false;
+  x = tail->units[k];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&tail->bars.u_free[k]);
+  return true;
 }
 
 }  // namespace tc
@@ -148,16 +220,15 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                      const __grid_constant__ CUtensorMap tm_vt, const __grid_constant__ AttnArgs a, const int box_rows) {
   using namespace tc;
   using C = Cfg<DH>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  static_assert(sizeof(Bars) <= 512, "barrier area");
-  Bars* bars = reinterpret_cast<Bars*>(smem + C::off_bar);
-  __shared__ uint32_t s_tmem;
-  __shared__ volatile int s_abort;
-  __shared__ union {
-    long long plan[68];  // set-up only
-    float2 ml[128];      // stream 1's row maxima and sums, for stream 0 to add
-  } sh;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  static_assert(C::smem <= 232448, "shared memory of a CTA");
+  Tail* tail = reinterpret_cast<Tail*>(smem + C::off_bar);
+  Bars* bars = &tail->bars;
+  volatile int& s_abort = tail->abort;
+  if (smem_u32(smem) & 1023u) {  // the same in every thread
+    if (threadIdx.x == 0) set_status(a.d_status, MEDUSA_DEV_TIMEOUT);
+    return;
+  }
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -170,16 +241,20 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       mbar_init(&bars->q_full[s], 1);
       mbar_init(&bars->q_empty[s], 2);
       mbar_init(&bars->s_full[s], 1);
-      mbar_init(&bars->p_full[s], 128);
+      for (int h = 0; h < 2; ++h) mbar_init(&bars->p_full[s][h], 128);
       mbar_init(&bars->o_full[s], 1);
       mbar_init(&bars->o_free[s], 128);
       mbar_init(&bars->drain[s], 1);
     }
     mbar_init(&bars->ml_full, 128);
+    for (int k = 0; k < kUnits; ++k) {
+      mbar_init(&bars->u_full[k], 1);
+      mbar_init(&bars->u_free[k], kUnitReaders);
+    }
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(&s_tmem, kTmemCols);
+    tmem_alloc(&tail->tmem, kTmemCols);
     tmem_relinquish();
   }
   if (warp == 0 && lane == 0) {
@@ -193,45 +268,68 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   // Nothing above reads memory an earlier kernel may write.
   pdl_wait();
   pdl_trigger();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = tail->tmem;
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < a.w.B; b += kThreads)
       if (!seq_of(a.w, b).ok) set_status(a.d_status, MEDUSA_DEV_BAD_LENGTH);
   Plan pl;
   Item it;
-  const bool any = plan_find(a.w, pl, it, sh.plan, [](const Plan& p) { return p.Q * blockIdx.x; });
-  const long long u0 = pl.Q * blockIdx.x, u1 = any ? (u0 + pl.Q < pl.U ? u0 + pl.Q : pl.U) : u0;
-  __syncthreads();  // sh.plan is no longer read
+  const bool any = plan_find(a.w, pl, it, tail->plan, [](const Plan& p) { return p.Q * blockIdx.x; });
+  if (threadIdx.x == 0) note_shared(a, pl, it, any);
+  __syncthreads();  // the plan is no longer read
 
-  if (warp == 0) {
+  if (warp == 3) {
+    // ------------------------------------------------------------ planner
+    setmaxnreg_dec();
+    const long long u0 = pl.Q * blockIdx.x;
+    long long left = !any ? 0 : u0 + pl.Q < pl.U ? pl.Q : pl.U - u0;
+    int t0 = any ? (int)(u0 - it.first) : 0;
+    for (int n = 0;; ++n) {
+      const int k = n % kUnits;
+      if (n >= kUnits && !warp_wait(&bars->u_free[k], (uint32_t)(n / kUnits - 1) & 1u, &s_abort)) break;
+      Unit x{};
+      const bool more = left > 0;
+      if (more) x = unit_of(a, it, t0, left);
+      if (lane == 0) {
+        tail->units[k] = x;
+        mbar_arrive(&bars->u_full[k]);
+      }
+      __syncwarp();
+      if (!more) break;
+      left -= x.t1 - x.t0;
+      t0 = 0;
+      if (left > 0 && !next_item(a.w, it)) left = 0;
+    }
+  } else if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    int c = 0, issued = 0;  // slots used
+    setmaxnreg_dec();
+    int c = 0, issued = 0;           // slots used
     int qn0 = 0, qn1 = 0, qsel = 0;  // loads into the two Q buffers
     bool alive = true;
     const int box = lane & 15, half = lane >> 4;
-    const long long pool_rows = (long long)a.cache.n_pages * a.cache.page_size;
-    for (long long u = u0; u < u1 && alive;) {
-      const Unit x = unit_of(a, it, u, u1);
-      const int row0 = x.l * a.w.T + it.s.q0 + it.i * a.w.ctok;
-      for (int k = 0; k < (x.two ? 2 : 1) && alive; ++k) {
+    Unit x;
+    for (int n = 0; (alive = read_unit(tail, n, x, &s_abort)) && x.t1 > 0; ++n) {
+      for (int k = 0; k < (x.two ? 2 : 1); ++k) {
         const int qb = x.two ? k : qsel, used = qb ? qn1 : qn0;
         if (used > 0 && !(alive = warp_wait(&bars->q_empty[qb], (used - 1) & 1, &s_abort))) break;
         if (lane == 0) {
           mbar_expect_tx(&bars->q_full[qb], (uint32_t)(C::halves * a.tile_tok * a.G * 128));
           for (int h = 0; h < C::halves; ++h)
-            tma_load_3d(smem + qb * C::slot + h * kHalf, &tm_q, &bars->q_full[qb], 64 * h, x.kvh * a.G, row0 + k * a.tile_tok);
+            tma_load_3d(smem + qb * C::slot + h * kHalf, &tm_q, &bars->q_full[qb], 64 * h, x.kvh * a.G, x.row0 + k * a.tile_tok);
         }
+        __syncwarp();
         qn0 += qb == 0;
         qn1 += qb == 1;
       }
+      if (!alive) break;
       if (!x.two) qsel ^= 1;
       // The pool row of this lane's box of tile t (behind the pool: zeros).
       auto box_row = [&](int t) {
         const int r = t * kKeys + box * box_rows;
-        int row = (int)(pool_rows * a.w.nl);
+        int row = a.cache.n_pages * a.cache.page_size * a.w.nl;
         if (t < x.pre && box < kKeys / box_rows && r < x.rows_end) {
-          const int in = pool_row(a.cache, it.b, r);
-          if (in >= 0) row = (int)(pool_rows * x.l) + in;
+          const int in = pool_row(a.cache, x.b, r);
+          if (in >= 0) row = x.pool0 + in;
           else if (half == 0) set_status(a.d_status, MEDUSA_DEV_BAD_INDEX);
         }
         return row;
@@ -241,7 +339,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const bool tree = t >= x.pre;
         const int step = tree ? 64 : box_rows;
         const int boxes = (tile_rows_loaded(a, x, t) + step - 1) / step;
-        const int at = tree ? x.l * a.w.T + it.s.q0 + (t - x.pre) * kKeys + box * 64 : row;
+        const int at = tree ? x.tree0 + (t - x.pre) * kKeys + box * 64 : row;
         if (t + 1 < x.t1) row = box_row(t + 1);  // its latency passes under this tile's waits
         for (int kv = 0; kv < 2; ++kv, ++c) {
           const int sl = c % C::slots;
@@ -254,8 +352,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                         kv ? (tree ? &tm_vt : &tm_v) : (tree ? &tm_kt : &tm_k), &bars->full[sl], 64 * half, x.kvh, at);
         }
       }
-      u = it.first + x.t1;
-      if (u < u1 && !next_item(a.w, it)) break;
+      if (!alive) break;
     }
     if (!alive) {
       // No copy may land after exit: wait (bounded) for the last phase of every load barrier.
@@ -264,22 +361,22 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       for (int i = issued - 1; i >= 0 && i >= issued - C::slots; --i)
         mbar_wait_bounded(&bars->full[i % C::slots], (uint32_t)(i / C::slots) & 1u, nullptr, kDrainNs);
     }
-  } else if (warp == 1 || warp == 2) {
+  } else if (warp < 4) {
     // ------------------------------------------------------------ MMA issuer of stream s
+    setmaxnreg_dec();
     const int s = warp - 1;
     const uint32_t ts = tmem + 128 * s, to = tmem + 256 + 128 * s;
-    int g = 0;                       // tiles of earlier units (two ring slots each)
-    int qn0 = 0, qn1 = 0, qsel = 0, n = 0, np = 0;  // n: units, np: tiles of this stream
+    int g = 0;                               // tiles of earlier units (two ring slots each)
+    int qn0 = 0, qn1 = 0, qsel = 0, np = 0;  // np: tiles of this stream
     bool alive = true;
-    for (long long u = u0; u < u1 && alive;) {
-      const Unit x = unit_of(a, it, u, u1);
-      const int qb = x.two ? s : qsel, end = stream_end(a, it, x, s);
-      const int other_end = stream_end(a, it, x, 1 - s);
+    Unit x;
+    for (int n = 0; (alive = read_unit(tail, n, x, &s_abort)) && x.t1 > 0; ++n) {
+      const int qb = x.two ? s : qsel, end = stream_end(x, s), other_end = stream_end(x, 1 - s);
       if (!(alive = warp_wait(&bars->q_full[qb], (qb ? qn1 : qn0) & 1, &s_abort))) break;
       // The other stream's rows too: every phase of a buffer is seen before a later one is waited for.
       if (x.two && !(alive = warp_wait(&bars->q_full[1 - qb], (qb ? qn0 : qn1) & 1, &s_abort))) break;
       const int first = x.two ? x.t0 : x.t0 + s, step = x.two ? 1 : 2;
-      bool freed = false;  // O read out by the unit before
+      bool freed = n == 0;  // O read out by the unit before
       const uint32_t qa = smem_u32(smem + qb * C::slot);
       for (int t = first; t < end; t += step, ++np) {
         const int ck = 2 * (g + t - x.t0), cv = ck + 1;
@@ -295,18 +392,18 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
             mma_bf16(ts, smem_desc_sw128(qa + off, 16, 1024), smem_desc_sw128(ka + off, 16, 1024), C::idesc_qk, kk > 0);
           }
+          mma_commit(&bars->s_full[s]);
           for (int r = 0; r < releases; ++r) mma_commit(ek);
           if (t + step >= end)
             for (int r = 0; r < (x.two ? 2 : 1); ++r) mma_commit(&bars->q_empty[qb]);
-          mma_commit(&bars->s_full[s]);
         }
         __syncwarp();
         if (!freed) {
-          if (n > 0 && !(alive = warp_wait(&bars->o_free[s], (n - 1) & 1, &s_abort))) break;
+          if (!(alive = warp_wait(&bars->o_free[s], (n - 1) & 1, &s_abort))) break;
           freed = true;
         }
         if (!(alive = warp_wait(&bars->full[cv % C::slots], (uint32_t)(cv / C::slots) & 1u, &s_abort))) break;
-        const int keys = tile_keys(a, it, x, s, t), steps = (keys + 15) >> 4, have = tile_rows_loaded(a, x, t);
+        const int keys = tile_keys(a, x, s, t), steps = (keys + 15) >> 4, have = tile_rows_loaded(a, x, t);
         uint8_t* vb = smem + C::off_ring + (cv % C::slots) * C::slot;
         if (have < steps * 16) {
           for (int i = lane; i < (steps * 16 - have) * 8 * C::halves; i += 32) {
@@ -316,14 +413,21 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (!(alive = warp_wait(&bars->p_full[s], np & 1, &s_abort))) break;
+        const uint32_t va = smem_u32(vb);
+        if (!(alive = warp_wait(&bars->p_full[s][0], np & 1, &s_abort))) break;
         tc_fence_after();
         if (lane == 0) {
-          const uint32_t va = smem_u32(vb);
-          for (int kk = 0; kk < steps; ++kk)
+          for (int kk = 0; kk < 4 && kk < steps; ++kk)
             mma_bf16_ts(to, ts + 8 * kk, smem_desc_sw128(va + kk * 2048, kHalf, 1024), C::idesc_pv, kk > 0 || t > first);
-          for (int r = 0; r < releases; ++r) mma_commit(ev);
+        }
+        __syncwarp();
+        if (!(alive = warp_wait(&bars->p_full[s][1], np & 1, &s_abort))) break;
+        tc_fence_after();
+        if (lane == 0) {
+          for (int kk = 4; kk < steps; ++kk)
+            mma_bf16_ts(to, ts + 8 * kk, smem_desc_sw128(va + kk * 2048, kHalf, 1024), C::idesc_pv, 1);
           if (t + step >= end) mma_commit(&bars->o_full[s]);
+          for (int r = 0; r < releases; ++r) mma_commit(ev);
         }
         __syncwarp();
       }
@@ -333,132 +437,135 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           for (int r = 0; r < (x.two ? 2 : 1); ++r) mbar_arrive(&bars->q_empty[qb]);
         __syncwarp();
       }
-      if (!freed && n > 0 && !(alive = warp_wait(&bars->o_free[s], (n - 1) & 1, &s_abort))) break;
+      if (!freed && !(alive = warp_wait(&bars->o_free[s], (n - 1) & 1, &s_abort))) break;
       qn0 += x.two || qsel == 0;
       qn1 += x.two || qsel == 1;
       if (!x.two) qsel ^= 1;
       g += x.t1 - x.t0;
-      ++n;
-      u = it.first + x.t1;
-      if (u < u1 && !next_item(a.w, it)) break;
     }
     if (lane == 0) {
       // This warp's MMAs and the arrives they signal, before TMEM and shared memory go away.
       mma_commit(&bars->drain[s]);
       mbar_wait_bounded(&bars->drain[s], 0, nullptr, kDrainNs);
     }
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------------ softmax and output of stream s
+    setmaxnreg_inc();
     const int s = (warp - 4) >> 2, q4 = warp & 3;
     const int m = 32 * q4 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16);
     const uint32_t ts = lanes + 128 * s, to = lanes + 256;
     const float sc = a.scale_log2;
-    int n = 0, ns = 0, nb = 0;       // units, tiles, units of one row tile
-    int no = 0, no1 = 0;             // accumulators finished: this stream's, and stream 1's as stream 0 counts them
+    const uint64_t sc2 = pack2(sc, sc);
+    const int mt = m / a.G, mh = m - mt * a.G;  // token and q head within the row tile
+    int ns = 0, nb = 0;                         // tiles, units of one row tile
+    int no = 0, no1 = 0;  // accumulators finished: this stream's, and stream 1's as stream 0 counts them
     bool alive = true;
-    for (long long u = u0; u < u1 && alive;) {
-      const Unit x = unit_of(a, it, u, u1);
-      const int rt = x.two ? s : 0, end = stream_end(a, it, x, s);
-      const Row row = row_of(a, it, rt * 128 + m);
-      const bool busy = __any_sync(0xffffffffu, row.ok);  // some row of this warp exists
+    Unit x;
+    for (int n = 0; (alive = read_unit(tail, n, x, &s_abort)) && x.t1 > 0; ++n) {
+      const int end = stream_end(x, s);
+      const int rt = x.two ? s : 0, tok = rt * a.tile_tok + mt;  // within the block
+      const bool row_ok = mt < a.tile_tok && tok < x.ntok;
+      const bool busy = __any_sync(0xffffffffu, row_ok);  // some row of this warp exists
       const int first = x.two ? x.t0 : x.t0 + s, step = x.two ? 1 : 2;
-      const int tok_first = it.i * a.w.ctok + rt * a.tile_tok;
-      const int sees = a.w.N ? it.s.L : it.s.L + row.tok + 1;                 // cache rows this row sees
-      const int all_see = a.w.N ? it.s.L : it.s.L + tok_first + 1;            // that every row sees
+      const int sees = a.w.N ? x.L : x.L + x.tok0 + tok + 1;                    // cache rows this row sees
+      const int all_see = a.w.N ? x.L : x.L + x.tok0 + rt * a.tile_tok + 1;     // that every row sees
       float mu = -INFINITY, sum = 0.f;
       for (int t = first; t < end; t += step, ++ns) {
         if (!(alive = warp_wait(&bars->s_full[s], ns & 1, &s_abort))) break;
-        if (busy) {
-          tc_fence_after();
-          // Two passes over S in halves of 64 columns (the second one reads tensor memory
-          // again: holding 128 scores took more registers than a thread has).
-          const int keys = tile_keys(a, it, x, s, t), hs = (keys + 63) >> 6;
-          const bool tree = t >= x.pre;
-          const bool masked = tree || keys < kKeys || t * kKeys + kKeys > all_see;
-          uint32_t w[4] = {0u, 0u, 0u, 0u};  // keys this row sees
-          if (masked) {
+        if (!busy) {
+          mbar_arrive(&bars->p_full[s][0]);
+          mbar_arrive(&bars->p_full[s][1]);
+          continue;
+        }
+        tc_fence_after();
+        const int keys = tile_keys(a, x, s, t);
+        const bool tree = t >= x.pre, more = keys > 64;
+        float v[128];
+        tmem_ld32(ts, v);
+        tmem_ld32(ts + 32, v + 32);
+        if (more) {
+          tmem_ld32(ts + 64, v + 64);
+          tmem_ld32(ts + 96, v + 96);
+        }
+        tmem_wait_ld();
+        if (tree || keys < kKeys || t * kKeys + kKeys > all_see) {
+          const int j = (tree ? t - x.pre : t) * kKeys;  // first key
+          const int lim = (tree ? a.w.N : sees) - j;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int j = (tree ? t - x.pre : t) * kKeys + 32 * q;  // first key of the word
-              const int lim = (tree ? a.w.N : sees) - j;
-              if (row.ok && lim > 0) {
-                w[q] = lim >= 32 ? 0xffffffffu : (1u << lim) - 1u;
-                if (tree) w[q] &= __ldg(a.mask + (size_t)row.tok * a.W + (j >> 5));
-              }
-            }
+          for (int q = 0; q < 4; ++q) {
+            const int c = lim - 32 * q;
+            uint32_t w = !row_ok || c <= 0 ? 0u : c >= 32 ? 0xffffffffu : (1u << c) - 1u;
+            if (tree && w) w &= __ldg(a.mask + (size_t)(x.tok0 + tok) * a.W + (j >> 5) + q);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[32 * q + i] = (w >> i) & 1u ? v[32 * q + i] : -INFINITY;
           }
-          float v[64];
-          auto load = [&](int h) {
-            tmem_ld32(ts + 64 * h, v);
-            tmem_ld32(ts + 64 * h + 32, v + 32);
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) m4[(i >> 1) & 3] = fmaxf(fmaxf(m4[(i >> 1) & 3], v[i]), v[i + 1]);
+        if (more) {
+#pragma unroll
+          for (int i = 64; i < 128; i += 2) m4[(i >> 1) & 3] = fmaxf(fmaxf(m4[(i >> 1) & 3], v[i]), v[i + 1]);
+        }
+        const float mn = fmaxf(mu, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc);
+        const bool need = row_ok && mn > mu + 8.f;
+        const float f = need ? fast_exp2(mu - mn) : 1.f;  // 0 for the first keys seen
+        if (need) mu = mn;
+        if (t > first && __any_sync(0xffffffffu, need)) {
+          sum *= f;
+#pragma unroll 1
+          for (int q = 0; q < DH / 32; ++q) {
+            float o[32];
+            tmem_ld32(to + 128 * s + 32 * q, o);
             tmem_wait_ld();
-            if (masked) {
-              const uint32_t wa = h ? w[2] : w[0], wb = h ? w[3] : w[1];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                v[i] = (wa >> i) & 1u ? v[i] : -INFINITY;
-                v[32 + i] = (wb >> i) & 1u ? v[32 + i] : -INFINITY;
-              }
-            }
-          };
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-          for (int h = 0; h < hs; ++h) {
-            load(h);
-#pragma unroll
-            for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], v[i]);
+            for (int i = 0; i < 32; ++i) o[i] *= f;
+            tmem_st32(to + 128 * s + 32 * q, o);
           }
-          const float mn = fmaxf(mu, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc);
-          const bool need = row.ok && mn > mu + 8.f;
-          const float f = need ? fast_exp2(mu - mn) : 1.f;  // 0 for the first keys seen
-          if (need) mu = mn;
-          const float off = mu == -INFINITY ? 0.f : -mu;  // nothing seen: every 2^x is of -inf
-          float r4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-          for (int h = 0; h < hs; ++h) {
-            load(h);
-            uint32_t pk[32];
+        }
+        const float off = mu == -INFINITY ? 0.f : -mu;  // nothing seen: every 2^x is of -inf
+        const uint64_t off2 = pack2(off, off);
+        uint64_t r2[2] = {0ull, 0ull};
+        // Probabilities of 64 keys, over columns of S that have been read.
+        auto half = [&](const float* w, uint32_t at) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float e0 = fast_exp2(fmaf(v[2 * i], sc, off)), e1 = fast_exp2(fmaf(v[2 * i + 1], sc, off));
-              r4[i & 3] += e0 + e1;
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 e = unpack2(fma2(pack2(w[32 * q + 2 * i], w[32 * q + 2 * i + 1]), sc2, off2));
+              const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
+              r2[i & 1] = add2(r2[i & 1], pack2(e0, e1));
               pk[i] = bf16x2_rn(e0, e1);
             }
-            tmem_st32u(ts + 32 * h, pk);  // over columns that are read
-          }
-          sum = fmaf(sum, f, (r4[0] + r4[1]) + (r4[2] + r4[3]));
-          if (t > first && __any_sync(0xffffffffu, need)) {
-#pragma unroll
-            for (int q = 0; q < DH / 32; ++q) {
-              float o[32];
-              tmem_ld32(to + 128 * s + 32 * q, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= f;
-              tmem_st32(to + 128 * s + 32 * q, o);
-            }
+            tmem_st16u(at + 16 * q, pk);
           }
           tmem_wait_st();
           tc_fence_before();
-        }
-        mbar_arrive(&bars->p_full[s]);
+        };
+        half(v, ts);
+        mbar_arrive(&bars->p_full[s][0]);
+        if (more) half(v + 64, ts + 32);
+        mbar_arrive(&bars->p_full[s][1]);
+        const float2 a0 = unpack2(r2[0]), a1 = unpack2(r2[1]);
+        sum += (a0.x + a0.y) + (a1.x + a1.y);
       }
       if (!alive) break;
 
       // The unit's result: O / sum, or a part of it for the merge.
-      const bool whole = x.t0 == 0 && x.t1 == it.tiles;
-      const int slot = 2 * blockIdx.x + (x.t0 == 0 ? 1 : 0);
+      const bool whole = x.t0 == 0 && x.t1 == x.tiles, has = first < end;
       bool o1 = false;
       float w0 = 1.f, w1 = 0.f;
+      // The sums area is free, and every phase of o_free[1] seen, once the unit before is out.
       if (s == 1 && n > 0 && !(alive = warp_wait(&bars->o_free[1], (n - 1) & 1, &s_abort))) break;
       if (!x.two) {
         if (s == 1) {
-          sh.ml[m] = make_float2(mu, sum);
+          tail->ml[m] = make_float2(mu, sum);
           mbar_arrive(&bars->ml_full);
         } else {
           if (!(alive = warp_wait(&bars->ml_full, nb & 1, &s_abort))) break;
-          const float2 q = sh.ml[m];
+          const float2 q = tail->ml[m];
           o1 = x.t1 - x.t0 > 1;  // stream 1 had a tile
           const float mm = fmaxf(mu, q.x), off = mm == -INFINITY ? 0.f : mm;
           w0 = fast_exp2(mu - off);
@@ -469,7 +576,6 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         ++nb;
       }
       if (x.two || s == 0) {
-        const bool has = first < end;
         if (has && !(alive = warp_wait(&bars->o_full[s], no & 1, &s_abort))) break;
         if (o1 && !(alive = warp_wait(&bars->o_full[1], no1 & 1, &s_abort))) break;
         if (busy) {
@@ -477,7 +583,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
           w0 *= inv;
           w1 *= inv;
-          const size_t orow = out_row(a, it, row), prow = (size_t)slot * a.R + rt * 128 + m;
+          const size_t orow = ((size_t)x.row0 + tok) * a.Hq + x.kvh * a.G + mh;
+          const size_t prow = (size_t)(2 * blockIdx.x + (x.t0 == 0 ? 1 : 0)) * a.R + rt * 128 + m;
 #pragma unroll
           for (int q = 0; q < DH / 32; ++q) {
             float o[32];
@@ -497,14 +604,22 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = 0.f;
             }
-            if (!row.ok) continue;
+            if (!row_ok) continue;
             if (whole) {
               uint16_t* dst = static_cast<uint16_t*>(a.out) + orow * a.d + 32 * q;
+              uint32_t pk[16];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (32 * q + 8 * i < a.d)
-                  *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(bf16x2_rn(o[8 * i], o[8 * i + 1]), bf16x2_rn(o[8 * i + 2], o[8 * i + 3]),
-                                                                      bf16x2_rn(o[8 * i + 4], o[8 * i + 5]), bf16x2_rn(o[8 * i + 6], o[8 * i + 7]));
+              for (int i = 0; i < 16; ++i) pk[i] = bf16x2_rn(o[2 * i], o[2 * i + 1]);
+              if (a.out32) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  if (32 * q + 16 * i < a.d) st_v8u(dst + 16 * i, pk + 8 * i);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (32 * q + 8 * i < a.d)
+                    *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+              }
             } else {
               float* dst = a.part_o + prow * a.d + 32 * q;
 #pragma unroll
@@ -512,24 +627,17 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 if (32 * q + 8 * i < a.d) st_v8(dst + 8 * i, o + 8 * i);
             }
           }
-          if (row.ok) {
+          if (row_ok) {
             if (!whole) a.part_ml[prow] = make_float2(mu, sum);
             else if (a.lse) a.lse[orow] = lse_of(mu, sum);
           }
           tc_fence_before();
         }
-        if (x.two) {
-          mbar_arrive(&bars->o_free[s]);
-        } else {
-          mbar_arrive(&bars->o_free[0]);
-          mbar_arrive(&bars->o_free[1]);
-        }
+        mbar_arrive(&bars->o_free[s]);
+        if (!x.two) mbar_arrive(&bars->o_free[1]);
       }
-      no += first < end;
+      no += has;
       no1 += x.two || x.t1 - x.t0 > 1;  // stream 1 sees every tile of a two-tile block
-      ++n;
-      u = it.first + x.t1;
-      if (u < u1 && !next_item(a.w, it)) break;
     }
   }
 

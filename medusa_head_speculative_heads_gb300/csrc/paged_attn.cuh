@@ -10,6 +10,14 @@
 namespace medusa {
 namespace paged {
 
+// What the merge of a CTA boundary needs: the item the boundary falls inside,
+// and the CTAs that have its parts.  first < 0: nothing, or an earlier
+// boundary's.
+struct __align__(16) Shared {
+  Item it;
+  int first, last;
+};
+
 struct AttnArgs {
   Work w;
   Cache cache;
@@ -19,6 +27,7 @@ struct AttnArgs {
   float* lse;
   float* part_o;    // [slot][R][d] unnormalised sums of shared items
   float2* part_ml;  // [slot][R] their row maxima (log2 domain) and row sums
+  Shared* shared;   // [CTA] the boundary its range starts at
   int32_t* d_status;
   long long ldq;
   int Hq, Hkv, d, G;
@@ -26,6 +35,7 @@ struct AttnArgs {
   int R;          // rows of a partial slot
   int tile_rows, tile_tok;  // a block is tiles of tile_rows rows: tile_tok tokens x sub heads each
   int W;
+  int out32;  // rows of out start on 32 bytes
   float scale_log2;
 };
 
@@ -47,6 +57,20 @@ __device__ __forceinline__ Row row_of(const AttnArgs& a, const Item& it, int r) 
 // Index of the row in q, out ([nl * T] tokens, Hq heads) and lse.
 __device__ __forceinline__ size_t out_row(const AttnArgs& a, const Item& it, const Row& x) {
   return ((size_t)(it.lg / a.w.nh) * a.w.T + it.s.q0 + x.tok) * a.Hq + x.h;
+}
+
+// One thread of every CTA: what its boundary's merge has to do (`any`: the CTA
+// has tiles, `it` the item that holds its first).
+__device__ __forceinline__ void note_shared(const AttnArgs& a, const Plan& pl, const Item& it, bool any) {
+  Shared x;
+  x.it = it;
+  x.first = x.last = -1;
+  const long long u0 = pl.Q * blockIdx.x;
+  if (any && it.first < u0 && it.first >= u0 - pl.Q) {
+    x.first = (int)blockIdx.x - 1;
+    x.last = (int)divided(it.first + it.tiles - 1, pl.Q);
+  }
+  a.shared[blockIdx.x] = x;
 }
 
 // Natural logarithm of the softmax's sum from its maximum (log2 domain) and scaled sum.
