@@ -60,7 +60,7 @@ struct Bars {
   uint64_t full[kMaxSlots], empty[kMaxSlots];  // empty: two releases (a sole user's two)
   uint64_t q_full[2], q_empty[2];              // likewise
   uint64_t s_full[2], p_full[2][2];            // p_full: stream, half of the keys
-  uint64_t o_full[2], o_free[2], ml_full, drain[2];
+  uint64_t o_full[2], o_free[2], ml_full, drain[2];  // o_full, o_free: one phase a unit
   uint64_t u_full[kUnits], u_free[kUnits];
 };
 
@@ -114,11 +114,81 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_
       : "memory");
 }
 
+// One lane of the converged warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(ok));
+  return ok != 0;
+}
+// A value that is the same in all lanes, known to be so by the compiler.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Products of 16 columns (S) or 16 keys (P V) are issued from descriptors whose
+// constant halves are immediates and whose addresses grow by constants: formed
+// one by one in a loop, the descriptors took 100 to 300 clocks a product, more
+// than the tensor pipe.  Fields as in smem_desc_sw128: 128-byte swizzle, 1024
+// bytes between 8-row groups.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
+template <int DH>
+__device__ __forceinline__ void issue_scores(uint32_t ts, uint32_t qa, uint32_t ka, uint32_t idesc) {
+  const uint32_t q = (qa >> 4) | (1u << 16), k = (ka >> 4) | (1u << 16);
+#pragma unroll
+  for (int kk = 0; kk < DH / 16; ++kk) {
+    const uint32_t off = (kk >> 2) * (kHalf >> 4) + (kk & 3) * 2;
+    mma_bf16(ts, desc_of(q + off), desc_of(k + off), idesc, kk > 0);
+  }
+}
+// Four 16-key steps from step `first` on, those below `steps`.
+__device__ __forceinline__ void issue_sums(uint32_t to, uint32_t tp, uint32_t va, uint32_t idesc, int first, int steps, bool add) {
+  const uint32_t v = (va >> 4) | ((kHalf >> 4) << 16);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (first + i < steps) mma_bf16_ts(to, tp + 8 * (first + i), desc_of(v + 128 * (first + i)), idesc, i > 0 || add);
+}
+
+// Whether a phase has ended, without suspending the thread.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+
+// Waits for a phase like mbar_wait_bounded, but looks at the abort flag and the
+// (slow) global timer only once in 64 failed tries: a try suspends the thread
+// for a while by itself, and what is asked between two of them delays the
+// wake-up.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if ((int64_t)(now - t0) > (int64_t)kWaitNs) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
 // All lanes wait; true when all saw the phase end (the tcgen05 operations that
 // follow are warp-collective).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const bool ok = mbar_wait_bounded(bar, parity, abort, kWaitNs);
+  const bool ok = wait_bounded(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
+}
+
+// All lanes, whose work so far the arrival of one of them announces.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // 2^x on the SFU: relative error about 2^-22, far below P's rounding to bf16.
@@ -128,6 +198,11 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // Two fp32 operations at once.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
@@ -195,12 +270,6 @@ __device__ __forceinline__ int tile_rows_loaded(const AttnArgs& a, const Unit& x
   return t >= x.pre ? min(kKeys, a.w.N - (t - x.pre) * kKeys) : min(kKeys, x.rows_end - t * kKeys);
 }
 
-// Registers move from the four issuing warps to the softmax warps, which hold
-// 128 scores a thread: 128 x 80 + 256 x 208 of the 384 x 168 that the CTA is
-// launched with.
-__device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
-__device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
-
 // The next description, `n` units after the first: false on a timeout.
 __device__ __forceinline__ bool read_unit(Tail* tail, int n, Unit& x, volatile int* abort) {
   const int k = n % kUnits;
@@ -241,12 +310,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       mbar_init(&bars->q_full[s], 1);
       mbar_init(&bars->q_empty[s], 2);
       mbar_init(&bars->s_full[s], 1);
-      for (int h = 0; h < 2; ++h) mbar_init(&bars->p_full[s][h], 128);
+      for (int h = 0; h < 2; ++h) mbar_init(&bars->p_full[s][h], 4);
       mbar_init(&bars->o_full[s], 1);
-      mbar_init(&bars->o_free[s], 128);
+      mbar_init(&bars->o_free[s], 4);
       mbar_init(&bars->drain[s], 1);
     }
-    mbar_init(&bars->ml_full, 128);
+    mbar_init(&bars->ml_full, 4);
     for (int k = 0; k < kUnits; ++k) {
       mbar_init(&bars->u_full[k], 1);
       mbar_init(&bars->u_free[k], kUnitReaders);
@@ -278,9 +347,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   if (threadIdx.x == 0) note_shared(a, pl, it, any);
   __syncthreads();  // the plan is no longer read
 
+  // Registers move from the four issuing warps to the softmax warps, which hold 128 scores a
+  // thread: 128 x 80 + 256 x 208 of the 384 x 168 that the CTA is launched with.
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   if (warp == 3) {
     // ------------------------------------------------------------ planner
-    setmaxnreg_dec();
     const long long u0 = pl.Q * blockIdx.x;
     long long left = !any ? 0 : u0 + pl.Q < pl.U ? pl.Q : pl.U - u0;
     int t0 = any ? (int)(u0 - it.first) : 0;
@@ -302,7 +374,6 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
   } else if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    setmaxnreg_dec();
     int c = 0, issued = 0;           // slots used
     int qn0 = 0, qn1 = 0, qsel = 0;  // loads into the two Q buffers
     bool alive = true;
@@ -361,9 +432,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       for (int i = issued - 1; i >= 0 && i >= issued - C::slots; --i)
         mbar_wait_bounded(&bars->full[i % C::slots], (uint32_t)(i / C::slots) & 1u, nullptr, kDrainNs);
     }
-  } else if (warp < 4) {
+  } else {
     // ------------------------------------------------------------ MMA issuer of stream s
-    setmaxnreg_dec();
     const int s = warp - 1;
     const uint32_t ts = tmem + 128 * s, to = tmem + 256 + 128 * s;
     int g = 0;                               // tiles of earlier units (two ring slots each)
@@ -376,32 +446,37 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       // The other stream's rows too: every phase of a buffer is seen before a later one is waited for.
       if (x.two && !(alive = warp_wait(&bars->q_full[1 - qb], (qb ? qn0 : qn1) & 1, &s_abort))) break;
       const int first = x.two ? x.t0 : x.t0 + s, step = x.two ? 1 : 2;
-      bool freed = n == 0;  // O read out by the unit before
       const uint32_t qa = smem_u32(smem + qb * C::slot);
+      bool scored = false;  // S of tile t is issued
       for (int t = first; t < end; t += step, ++np) {
-        const int ck = 2 * (g + t - x.t0), cv = ck + 1;
-        const int releases = x.two && t < other_end ? 1 : 2;
-        uint64_t* ek = &bars->empty[ck % C::slots];
-        uint64_t* ev = &bars->empty[cv % C::slots];
-        if (!(alive = warp_wait(&bars->full[ck % C::slots], (uint32_t)(ck / C::slots) & 1u, &s_abort))) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t ka = smem_u32(smem + C::off_ring + (ck % C::slots) * C::slot);
-#pragma unroll
-          for (int kk = 0; kk < DH / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-            mma_bf16(ts, smem_desc_sw128(qa + off, 16, 1024), smem_desc_sw128(ka + off, 16, 1024), C::idesc_qk, kk > 0);
+        auto k_bar = [&](int tt) { return &bars->full[(2 * (g + tt - x.t0)) % C::slots]; };
+        auto k_par = [&](int tt) { return (uint32_t)((2 * (g + tt - x.t0)) / C::slots) & 1u; };
+        auto releases = [&](int tt) { return x.two && tt < other_end ? 1 : 2; };
+        auto scores = [&](int tt) {
+          const int ck = 2 * (g + tt - x.t0);
+          const uint32_t uk = uniform(smem_u32(smem + C::off_ring + (ck % C::slots) * C::slot)), uq = uniform(qa), ut = uniform(ts);
+          const int rel = releases(tt);
+          const bool last = tt + step >= end;
+          if (elect_one()) {
+            issue_scores<DH>(ut, uq, uk, C::idesc_qk);
+            mma_commit(&bars->s_full[s]);
+            mma_commit(&bars->empty[ck % C::slots]);
+            if (rel > 1) mma_commit(&bars->empty[ck % C::slots]);
+            if (last) {
+              mma_commit(&bars->q_empty[qb]);
+              if (x.two) mma_commit(&bars->q_empty[qb]);
+            }
           }
-          mma_commit(&bars->s_full[s]);
-          for (int r = 0; r < releases; ++r) mma_commit(ek);
-          if (t + step >= end)
-            for (int r = 0; r < (x.two ? 2 : 1); ++r) mma_commit(&bars->q_empty[qb]);
+          __syncwarp();
+        };
+        if (!scored) {
+          if (!(alive = warp_wait(k_bar(t), k_par(t), &s_abort))) break;
+          tc_fence_after();
+          scores(t);
+          __syncwarp();
         }
-        __syncwarp();
-        if (!freed) {
-          if (!(alive = warp_wait(&bars->o_free[s], (n - 1) & 1, &s_abort))) break;
-          freed = true;
-        }
+        const int cv = 2 * (g + t - x.t0) + 1;
+        if (t == first && n > 0 && !(alive = warp_wait(&bars->o_free[s], (n - 1) & 1, &s_abort))) break;
         if (!(alive = warp_wait(&bars->full[cv % C::slots], (uint32_t)(cv / C::slots) & 1u, &s_abort))) break;
         const int keys = tile_keys(a, x, s, t), steps = (keys + 15) >> 4, have = tile_rows_loaded(a, x, t);
         uint8_t* vb = smem + C::off_ring + (cv % C::slots) * C::slot;
@@ -416,41 +491,49 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const uint32_t va = smem_u32(vb);
         if (!(alive = warp_wait(&bars->p_full[s][0], np & 1, &s_abort))) break;
         tc_fence_after();
-        if (lane == 0) {
-          for (int kk = 0; kk < 4 && kk < steps; ++kk)
-            mma_bf16_ts(to, ts + 8 * kk, smem_desc_sw128(va + kk * 2048, kHalf, 1024), C::idesc_pv, kk > 0 || t > first);
-        }
+        const uint32_t uv = uniform(va), ut = uniform(ts), uo = uniform(to);
+        if (elect_one()) issue_sums(uo, ut, uv, C::idesc_pv, 0, steps, t > first);
         __syncwarp();
         if (!(alive = warp_wait(&bars->p_full[s][1], np & 1, &s_abort))) break;
         tc_fence_after();
-        if (lane == 0) {
-          for (int kk = 4; kk < steps; ++kk)
-            mma_bf16_ts(to, ts + 8 * kk, smem_desc_sw128(va + kk * 2048, kHalf, 1024), C::idesc_pv, 1);
-          if (t + step >= end) mma_commit(&bars->o_full[s]);
-          for (int r = 0; r < releases; ++r) mma_commit(ev);
+        scored = t + step < end && __all_sync(0xffffffffu, mbar_test_wait(k_bar(t + step), k_par(t + step)));
+        const int rel = releases(t);
+        const bool last = t + step >= end;
+        if (elect_one()) {
+          issue_sums(uo, ut, uv, C::idesc_pv, 4, steps, true);
+          if (last) mma_commit(&bars->o_full[s]);
+          mma_commit(&bars->empty[cv % C::slots]);
+          if (rel > 1) mma_commit(&bars->empty[cv % C::slots]);
         }
         __syncwarp();
+        if (scored) {
+          tc_fence_after();
+          scores(t + step);
+        }
       }
       if (!alive) break;
       if (first >= end) {  // no tile of this unit is this stream's
-        if (lane == 0)
+        if (n > 0 && !(alive = warp_wait(&bars->o_free[s], (n - 1) & 1, &s_abort))) break;
+        if (lane == 0) {
           for (int r = 0; r < (x.two ? 2 : 1); ++r) mbar_arrive(&bars->q_empty[qb]);
+          mbar_arrive(&bars->o_full[s]);  // so that no unit's output passes this wait for the one before
+        }
         __syncwarp();
       }
-      if (!freed && !(alive = warp_wait(&bars->o_free[s], (n - 1) & 1, &s_abort))) break;
       qn0 += x.two || qsel == 0;
       qn1 += x.two || qsel == 1;
       if (!x.two) qsel ^= 1;
       g += x.t1 - x.t0;
     }
-    if (lane == 0) {
+    if (elect_one()) {
       // This warp's MMAs and the arrives they signal, before TMEM and shared memory go away.
       mma_commit(&bars->drain[s]);
       mbar_wait_bounded(&bars->drain[s], 0, nullptr, kDrainNs);
     }
+  }
   } else {
     // ------------------------------------------------------------ softmax and output of stream s
-    setmaxnreg_inc();
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int s = (warp - 4) >> 2, q4 = warp & 3;
     const int m = 32 * q4 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16);
@@ -459,7 +542,6 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const uint64_t sc2 = pack2(sc, sc);
     const int mt = m / a.G, mh = m - mt * a.G;  // token and q head within the row tile
     int ns = 0, nb = 0;                         // tiles, units of one row tile
-    int no = 0, no1 = 0;  // accumulators finished: this stream's, and stream 1's as stream 0 counts them
     bool alive = true;
     Unit x;
     for (int n = 0; (alive = read_unit(tail, n, x, &s_abort)) && x.t1 > 0; ++n) {
@@ -474,14 +556,15 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       for (int t = first; t < end; t += step, ++ns) {
         if (!(alive = warp_wait(&bars->s_full[s], ns & 1, &s_abort))) break;
         if (!busy) {
-          mbar_arrive(&bars->p_full[s][0]);
-          mbar_arrive(&bars->p_full[s][1]);
+          warp_arrive(&bars->p_full[s][0]);
+          warp_arrive(&bars->p_full[s][1]);
           continue;
         }
         tc_fence_after();
         const int keys = tile_keys(a, x, s, t);
         const bool tree = t >= x.pre, more = keys > 64;
         float v[128];
+        __syncwarp();
         tmem_ld32(ts, v);
         tmem_ld32(ts + 32, v + 32);
         if (more) {
@@ -503,10 +586,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) m4[(i >> 1) & 3] = fmaxf(fmaxf(m4[(i >> 1) & 3], v[i]), v[i + 1]);
+        for (int i = 0; i < 64; i += 2) m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], v[i], v[i + 1]);
         if (more) {
 #pragma unroll
-          for (int i = 64; i < 128; i += 2) m4[(i >> 1) & 3] = fmaxf(fmaxf(m4[(i >> 1) & 3], v[i]), v[i + 1]);
+          for (int i = 64; i < 128; i += 2) m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], v[i], v[i + 1]);
         }
         const float mn = fmaxf(mu, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc);
         const bool need = row_ok && mn > mu + 8.f;
@@ -517,6 +600,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll 1
           for (int q = 0; q < DH / 32; ++q) {
             float o[32];
+            __syncwarp();
             tmem_ld32(to + 128 * s + 32 * q, o);
             tmem_wait_ld();
 #pragma unroll
@@ -529,6 +613,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         uint64_t r2[2] = {0ull, 0ull};
         // Probabilities of 64 keys, over columns of S that have been read.
         auto half = [&](const float* w, uint32_t at) {
+          __syncwarp();
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             uint32_t pk[16];
@@ -545,9 +630,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           tc_fence_before();
         };
         half(v, ts);
-        mbar_arrive(&bars->p_full[s][0]);
+        warp_arrive(&bars->p_full[s][0]);
         if (more) half(v + 64, ts + 32);
-        mbar_arrive(&bars->p_full[s][1]);
+        warp_arrive(&bars->p_full[s][1]);
         const float2 a0 = unpack2(r2[0]), a1 = unpack2(r2[1]);
         sum += (a0.x + a0.y) + (a1.x + a1.y);
       }
@@ -562,7 +647,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       if (!x.two) {
         if (s == 1) {
           tail->ml[m] = make_float2(mu, sum);
-          mbar_arrive(&bars->ml_full);
+          warp_arrive(&bars->ml_full);
         } else {
           if (!(alive = warp_wait(&bars->ml_full, nb & 1, &s_abort))) break;
           const float2 q = tail->ml[m];
@@ -576,8 +661,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         ++nb;
       }
       if (x.two || s == 0) {
-        if (has && !(alive = warp_wait(&bars->o_full[s], no & 1, &s_abort))) break;
-        if (o1 && !(alive = warp_wait(&bars->o_full[1], no1 & 1, &s_abort))) break;
+        if (!(alive = warp_wait(&bars->o_full[s], n & 1, &s_abort))) break;
+        if (!x.two && !(alive = warp_wait(&bars->o_full[1], n & 1, &s_abort))) break;
         if (busy) {
           tc_fence_after();
           const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
@@ -588,6 +673,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll
           for (int q = 0; q < DH / 32; ++q) {
             float o[32];
+            __syncwarp();
             if (has) {
               tmem_ld32(to + 128 * s + 32 * q, o);
               tmem_wait_ld();
@@ -633,11 +719,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           }
           tc_fence_before();
         }
-        mbar_arrive(&bars->o_free[s]);
-        if (!x.two) mbar_arrive(&bars->o_free[1]);
+        warp_arrive(&bars->o_free[s]);
+        if (!x.two) warp_arrive(&bars->o_free[1]);
       }
-      no += has;
-      no1 += x.two || x.t1 - x.t0 > 1;  // stream 1 sees every tile of a two-tile block
     }
   }
 
