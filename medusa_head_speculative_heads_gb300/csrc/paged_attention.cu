@@ -350,7 +350,8 @@ static Division divide(int T, int B, int Hq, int Hkv, int d, int page_size, medu
 }
 
 static size_t ws_bytes_of(const Division& v, int d) {
-  return (size_t)v.ctas * (2 * v.R * (d + 2) * sizeof(float) + sizeof(Shared));
+  // 16 bytes more: the parts start on 32 (stores of that width), the caller's buffer on 16.
+  return (size_t)v.ctas * (2 * v.R * (d + 2) * sizeof(float) + sizeof(Shared)) + 16;
 }
 
 template <typename T, int DC, int RM>
@@ -383,7 +384,7 @@ static medusa_status attend(AttnArgs& a, int n_layers, int T, int B, int Hq, int
   a.ldq = ldq;
   a.scale_log2 = scale * 1.4426950408889634f;
   if (!ws || !aligned16(ws) || ws_bytes < ws_bytes_of(v, d)) return MEDUSA_ERR_WORKSPACE;
-  a.part_o = static_cast<float*>(ws);
+  a.part_o = reinterpret_cast<float*>(align_up(reinterpret_cast<uintptr_t>(ws), 32));
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)v.ctas * 2 * v.R * d);
   a.shared = reinterpret_cast<Shared*>(a.part_ml + (size_t)v.ctas * 2 * v.R);
   a.R = v.R;

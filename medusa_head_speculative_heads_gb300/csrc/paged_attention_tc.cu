@@ -57,9 +57,12 @@ constexpr int kUnits = 4;              // described units in flight
 constexpr int kUnitReaders = 11;       // warps that read a description
 
 struct Bars {
-  uint64_t full[kMaxSlots], empty[kMaxSlots];  // empty: two releases (a sole user's two)
-  uint64_t q_full[2], q_empty[2];              // likewise
+  // Both streams see every phase of full and q_full, whether the rows are theirs or not, and each
+  // releases every slot once: a wait tells phases apart by their parity, so none may be skipped.
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2][2];            // p_full: stream, half of the keys
+  uint64_t turn[2];                            // a stream may issue its products of the next tile
   uint64_t o_full[2], o_free[2], ml_full, drain[2];  // o_full, o_free: one phase a unit
   uint64_t u_full[kUnits], u_free[kUnits];
 };
@@ -310,6 +313,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       mbar_init(&bars->q_full[s], 1);
       mbar_init(&bars->q_empty[s], 2);
       mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->turn[s], 1);
       for (int h = 0; h < 2; ++h) mbar_init(&bars->p_full[s][h], 4);
       mbar_init(&bars->o_full[s], 1);
       mbar_init(&bars->o_free[s], 4);
@@ -323,6 +327,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     fence_mbar_init();
   }
   if (warp == 1) {
+    __syncwarp();
     tmem_alloc(&tail->tmem, kTmemCols);
     tmem_relinquish();
   }
@@ -349,6 +354,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 
   // Registers move from the four issuing warps to the softmax warps, which hold 128 scores a
   // thread: 128 x 80 + 256 x 208 of the 384 x 168 that the CTA is launched with.
+  __syncwarp();  // one lane may have come out of the set-up on its own
   if (warp < 4) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   if (warp == 3) {
@@ -438,49 +444,57 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const uint32_t ts = tmem + 128 * s, to = tmem + 256 + 128 * s;
     int g = 0;                               // tiles of earlier units (two ring slots each)
     int qn0 = 0, qn1 = 0, qsel = 0, np = 0;  // np: tiles of this stream
+    int turns = 0;                           // taken
     bool alive = true;
     Unit x;
     for (int n = 0; (alive = read_unit(tail, n, x, &s_abort)) && x.t1 > 0; ++n) {
-      const int qb = x.two ? s : qsel, end = stream_end(x, s), other_end = stream_end(x, 1 - s);
+      const int qb = x.two ? s : qsel, end = stream_end(x, s);
       if (!(alive = warp_wait(&bars->q_full[qb], (qb ? qn1 : qn0) & 1, &s_abort))) break;
-      // The other stream's rows too: every phase of a buffer is seen before a later one is waited for.
-      if (x.two && !(alive = warp_wait(&bars->q_full[1 - qb], (qb ? qn0 : qn1) & 1, &s_abort))) break;
+      if (x.two) {  // the other stream's rows
+        if (!(alive = warp_wait(&bars->q_full[1 - qb], (qb ? qn0 : qn1) & 1, &s_abort))) break;
+        if (lane == 0) mbar_arrive(&bars->q_empty[1 - qb]);
+        __syncwarp();
+      }
       const int first = x.two ? x.t0 : x.t0 + s, step = x.two ? 1 : 2;
       const uint32_t qa = smem_u32(smem + qb * C::slot);
-      bool scored = false;  // S of tile t is issued
-      for (int t = first; t < end; t += step, ++np) {
-        auto k_bar = [&](int tt) { return &bars->full[(2 * (g + tt - x.t0)) % C::slots]; };
-        auto k_par = [&](int tt) { return (uint32_t)((2 * (g + tt - x.t0)) / C::slots) & 1u; };
-        auto releases = [&](int tt) { return x.two && tt < other_end ? 1 : 2; };
-        auto scores = [&](int tt) {
-          const int ck = 2 * (g + tt - x.t0);
-          const uint32_t uk = uniform(smem_u32(smem + C::off_ring + (ck % C::slots) * C::slot)), uq = uniform(qa), ut = uniform(ts);
-          const int rel = releases(tt);
-          const bool last = tt + step >= end;
-          if (elect_one()) {
-            issue_scores<DH>(ut, uq, uk, C::idesc_qk);
-            mma_commit(&bars->s_full[s]);
-            mma_commit(&bars->empty[ck % C::slots]);
-            if (rel > 1) mma_commit(&bars->empty[ck % C::slots]);
-            if (last) {
-              mma_commit(&bars->q_empty[qb]);
-              if (x.two) mma_commit(&bars->q_empty[qb]);
-            }
-          }
-          __syncwarp();
-        };
-        if (!scored) {
-          if (!(alive = warp_wait(k_bar(t), k_par(t), &s_abort))) break;
-          tc_fence_after();
-          scores(t);
-          __syncwarp();
+      auto slot_k = [&](int t) { return 2 * (g + t - x.t0); };  // K's place in the ring's order; V's is the next
+      auto came = [&](int c) { return warp_wait(&bars->full[c % C::slots], (uint32_t)(c / C::slots) & 1u, &s_abort); };
+      auto here = [&](int c) { return __all_sync(0xffffffffu, mbar_test_wait(&bars->full[c % C::slots], (uint32_t)(c / C::slots) & 1u)); };
+      // A tile that is the other stream's alone.
+      auto release = [&](int t) {
+        if (lane == 0) {
+          mbar_arrive(&bars->empty[slot_k(t) % C::slots]);
+          mbar_arrive(&bars->empty[(slot_k(t) + 1) % C::slots]);
         }
-        const int cv = 2 * (g + t - x.t0) + 1;
-        if (t == first && n > 0 && !(alive = warp_wait(&bars->o_free[s], (n - 1) & 1, &s_abort))) break;
-        if (!(alive = warp_wait(&bars->full[cv % C::slots], (uint32_t)(cv / C::slots) & 1u, &s_abort))) break;
-        const int keys = tile_keys(a, x, s, t), steps = (keys + 15) >> 4, have = tile_rows_loaded(a, x, t);
-        uint8_t* vb = smem + C::off_ring + (cv % C::slots) * C::slot;
+        __syncwarp();
+      };
+      auto skip = [&](int t) {
+        if (!came(slot_k(t)) || !came(slot_k(t) + 1)) return false;
+        release(t);
+        return true;
+      };
+      // S of tile t.
+      auto scores = [&](int t) {
+        const int ck = slot_k(t);
+        const uint32_t uk = uniform(smem_u32(smem + C::off_ring + (ck % C::slots) * C::slot)), uq = uniform(qa), ut = uniform(ts);
+        const bool last = t + step >= end;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_scores<DH>(ut, uq, uk, C::idesc_qk);
+          mma_commit(&bars->s_full[s]);
+          mma_commit(&bars->empty[ck % C::slots]);
+          if (last) mma_commit(&bars->q_empty[qb]);
+        }
+        __syncwarp();
+      };
+      // What P V of tile t needs but P: O read out by the unit before, and V, its rows behind the last one zeros.
+      auto v_ready = [&](int t) {
+        const int cv = slot_k(t) + 1;
+        if (t == first && n > 0 && !warp_wait(&bars->o_free[s], (n - 1) & 1, &s_abort)) return false;
+        if (!came(cv)) return false;
+        const int steps = (tile_keys(a, x, s, t) + 15) >> 4, have = tile_rows_loaded(a, x, t);
         if (have < steps * 16) {
+          uint8_t* vb = smem + C::off_ring + (cv % C::slots) * C::slot;
           for (int i = lane; i < (steps * 16 - have) * 8 * C::halves; i += 32) {
             const int r = have + i / (8 * C::halves), cc = i % (8 * C::halves);
             *reinterpret_cast<uint4*>(vb + (cc >> 3) * kHalf + r * 128 + (cc & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -488,34 +502,87 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           fence_proxy_async_smem();
           __syncwarp();
         }
-        const uint32_t va = smem_u32(vb);
-        if (!(alive = warp_wait(&bars->p_full[s][0], np & 1, &s_abort))) break;
-        tc_fence_after();
-        const uint32_t uv = uniform(va), ut = uniform(ts), uo = uniform(to);
-        if (elect_one()) issue_sums(uo, ut, uv, C::idesc_pv, 0, steps, t > first);
-        __syncwarp();
-        if (!(alive = warp_wait(&bars->p_full[s][1], np & 1, &s_abort))) break;
-        tc_fence_after();
-        scored = t + step < end && __all_sync(0xffffffffu, mbar_test_wait(k_bar(t + step), k_par(t + step)));
-        const int rel = releases(t);
+        return true;
+      };
+      // O += P V over one half of tile t's keys.
+      auto sums = [&](int t, int half) {
+        const int cv = slot_k(t) + 1, steps = (tile_keys(a, x, s, t) + 15) >> 4;
+        const uint32_t uv = uniform(smem_u32(smem + C::off_ring + (cv % C::slots) * C::slot)), ut = uniform(ts), uo = uniform(to);
         const bool last = t + step >= end;
+        tc_fence_after();
         if (elect_one()) {
-          issue_sums(uo, ut, uv, C::idesc_pv, 4, steps, true);
-          if (last) mma_commit(&bars->o_full[s]);
-          mma_commit(&bars->empty[cv % C::slots]);
-          if (rel > 1) mma_commit(&bars->empty[cv % C::slots]);
+          issue_sums(uo, ut, uv, C::idesc_pv, 4 * half, steps, half || t > first);
+          if (half) {
+            if (last) mma_commit(&bars->o_full[s]);
+            mma_commit(&bars->empty[cv % C::slots]);
+          }
         }
         __syncwarp();
-        if (scored) {
-          tc_fence_after();
-          scores(t + step);
+      };
+      if (x.two) {
+        // The streams take turns, a stream's P V of a tile and its S of the next one to a turn.  The
+        // tensor pipe takes products in the order of their issue: when both streams issued at will,
+        // theirs came in turns of one product, ended together, and both softmaxes then ran together
+        // with nothing in the pipe (prompt 1324 us).
+        auto my_turn = [&] { return (s == 0 && turns == 0) || warp_wait(&bars->turn[s], (turns - (s == 0)) & 1, &s_abort); };
+        auto pass = [&] {
+          ++turns;
+          if (lane == 0) mbar_arrive(&bars->turn[1 - s]);
+          __syncwarp();
+        };
+        if (first < end && !(alive = came(slot_k(first)))) break;
+        if (!(alive = my_turn())) break;
+        if (first < end) scores(first);
+        pass();
+        for (int t = x.t0; t < x.t1; ++t) {
+          const bool mine = t < end;
+          if (mine) {
+            if (!(alive = v_ready(t))) break;
+            if (t + 1 < end && !(alive = came(slot_k(t + 1)))) break;
+            if (!(alive = warp_wait(&bars->p_full[s][0], np & 1, &s_abort))) break;
+            if (!(alive = warp_wait(&bars->p_full[s][1], np & 1, &s_abort))) break;
+          } else if (!(alive = skip(t))) {
+            break;
+          }
+          if (!(alive = my_turn())) break;
+          if (mine) {
+            sums(t, 0);
+            sums(t, 1);
+            if (t + 1 < end) scores(t + 1);
+            ++np;
+          }
+          pass();
+        }
+      } else {
+        bool scored = false;  // S of tile t is issued, and the tile before it dealt with
+        for (int t = x.t0; t < x.t1; ++t) {
+          if (((t - x.t0) & 1) != s) {
+            if (scored) continue;
+            if (!(alive = skip(t))) break;
+            continue;
+          }
+          if (!scored) {
+            if (!(alive = came(slot_k(t)))) break;
+            scores(t);
+          }
+          if (!(alive = v_ready(t))) break;
+          if (!(alive = warp_wait(&bars->p_full[s][0], np & 1, &s_abort))) break;
+          sums(t, 0);
+          if (!(alive = warp_wait(&bars->p_full[s][1], np & 1, &s_abort))) break;
+          sums(t, 1);
+          ++np;
+          scored = t + 2 < end && here(slot_k(t + 1)) && here(slot_k(t + 1) + 1) && here(slot_k(t + 2));
+          if (scored) {
+            release(t + 1);
+            scores(t + 2);
+          }
         }
       }
       if (!alive) break;
       if (first >= end) {  // no tile of this unit is this stream's
         if (n > 0 && !(alive = warp_wait(&bars->o_free[s], (n - 1) & 1, &s_abort))) break;
         if (lane == 0) {
-          for (int r = 0; r < (x.two ? 2 : 1); ++r) mbar_arrive(&bars->q_empty[qb]);
+          mbar_arrive(&bars->q_empty[qb]);
           mbar_arrive(&bars->o_full[s]);  // so that no unit's output passes this wait for the one before
         }
         __syncwarp();
@@ -530,6 +597,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       mma_commit(&bars->drain[s]);
       mbar_wait_bounded(&bars->drain[s], 0, nullptr, kDrainNs);
     }
+    __syncwarp();
   }
   } else {
     // ------------------------------------------------------------ softmax and output of stream s
@@ -725,11 +793,15 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
   }
 
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (threadIdx.x == 0 && s_abort) set_status(a.d_status, MEDUSA_DEV_TIMEOUT);
-  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 1) {
+    __syncwarp();  // the lanes may come out of the barrier apart, and the warp frees once
+    tmem_dealloc(tmem, kTmemCols);
+  }
 }
 
 // ------------------------------------------------------------------ host side
