@@ -57,9 +57,10 @@ constexpr int kUnits = 4;              // described units in flight
 constexpr int kUnitReaders = 11;       // warps that read a description
 
 struct Bars {
-  // Both streams see every phase of full and q_full, whether the rows are theirs or not, and each
-  // releases every slot once: a wait tells phases apart by their parity, so none may be skipped.
-  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  // A wait tells phases apart by their parity, so a waiter may skip none: rows for stream 0 or 1 alone
+  // are announced in full[0] or full[1], rows for both in full[2], which both streams watch whether
+  // they need them or not.  Every slot and Q buffer is released twice.
+  uint64_t full[3][kMaxSlots], empty[kMaxSlots];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2][2];            // p_full: stream, half of the keys
   uint64_t turn[2];                            // a stream may issue its products of the next tile
@@ -306,7 +307,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   if (threadIdx.x == 0) {
     s_abort = 0;
     for (int i = 0; i < C::slots; ++i) {
-      mbar_init(&bars->full[i], 1);
+      for (int k = 0; k < 3; ++k) mbar_init(&bars->full[k][i], 1);
       mbar_init(&bars->empty[i], 2);
     }
     for (int s = 0; s < 2; ++s) {
@@ -380,8 +381,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
   } else if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    int c = 0, issued = 0;           // slots used
+    int c = 0;                       // slots used
     int qn0 = 0, qn1 = 0, qsel = 0;  // loads into the two Q buffers
+    uint32_t flips[3] = {0, 0, 0}, used[3] = {0, 0, 0};  // bits: a barrier has been used an odd number of times, at all
     bool alive = true;
     const int box = lane & 15, half = lane >> 4;
     Unit x;
@@ -421,12 +423,19 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         for (int kv = 0; kv < 2; ++kv, ++c) {
           const int sl = c % C::slots;
           if (c >= C::slots && !(alive = warp_wait(&bars->empty[sl], (uint32_t)(c / C::slots - 1) & 1u, &s_abort))) break;
-          if (lane == 0) mbar_expect_tx(&bars->full[sl], (uint32_t)(boxes * step * 128 * C::halves));
+          uint64_t* bar = &bars->full[x.two ? 2 : (t - x.t0) & 1][sl];
+          if (lane == 0) mbar_expect_tx(bar, (uint32_t)(boxes * step * 128 * C::halves));
           __syncwarp();
-          issued = c + 1;
           if (box < boxes && half < C::halves)
             tma_load_3d(smem + C::off_ring + sl * C::slot + half * kHalf + box * step * 128,
-                        kv ? (tree ? &tm_vt : &tm_v) : (tree ? &tm_kt : &tm_k), &bars->full[sl], 64 * half, x.kvh, at);
+                        kv ? (tree ? &tm_vt : &tm_v) : (tree ? &tm_kt : &tm_k), bar, 64 * half, x.kvh, at);
+          const int set = x.two ? 2 : (t - x.t0) & 1;
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            if (k == set) {
+              flips[k] ^= 1u << sl;
+              used[k] |= 1u << sl;
+            }
         }
       }
       if (!alive) break;
@@ -435,8 +444,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       // No copy may land after exit: wait (bounded) for the last phase of every load barrier.
       if (qn0 > 0) mbar_wait_bounded(&bars->q_full[0], (qn0 - 1) & 1, nullptr, kDrainNs);
       if (qn1 > 0) mbar_wait_bounded(&bars->q_full[1], (qn1 - 1) & 1, nullptr, kDrainNs);
-      for (int i = issued - 1; i >= 0 && i >= issued - C::slots; --i)
-        mbar_wait_bounded(&bars->full[i % C::slots], (uint32_t)(i / C::slots) & 1u, nullptr, kDrainNs);
+      for (int i = 0; i < C::slots; ++i)
+        for (int k = 0; k < 3; ++k)
+          if ((used[k] >> i) & 1) mbar_wait_bounded(&bars->full[k][i], ((flips[k] >> i) & 1) ^ 1, nullptr, kDrainNs);
     }
   } else {
     // ------------------------------------------------------------ MMA issuer of stream s
@@ -445,6 +455,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     int g = 0;                               // tiles of earlier units (two ring slots each)
     int qn0 = 0, qn1 = 0, qsel = 0, np = 0;  // np: tiles of this stream
     int turns = 0;                           // taken
+    uint32_t alone = 0, shared = 0;          // bit: parity of the next phase of full[s], full[2]
     bool alive = true;
     Unit x;
     for (int n = 0; (alive = read_unit(tail, n, x, &s_abort)) && x.t1 > 0; ++n) {
@@ -458,20 +469,17 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       const int first = x.two ? x.t0 : x.t0 + s, step = x.two ? 1 : 2;
       const uint32_t qa = smem_u32(smem + qb * C::slot);
       auto slot_k = [&](int t) { return 2 * (g + t - x.t0); };  // K's place in the ring's order; V's is the next
-      auto came = [&](int c) { return warp_wait(&bars->full[c % C::slots], (uint32_t)(c / C::slots) & 1u, &s_abort); };
-      auto here = [&](int c) { return __all_sync(0xffffffffu, mbar_test_wait(&bars->full[c % C::slots], (uint32_t)(c / C::slots) & 1u)); };
-      // A tile that is the other stream's alone.
-      auto release = [&](int t) {
-        if (lane == 0) {
-          mbar_arrive(&bars->empty[slot_k(t) % C::slots]);
-          mbar_arrive(&bars->empty[(slot_k(t) + 1) % C::slots]);
-        }
-        __syncwarp();
+      // Waits for slot c of a tile that this stream uses (or, of two row tiles, of any), each once.
+      auto came = [&](int c) {
+        const int sl = c % C::slots;
+        const bool ok = warp_wait(&bars->full[x.two ? 2 : s][sl], ((x.two ? shared : alone) >> sl) & 1u, &s_abort);
+        if (x.two) shared ^= 1u << sl;
+        else alone ^= 1u << sl;
+        return ok;
       };
-      auto skip = [&](int t) {
-        if (!came(slot_k(t)) || !came(slot_k(t) + 1)) return false;
-        release(t);
-        return true;
+      auto here = [&](int c) {  // without the flip
+        const int sl = c % C::slots;
+        return __all_sync(0xffffffffu, mbar_test_wait(&bars->full[s][sl], (alone >> sl) & 1u));
       };
       // S of tile t.
       auto scores = [&](int t) {
@@ -483,6 +491,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           issue_scores<DH>(ut, uq, uk, C::idesc_qk);
           mma_commit(&bars->s_full[s]);
           mma_commit(&bars->empty[ck % C::slots]);
+          if (!x.two) mma_commit(&bars->empty[ck % C::slots]);
           if (last) mma_commit(&bars->q_empty[qb]);
         }
         __syncwarp();
@@ -515,6 +524,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           if (half) {
             if (last) mma_commit(&bars->o_full[s]);
             mma_commit(&bars->empty[cv % C::slots]);
+            if (!x.two) mma_commit(&bars->empty[cv % C::slots]);
           }
         }
         __syncwarp();
@@ -541,8 +551,13 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             if (t + 1 < end && !(alive = came(slot_k(t + 1)))) break;
             if (!(alive = warp_wait(&bars->p_full[s][0], np & 1, &s_abort))) break;
             if (!(alive = warp_wait(&bars->p_full[s][1], np & 1, &s_abort))) break;
-          } else if (!(alive = skip(t))) {
-            break;
+          } else {
+            if (!(alive = came(slot_k(t)) && came(slot_k(t) + 1))) break;
+            if (lane == 0) {
+              mbar_arrive(&bars->empty[slot_k(t) % C::slots]);
+              mbar_arrive(&bars->empty[(slot_k(t) + 1) % C::slots]);
+            }
+            __syncwarp();
           }
           if (!(alive = my_turn())) break;
           if (mine) {
@@ -554,13 +569,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           pass();
         }
       } else {
-        bool scored = false;  // S of tile t is issued, and the tile before it dealt with
-        for (int t = x.t0; t < x.t1; ++t) {
-          if (((t - x.t0) & 1) != s) {
-            if (scored) continue;
-            if (!(alive = skip(t))) break;
-            continue;
-          }
+        bool scored = false;  // S of tile t is issued
+        for (int t = first; t < end; t += 2, ++np) {
           if (!scored) {
             if (!(alive = came(slot_k(t)))) break;
             scores(t);
@@ -570,10 +580,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           sums(t, 0);
           if (!(alive = warp_wait(&bars->p_full[s][1], np & 1, &s_abort))) break;
           sums(t, 1);
-          ++np;
-          scored = t + 2 < end && here(slot_k(t + 1)) && here(slot_k(t + 1) + 1) && here(slot_k(t + 2));
+          scored = t + 2 < end && here(slot_k(t + 2));
           if (scored) {
-            release(t + 1);
+            alone ^= 1u << (slot_k(t + 2) % C::slots);
             scores(t + 2);
           }
         }
@@ -631,6 +640,27 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         tc_fence_after();
         const int keys = tile_keys(a, x, s, t);
         const bool tree = t >= x.pre, more = keys > 64;
+        if (tree || keys < kKeys || t * kKeys + kKeys > all_see) {
+          // Tiles at the end of what a row sees: keys it does not see get -inf, in a pass of its own
+          // in tensor memory.  Code that runs once in many tiles is kept short: fetched cold, the
+          // unrolled form (and an unrolled output below) took 3000 and 6000 clocks.
+          const int j = (tree ? t - x.pre : t) * kKeys;  // first key
+          const int lim = (tree ? a.w.N : sees) - j;
+#pragma unroll 1
+          for (int q = 0; q < (more ? 4 : 2); ++q) {
+            const int c = lim - 32 * q;
+            uint32_t w = !row_ok || c <= 0 ? 0u : c >= 32 ? 0xffffffffu : (1u << c) - 1u;
+            if (tree && w) w &= __ldg(a.mask + (size_t)(x.tok0 + tok) * a.W + (j >> 5) + q);
+            float z[32];
+            __syncwarp();
+            tmem_ld32(ts + 32 * q, z);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = (w >> i) & 1u ? z[i] : -INFINITY;
+            tmem_st32(ts + 32 * q, z);
+          }
+          tmem_wait_st();
+        }
         float v[128];
         __syncwarp();
         tmem_ld32(ts, v);
@@ -640,18 +670,6 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           tmem_ld32(ts + 96, v + 96);
         }
         tmem_wait_ld();
-        if (tree || keys < kKeys || t * kKeys + kKeys > all_see) {
-          const int j = (tree ? t - x.pre : t) * kKeys;  // first key
-          const int lim = (tree ? a.w.N : sees) - j;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int c = lim - 32 * q;
-            uint32_t w = !row_ok || c <= 0 ? 0u : c >= 32 ? 0xffffffffu : (1u << c) - 1u;
-            if (tree && w) w &= __ldg(a.mask + (size_t)(x.tok0 + tok) * a.W + (j >> 5) + q);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[32 * q + i] = (w >> i) & 1u ? v[32 * q + i] : -INFINITY;
-          }
-        }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < 64; i += 2) m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], v[i], v[i + 1]);
@@ -738,7 +756,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           w1 *= inv;
           const size_t orow = ((size_t)x.row0 + tok) * a.Hq + x.kvh * a.G + mh;
           const size_t prow = (size_t)(2 * blockIdx.x + (x.t0 == 0 ? 1 : 0)) * a.R + rt * 128 + m;
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < DH / 32; ++q) {
             float o[32];
             __syncwarp();
