@@ -38,6 +38,7 @@ struct Work {
   int ctok, KT;               // tokens per block and keys per tile
   int ctok_log2, KT_log2;     // both are powers of two
   int ctas, min_tiles;
+  unsigned long long ctas_inv;  // 2^64 / ctas, rounded up
 };
 
 struct Seq {
@@ -110,66 +111,79 @@ struct Item {
 };
 
 // Block-wide set-up: every thread of the CTA calls plan_find() once.  It sums the
-// tiles per layer-head over the sequences and, for the tile `want(plan)` picks,
-// finds the item that holds it; false when that tile does not exist.  sh: 70 long
-// longs of shared memory.  Up to blockDim sequences take one round of loads and
-// two barriers.
+// tiles per layer-head over the sequences and finds the item that holds tile
+// Q `cta`; false when that tile does not exist.  sh: 70 long longs of shared
+// memory.  Up to blockDim sequences take one round of loads and two barriers.
+// Kept small, without 64-bit divisions: it runs once, so its instructions are
+// fetched cold.
 struct Plan {
   long long per, U, Q;  // tiles per layer-head, in all, per CTA
 };
 
-__device__ __forceinline__ long long divided(long long a, long long b) {  // a, b >= 0; most fit 32 bits
-  return (a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
-}
-
-template <typename Want>
-__device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, long long* sh, Want want) {
+__device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, long long* sh, int cta) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wp = tid >> 5, nw = nt >> 5;
-  // Inclusive sums over the warp, the first blockDim sequences' kept for the search.
+  const int rounds = (w.B + nt - 1) / nt;
   Seq s{};
-  long long v = 0, rest = 0;
-  if (tid < w.B) {
-    s = seq_of(w, tid);
-    v = seq_tiles(w, s);
-  }
-  for (int b = tid + nt; b < w.B; b += nt) rest += seq_tiles(w, seq_of(w, b));
-  long long inc = v;
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
-  }
-  for (int o = 16; o; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
-  if (lane == 31) {
-    sh[wp] = inc;
-    sh[32 + wp] = rest;
-  }
-  __syncthreads();
-  long long before = 0, total = 0, per = 0;
-  for (int j = 0; j < nw; ++j) {
-    if (j < wp) before += sh[j];
-    total += sh[j];
-    per += sh[32 + j];
-  }
-  per += total;
-  pl.per = per;
-  pl.U = per * ((long long)w.nl * w.nh);
-  pl.Q = divided(pl.U + w.ctas - 1, w.ctas);
-  if (pl.Q < w.min_tiles) pl.Q = w.min_tiles;
-  const long long u = want(pl);
-  if (u < 0 || u >= pl.U) return false;
-  const long long lg = divided(u, per), off = u - lg * per;
-  // The sequence whose tiles hold `off`, blockDim sequences at a time.
-  long long base = 0;
-  for (int b0 = 0;;) {
+  long long v = 0, inc = 0, before = 0, total = 0;
+  // This thread's sequence of a round, and the tiles of the round's sequences up to it and in all.
+  auto round = [&](int k) {
+    const int b = k * nt + tid;
+    v = 0;
+    if (b < w.B) {
+      s = seq_of(w, b);
+      v = seq_tiles(w, s);
+    }
+    inc = v;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    __syncthreads();  // the round before is read
+    if (lane == 31) sh[wp] = inc;
+    __syncthreads();
+    before = total = 0;
+#pragma unroll 1
+    for (int j = 0; j < nw; ++j) {
+      const long long y = sh[j];
+      if (j < wp) before += y;
+      total += y;
+    }
+  };
+  // First the sums of all rounds, then, the last round first being the one in hand, the search.
+  long long per = 0, u = -1, off = 0, base = 0;
+  int lg = 0;
+  bool found = false;
+#pragma unroll 1
+  for (int k = 0; k < 2 * rounds && !found; ++k) {
+    if (k < rounds || rounds > 1) round(k < rounds ? k : k - rounds);
+    if (k < rounds) {
+      per += total;
+      if (k + 1 < rounds) continue;
+      pl.per = per;
+      pl.U = per * ((long long)w.nl * w.nh);
+      pl.Q = (long long)__umul64hi((unsigned long long)(pl.U + w.ctas - 1), w.ctas_inv);
+      if (pl.Q < w.min_tiles) pl.Q = w.min_tiles;
+      u = pl.Q * cta;
+      if (u >= pl.U) return false;
+      lg = (int)((float)u / (float)per);  // to within a few
+#pragma unroll 1
+      while (lg * per > u) --lg;
+#pragma unroll 1
+      while ((lg + 1ll) * per <= u) ++lg;
+      off = u - lg * per;
+      continue;
+    }
     const long long lo = base + before + inc - v;
     if (v > 0 && off >= lo && off < lo + v) {  // one thread
       int i0 = 0, i1 = n_blocks(w, s);
+#pragma unroll 1
       while (i1 - i0 > 1) {
         const int m = (i0 + i1) >> 1;
         if (tiles_before(w, s, m) <= off - lo) i0 = m;
         else i1 = m;
       }
-      sh[64] = b0 + tid;
+      sh[64] = (k - rounds) * nt + tid;
       sh[65] = i0;
       sh[66] = lo + tiles_before(w, s, i0);
       sh[67] = s.q0;
@@ -177,30 +191,10 @@ __device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, lon
       sh[69] = s.L;
     }
     base += total;
-    b0 += nt;
-    if (base > off || b0 >= w.B) break;  // the same in every thread
-    const int b = b0 + tid;
-    v = 0;
-    if (b < w.B) {
-      s = seq_of(w, b);
-      v = seq_tiles(w, s);
-    }
-    inc = v;
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    __syncthreads();  // the last use of sh[0 .. 31] is over
-    if (lane == 31) sh[wp] = inc;
-    __syncthreads();
-    before = total = 0;
-    for (int j = 0; j < nw; ++j) {
-      if (j < wp) before += sh[j];
-      total += sh[j];
-    }
+    found = base > off;  // the same in every thread
   }
   __syncthreads();
-  it.lg = (int)lg;
+  it.lg = lg;
   it.b = (int)sh[64];
   it.i = (int)sh[65];
   it.s = Seq{(int)sh[67], (int)sh[68], (int)sh[69], true};
@@ -213,6 +207,7 @@ __device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, lon
 __device__ __forceinline__ bool next_item(const Work& w, Item& it) {
   it.first += it.tiles;
   ++it.i;
+#pragma unroll 1
   while (it.s.len == 0 || it.i >= n_blocks(w, it.s)) {
     it.i = 0;
     if (++it.b == w.B) {

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt_kernel(const __g
       if (!seq_of(a.w, b).ok) set_status(a.d_status, MEDUSA_DEV_BAD_LENGTH);
   Plan pl;
   Item it;
-  const bool any = plan_find(a.w, pl, it, sh, [](const Plan& p) { return p.Q * blockIdx.x; });
+  const bool any = plan_find(a.w, pl, it, sh, blockIdx.x);
   if (tid == 0) note_shared(a, pl, it, any);
   if (!any) return;
   const long long u0 = pl.Q * blockIdx.x, u1 = u0 + pl.Q < pl.U ? u0 + pl.Q : pl.U;
@@ -325,15 +325,19 @@ static Division divide(int T, int B, int Hq, int Hkv, int d, int page_size, medu
   const int G = Hq / Hkv, sms = device_sm_count();
   v.tc = tc_shape(G, d, page_size, dt);
   if (v.tc) {
-    v.R = 256;
-    v.tile_rows = 128;
+    // Blocks of up to 64 rows where a sequence has no more on average (decoding, trees), else of
+    // two tiles of 128: right for any lengths, but the first streams keys faster and the second
+    // reads them less often.
+    const bool narrow = (long long)T * G <= 64ll * B && G <= 64;
+    v.R = narrow ? 64 : 256;
+    v.tile_rows = narrow ? 64 : 128;
     v.ctas = sms;
     v.KT = 128;
     v.min_tiles = 2;
     v.sub = G;
     v.nsub = 1;
-    v.tile_tok = pow2_at_most(128 / G);
-    v.ctok = 2 * v.tile_tok;
+    v.tile_tok = pow2_at_most(v.tile_rows / G);
+    v.ctok = narrow ? v.tile_tok : 2 * v.tile_tok;
     return v;
   }
   // Rows of a tile: 16 when a sequence has at most 16 on average (decoding), else 64.
@@ -401,6 +405,7 @@ static medusa_status attend(AttnArgs& a, int n_layers, int T, int B, int Hq, int
   a.w.ctok_log2 = log2_of(v.ctok);
   a.w.KT_log2 = log2_of(v.KT);
   a.w.ctas = v.ctas;
+  a.w.ctas_inv = ~0ull / v.ctas + 1;
   a.w.min_tiles = v.min_tiles;
   a.w.B = B;
   a.w.T = T;

@@ -16,20 +16,21 @@
 //    same rows, stream s the key tiles t0 + s, t0 + s + 2, ...; their two
 //    results are added as two parts of a row are.
 // Within a stream S = Q K^T, softmax, O += P V follow one another; P (bf16)
-// overwrites S (its first 64 keys are handed over before the last 64 are
-// computed), and the next tile's S is issued by the same thread behind the
+// overwrites S, and the next tile's S is issued by the same thread behind the
 // P V that reads P, which orders the two.  A completed S therefore also says
 // that the P V before it is done, and O may be rescaled; that happens only when
 // a row's maximum has grown by more than 2^8 (the stale maximum is exact
 // arithmetic: the same power of two scales P and the sum).
 //
-// Warp 3 walks through the CTA's items and describes each one to the others in
-// shared memory.  Warp 0 brings Q and the K and V tiles by TMA into a ring of 128-row slots.
-// A tile is copied in boxes of gcd(page_size, 128) rows, one lane each looking
-// its page up; a page that does not exist is read as rows behind the pool,
-// which arrive as zeros.  Rows behind the last one are masked in S; the rows
-// of V up to the next multiple of 16 are zeroed before P V reads them (0 times
-// what a stale row holds could be NaN), and the products stop there.
+// Warp 0 walks through the CTA's items, describes each one to the others in
+// shared memory, and brings Q and the K tiles by TMA; warp 3 brings the V
+// tiles, each into a ring of its own (a warp alone took longer to issue a tile's
+// copies from 16-row pages than memory took to bring them).  A tile is copied
+// in boxes of gcd(page_size, 128) rows, each lane looking one page up a tile
+// ahead; a page that does not exist is read as rows behind the pool, which
+// arrive as zeros.  Rows behind the last one are masked in S; the rows of V up
+// to the next multiple of 16 are zeroed before P V reads them (0 times what a
+// stale row holds could be NaN), and the products stop there.
 //
 // Every wait is bounded: a timeout sets MEDUSA_DEV_TIMEOUT, all roles stop,
 // copies and MMAs in flight are waited for and tensor memory is freed.
@@ -46,13 +47,13 @@ using namespace sm100;
 
 namespace tc {
 
-constexpr int kThreads = 384;          // TMA, two MMA issuers, planner; 2 x 4 softmax warps
+constexpr int kThreads = 384;          // items and K, two MMA issuers, V; 2 x 4 softmax warps
 constexpr int kKeys = 128;             // keys of a tile
 constexpr uint32_t kHalf = 16384;      // 128 rows x 128 bytes (64 columns)
-constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr int kTries = 1 << 23;
 constexpr uint64_t kDrainNs = 100000000ull;
 constexpr uint32_t kTmemCols = 512;    // S0, S1, O0, O1
-constexpr int kMaxSlots = 10;
+constexpr int kMaxSlots = 12;
 constexpr int kUnits = 4;              // described units in flight
 constexpr int kUnitReaders = 11;       // warps that read a description
 
@@ -60,9 +61,9 @@ struct Bars {
   // A wait tells phases apart by their parity, so a waiter may skip none: rows for stream 0 or 1 alone
   // are announced in full[0] or full[1], rows for both in full[2], which both streams watch whether
   // they need them or not.  Every slot and Q buffer is released twice.
-  uint64_t full[3][kMaxSlots], empty[kMaxSlots];
+  uint64_t full[3][kMaxSlots], empty[kMaxSlots];  // K's slots, then V's
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_full[2][2];            // p_full: stream, half of the keys
+  uint64_t s_full[2], p_full[2];
   uint64_t turn[2];                            // a stream may issue its products of the next tile
   uint64_t o_full[2], o_free[2], ml_full, drain[2];  // o_full, o_free: one phase a unit
   uint64_t u_full[kUnits], u_free[kUnits];
@@ -97,13 +98,19 @@ struct Tail {
   volatile int abort;
 };
 
-// DH: columns computed, 64 or 128.
-template <int DH>
+// DH: columns computed, 64 or 128.  NARROW: blocks of one tile of at most 64 rows, whose Q buffers
+// (two 64-row halves of 128-row tiles; an MMA reads what follows as rows 64 .. 127, which do not
+// exist) leave room for more slots.
+template <int DH, bool NARROW>
 struct Cfg {
   static constexpr int halves = DH / 64;
-  static constexpr uint32_t slot = halves * kHalf;  // K or V of one tile; also Q of one stream
-  static constexpr int slots = DH == 128 ? 5 : 10;
-  static constexpr uint32_t off_ring = 2 * slot;
+  static constexpr uint32_t slot = halves * kHalf;  // K or V of one tile
+  static constexpr uint32_t q_step = NARROW ? kHalf / 2 : slot;  // from one Q buffer to the other
+  // Slots of K and of V.  A V tile stays longer: until its row's softmax and product are done.
+  static constexpr int nk = DH == 128 ? (NARROW ? 3 : 2) : (NARROW ? 6 : 5);
+  static constexpr int nv = DH == 128 ? 3 : (NARROW ? 6 : 5);
+  static constexpr int slots = nk + nv;
+  static constexpr uint32_t off_ring = NARROW ? slot : 2 * slot;
   static constexpr uint32_t off_bar = off_ring + slots * slot;
   static constexpr uint32_t smem = off_bar + sizeof(Tail);
   static constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false, false);
@@ -143,43 +150,26 @@ __device__ __forceinline__ void issue_scores(uint32_t ts, uint32_t qa, uint32_t 
     mma_bf16(ts, desc_of(q + off), desc_of(k + off), idesc, kk > 0);
   }
 }
-// Four 16-key steps from step `first` on, those below `steps`.
-__device__ __forceinline__ void issue_sums(uint32_t to, uint32_t tp, uint32_t va, uint32_t idesc, int first, int steps, bool add) {
+// The first `steps` 16-key steps; `add`: to what O holds.
+__device__ __forceinline__ void issue_sums(uint32_t to, uint32_t tp, uint32_t va, uint32_t idesc, int steps, bool add) {
   const uint32_t v = (va >> 4) | ((kHalf >> 4) << 16);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (first + i < steps) mma_bf16_ts(to, tp + 8 * (first + i), desc_of(v + 128 * (first + i)), idesc, i > 0 || add);
+  for (int i = 0; i < 8; ++i)
+    if (i < steps) mma_bf16_ts(to, tp + 8 * i, desc_of(v + 128 * i), idesc, i > 0 || add);
 }
 
-// Whether a phase has ended, without suspending the thread.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-               : "=r"(ok)
-               : "r"(smem_u32(bar)), "r"(parity)
-               : "memory");
-  return ok != 0;
-}
-
-// Waits for a phase like mbar_wait_bounded, but looks at the abort flag and the
-// (slow) global timer only once in 64 failed tries: a try suspends the thread
-// for a while by itself, and what is asked between two of them delays the
-// wake-up.
+// Waits for a phase, at most kTries tries (each takes 100 clocks or more: half a second at the
+// least); false when they have run out or *abort is set.  Short on purpose: there are some fifty
+// waits, and with a timer in each of them the kernel's code was 150 KB, of which every warp fetched
+// its share anew.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  uint64_t t0 = 0;
-  while (true) {
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-    const uint64_t now = global_timer_ns();
-    if (t0 == 0) t0 = now;
-    if ((int64_t)(now - t0) > (int64_t)kWaitNs) {
-      *abort = 1;
-      return false;
-    }
+  for (int n = kTries; n > 0; --n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 15) == 0 && *abort) return false;
   }
+  *abort = 1;
+  return false;
 }
 
 // All lanes wait; true when all saw the phase end (the tcgen05 operations that
@@ -274,6 +264,44 @@ __device__ __forceinline__ int tile_rows_loaded(const AttnArgs& a, const Unit& x
   return t >= x.pre ? min(kKeys, a.w.N - (t - x.pre) * kKeys) : min(kKeys, x.rows_end - t * kKeys);
 }
 
+// One lane per box of a tile of cache rows: its page's entry in the table, and its row within the
+// page; entry -1: the tile has no such box.
+struct Box {
+  int id, off;
+};
+__device__ __forceinline__ Box box_of(const AttnArgs& a, const Unit& x, int t, int lane, int box_rows) {
+  const int r = t * kKeys + lane * box_rows;
+  Box b{-1, 0};
+  if (t < x.pre && lane < kKeys / box_rows && r < x.rows_end) {
+    const int pg = r / a.cache.page_size;
+    b.off = r - pg * a.cache.page_size;
+    b.id = __ldg(a.cache.page_table + (size_t)x.b * a.cache.max_pages + pg);
+  }
+  return b;
+}
+// Copies tile t of K or V into `dst` (all lanes; `b`: box_of the tile).  A page that does not exist:
+// rows behind the pool, which arrive as zeros.
+template <int HALVES>
+__device__ __forceinline__ void copy_tile(const AttnArgs& a, const Unit& x, int t, const Box& b, int box_rows, const void* cache,
+                                          const void* tree_rows, uint8_t* dst, uint64_t* bar) {
+  const int lane = threadIdx.x & 31;
+  const bool tree = t >= x.pre;
+  const int step = tree ? 64 : box_rows, boxes = (tile_rows_loaded(a, x, t) + step - 1) / step;
+  int row = x.tree0 + (t - x.pre) * kKeys + lane * 64;
+  if (!tree) {
+    const bool exists = b.id >= 0 && b.id < a.cache.n_pages;
+    row = exists ? x.pool0 + b.id * a.cache.page_size + b.off : a.cache.n_pages * a.cache.page_size * a.w.nl;
+    if (!exists && lane < boxes) set_status(a.d_status, MEDUSA_DEV_BAD_INDEX);
+  }
+  __syncwarp();
+  if (elect_one()) mbar_expect_tx(bar, (uint32_t)(boxes * step * 128 * HALVES));
+  const void* map = tree ? tree_rows : cache;
+  __syncwarp();
+  const int r = __shfl_sync(0xffffffffu, row, lane & 15), box = lane & 15, h = lane >> 4;
+  if (box < boxes && h < HALVES) tma_load_3d(dst + h * kHalf + box * step * 128, map, bar, 64 * h, x.kvh, r);
+  __syncwarp();
+}
+
 // The next description, `n` units after the first: false on a timeout.
 __device__ __forceinline__ bool read_unit(Tail* tail, int n, Unit& x, volatile int* abort) {
   const int k = n % kUnits;
@@ -286,13 +314,14 @@ __device__ __forceinline__ bool read_unit(Tail* tail, int n, Unit& x, volatile i
 
 }  // namespace tc
 
-template <int DH>
+template <int DH, bool NARROW>
 __global__ void __launch_bounds__(tc::kThreads, 1)
 paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kt,
                      const __grid_constant__ CUtensorMap tm_vt, const __grid_constant__ AttnArgs a, const int box_rows) {
   using namespace tc;
-  using C = Cfg<DH>;
+  using C = Cfg<DH, NARROW>;
+  auto two = [](const Unit& x) { return !NARROW && x.two; };  // two row tiles
   extern __shared__ __align__(1024) uint8_t smem[];
   static_assert(C::smem <= 232448, "shared memory of a CTA");
   Tail* tail = reinterpret_cast<Tail*>(smem + C::off_bar);
@@ -306,6 +335,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     s_abort = 0;
+#pragma unroll 1
     for (int i = 0; i < C::slots; ++i) {
       for (int k = 0; k < 3; ++k) mbar_init(&bars->full[k][i], 1);
       mbar_init(&bars->empty[i], 2);
@@ -315,7 +345,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       mbar_init(&bars->q_empty[s], 2);
       mbar_init(&bars->s_full[s], 1);
       mbar_init(&bars->turn[s], 1);
-      for (int h = 0; h < 2; ++h) mbar_init(&bars->p_full[s][h], 4);
+      mbar_init(&bars->p_full[s], 4);
       mbar_init(&bars->o_full[s], 1);
       mbar_init(&bars->o_free[s], 4);
       mbar_init(&bars->drain[s], 1);
@@ -332,7 +362,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     tmem_alloc(&tail->tmem, kTmemCols);
     tmem_relinquish();
   }
-  if (warp == 0 && lane == 0) {
+  if (lane == 0 && (warp == 0 || warp == 3)) {
     tma_prefetch(&tm_q);
     tma_prefetch(&tm_k);
     tma_prefetch(&tm_v);
@@ -345,11 +375,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   pdl_trigger();
   const uint32_t tmem = tail->tmem;
   if (blockIdx.x == 0)
+#pragma unroll 1
     for (int b = threadIdx.x; b < a.w.B; b += kThreads)
       if (!seq_of(a.w, b).ok) set_status(a.d_status, MEDUSA_DEV_BAD_LENGTH);
   Plan pl;
   Item it;
-  const bool any = plan_find(a.w, pl, it, tail->plan, [](const Plan& p) { return p.Q * blockIdx.x; });
+  const bool any = plan_find(a.w, pl, it, tail->plan, blockIdx.x);
   if (threadIdx.x == 0) note_shared(a, pl, it, any);
   __syncthreads();  // the plan is no longer read
 
@@ -358,93 +389,112 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   __syncwarp();  // one lane may have come out of the set-up on its own
   if (warp < 4) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-  if (warp == 3) {
-    // ------------------------------------------------------------ planner
+  if (warp == 0) {
+    // ------------------------------------------------------------ items, Q and K
     const long long u0 = pl.Q * blockIdx.x;
     long long left = !any ? 0 : u0 + pl.Q < pl.U ? pl.Q : pl.U - u0;
     int t0 = any ? (int)(u0 - it.first) : 0;
+    int c = 0;                                           // tiles
+    int qn0 = 0, qn1 = 0, qsel = 0;                      // loads into the two Q buffers
+    uint32_t flips[3] = {0, 0, 0}, used[3] = {0, 0, 0};  // bits: a barrier has been used an odd number of times, at all
+    Unit x{};
+    bool alive = true;
+#pragma unroll 1
     for (int n = 0;; ++n) {
+      // Unit n is described (t1 = 0: there is none) before unit n - 1, x, is copied.
       const int k = n % kUnits;
-      if (n >= kUnits && !warp_wait(&bars->u_free[k], (uint32_t)(n / kUnits - 1) & 1u, &s_abort)) break;
-      Unit x{};
-      const bool more = left > 0;
-      if (more) x = unit_of(a, it, t0, left);
+      if (n >= kUnits && !(alive = warp_wait(&bars->u_free[k], (uint32_t)(n / kUnits - 1) & 1u, &s_abort))) break;
+      Unit y{};
+      if (left > 0) {
+        y = unit_of(a, it, t0, left);
+        left -= y.t1 - y.t0;
+        t0 = 0;
+        if (left > 0 && !next_item(a.w, it)) left = 0;
+      }
       if (lane == 0) {
-        tail->units[k] = x;
+        tail->units[k] = y;
         mbar_arrive(&bars->u_full[k]);
       }
       __syncwarp();
-      if (!more) break;
-      left -= x.t1 - x.t0;
-      t0 = 0;
-      if (left > 0 && !next_item(a.w, it)) left = 0;
-    }
-  } else if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
-    int c = 0;                       // slots used
-    int qn0 = 0, qn1 = 0, qsel = 0;  // loads into the two Q buffers
-    uint32_t flips[3] = {0, 0, 0}, used[3] = {0, 0, 0};  // bits: a barrier has been used an odd number of times, at all
-    bool alive = true;
-    const int box = lane & 15, half = lane >> 4;
-    Unit x;
-    for (int n = 0; (alive = read_unit(tail, n, x, &s_abort)) && x.t1 > 0; ++n) {
-      for (int k = 0; k < (x.two ? 2 : 1); ++k) {
-        const int qb = x.two ? k : qsel, used = qb ? qn1 : qn0;
-        if (used > 0 && !(alive = warp_wait(&bars->q_empty[qb], (used - 1) & 1, &s_abort))) break;
-        if (lane == 0) {
-          mbar_expect_tx(&bars->q_full[qb], (uint32_t)(C::halves * a.tile_tok * a.G * 128));
-          for (int h = 0; h < C::halves; ++h)
-            tma_load_3d(smem + qb * C::slot + h * kHalf, &tm_q, &bars->q_full[qb], 64 * h, x.kvh * a.G, x.row0 + k * a.tile_tok);
-        }
-        __syncwarp();
-        qn0 += qb == 0;
-        qn1 += qb == 1;
-      }
-      if (!alive) break;
-      if (!x.two) qsel ^= 1;
-      // The pool row of this lane's box of tile t (behind the pool: zeros).
-      auto box_row = [&](int t) {
-        const int r = t * kKeys + box * box_rows;
-        int row = a.cache.n_pages * a.cache.page_size * a.w.nl;
-        if (t < x.pre && box < kKeys / box_rows && r < x.rows_end) {
-          const int in = pool_row(a.cache, x.b, r);
-          if (in >= 0) row = x.pool0 + in;
-          else if (half == 0) set_status(a.d_status, MEDUSA_DEV_BAD_INDEX);
-        }
-        return row;
-      };
-      int row = box_row(x.t0);
-      for (int t = x.t0; t < x.t1 && alive; ++t) {
-        const bool tree = t >= x.pre;
-        const int step = tree ? 64 : box_rows;
-        const int boxes = (tile_rows_loaded(a, x, t) + step - 1) / step;
-        const int at = tree ? x.tree0 + (t - x.pre) * kKeys + box * 64 : row;
-        if (t + 1 < x.t1) row = box_row(t + 1);  // its latency passes under this tile's waits
-        for (int kv = 0; kv < 2; ++kv, ++c) {
-          const int sl = c % C::slots;
-          if (c >= C::slots && !(alive = warp_wait(&bars->empty[sl], (uint32_t)(c / C::slots - 1) & 1u, &s_abort))) break;
-          uint64_t* bar = &bars->full[x.two ? 2 : (t - x.t0) & 1][sl];
-          if (lane == 0) mbar_expect_tx(bar, (uint32_t)(boxes * step * 128 * C::halves));
+      if (n > 0) {
+#pragma unroll 1
+        for (int k = 0; k < (two(x) ? 2 : 1); ++k) {
+          const int qb = two(x) ? k : qsel, before = qb ? qn1 : qn0;
+          if (before > 0 && !(alive = warp_wait(&bars->q_empty[qb], (before - 1) & 1, &s_abort))) break;
+          if (elect_one()) {
+            mbar_expect_tx(&bars->q_full[qb], (uint32_t)(C::halves * a.tile_tok * a.G * 128));
+            for (int h = 0; h < C::halves; ++h)
+              tma_load_3d(smem + qb * C::q_step + h * kHalf, &tm_q, &bars->q_full[qb], 64 * h, x.kvh * a.G, x.row0 + k * a.tile_tok);
+          }
           __syncwarp();
-          if (box < boxes && half < C::halves)
-            tma_load_3d(smem + C::off_ring + sl * C::slot + half * kHalf + box * step * 128,
-                        kv ? (tree ? &tm_vt : &tm_v) : (tree ? &tm_kt : &tm_k), bar, 64 * half, x.kvh, at);
-          const int set = x.two ? 2 : (t - x.t0) & 1;
+          qn0 += qb == 0;
+          qn1 += qb == 1;
+        }
+        if (!alive) break;
+        if (!two(x)) qsel ^= 1;
+        Box b{-1, 0};
+#pragma unroll 1
+        for (int t = x.t0 - 1; t < x.t1; ++t) {
+          const Box next = box_of(a, x, t + 1, lane, box_rows);  // on its way while this tile waits
+          if (t >= x.t0) {
+            const int sl = c % C::nk, set = two(x) ? 2 : (t - x.t0) & 1;
+            if (c >= C::nk && !(alive = warp_wait(&bars->empty[sl], (uint32_t)(c / C::nk - 1) & 1u, &s_abort))) break;
+            copy_tile<C::halves>(a, x, t, b, box_rows, &tm_k, &tm_kt, smem + C::off_ring + sl * C::slot, &bars->full[set][sl]);
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+              if (k == set) {
+                flips[k] ^= 1u << sl;
+                used[k] |= 1u << sl;
+              }
+            ++c;
+          }
+          b = next;
+        }
+        if (!alive) break;
+      }
+      if (y.t1 <= 0) break;
+      x = y;
+    }
+    if (!alive) {
+      // No copy may land after exit: wait (bounded) for the last phase of every load barrier.
+      if (qn0 > 0) mbar_wait_bounded(&bars->q_full[0], (qn0 - 1) & 1, nullptr, kDrainNs);
+      if (qn1 > 0) mbar_wait_bounded(&bars->q_full[1], (qn1 - 1) & 1, nullptr, kDrainNs);
+#pragma unroll 1
+      for (int i = 0; i < C::nk; ++i)
+        for (int k = 0; k < 3; ++k)
+          if ((used[k] >> i) & 1) mbar_wait_bounded(&bars->full[k][i], ((flips[k] >> i) & 1) ^ 1, nullptr, kDrainNs);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ V
+    int c = 0;
+    uint32_t flips[3] = {0, 0, 0}, used[3] = {0, 0, 0};
+    bool alive = true;
+    Unit x;
+#pragma unroll 1
+    for (int n = 0; (alive = read_unit(tail, n, x, &s_abort)) && x.t1 > 0; ++n) {
+      Box b{-1, 0};
+#pragma unroll 1
+      for (int t = x.t0 - 1; t < x.t1; ++t) {
+        const Box next = box_of(a, x, t + 1, lane, box_rows);
+        if (t >= x.t0) {
+          const int i = c % C::nv, sl = C::nk + i, set = two(x) ? 2 : (t - x.t0) & 1;
+          if (c >= C::nv && !(alive = warp_wait(&bars->empty[sl], (uint32_t)(c / C::nv - 1) & 1u, &s_abort))) break;
+          copy_tile<C::halves>(a, x, t, b, box_rows, &tm_v, &tm_vt, smem + C::off_ring + sl * C::slot, &bars->full[set][sl]);
 #pragma unroll
           for (int k = 0; k < 3; ++k)
             if (k == set) {
               flips[k] ^= 1u << sl;
               used[k] |= 1u << sl;
             }
+          ++c;
         }
+        b = next;
       }
       if (!alive) break;
     }
     if (!alive) {
-      // No copy may land after exit: wait (bounded) for the last phase of every load barrier.
-      if (qn0 > 0) mbar_wait_bounded(&bars->q_full[0], (qn0 - 1) & 1, nullptr, kDrainNs);
-      if (qn1 > 0) mbar_wait_bounded(&bars->q_full[1], (qn1 - 1) & 1, nullptr, kDrainNs);
-      for (int i = 0; i < C::slots; ++i)
+#pragma unroll 1
+      for (int i = C::nk; i < C::slots; ++i)
         for (int k = 0; k < 3; ++k)
           if ((used[k] >> i) & 1) mbar_wait_bounded(&bars->full[k][i], ((flips[k] >> i) & 1) ^ 1, nullptr, kDrainNs);
     }
@@ -458,52 +508,50 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     uint32_t alone = 0, shared = 0;          // bit: parity of the next phase of full[s], full[2]
     bool alive = true;
     Unit x;
+#pragma unroll 1
     for (int n = 0; (alive = read_unit(tail, n, x, &s_abort)) && x.t1 > 0; ++n) {
-      const int qb = x.two ? s : qsel, end = stream_end(x, s);
+      const int qb = two(x) ? s : qsel, end = stream_end(x, s);
       if (!(alive = warp_wait(&bars->q_full[qb], (qb ? qn1 : qn0) & 1, &s_abort))) break;
-      if (x.two) {  // the other stream's rows
+      if (two(x)) {  // the other stream's rows
         if (!(alive = warp_wait(&bars->q_full[1 - qb], (qb ? qn0 : qn1) & 1, &s_abort))) break;
         if (lane == 0) mbar_arrive(&bars->q_empty[1 - qb]);
         __syncwarp();
       }
-      const int first = x.two ? x.t0 : x.t0 + s, step = x.two ? 1 : 2;
-      const uint32_t qa = smem_u32(smem + qb * C::slot);
-      auto slot_k = [&](int t) { return 2 * (g + t - x.t0); };  // K's place in the ring's order; V's is the next
-      // Waits for slot c of a tile that this stream uses (or, of two row tiles, of any), each once.
-      auto came = [&](int c) {
-        const int sl = c % C::slots;
-        const bool ok = warp_wait(&bars->full[x.two ? 2 : s][sl], ((x.two ? shared : alone) >> sl) & 1u, &s_abort);
-        if (x.two) shared ^= 1u << sl;
+      const int first = two(x) ? x.t0 : x.t0 + s, step = two(x) ? 1 : 2;
+      const uint32_t qa = smem_u32(smem + qb * C::q_step);
+      auto slot_k = [&](int t) { return (g + t - x.t0) % C::nk; };
+      auto slot_v = [&](int t) { return C::nk + (g + t - x.t0) % C::nv; };
+      // Waits for a slot of a tile that this stream uses (or, of two row tiles, of any), each once.
+      auto came = [&](int sl) {
+        const bool ok = warp_wait(&bars->full[two(x) ? 2 : s][sl], ((two(x) ? shared : alone) >> sl) & 1u, &s_abort);
+        if (two(x)) shared ^= 1u << sl;
         else alone ^= 1u << sl;
         return ok;
-      };
-      auto here = [&](int c) {  // without the flip
-        const int sl = c % C::slots;
-        return __all_sync(0xffffffffu, mbar_test_wait(&bars->full[s][sl], (alone >> sl) & 1u));
       };
       // S of tile t.
       auto scores = [&](int t) {
         const int ck = slot_k(t);
-        const uint32_t uk = uniform(smem_u32(smem + C::off_ring + (ck % C::slots) * C::slot)), uq = uniform(qa), ut = uniform(ts);
+        const uint32_t uk = uniform(smem_u32(smem + C::off_ring + ck * C::slot)), uq = uniform(qa), ut = uniform(ts);
         const bool last = t + step >= end;
         tc_fence_after();
         if (elect_one()) {
           issue_scores<DH>(ut, uq, uk, C::idesc_qk);
           mma_commit(&bars->s_full[s]);
-          mma_commit(&bars->empty[ck % C::slots]);
-          if (!x.two) mma_commit(&bars->empty[ck % C::slots]);
+          mma_commit(&bars->empty[ck]);
+          if (!two(x)) mma_commit(&bars->empty[ck]);
           if (last) mma_commit(&bars->q_empty[qb]);
         }
         __syncwarp();
       };
       // What P V of tile t needs but P: O read out by the unit before, and V, its rows behind the last one zeros.
       auto v_ready = [&](int t) {
-        const int cv = slot_k(t) + 1;
+        const int cv = slot_v(t);
         if (t == first && n > 0 && !warp_wait(&bars->o_free[s], (n - 1) & 1, &s_abort)) return false;
         if (!came(cv)) return false;
         const int steps = (tile_keys(a, x, s, t) + 15) >> 4, have = tile_rows_loaded(a, x, t);
         if (have < steps * 16) {
-          uint8_t* vb = smem + C::off_ring + (cv % C::slots) * C::slot;
+          uint8_t* vb = smem + C::off_ring + cv * C::slot;
+#pragma unroll 1
           for (int i = lane; i < (steps * 16 - have) * 8 * C::halves; i += 32) {
             const int r = have + i / (8 * C::halves), cc = i % (8 * C::halves);
             *reinterpret_cast<uint4*>(vb + (cc >> 3) * kHalf + r * 128 + (cc & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -513,79 +561,52 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         return true;
       };
-      // O += P V over one half of tile t's keys.
-      auto sums = [&](int t, int half) {
-        const int cv = slot_k(t) + 1, steps = (tile_keys(a, x, s, t) + 15) >> 4;
-        const uint32_t uv = uniform(smem_u32(smem + C::off_ring + (cv % C::slots) * C::slot)), ut = uniform(ts), uo = uniform(to);
+      // O += P V of tile t.
+      auto sums = [&](int t) {
+        const int cv = slot_v(t), steps = (tile_keys(a, x, s, t) + 15) >> 4;
+        const uint32_t uv = uniform(smem_u32(smem + C::off_ring + cv * C::slot)), ut = uniform(ts), uo = uniform(to);
         const bool last = t + step >= end;
         tc_fence_after();
         if (elect_one()) {
-          issue_sums(uo, ut, uv, C::idesc_pv, 4 * half, steps, half || t > first);
-          if (half) {
-            if (last) mma_commit(&bars->o_full[s]);
-            mma_commit(&bars->empty[cv % C::slots]);
-            if (!x.two) mma_commit(&bars->empty[cv % C::slots]);
-          }
+          issue_sums(uo, ut, uv, C::idesc_pv, steps, t > first);
+          if (last) mma_commit(&bars->o_full[s]);
+          mma_commit(&bars->empty[cv]);
+          if (!two(x)) mma_commit(&bars->empty[cv]);
         }
         __syncwarp();
       };
-      if (x.two) {
-        // The streams take turns, a stream's P V of a tile and its S of the next one to a turn.  The
-        // tensor pipe takes products in the order of their issue: when both streams issued at will,
-        // theirs came in turns of one product, ended together, and both softmaxes then ran together
-        // with nothing in the pipe (prompt 1324 us).
-        auto my_turn = [&] { return (s == 0 && turns == 0) || warp_wait(&bars->turn[s], (turns - (s == 0)) & 1, &s_abort); };
-        auto pass = [&] {
+      // Step by step: P V of tile t - step, then S of tile t, back to back.  Of a block of two row
+      // tiles the streams take turns.  The tensor pipe takes products in the order of their issue:
+      // when both streams issued at will, theirs came in turns of one product, ended together, and
+      // both softmaxes then ran together with nothing in the pipe.
+#pragma unroll 1
+      for (int t = first;; t += step) {
+        const bool had = t > first && t - step < end, has = t < end;
+        if (had) {
+          if (!(alive = v_ready(t - step) && warp_wait(&bars->p_full[s], np & 1, &s_abort))) break;
+          ++np;
+        } else if (two(x) && t > first) {  // a tile of the other stream's alone
+          if (!(alive = came(slot_k(t - 1)) && came(slot_v(t - 1)))) break;
+          if (lane == 0) {
+            mbar_arrive(&bars->empty[slot_k(t - 1)]);
+            mbar_arrive(&bars->empty[slot_v(t - 1)]);
+          }
+          __syncwarp();
+        }
+        if (two(x)) {
+          if ((s || turns) && !(alive = warp_wait(&bars->turn[s], (turns - (s == 0)) & 1, &s_abort))) break;
           ++turns;
+        }
+        if (had) sums(t - step);
+        if (has) {
+          if (!(alive = came(slot_k(t)))) break;
+          scores(t);
+        }
+        if (two(x)) {
           if (lane == 0) mbar_arrive(&bars->turn[1 - s]);
           __syncwarp();
-        };
-        if (first < end && !(alive = came(slot_k(first)))) break;
-        if (!(alive = my_turn())) break;
-        if (first < end) scores(first);
-        pass();
-        for (int t = x.t0; t < x.t1; ++t) {
-          const bool mine = t < end;
-          if (mine) {
-            if (!(alive = v_ready(t))) break;
-            if (t + 1 < end && !(alive = came(slot_k(t + 1)))) break;
-            if (!(alive = warp_wait(&bars->p_full[s][0], np & 1, &s_abort))) break;
-            if (!(alive = warp_wait(&bars->p_full[s][1], np & 1, &s_abort))) break;
-          } else {
-            if (!(alive = came(slot_k(t)) && came(slot_k(t) + 1))) break;
-            if (lane == 0) {
-              mbar_arrive(&bars->empty[slot_k(t) % C::slots]);
-              mbar_arrive(&bars->empty[(slot_k(t) + 1) % C::slots]);
-            }
-            __syncwarp();
-          }
-          if (!(alive = my_turn())) break;
-          if (mine) {
-            sums(t, 0);
-            sums(t, 1);
-            if (t + 1 < end) scores(t + 1);
-            ++np;
-          }
-          pass();
         }
-      } else {
-        bool scored = false;  // S of tile t is issued
-        for (int t = first; t < end; t += 2, ++np) {
-          if (!scored) {
-            if (!(alive = came(slot_k(t)))) break;
-            scores(t);
-          }
-          if (!(alive = v_ready(t))) break;
-          if (!(alive = warp_wait(&bars->p_full[s][0], np & 1, &s_abort))) break;
-          sums(t, 0);
-          if (!(alive = warp_wait(&bars->p_full[s][1], np & 1, &s_abort))) break;
-          sums(t, 1);
-          scored = t + 2 < end && here(slot_k(t + 2));
-          if (scored) {
-            alone ^= 1u << (slot_k(t + 2) % C::slots);
-            scores(t + 2);
-          }
-        }
+        if (two(x) ? t == x.t1 : !has) break;
       }
       if (!alive) break;
       if (first >= end) {  // no tile of this unit is this stream's
@@ -596,9 +617,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         __syncwarp();
       }
-      qn0 += x.two || qsel == 0;
-      qn1 += x.two || qsel == 1;
-      if (!x.two) qsel ^= 1;
+      qn0 += two(x) || qsel == 0;
+      qn1 += two(x) || qsel == 1;
+      if (!two(x)) qsel ^= 1;
       g += x.t1 - x.t0;
     }
     if (elect_one()) {
@@ -621,20 +642,21 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     int ns = 0, nb = 0;                         // tiles, units of one row tile
     bool alive = true;
     Unit x;
+#pragma unroll 1
     for (int n = 0; (alive = read_unit(tail, n, x, &s_abort)) && x.t1 > 0; ++n) {
       const int end = stream_end(x, s);
-      const int rt = x.two ? s : 0, tok = rt * a.tile_tok + mt;  // within the block
+      const int rt = two(x) ? s : 0, tok = rt * a.tile_tok + mt;  // within the block
       const bool row_ok = mt < a.tile_tok && tok < x.ntok;
       const bool busy = __any_sync(0xffffffffu, row_ok);  // some row of this warp exists
-      const int first = x.two ? x.t0 : x.t0 + s, step = x.two ? 1 : 2;
+      const int first = two(x) ? x.t0 : x.t0 + s, step = two(x) ? 1 : 2;
       const int sees = a.w.N ? x.L : x.L + x.tok0 + tok + 1;                    // cache rows this row sees
       const int all_see = a.w.N ? x.L : x.L + x.tok0 + rt * a.tile_tok + 1;     // that every row sees
       float mu = -INFINITY, sum = 0.f;
+#pragma unroll 1
       for (int t = first; t < end; t += step, ++ns) {
         if (!(alive = warp_wait(&bars->s_full[s], ns & 1, &s_abort))) break;
         if (!busy) {
-          warp_arrive(&bars->p_full[s][0]);
-          warp_arrive(&bars->p_full[s][1]);
+          warp_arrive(&bars->p_full[s]);
           continue;
         }
         tc_fence_after();
@@ -697,28 +719,24 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const float off = mu == -INFINITY ? 0.f : -mu;  // nothing seen: every 2^x is of -inf
         const uint64_t off2 = pack2(off, off);
         uint64_t r2[2] = {0ull, 0ull};
-        // Probabilities of 64 keys, over columns of S that have been read.
-        auto half = [&](const float* w, uint32_t at) {
-          __syncwarp();
+        // Probabilities, over columns of S that have been read.
+        __syncwarp();
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t pk[16];
+        for (int q = 0; q < 4; ++q) {
+          if (q >= 2 && !more) continue;
+          uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 e = unpack2(fma2(pack2(w[32 * q + 2 * i], w[32 * q + 2 * i + 1]), sc2, off2));
-              const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
-              r2[i & 1] = add2(r2[i & 1], pack2(e0, e1));
-              pk[i] = bf16x2_rn(e0, e1);
-            }
-            tmem_st16u(at + 16 * q, pk);
+          for (int i = 0; i < 16; ++i) {
+            const float2 e = unpack2(fma2(pack2(v[32 * q + 2 * i], v[32 * q + 2 * i + 1]), sc2, off2));
+            const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
+            r2[i & 1] = add2(r2[i & 1], pack2(e0, e1));
+            pk[i] = bf16x2_rn(e0, e1);
           }
-          tmem_wait_st();
-          tc_fence_before();
-        };
-        half(v, ts);
-        warp_arrive(&bars->p_full[s][0]);
-        if (more) half(v + 64, ts + 32);
-        warp_arrive(&bars->p_full[s][1]);
+          tmem_st16u(ts + 16 * q, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&bars->p_full[s]);
         const float2 a0 = unpack2(r2[0]), a1 = unpack2(r2[1]);
         sum += (a0.x + a0.y) + (a1.x + a1.y);
       }
@@ -730,7 +748,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       float w0 = 1.f, w1 = 0.f;
       // The sums area is free, and every phase of o_free[1] seen, once the unit before is out.
       if (s == 1 && n > 0 && !(alive = warp_wait(&bars->o_free[1], (n - 1) & 1, &s_abort))) break;
-      if (!x.two) {
+      if (!two(x)) {
         if (s == 1) {
           tail->ml[m] = make_float2(mu, sum);
           warp_arrive(&bars->ml_full);
@@ -746,9 +764,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         ++nb;
       }
-      if (x.two || s == 0) {
+      if (two(x) || s == 0) {
         if (!(alive = warp_wait(&bars->o_full[s], n & 1, &s_abort))) break;
-        if (!x.two && !(alive = warp_wait(&bars->o_full[1], n & 1, &s_abort))) break;
+        if (!two(x) && !(alive = warp_wait(&bars->o_full[1], n & 1, &s_abort))) break;
         if (busy) {
           tc_fence_after();
           const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
@@ -806,7 +824,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           tc_fence_before();
         }
         warp_arrive(&bars->o_free[s]);
-        if (!x.two) warp_arrive(&bars->o_free[1]);
+        if (!two(x)) warp_arrive(&bars->o_free[1]);
       }
     }
   }
@@ -847,12 +865,12 @@ static bool make_map(CUtensorMap* m, const void* base, int d, int heads, long lo
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DH>
+template <int DH, bool NARROW>
 static medusa_status go(const AttnArgs& a, const CUtensorMap* m, int box_rows, cudaStream_t s) {
-  auto kern = paged_attn_tc_kernel<DH>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tc::Cfg<DH>::smem) != cudaSuccess)
+  auto kern = paged_attn_tc_kernel<DH, NARROW>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tc::Cfg<DH, NARROW>::smem) != cudaSuccess)
     return MEDUSA_ERR_CUDA;
-  launch_pdl(kern, dim3(a.w.ctas), dim3(tc::kThreads), tc::Cfg<DH>::smem, s, m[0], m[1], m[2], m[3], m[4], a, box_rows);
+  launch_pdl(kern, dim3(a.w.ctas), dim3(tc::kThreads), tc::Cfg<DH, NARROW>::smem, s, m[0], m[1], m[2], m[3], m[4], a, box_rows);
   return MEDUSA_OK;
 }
 
@@ -872,7 +890,8 @@ medusa_status paged_attention_tc(const AttnArgs& a, cudaStream_t s) {
     m[3] = m[1];
     m[4] = m[2];
   }
-  return a.d <= 64 ? go<64>(a, m, box_rows, s) : go<128>(a, m, box_rows, s);
+  if (a.R == 64) return a.d <= 64 ? go<64, true>(a, m, box_rows, s) : go<128, true>(a, m, box_rows, s);
+  return a.d <= 64 ? go<64, false>(a, m, box_rows, s) : go<128, false>(a, m, box_rows, s);
 }
 
 }  // namespace paged

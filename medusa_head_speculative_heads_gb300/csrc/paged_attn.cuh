@@ -68,7 +68,8 @@ __device__ __forceinline__ void note_shared(const AttnArgs& a, const Plan& pl, c
   const long long u0 = pl.Q * blockIdx.x;
   if (any && it.first < u0 && it.first >= u0 - pl.Q) {
     x.first = (int)blockIdx.x - 1;
-    x.last = (int)divided(it.first + it.tiles - 1, pl.Q);
+    const long long rest = it.first + it.tiles - u0;  // tiles from the boundary on
+    x.last = (int)blockIdx.x + (rest <= pl.Q ? 0 : (int)((unsigned)(rest - 1) / (unsigned)pl.Q));
   }
   a.shared[blockIdx.x] = x;
 }
