@@ -141,11 +141,12 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xf
 // bytes between 8-row groups.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
-template <int DH>
+// The first (H = 0) or second half of S's products.
+template <int DH, int H>
 __device__ __forceinline__ void issue_scores(uint32_t ts, uint32_t qa, uint32_t ka, uint32_t idesc) {
   const uint32_t q = (qa >> 4) | (1u << 16), k = (ka >> 4) | (1u << 16);
 #pragma unroll
-  for (int kk = 0; kk < DH / 16; ++kk) {
+  for (int kk = H * DH / 32; kk < (H + 1) * DH / 32; ++kk) {
     const uint32_t off = (kk >> 2) * (kHalf >> 4) + (kk & 3) * 2;
     mma_bf16(ts, desc_of(q + off), desc_of(k + off), idesc, kk > 0);
   }
@@ -528,21 +529,6 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         else alone ^= 1u << sl;
         return ok;
       };
-      // S of tile t.
-      auto scores = [&](int t) {
-        const int ck = slot_k(t);
-        const uint32_t uk = uniform(smem_u32(smem + C::off_ring + ck * C::slot)), uq = uniform(qa), ut = uniform(ts);
-        const bool last = t + step >= end;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_scores<DH>(ut, uq, uk, C::idesc_qk);
-          mma_commit(&bars->s_full[s]);
-          mma_commit(&bars->empty[ck]);
-          if (!two(x)) mma_commit(&bars->empty[ck]);
-          if (last) mma_commit(&bars->q_empty[qb]);
-        }
-        __syncwarp();
-      };
       // What P V of tile t needs but P: O read out by the unit before, and V, its rows behind the last one zeros.
       auto v_ready = [&](int t) {
         const int cv = slot_v(t);
@@ -561,30 +547,16 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         return true;
       };
-      // O += P V of tile t.
-      auto sums = [&](int t) {
-        const int cv = slot_v(t), steps = (tile_keys(a, x, s, t) + 15) >> 4;
-        const uint32_t uv = uniform(smem_u32(smem + C::off_ring + cv * C::slot)), ut = uniform(ts), uo = uniform(to);
-        const bool last = t + step >= end;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_sums(uo, ut, uv, C::idesc_pv, steps, t > first);
-          if (last) mma_commit(&bars->o_full[s]);
-          mma_commit(&bars->empty[cv]);
-          if (!two(x)) mma_commit(&bars->empty[cv]);
-        }
-        __syncwarp();
-      };
       // Step by step: P V of tile t - step, then S of tile t, back to back.  Of a block of two row
       // tiles the streams take turns.  The tensor pipe takes products in the order of their issue:
       // when both streams issued at will, theirs came in turns of one product, ended together, and
-      // both softmaxes then ran together with nothing in the pipe.
+      // both softmaxes then ran together with nothing in the pipe.  A turn is passed on before the
+      // last products are issued: the other warp needs some 400 clocks to see it.
 #pragma unroll 1
       for (int t = first;; t += step) {
         const bool had = t > first && t - step < end, has = t < end;
         if (had) {
-          if (!(alive = v_ready(t - step) && warp_wait(&bars->p_full[s], np & 1, &s_abort))) break;
-          ++np;
+          if (!(alive = v_ready(t - step))) break;
         } else if (two(x) && t > first) {  // a tile of the other stream's alone
           if (!(alive = came(slot_k(t - 1)) && came(slot_v(t - 1)))) break;
           if (lane == 0) {
@@ -593,20 +565,64 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           }
           __syncwarp();
         }
-        if (two(x)) {
+        // Of one row tile the next K may still be far: P V does not wait for it.
+        bool k_came = false;
+        if (has && (two(x) || !had)) {
+          if (!(alive = came(slot_k(t)))) break;
+          k_came = true;
+        }
+        const int cv = slot_v(t - step), ck = slot_k(t), steps = had ? (tile_keys(a, x, s, t - step) + 15) >> 4 : 0;
+        const uint32_t uv = uniform(smem_u32(smem + C::off_ring + cv * C::slot)), uk = uniform(smem_u32(smem + C::off_ring + ck * C::slot));
+        const uint32_t uq = uniform(qa), ut = uniform(ts), uo = uniform(to);
+        if (two(x)) {  // before P, which comes last as a rule
           if ((s || turns) && !(alive = warp_wait(&bars->turn[s], (turns - (s == 0)) & 1, &s_abort))) break;
           ++turns;
         }
-        if (had) sums(t - step);
-        if (has) {
-          if (!(alive = came(slot_k(t)))) break;
-          scores(t);
+        if (had) {
+          if (!(alive = warp_wait(&bars->p_full[s], np & 1, &s_abort))) break;
+          ++np;
         }
+        tc_fence_after();
         if (two(x)) {
-          if (lane == 0) mbar_arrive(&bars->turn[1 - s]);
+          if (elect_one()) {
+            if (had) issue_sums(uo, ut, uv, C::idesc_pv, steps, t - step > first);
+            if (has) issue_scores<DH, 0>(ut, uq, uk, C::idesc_qk);
+            mbar_arrive(&bars->turn[1 - s]);
+            if (has) {
+              issue_scores<DH, 1>(ut, uq, uk, C::idesc_qk);
+              mma_commit(&bars->s_full[s]);
+              mma_commit(&bars->empty[ck]);
+              if (t + step >= end) mma_commit(&bars->q_empty[qb]);
+            } else if (had) {
+              mma_commit(&bars->o_full[s]);
+            }
+            if (had) mma_commit(&bars->empty[cv]);
+          }
+          __syncwarp();
+          if (t == x.t1) break;
+        } else {
+          if (had && elect_one()) {
+            issue_sums(uo, ut, uv, C::idesc_pv, steps, t - step > first);
+            if (!has) mma_commit(&bars->o_full[s]);
+            mma_commit(&bars->empty[cv]);
+            mma_commit(&bars->empty[cv]);
+          }
+          __syncwarp();
+          if (!has) break;
+          if (!k_came) {
+            if (!(alive = came(ck))) break;
+            tc_fence_after();
+          }
+          if (elect_one()) {
+            issue_scores<DH, 0>(ut, uq, uk, C::idesc_qk);
+            issue_scores<DH, 1>(ut, uq, uk, C::idesc_qk);
+            mma_commit(&bars->s_full[s]);
+            mma_commit(&bars->empty[ck]);
+            mma_commit(&bars->empty[ck]);
+            if (t + step >= end) mma_commit(&bars->q_empty[qb]);
+          }
           __syncwarp();
         }
-        if (two(x) ? t == x.t1 : !has) break;
       }
       if (!alive) break;
       if (first >= end) {  // no tile of this unit is this stream's
@@ -654,22 +670,22 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       float mu = -INFINITY, sum = 0.f;
 #pragma unroll 1
       for (int t = first; t < end; t += step, ++ns) {
+        const int keys = tile_keys(a, x, s, t);
+        const bool tree = t >= x.pre, masked = tree || keys < kKeys || t * kKeys + kKeys > all_see;
         if (!(alive = warp_wait(&bars->s_full[s], ns & 1, &s_abort))) break;
         if (!busy) {
           warp_arrive(&bars->p_full[s]);
           continue;
         }
         tc_fence_after();
-        const int keys = tile_keys(a, x, s, t);
-        const bool tree = t >= x.pre, more = keys > 64;
-        if (tree || keys < kKeys || t * kKeys + kKeys > all_see) {
+        if (masked) {
           // Tiles at the end of what a row sees: keys it does not see get -inf, in a pass of its own
           // in tensor memory.  Code that runs once in many tiles is kept short: fetched cold, the
           // unrolled form (and an unrolled output below) took 3000 and 6000 clocks.
           const int j = (tree ? t - x.pre : t) * kKeys;  // first key
           const int lim = (tree ? a.w.N : sees) - j;
 #pragma unroll 1
-          for (int q = 0; q < (more ? 4 : 2); ++q) {
+          for (int q = 0; q < 4; ++q) {
             const int c = lim - 32 * q;
             uint32_t w = !row_ok || c <= 0 ? 0u : c >= 32 ? 0xffffffffu : (1u << c) - 1u;
             if (tree && w) w &= __ldg(a.mask + (size_t)(x.tok0 + tok) * a.W + (j >> 5) + q);
@@ -687,22 +703,33 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         __syncwarp();
         tmem_ld32(ts, v);
         tmem_ld32(ts + 32, v + 32);
-        if (more) {
-          tmem_ld32(ts + 64, v + 64);
-          tmem_ld32(ts + 96, v + 96);
-        }
+        tmem_ld32(ts + 64, v + 64);
+        tmem_ld32(ts + 96, v + 96);
         tmem_wait_ld();
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], v[i], v[i + 1]);
-        if (more) {
-#pragma unroll
-          for (int i = 64; i < 128; i += 2) m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], v[i], v[i + 1]);
-        }
+        for (int i = 0; i < 128; i += 2) m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], v[i], v[i + 1]);
         const float mn = fmaxf(mu, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc);
         const bool need = row_ok && mn > mu + 8.f;
         const float f = need ? fast_exp2(mu - mn) : 1.f;  // 0 for the first keys seen
         if (need) mu = mn;
+        const float off = mu == -INFINITY ? 0.f : -mu;  // nothing seen: every 2^x is of -inf
+        const uint64_t off2 = pack2(off, off);
+        uint64_t r2[2] = {0ull, 0ull};
+        // Probabilities, over columns of S that have been read.
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 e = unpack2(fma2(pack2(v[32 * q + 2 * i], v[32 * q + 2 * i + 1]), sc2, off2));
+            const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
+            r2[i & 1] = add2(r2[i & 1], pack2(e0, e1));
+            pk[i] = bf16x2_rn(e0, e1);
+          }
+          tmem_st16u(ts + 16 * q, pk);
+        }
         if (t > first && __any_sync(0xffffffffu, need)) {
           sum *= f;
 #pragma unroll 1
@@ -715,24 +742,6 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             for (int i = 0; i < 32; ++i) o[i] *= f;
             tmem_st32(to + 128 * s + 32 * q, o);
           }
-        }
-        const float off = mu == -INFINITY ? 0.f : -mu;  // nothing seen: every 2^x is of -inf
-        const uint64_t off2 = pack2(off, off);
-        uint64_t r2[2] = {0ull, 0ull};
-        // Probabilities, over columns of S that have been read.
-        __syncwarp();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (q >= 2 && !more) continue;
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 e = unpack2(fma2(pack2(v[32 * q + 2 * i], v[32 * q + 2 * i + 1]), sc2, off2));
-            const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
-            r2[i & 1] = add2(r2[i & 1], pack2(e0, e1));
-            pk[i] = bf16x2_rn(e0, e1);
-          }
-          tmem_st16u(ts + 16 * q, pk);
         }
         tmem_wait_st();
         tc_fence_before();
