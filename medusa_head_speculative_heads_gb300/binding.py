@@ -221,28 +221,6 @@ class medusa_rope_plan(ctypes.Structure):
                 ("reserved", ctypes.c_int32), ("turn", ctypes.c_uint64 * 128)]
 
 
-class RopeSpec:
-    """How a rotary embedding turns (medusa_rope_plan): built once, passed to
-    medusa_rope and medusa_paged_append.  scaling is "none", "linear", "bands" or
-    "ramp"; see include/medusa.h for the formulas."""
-
-    SCALINGS = ("none", "linear", "bands", "ramp")
-
-    def __init__(self, rotary_dim: int, interleaved: bool = False, base: float = 10000.0, scaling: str = "none",
-                 factor: float = 1.0, low: float = 1.0, high: float = 4.0, original_len: int = 4096,
-                 magnitude: float = 1.0):
-        if scaling not in self.SCALINGS:
-            raise ValueError(f"scaling must be one of {self.SCALINGS}")
-        self.st = medusa_rope_plan()
-        self.ref = ctypes.byref(self.st)
-        _check("medusa_rope_plan_init", lib().medusa_rope_plan_init(
-            rotary_dim, int(interleaved), float(base), self.SCALINGS.index(scaling), float(factor), float(low),
-            float(high), original_len, float(magnitude), self.ref))
-
-    rotary_dim = property(lambda self: self.st.rotary_dim)
-    interleaved = property(lambda self: bool(self.st.interleaved))
-
-
 class DevTopology:
     def __init__(self, st: medusa_dev_topology, buf):
         self.st, self.buf = st, buf  # buf keeps the device memory alive
@@ -490,277 +468,6 @@ def medusa_topology_greedy_device(acc, n_nodes: int, d_status=None, stream=None)
     _check("medusa_topology_greedy_device", lib().medusa_topology_greedy_device(
         _ptr(acc), K, R, n_nodes, _ptr(buf), elems, _ptr(meta), ctypes.byref(st), _ptr(d_status), _stream(stream)))
     return DevTopology(st, (buf, meta)), meta
-
-
-# ----------------------------------------------------------------------------- paged cache
-
-def _on(what: str, dev, dtype, **tensors):
-    """Every given tensor is on `dev` with `dtype`, and dense."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.device != dev or t.dtype != dtype:
-            raise ValueError(f"{what}: {name} must be {dtype} on {dev}, not {t.dtype} on {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: {name} must be dense")
-
-
-def _token_stride(what: str, name: str, t, nl: int, T: int, H: int, d: int) -> int:
-    """Elements from one token to the next of t [nl, T, H, d], whose heads are dense
-    and whose layers are T tokens apart."""
-    st = t.stride()
-    ld = st[1] if T > 1 else (st[0] if nl > 1 else H * d)
-    if tuple(t.shape) != (nl, T, H, d):
-        raise ValueError(f"{what}: {name} must be [{nl}, {T}, {H}, {d}], not {list(t.shape)}")
-    if st[3] != 1 or (H > 1 and st[2] != d) or (nl > 1 and st[0] != T * ld):
-        raise ValueError(f"{what}: {name} must have dense heads and evenly spaced tokens (strides {st})")
-    return ld
-
-
-class _on_device:
-    """The device of the tensors is current inside (the library launches on the current one)."""
-    __slots__ = ("prev", "idx")
-
-    def __init__(self, dev):
-        self.idx = dev.index
-
-    def __enter__(self):
-        import torch
-        self.prev = torch.cuda.current_device()
-        if self.prev != self.idx:
-            torch.cuda.set_device(self.idx)
-
-    def __exit__(self, *exc):
-        import torch
-        if self.prev != self.idx:
-            torch.cuda.set_device(self.prev)
-
-
-def _stream_of(dev, stream):
-    import torch
-    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
-
-
-def _paged_ws(nbytes: int, dev, ws, stream):
-    """A workspace of at least nbytes; a fresh one stays alive until `stream` is past the call."""
-    import torch
-    if ws is not None:
-        if ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < nbytes:
-            raise ValueError("workspace too small, not dense or on another device")
-        return ws, ws.numel() * ws.element_size()
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws, nbytes
-
-
-def _kept(stream, *fresh):
-    """Tensors made here on the current stream that `stream` writes."""
-    if stream is not None:
-        for t in fresh:
-            if t is not None:
-                t.record_stream(stream)
-
-
-def _cache_dims(what: str, k_pages, v_pages, page_table, dtype):
-    import torch
-    if k_pages.dim() != 5 or k_pages.shape != v_pages.shape or page_table.dim() != 2:
-        raise ValueError(f"{what}: k_pages and v_pages must be [nl, n_pages, page_size, Hkv, d], page_table [B, max_pages]")
-    if not k_pages.is_cuda:
-        raise ValueError(f"{what}: tensors must be on a GPU")
-    _on(what, k_pages.device, dtype, k_pages=k_pages, v_pages=v_pages)
-    _on(what, k_pages.device, torch.int32, page_table=page_table)
-    return tuple(k_pages.shape) + tuple(page_table.shape)
-
-
-def medusa_rope(q, k, pos, rope: RopeSpec, q_out=None, k_out=None, inverse: bool = False, stream=None):
-    """Rotary embedding of q [nl, T, Hq, d] and k [nl, T, Hkv, d] (or None) at pos
-    [T] int32; returns (q_out, k_out), new tensors unless given (q_out may be q,
-    k_out may be k).  inverse=True maps gradients of the outputs to those of the
-    inputs."""
-    import torch
-    nl, T, Hq, d = q.shape
-    Hkv = 0 if k is None else k.shape[2]
-    dt = _dtype_code(q)
-    if not q.is_cuda or (k is not None and (k.dtype != q.dtype or k.device != q.device)):
-        raise ValueError("medusa_rope: q and k must have one dtype and be on one GPU")
-    ldq = _token_stride("medusa_rope", "q", q, nl, T, Hq, d)
-    ldk = 0 if k is None else _token_stride("medusa_rope", "k", k, nl, T, Hkv, d)
-    if k is None and k_out is not None:
-        raise ValueError("medusa_rope: k_out without k")
-    dev = q.device
-    _on("medusa_rope", dev, torch.int32, pos=pos)
-    if pos.numel() != T:
-        raise ValueError("medusa_rope: pos must hold one position per token")
-    fresh = []
-    if q_out is None:
-        q_out = torch.empty((nl, T, Hq, d), dtype=q.dtype, device=dev)
-        fresh.append(q_out)
-    if k is not None and k_out is None:
-        k_out = torch.empty((nl, T, Hkv, d), dtype=q.dtype, device=dev)
-        fresh.append(k_out)
-    _on("medusa_rope", dev, q.dtype, q_out=q_out, k_out=k_out)
-    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
-        raise ValueError("medusa_rope: q_out and k_out must have the shapes of q and k")
-    _kept(stream, *fresh)
-    with _on_device(dev):
-        code = lib().medusa_rope(
-            q.data_ptr(), ldq, None if k is None else k.data_ptr(), ldk, pos.data_ptr(), rope.ref, int(inverse), nl, T,
-            Hq, Hkv, d, dt, q_out.data_ptr(), None if k is None else k_out.data_ptr(), _stream_of(dev, stream))
-    _check("medusa_rope", code)
-    return q_out, k_out
-
-
-def medusa_paged_append(k, v, k_pages, v_pages, page_table, q_start, prefix_len, q=None, pos=None,
-                        rope: RopeSpec | None = None, q_out=None, d_status=None, stream=None):
-    """Enters the chunk's k, v [nl, T, Hkv, d] (k rotated by `rope`, at pos [T] or at
-    the row numbers) into the pages behind prefix_len [B] rows; returns q
-    [nl, T, Hq, d] rotated into q_out (new unless given), or None without q.
-    q, k and v may be slices of one projection's output."""
-    import torch
-    what = "medusa_paged_append"
-    nl, n_pages, ps, Hkv, d, B, max_pages = _cache_dims(what, k_pages, v_pages, page_table, k.dtype)
-    dev = k_pages.device
-    T = k.shape[1] if k.dim() == 4 else 0
-    dt = _dtype_code(k)
-    ldk, ldv = _token_stride(what, "k", k, nl, T, Hkv, d), _token_stride(what, "v", v, nl, T, Hkv, d)
-    if v.dtype != k.dtype or k.device != dev or v.device != dev:
-        raise ValueError(f"{what}: k and v must have the cache's dtype and device")
-    _on(what, dev, torch.int32, q_start=q_start, prefix_len=prefix_len, pos=pos, d_status=d_status)
-    if q_start.numel() != B + 1 or prefix_len.numel() != B or (pos is not None and pos.numel() != T):
-        raise ValueError(f"{what}: q_start must be [B + 1], prefix_len [B] and pos [T]")
-    Hq = ldq = 0
-    if q is None:
-        if q_out is not None:
-            raise ValueError(f"{what}: q_out without q")
-    else:
-        Hq = q.shape[2]
-        ldq = _token_stride(what, "q", q, nl, T, Hq, d)
-        if q.dtype != k.dtype or q.device != dev:
-            raise ValueError(f"{what}: q must have the cache's dtype and device")
-        if q_out is None:
-            q_out = torch.empty((nl, T, Hq, d), dtype=q.dtype, device=dev)
-            _kept(stream, q_out)
-        else:
-            _on(what, dev, q.dtype, q_out=q_out)
-            if q_out.shape != q.shape:
-                raise ValueError(f"{what}: q_out must have q's shape")
-    with _on_device(dev):
-        code = lib().medusa_paged_append(
-            None if q is None else q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
-            None if pos is None else pos.data_ptr(), None if rope is None else rope.ref, page_table.data_ptr(),
-            q_start.data_ptr(), prefix_len.data_ptr(), nl, T, B, Hq, Hkv, d, n_pages, ps, max_pages, dt,
-            None if q is None else q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-            None if d_status is None else d_status.data_ptr(), _stream_of(dev, stream))
-    _check(what, code)
-    return q_out
-
-
-def _attention_outputs(what, q, shape, out, lse, want_lse, stream):
-    import torch
-    fresh = []
-    if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
-        fresh.append(out)
-    if lse is None and want_lse:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
-        fresh.append(lse)
-    _on(what, q.device, q.dtype, out=out)
-    _on(what, q.device, torch.float32, lse=lse)
-    if tuple(out.shape) != shape or (lse is not None and tuple(lse.shape) != shape[:-1]):
-        raise ValueError(f"{what}: out must have q's shape, lse that without the last dimension")
-    _kept(stream, *fresh)
-    return out, lse
-
-
-def medusa_paged_attention(q, k_pages, v_pages, page_table, q_start, prefix_len, scale: float | None = None, out=None,
-                           lse=None, want_lse: bool = False, ws=None, d_status=None, stream=None):
-    """Causal attention of the chunk q [nl, T, Hq, d] over the paged cache, which
-    already holds the chunk's rows; returns (out like q, lse fp32 [nl, T, Hq] or
-    None).  q may be a slice of a projection's output."""
-    import torch
-    what = "medusa_paged_attention"
-    nl, n_pages, ps, Hkv, d, B, max_pages = _cache_dims(what, k_pages, v_pages, page_table, q.dtype)
-    dev = k_pages.device
-    _, T, Hq, _ = q.shape
-    ldq = _token_stride(what, "q", q, nl, T, Hq, d)
-    if q.device != dev:
-        raise ValueError(f"{what}: q must be on the cache's device")
-    _on(what, dev, torch.int32, q_start=q_start, prefix_len=prefix_len, d_status=d_status)
-    if q_start.numel() != B + 1 or prefix_len.numel() != B:
-        raise ValueError(f"{what}: q_start must be [B + 1] and prefix_len [B]")
-    dt = _dtype_code(q)
-    out, lse = _attention_outputs(what, q, (nl, T, Hq, d), out, lse, want_lse, stream)
-    L = lib()
-    with _on_device(dev):
-        ws, nbytes = _paged_ws(L.medusa_paged_attention_workspace_size(nl, T, B, Hq, Hkv, d, ps, dt), dev, ws, stream)
-        code = L.medusa_paged_attention(
-            q.data_ptr(), ldq, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), q_start.data_ptr(),
-            prefix_len.data_ptr(), nl, T, B, Hq, Hkv, d, n_pages, ps, max_pages, d ** -0.5 if scale is None else scale,
-            dt, out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), nbytes,
-            None if d_status is None else d_status.data_ptr(), _stream_of(dev, stream))
-    _check(what, code)
-    return out, lse
-
-
-def medusa_paged_tree_attention(q, k_pages, v_pages, page_table, kt, vt, mask, prefix_len, scale: float | None = None,
-                                out=None, lse=None, want_lse: bool = False, ws=None, d_status=None, stream=None):
-    """Tree attention of q [nl, B, N, Hq, d] over a paged prefix and the tree rows
-    kt, vt [nl, B, N, Hkv, d]; returns (out like q, lse fp32 [nl, B, N, Hq] or None)."""
-    import torch
-    what = "medusa_paged_tree_attention"
-    nl, n_pages, ps, Hkv, d, B, max_pages = _cache_dims(what, k_pages, v_pages, page_table, q.dtype)
-    dev = k_pages.device
-    N, Hq = q.shape[2], q.shape[3]
-    if tuple(q.shape) != (nl, B, N, Hq, d) or tuple(kt.shape) != (nl, B, N, Hkv, d) or vt.shape != kt.shape:
-        raise ValueError(f"{what}: q must be [nl, B, N, Hq, d], kt and vt [nl, B, N, Hkv, d]")
-    _on(what, dev, q.dtype, q=q, kt=kt, vt=vt)
-    _on(what, dev, torch.int32, mask=mask, prefix_len=prefix_len, d_status=d_status)
-    if tuple(mask.shape) != (N, (N + 31) // 32) or prefix_len.numel() != B:
-        raise ValueError(f"{what}: mask must be [N, ceil(N / 32)] and prefix_len [B]")
-    dt = _dtype_code(q)
-    out, lse = _attention_outputs(what, q, (nl, B, N, Hq, d), out, lse, want_lse, stream)
-    L = lib()
-    with _on_device(dev):
-        ws, nbytes = _paged_ws(L.medusa_paged_attention_workspace_size(nl, B * N, B, Hq, Hkv, d, ps, dt), dev, ws, stream)
-        code = L.medusa_paged_tree_attention(
-            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), kt.data_ptr(), vt.data_ptr(),
-            mask.data_ptr(), prefix_len.data_ptr(), nl, B, N, Hq, Hkv, d, n_pages, ps, max_pages,
-            d ** -0.5 if scale is None else scale, dt, out.data_ptr(), None if lse is None else lse.data_ptr(),
-            ws.data_ptr(), nbytes, None if d_status is None else d_status.data_ptr(), _stream_of(dev, stream))
-    _check(what, code)
-    return out, lse
-
-
-def medusa_paged_compact(k_pages, v_pages, page_table, kt, vt, path_nodes, accept_len, prefix_len, new_len=None,
-                         d_status=None, stream=None):
-    """Appends the accepted paths path_nodes [B, Dmax + 1], accept_len [B] of the tree
-    rows kt, vt [nl, B, N, Hkv, d] to the pages; returns new_len [B] (new unless
-    given; may be prefix_len)."""
-    import torch
-    what = "medusa_paged_compact"
-    nl, n_pages, ps, Hkv, d, B, max_pages = _cache_dims(what, k_pages, v_pages, page_table, kt.dtype)
-    dev = k_pages.device
-    N = kt.shape[2]
-    if tuple(kt.shape) != (nl, B, N, Hkv, d) or vt.shape != kt.shape or path_nodes.dim() != 2 or path_nodes.shape[0] != B:
-        raise ValueError(f"{what}: kt and vt must be [nl, B, N, Hkv, d], path_nodes [B, Dmax + 1]")
-    dt = _dtype_code(kt)
-    _on(what, dev, kt.dtype, kt=kt, vt=vt)
-    if new_len is None:
-        new_len = torch.empty(B, dtype=torch.int32, device=dev)
-        _kept(stream, new_len)
-    _on(what, dev, torch.int32, path_nodes=path_nodes, accept_len=accept_len, prefix_len=prefix_len, new_len=new_len,
-        d_status=d_status)
-    if accept_len.numel() != B or prefix_len.numel() != B or new_len.numel() != B:
-        raise ValueError(f"{what}: accept_len, prefix_len and new_len must be [B]")
-    with _on_device(dev):
-        code = lib().medusa_paged_compact(
-            k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), kt.data_ptr(), vt.data_ptr(),
-            path_nodes.data_ptr(), accept_len.data_ptr(), prefix_len.data_ptr(), new_len.data_ptr(), nl, B, N, Hkv, d,
-            n_pages, ps, max_pages, path_nodes.shape[1] - 1, dt, None if d_status is None else d_status.data_ptr(),
-            _stream_of(dev, stream))
-    _check(what, code)
-    return new_len
 
 
 def medusa_status_check(d_status, stream=None) -> int:

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 import medusa_head_speculative_heads_gb300 as mg
-from medusa_head_speculative_heads_gb300 import binding
+from medusa_head_speculative_heads_gb300 import paged
 from oracle import paged as ref
 
 torch = pytest.importorskip("torch")
@@ -169,7 +169,7 @@ def test_the_binding_refuses_other_shapes_types_and_places():
         mg.medusa_paged_attention(z(1, 2, 4, 32), z(1, 3, 8, 2, 32), z(1, 3, 8, 2, 32), z(1, 2, dt=i32), z(2, dt=i32), z(1, dt=i32))
     with pytest.raises(TypeError):  # no kernel for fp16
         mg.medusa_rope(z(1, 2, 4, 32, dt=torch.float16), None, z(2, dt=i32), spec)
-    stride = binding._token_stride
+    stride = paged._token_stride
     assert stride("x", "q", z(2, 5, 6, 32)[:, :, :4], 2, 5, 4, 32) == 192 and stride("x", "q", z(2, 1, 6, 32)[:, :, :4], 2, 1, 4, 32) == 192
     for t, dims in ((z(2, 5, 4, 64)[..., ::2], (2, 5, 4, 32)), (z(2, 4, 5, 32).transpose(1, 2), (2, 5, 4, 32)), (z(2, 6, 4, 32)[:, :5], (2, 5, 4, 32)),
                     (z(2, 5, 4, 32), (2, 5, 4, 64))):
