@@ -12,11 +12,15 @@
 // double frequency.  The nearest quarter turn is split off in the integer, so
 // sincospif sees at most an eighth of a turn, rounded to 24 bits.
 //
-// Bandwidth bounds both calls (each element is read and written once, about 20
-// operations a pair).  A CTA takes one to eight tokens so that a thread has about four
-// 32-byte tasks (two vectors, a pair's halves): their angles are formed once,
-// by all threads, while the first tasks' loads are in flight, and kept in
-// shared memory for every head.
+// Bandwidth bounds both calls (each element is read and written once, about 10
+// instructions a pair).  Many small CTAs hide the loads: 128 threads, a token each
+// (more when a token has fewer than 128 tasks of two vectors), one task in flight a
+// thread, its angles formed once into shared memory while the first loads are on
+// their way.  Measured, 10782 prompt tokens with 32 + 8 + 8 heads entered into
+// the cache: 44 us (6.0 TB/s); with 256 threads 56 us, with two, three or four
+// tasks in flight 49 to 52 us, with the next task's loads ahead of the turn 48 us
+// (registers: fewer CTAs on an SM).  32 layers of 64 tokens with 32 + 32 heads: 13.5
+// us; 16384 fp32 tokens with 32 + 8 heads: 99 us (6.8 TB/s).
 #include <cmath>
 
 #include "host_util.h"
@@ -25,9 +29,8 @@
 namespace medusa {
 namespace paged {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeMaxTokens = 8;  // tokens per CTA
-constexpr int kRopeUnroll = 4;     // tasks in flight per thread
 
 struct RopeArgs {
   const void *q, *k, *v;  // q, k, v may be NULL
@@ -39,6 +42,7 @@ struct RopeArgs {
   Cache cache;
   int nl, T, B, Hq, Hkv, d, rotary, inverse;
   int tokens;  // per CTA
+  unsigned per_tok_inv, per_head_inv;  // floor(2^32 / n) + 1: the high word of a product divides by n
   float magnitude;
   unsigned long long turn[MEDUSA_MAX_HEAD_DIM / 2];
 };
@@ -54,16 +58,45 @@ struct Vec<4> { using type = uint32_t; };
 template <>
 struct Vec<2> { using type = uint16_t; };
 
+// W elements as one load or store.
 template <typename T, int W>
-union Chunk {  // W elements as one load or store
-  typename Vec<W * sizeof(T)>::type v;
-  T e[W];
-};
+using Chunk = typename Vec<W * sizeof(T)>::type;
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(uint16_t x) { return bf16_bits_to_f32(x); }
-__device__ __forceinline__ void put(float& d, float x) { d = x; }
-__device__ __forceinline__ void put(uint16_t& d, float x) { d = (uint16_t)f32_to_bf16_bits(x); }
+template <int W>
+__device__ __forceinline__ void unpack(const Chunk<float, W>& c, float* f) {
+  const float* e = reinterpret_cast<const float*>(&c);
+#pragma unroll
+  for (int i = 0; i < W; ++i) f[i] = e[i];
+}
+template <int W>
+__device__ __forceinline__ void unpack(const Chunk<uint16_t, W>& c, float* f) {
+  if constexpr (W == 1) {
+    f[0] = bf16_bits_to_f32(c);
+  } else {
+    const uint32_t* e = reinterpret_cast<const uint32_t*>(&c);
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) {
+      f[2 * i] = __uint_as_float(e[i] << 16);
+      f[2 * i + 1] = __uint_as_float(e[i] & 0xffff0000u);
+    }
+  }
+}
+template <int W>
+__device__ __forceinline__ void pack(const float* f, Chunk<float, W>& c) {
+  float* e = reinterpret_cast<float*>(&c);
+#pragma unroll
+  for (int i = 0; i < W; ++i) e[i] = f[i];
+}
+template <int W>
+__device__ __forceinline__ void pack(const float* f, Chunk<uint16_t, W>& c) {
+  if constexpr (W == 1) {
+    c = (uint16_t)bf16x2_rn(f[0], 0.f);
+  } else {
+    uint32_t* e = reinterpret_cast<uint32_t*>(&c);
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) e[i] = bf16x2_rn(f[2 * i], f[2 * i + 1]);
+  }
+}
 
 // (cos, sin) of p turns of `turn` 2^-64, times m.
 __device__ __forceinline__ float2 turn_of(int p, unsigned long long turn, int inverse, float m) {
@@ -84,8 +117,9 @@ __device__ __forceinline__ float2 turn_of(int p, unsigned long long turn, int in
 template <typename T, int W, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   using C = Chunk<T, W>;
-  using V = typename Vec<W * sizeof(T)>::type;
-  __shared__ float2 cs[kRopeMaxTokens][MEDUSA_MAX_HEAD_DIM / 2];
+  // Angle e of the W that vector c needs lies at (e / 2, c, e % 2): lanes with
+  // neighbouring vectors then read neighbouring words.
+  __shared__ __align__(16) float2 cs[kRopeMaxTokens][MEDUSA_MAX_HEAD_DIM / 2];
   __shared__ int s_slot[kRopeMaxTokens];  // pool row, -1: not entered, -2: nothing of the token is written
   __shared__ int s_pos[kRopeMaxTokens];
   pdl_wait();
@@ -105,9 +139,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   };
   auto find = [&](unsigned id) {
     Task t;
-    t.tok = id / per_tok;
+    t.tok = a.tokens == 1 ? 0u : __umulhi(id, a.per_tok_inv);
     const unsigned r = id - t.tok * per_tok;
-    t.head = r / per_head;
+    t.head = per_head == 1 ? r : __umulhi(r, a.per_head_inv);
     t.c = r - t.head * per_head;
     const long long at = tok0 + t.tok;
     const T* base;
@@ -121,20 +155,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     return t;
   };
 
-  Task task[kRopeUnroll];
-  C x0[kRopeUnroll], x1[kRopeUnroll];
-  auto load = [&](unsigned first) {
-#pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      const unsigned id = first + u * kRopeThreads;
-      if (id < tasks) {
-        task[u] = find(id);
-        x0[u].v = *reinterpret_cast<const V*>(task[u].s0);
-        x1[u].v = *reinterpret_cast<const V*>(task[u].s1);
-      }
-    }
+  Task t;
+  C x0, x1;
+  auto load = [&](unsigned id) {
+    t = find(id);
+    x0 = *reinterpret_cast<const C*>(t.s0);
+    x1 = *reinterpret_cast<const C*>(t.s1);
   };
-  load(threadIdx.x);
+  if (threadIdx.x < tasks) load(threadIdx.x);  // in flight while the angles are formed
 
   if (a.k_pages) {
     // Token tok: its sequence is the number of starts q_start[1 .. B] at or before it.
@@ -168,80 +196,58 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   for (unsigned j = threadIdx.x; j < half * n_tok; j += kRopeThreads) {
     const unsigned tk = j / half, i = j - tk * half;
     const int p = a.k_pages ? s_pos[tk] : __ldg(a.pos + (tok0 + tk) % a.T);
-    cs[tk][i] = turn_of(p, a.turn[i], a.inverse, a.magnitude);
+    const unsigned c = i / W, e = i % W;
+    cs[tk][W == 1 ? c : ((e >> 1) * turned + c) * 2 + (e & 1)] = turn_of(p, a.turn[i], a.inverse, a.magnitude);
   }
   __syncthreads();
 
-  for (unsigned first = threadIdx.x; first < tasks; first += kRopeUnroll * kRopeThreads) {
-    if (first != threadIdx.x) load(first);
-#pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      if (first + u * kRopeThreads >= tasks) break;
-      const Task& t = task[u];
-      const long long at = tok0 + t.tok;
-      const int slot = a.k_pages ? s_slot[t.tok] : 0;
-      if (slot == -2) continue;
-      T* dst;
-      if (t.head < hq) {
-        dst = static_cast<T*>(a.q_out) + (at * a.Hq + t.head) * a.d;
+  for (unsigned id = threadIdx.x; id < tasks; id += kRopeThreads) {
+    if (id != threadIdx.x) load(id);
+    const long long at = tok0 + t.tok;
+    const int slot = a.k_pages ? s_slot[t.tok] : 0;
+    if (slot == -2) continue;
+    T* dst;
+    if (t.head < hq) {
+      dst = static_cast<T*>(a.q_out) + (at * a.Hq + t.head) * a.d;
+    } else {
+      const bool value = t.head >= hq + hk;
+      const unsigned h = t.head - hq - (value ? hk : 0u);
+      if (a.k_pages) {
+        if (slot < 0) continue;
+        const long long row = (at / a.T) * ((long long)a.cache.n_pages * a.cache.page_size) + slot;
+        dst = static_cast<T*>(value ? a.v_pages : a.k_pages) + (row * a.Hkv + h) * a.d;
       } else {
-        const bool value = t.head >= hq + hk;
-        const unsigned h = t.head - hq - (value ? hk : 0u);
-        if (a.k_pages) {
-          if (slot < 0) continue;
-          const long long row = (at / a.T) * ((long long)a.cache.n_pages * a.cache.page_size) + slot;
-          dst = static_cast<T*>(value ? a.v_pages : a.k_pages) + (row * a.Hkv + h) * a.d;
-        } else {
-          dst = static_cast<T*>(a.k_out) + (at * a.Hkv + h) * a.d;
-        }
-        if (value) {
-          dst += t.c * 2 * W;
-          *reinterpret_cast<V*>(dst) = x0[u].v;
-          *reinterpret_cast<V*>(dst + W) = x1[u].v;
-          continue;
-        }
+        dst = static_cast<T*>(a.k_out) + (at * a.Hkv + h) * a.d;
       }
-      if (t.c >= turned) {  // behind the turned part
-        dst += a.rotary + (t.c - turned) * 2 * W;
-        *reinterpret_cast<V*>(dst) = x0[u].v;
-        *reinterpret_cast<V*>(dst + W) = x1[u].v;
+      if (value) {
+        dst += t.c * 2 * W;
+        *reinterpret_cast<C*>(dst) = x0;
+        *reinterpret_cast<C*>(dst + W) = x1;
         continue;
       }
-      const float2* f = cs[t.tok] + t.c * W;
-      C y0, y1;
-      if constexpr (INTER) {  // pairs follow one another through both vectors
-        T xs[2 * W], ys[2 * W];
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-          xs[e] = x0[u].e[e];
-          xs[W + e] = x1[u].e[e];
-        }
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-          const float p0 = to_f32(xs[2 * e]), p1 = to_f32(xs[2 * e + 1]);
-          put(ys[2 * e], p0 * f[e].x - p1 * f[e].y);
-          put(ys[2 * e + 1], p1 * f[e].x + p0 * f[e].y);
-        }
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-          y0.e[e] = ys[e];
-          y1.e[e] = ys[W + e];
-        }
-        dst += t.c * 2 * W;
-        *reinterpret_cast<V*>(dst) = y0.v;
-        *reinterpret_cast<V*>(dst + W) = y1.v;
-      } else {
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-          const float p0 = to_f32(x0[u].e[e]), p1 = to_f32(x1[u].e[e]);
-          put(y0.e[e], p0 * f[e].x - p1 * f[e].y);
-          put(y1.e[e], p1 * f[e].x + p0 * f[e].y);
-        }
-        dst += t.c * W;
-        *reinterpret_cast<V*>(dst) = y0.v;
-        *reinterpret_cast<V*>(dst + half) = y1.v;
-      }
     }
+    if (t.c >= turned) {  // behind the turned part
+      dst += a.rotary + (t.c - turned) * 2 * W;
+      *reinterpret_cast<C*>(dst) = x0;
+      *reinterpret_cast<C*>(dst + W) = x1;
+      continue;
+    }
+    float x[2 * W], y[2 * W];
+    unpack<W>(x0, x);
+    unpack<W>(x1, x + W);
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      const float2 f = cs[t.tok][W == 1 ? t.c : ((e >> 1) * turned + t.c) * 2 + (e & 1)];
+      const int i0 = INTER ? 2 * e : e, i1 = INTER ? 2 * e + 1 : W + e;
+      y[i0] = x[i0] * f.x - x[i1] * f.y;
+      y[i1] = x[i1] * f.x + x[i0] * f.y;
+    }
+    C y0, y1;
+    pack<W>(y, y0);
+    pack<W>(y + W, y1);
+    dst += INTER ? t.c * 2 * W : t.c * W;
+    *reinterpret_cast<C*>(dst) = y0;
+    *reinterpret_cast<C*>(dst + (INTER ? W : half)) = y1;
   }
 }
 
@@ -274,11 +280,17 @@ static medusa_status rope_launch(RopeArgs& a, const medusa_rope_plan* plan, medu
   const int w = rope_width(a, dtype_bytes(dt));
   const long long all = (long long)a.nl * a.T;
   const long long per_tok = (long long)((a.q ? a.Hq : 0) + (a.k ? a.Hkv : 0) + (a.v ? a.Hkv : 0)) * (a.d / (2 * w));
-  // Tokens per CTA: enough for a thread's tasks in flight, but first one CTA per SM.
-  long long n = (kRopeThreads * kRopeUnroll + per_tok - 1) / per_tok;
+  // Tokens per CTA: as many as give every thread a task, but first two CTAs per SM.
+  long long n = kRopeThreads / per_tok;
   const long long spread = all / (2 * device_sm_count());
   if (n > spread) n = spread;
   a.tokens = n < 1 ? 1 : n > kRopeMaxTokens ? kRopeMaxTokens : (int)n;
+  // Exact: with several tokens there are at most kRopeThreads tasks, and a vector's
+  // number within its token times the vectors of a head stays below 2^32 (3 x 65535
+  // heads of at most 128 vectors).
+  const unsigned per_head = (unsigned)(a.d / (2 * w));
+  a.per_tok_inv = (unsigned)((1ull << 32) / (unsigned long long)per_tok) + 1;
+  a.per_head_inv = (unsigned)((1ull << 32) / per_head) + 1;
   const unsigned grid = (unsigned)((all + a.tokens - 1) / a.tokens);
   const bool inter = plan && plan->interleaved;
   if (dt == MEDUSA_BF16) {
