@@ -34,25 +34,44 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v) {
 
 // A tile is 16 RM rows x 64 keys; thread (ty, tx) of 16 x 16 holds rows
 // ty RM .. + RM - 1: their scores of keys tx + 16 j and their columns
-// 4 tx + 64 j .. + 3 of O, in registers.  Operands are fp32 in shared memory,
-// rows padded by 16 bytes, so the sixteen rows a quarter warp reads lie in
-// different banks.  Probabilities pass through shared memory between threads
-// of one half warp.
+// 4 tx + 64 j .. + 3 of O, in registers.  Q is fp32 in shared memory, K and V as
+// they are stored, rows padded by four elements, so the sixteen rows a quarter
+// or half warp reads lie in different banks.  Probabilities pass through shared
+// memory between threads of one half warp.  K and V have one buffer each, filled by
+// asynchronous copies: the next K under the products with V, V under the scores.
+// A warp none of whose rows exists takes part in the copies only.
+// Issue slots bound it, so products are taken two at a time (fma.rn.f32x2: over even
+// and odd columns in the scores, over pairs of columns in the sums).  Measured, fp32,
+// 5 ragged sequences of up to 331 tokens behind up to 1338 rows, 8 + 4 heads of 64: 91
+// us, 22 TFLOP/s (with single products and loads between two barriers 114 us).
 template <int DC>
 __host__ __device__ constexpr int simt_pitch() { return 16 * DC + 4; }
-template <int DC, int RM>
+template <typename T, int DC, int RM>
 constexpr size_t simt_smem() {
-  return ((size_t)(16 * RM + 2 * kSimtKeys) * simt_pitch<DC>() + (size_t)16 * RM * (kSimtKeys + 4)) * sizeof(float);
+  return (size_t)16 * RM * (simt_pitch<DC>() + kSimtKeys + 4) * sizeof(float) + (size_t)2 * kSimtKeys * simt_pitch<DC>() * sizeof(T);
 }
 
+// Four elements into shared memory; `some` false: zeros, and `from` is not read.
+template <typename T>
+__device__ __forceinline__ void copy4_async(T* to, const T* from, bool some) {
+  const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(from), "n"(4 * sizeof(T)),
+               "r"(some ? (int)(4 * sizeof(T)) : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// CTAs that fit an SM, by registers and shared memory.
+constexpr int simt_ctas(int DC, int RM) { return RM == 1 ? (DC <= 4 ? 3 : DC <= 8 ? 2 : 1) : DC <= 4 ? 2 : 1; }
+
 template <typename T, int DC, int RM>
-__global__ void __launch_bounds__(kSimtThreads) paged_attn_simt_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kSimtThreads, simt_ctas(DC, RM)) paged_attn_simt_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int R = 16 * RM, DP = simt_pitch<DC>(), PP = kSimtKeys + 4;
   extern __shared__ float4 smem4[];
   float* Qs = reinterpret_cast<float*>(smem4);
-  float* Ks = Qs + R * DP;
-  float* Vs = Ks + kSimtKeys * DP;
-  float* Ps = Vs + kSimtKeys * DP;
+  float* Ps = Qs + R * DP;
+  T* Ks = reinterpret_cast<T*>(Ps + R * PP);
+  T* Vs = Ks + kSimtKeys * DP;
   __shared__ long long sh[70];
   __shared__ const T *s_k[2][kSimtKeys], *s_v[2][kSimtKeys];  // row starts of a tile's keys (NULL: zeros)
   pdl_wait();
@@ -102,50 +121,67 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt_kernel(const __g
       s_k[t & 1][tid] = k;
       s_v[t & 1][tid] = v;
     };
+    // Brings a tile's rows into Ks or Vs.
+    auto bring = [&](T* to, const T* const* from) {
+#pragma unroll
+      for (int i = 0; i < DC; ++i) {
+        const int idx = tid + i * kSimtThreads, r = idx / (4 * DC), c = idx - r * (4 * DC);
+        const T* x = from[r];
+        const bool some = x && c < dv;
+        copy4_async(to + r * DP + 4 * c, some ? x + 4 * c : static_cast<const T*>(a.k_pages), some);
+      }
+    };
     find_rows(t0);
-    __syncthreads();  // Qs, Ks, Vs of the item before are no longer read
-    for (int idx = tid; idx < R * 4 * DC; idx += kSimtThreads) {
-      const int r = idx / (4 * DC), c = idx - r * (4 * DC);
-      const Row x = row_of(a, it, r);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (x.ok && c < dv)
-        v = load4(static_cast<const T*>(a.q) + ((long long)l * a.w.T + it.s.q0 + x.tok) * a.ldq + (long long)x.h * a.d + 4 * c);
-      store4(Qs + r * DP + 4 * c, v);
+    __syncthreads();  // Qs and Ks of the item before are no longer read
+    bring(Ks, s_k[t0 & 1]);
+    {
+      constexpr int kAtOnce = 4;
+      for (int i0 = tid; i0 < R * 4 * DC; i0 += kAtOnce * kSimtThreads) {
+        float4 v[kAtOnce];
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) {
+          const int idx = i0 + e * kSimtThreads, r = idx / (4 * DC), c = idx - r * (4 * DC);
+          v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (idx >= R * 4 * DC) continue;
+          const Row x = row_of(a, it, r);
+          if (x.ok && c < dv)
+            v[e] = load4(static_cast<const T*>(a.q) + ((long long)l * a.w.T + it.s.q0 + x.tok) * a.ldq + (long long)x.h * a.d + 4 * c);
+        }
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) {
+          const int idx = i0 + e * kSimtThreads, r = idx / (4 * DC), c = idx - r * (4 * DC);
+          if (idx < R * 4 * DC) store4(Qs + r * DP + 4 * c, v[e]);
+        }
+      }
     }
     Row row[RM];
     float m[RM], sum[RM];
-    float4 o[RM][DC / 4];
+    uint64_t o[RM][DC / 4][2];
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
       row[i] = row_of(a, it, ty * RM + i);
       m[i] = -INFINITY;
       sum[i] = 0.f;
 #pragma unroll
-      for (int c = 0; c < DC / 4; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = 0; c < DC / 4; ++c) o[i][c][0] = o[i][c][1] = 0;
     }
 
-    for (int t = t0; t < t1; ++t) {
-      if (t > t0) __syncthreads();  // the tile before is no longer read; s_k of this one is written
-      for (int idx = tid; idx < kSimtKeys * 4 * DC; idx += kSimtThreads) {
-        const int r = idx / (4 * DC), c = idx - r * (4 * DC);
-        const T *k = s_k[t & 1][r], *v = s_v[t & 1][r];
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-        if (k && c < dv) {
-          x = load4(k + 4 * c);
-          y = load4(v + 4 * c);
-        }
-        store4(Ks + r * DP + 4 * c, x);
-        store4(Vs + r * DP + 4 * c, y);
-      }
-      if (t + 1 < t1) find_rows(t + 1);
-      __syncthreads();
+    bool live = false;
+#pragma unroll
+    for (int i = 0; i < RM; ++i) live |= row[i].ok;
+    live = __any_sync(0xffffffffu, live);
 
-      float s[RM][4];
+    for (int t = t0; t < t1; ++t) {
+      copies_done();
+      __syncthreads();  // K has arrived, V of the tile before is no longer read
+      bring(Vs, s_v[t & 1]);
+      if (t + 1 < t1) find_rows(t + 1);
+      uint64_t s2[RM][4];  // sums over even and over odd columns
 #pragma unroll
       for (int i = 0; i < RM; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-      for (int c = 0; c < dv; ++c) {
+        for (int j = 0; j < 4; ++j) s2[i][j] = 0;
+      for (int c = 0; live && c < dv; ++c) {
         float4 kk[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) kk[j] = load4(Ks + (tx + 16 * j) * DP + 4 * c);
@@ -154,9 +190,10 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt_kernel(const __g
           const float4 qq = load4(Qs + (ty * RM + i) * DP + 4 * c);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            s[i][j] = fmaf(qq.w, kk[j].w, fmaf(qq.z, kk[j].z, fmaf(qq.y, kk[j].y, fmaf(qq.x, kk[j].x, s[i][j]))));
+            s2[i][j] = fma2(pack2(qq.z, qq.w), pack2(kk[j].z, kk[j].w), fma2(pack2(qq.x, qq.y), pack2(kk[j].x, kk[j].y), s2[i][j]));
         }
       }
+      float s[RM][4];
 #pragma unroll
       for (int i = 0; i < RM; ++i) {
         float mx = -INFINITY;
@@ -166,7 +203,8 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt_kernel(const __g
           bool see;
           if (t >= pre) see = row[i].ok && key < a.w.N && ((__ldg(a.mask + (size_t)row[i].tok * a.W + (key >> 5)) >> (key & 31)) & 1u);
           else see = row[i].ok && key < (a.w.N ? it.s.L : it.s.L + row[i].tok + 1);
-          s[i][j] = see ? s[i][j] * a.scale_log2 : -INFINITY;
+          const float2 z = unpack2(s2[i][j]);
+          s[i][j] = see ? (z.x + z.y) * a.scale_log2 : -INFINITY;
           mx = fmaxf(mx, s[i][j]);
         }
 #pragma unroll
@@ -184,13 +222,14 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt_kernel(const __g
         sum[i] = fmaf(sum[i], f, rs);  // this thread's share; its sixteen are added at the end
 #pragma unroll
         for (int c = 0; c < DC / 4; ++c) {
-          o[i][c].x *= f;
-          o[i][c].y *= f;
-          o[i][c].z *= f;
-          o[i][c].w *= f;
+          o[i][c][0] = fma2(o[i][c][0], pack2(f, f), 0);
+          o[i][c][1] = fma2(o[i][c][1], pack2(f, f), 0);
         }
       }
-      __syncwarp();  // a row's probabilities are written and read by one half warp
+      copies_done();
+      __syncthreads();  // V has arrived, K is no longer read, the probabilities are written
+      if (t + 1 < t1) bring(Ks, s_k[(t + 1) & 1]);
+      if (!live) continue;
 #pragma unroll 2
       for (int j = 0; j < kSimtKeys; j += 4) {
         float4 p[RM];
@@ -204,10 +243,8 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt_kernel(const __g
 #pragma unroll
             for (int i = 0; i < RM; ++i) {
               const float pe = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
-              o[i][c].x = fmaf(pe, v.x, o[i][c].x);
-              o[i][c].y = fmaf(pe, v.y, o[i][c].y);
-              o[i][c].z = fmaf(pe, v.z, o[i][c].z);
-              o[i][c].w = fmaf(pe, v.w, o[i][c].w);
+              o[i][c][0] = fma2(pack2(pe, pe), pack2(v.x, v.y), o[i][c][0]);
+              o[i][c][1] = fma2(pack2(pe, pe), pack2(v.z, v.w), o[i][c][1]);
             }
           }
         }
@@ -229,7 +266,8 @@ __global__ void __launch_bounds__(kSimtThreads) paged_attn_simt_kernel(const __g
       for (int c = 0; c < DC / 4; ++c) {
         const int col = 4 * tx + 64 * c;
         if (col >= a.d) continue;
-        const float4 v = make_float4(o[i][c].x * f, o[i][c].y * f, o[i][c].z * f, o[i][c].w * f);
+        const float2 lo = unpack2(o[i][c][0]), hi = unpack2(o[i][c][1]);
+        const float4 v = make_float4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
         if (whole) store4(static_cast<T*>(a.out) + at * a.d + col, v);
         else store4(a.part_o + at * a.d + col, v);
       }
@@ -343,8 +381,7 @@ static Division divide(int T, int B, int Hq, int Hkv, int d, int page_size, medu
   // Rows of a tile: 16 when a sequence has at most 16 on average (decoding), else 64.
   v.R = (long long)T * G <= 16ll * B || d > 128 ? 16 : 64;
   v.tile_rows = v.R;
-  // CTAs that fit an SM (registers and shared memory).
-  v.ctas = sms * (v.R == 16 ? (d <= 64 ? 3 : d <= 128 ? 2 : 1) : (d <= 64 ? 2 : 1));
+  v.ctas = sms * simt_ctas(d <= 64 ? 4 : d <= 128 ? 8 : 16, v.R / 16);
   v.KT = kSimtKeys;
   v.min_tiles = 2;
   v.nsub = (G + v.R - 1) / v.R;
@@ -360,7 +397,7 @@ static size_t ws_bytes_of(const Division& v, int d) {
 
 template <typename T, int DC, int RM>
 static medusa_status simt_go(const AttnArgs& a, cudaStream_t s) {
-  constexpr size_t smem = simt_smem<DC, RM>();
+  constexpr size_t smem = simt_smem<T, DC, RM>();
   auto kern = paged_attn_simt_kernel<T, DC, RM>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return MEDUSA_ERR_CUDA;
   launch_pdl(kern, dim3(a.w.ctas), dim3(kSimtThreads), smem, s, a);
@@ -411,7 +448,7 @@ static medusa_status attend(AttnArgs& a, int n_layers, int T, int B, int Hq, int
   a.w.T = T;
   const medusa_status st = v.tc ? paged_attention_tc(a, s) : dt == MEDUSA_BF16 ? simt_launch<uint16_t>(a, s) : simt_launch<float>(a, s);
   if (st != MEDUSA_OK) return st;
-  const dim3 grid(v.ctas - 1, v.R > 64 ? 4 : 1);
+  const dim3 grid(v.ctas - 1, v.R < 64 ? v.R / 8 : 8);
   if (dt == MEDUSA_BF16) launch_pdl(paged_attn_merge_kernel<uint16_t>, grid, dim3(256), 0, s, a);
   else launch_pdl(paged_attn_merge_kernel<float>, grid, dim3(256), 0, s, a);
   return launch_status();
