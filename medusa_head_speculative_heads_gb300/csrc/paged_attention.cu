@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kSimtThreads, simt_ctas(DC, RM)) paged_attn_si
 #pragma unroll
       for (int e = 8; e; e >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, e);
       if (!row[i].ok) continue;
-      const size_t at = whole ? out_row(a, it, row[i]) : (size_t)slot * a.R + ty * RM + i;
+      const size_t at = whole ? out_row(a, it, row[i]) : (size_t)slot * a.R + ty * RM + i;  // in lse or part_ml
       const float f = !whole ? 1.f : ls > 0.f ? 1.f / ls : 0.f;
 #pragma unroll
       for (int c = 0; c < DC / 4; ++c) {
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kSimtThreads, simt_ctas(DC, RM)) paged_attn_si
         const float2 lo = unpack2(o[i][c][0]), hi = unpack2(o[i][c][1]);
         const float4 v = make_float4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
         if (whole) store4(static_cast<T*>(a.out) + at * a.d + col, v);
-        else store4(a.part_o + at * a.d + col, v);
+        else store4(part_at(a, slot, ty * RM + i, col / 4), v);
       }
       if (tx == 0) {
         if (!whole) a.part_ml[at] = make_float2(m[i], ls);
@@ -284,9 +284,10 @@ __global__ void __launch_bounds__(kSimtThreads, simt_ctas(DC, RM)) paged_attn_si
 // Adds the parts of every item that several CTAs share.  The CTA boundary c
 // (tile c Q, c = 1 .. C - 1) belongs to the item it falls inside; the first
 // boundary inside an item merges all of its parts, in the order of the CTAs:
-// O = sum 2^(m_p - M) O_p, l = sum 2^(m_p - M) l_p, M = max m_p.  One warp per
-// row (its lanes share the columns); blockIdx.y takes every gridDim.y-th group
-// of eight rows.  The attention kernel's CTAs have left the items they found.
+// O = sum 2^(m_p - M) O_p, l = sum 2^(m_p - M) l_p, M = max m_p.  The attention
+// kernel's CTAs have left the items they found.  Latency bounds it, so it is spread
+// over all SMs.  Slots of up to 64 rows: one warp per row (its lanes share the
+// columns, there may be one row and a hundred parts), eight warps a CTA, eight CTAs a boundary.
 template <typename T>
 __global__ void __launch_bounds__(256) paged_attn_merge_kernel(const __grid_constant__ AttnArgs a) {
   pdl_wait();
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(256) paged_attn_merge_kernel(const __grid_cons
         const size_t w = at(p);
         const float2 ml = a.part_ml[w];
         const float f = ml.y > 0.f ? exp2f(ml.x - off) : 0.f;
-        const float4 v = *reinterpret_cast<const float4*>(a.part_o + w * a.d + col);
+        const float4 v = *reinterpret_cast<const float4*>(a.part_o + w * a.d + col);  // as part_at
         if (f > 0.f) {  // a part that saw no key may hold anything
           o.x = fmaf(f, v.x, o.x);
           o.y = fmaf(f, v.y, o.y);
@@ -332,6 +333,56 @@ __global__ void __launch_bounds__(256) paged_attn_merge_kernel(const __grid_cons
     }
     if (a.lse && lane == 0) a.lse[to] = lse_of(M, l);
   }
+}
+
+
+// Slots of more rows (few parts): a lane takes one row's sixteen columns, a CTA a
+// group of 32 rows.  151 boundaries in blocks of 32 tokens x 7 heads, cold caches: 24 us with a
+// warp per row, 12.6 us so.
+__global__ void __launch_bounds__(256) paged_attn_merge_wide_kernel(const __grid_constant__ AttnArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const Shared sd = a.shared[blockIdx.x + 1];
+  if (sd.first < 0) return;
+  const int lane = threadIdx.x & 31, c0 = 4 * (threadIdx.x >> 5), r = blockIdx.y * 32 + lane;
+  if (4 * c0 >= a.d) return;
+  const Row x = row_of(a, sd.it, r);
+  if (!__any_sync(0xffffffffu, x.ok)) return;
+  float M = -INFINITY, l = 0.f;
+  float4 o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int p = sd.first; p <= sd.last; ++p) {
+    // CTA p's part: slot 1 of the CTA the item starts in, slot 0 of the others.
+    const int slot = 2 * p + (p == sd.first ? 1 : 0);
+    const float4* from = reinterpret_cast<const float4*>(part_at(a, slot, r, c0));
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (4 * (c0 + k) < a.d) v[k] = from[k * part_rows(256)];
+    const float2 q = x.ok ? a.part_ml[(size_t)slot * a.R + r] : make_float2(-INFINITY, 0.f);
+    const float m = fmaxf(M, q.x), off = m == -INFINITY ? 0.f : m;
+    const float f = exp2f(M - off), g = q.y > 0.f ? exp2f(q.x - off) : 0.f;
+    M = m;
+    l = fmaf(l, f, g * q.y);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (!(g > 0.f) || 4 * (c0 + k) >= a.d) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);  // a part that saw no key may hold anything
+      o[k].x = fmaf(o[k].x, f, g * v[k].x);
+      o[k].y = fmaf(o[k].y, f, g * v[k].y);
+      o[k].z = fmaf(o[k].z, f, g * v[k].z);
+      o[k].w = fmaf(o[k].w, f, g * v[k].w);
+    }
+  }
+  if (!x.ok) return;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const size_t to = out_row(a, sd.it, x);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (4 * (c0 + k) < a.d)
+      store4(static_cast<uint16_t*>(a.out) + to * a.d + 4 * (c0 + k), make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv));
+  if (a.lse && c0 == 0) a.lse[to] = lse_of(M, l);
 }
 
 // ------------------------------------------------------------------ host side
@@ -391,8 +442,7 @@ static Division divide(int T, int B, int Hq, int Hkv, int d, int page_size, medu
 }
 
 static size_t ws_bytes_of(const Division& v, int d) {
-  // 16 bytes more: the parts start on 32 (stores of that width), the caller's buffer on 16.
-  return (size_t)v.ctas * (2 * v.R * (d + 2) * sizeof(float) + sizeof(Shared)) + 16;
+  return (size_t)v.ctas * (2 * v.R * (d + 2) * sizeof(float) + sizeof(Shared));
 }
 
 template <typename T, int DC, int RM>
@@ -425,7 +475,7 @@ static medusa_status attend(AttnArgs& a, int n_layers, int T, int B, int Hq, int
   a.ldq = ldq;
   a.scale_log2 = scale * 1.4426950408889634f;
   if (!ws || !aligned16(ws) || ws_bytes < ws_bytes_of(v, d)) return MEDUSA_ERR_WORKSPACE;
-  a.part_o = reinterpret_cast<float*>(align_up(reinterpret_cast<uintptr_t>(ws), 32));
+  a.part_o = static_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)v.ctas * 2 * v.R * d);
   a.shared = reinterpret_cast<Shared*>(a.part_ml + (size_t)v.ctas * 2 * v.R);
   a.R = v.R;
@@ -448,9 +498,9 @@ static medusa_status attend(AttnArgs& a, int n_layers, int T, int B, int Hq, int
   a.w.T = T;
   const medusa_status st = v.tc ? paged_attention_tc(a, s) : dt == MEDUSA_BF16 ? simt_launch<uint16_t>(a, s) : simt_launch<float>(a, s);
   if (st != MEDUSA_OK) return st;
-  const dim3 grid(v.ctas - 1, v.R < 64 ? v.R / 8 : 8);
-  if (dt == MEDUSA_BF16) launch_pdl(paged_attn_merge_kernel<uint16_t>, grid, dim3(256), 0, s, a);
-  else launch_pdl(paged_attn_merge_kernel<float>, grid, dim3(256), 0, s, a);
+  if (v.R > 64) launch_pdl(paged_attn_merge_wide_kernel, dim3(v.ctas - 1, v.R / 32), dim3(256), 0, s, a);
+  else if (dt == MEDUSA_BF16) launch_pdl(paged_attn_merge_kernel<uint16_t>, dim3(v.ctas - 1, v.R / 8), dim3(256), 0, s, a);
+  else launch_pdl(paged_attn_merge_kernel<float>, dim3(v.ctas - 1, v.R / 8), dim3(256), 0, s, a);
   return launch_status();
 }
 

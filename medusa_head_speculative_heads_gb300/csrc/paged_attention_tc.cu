@@ -203,12 +203,6 @@ __device__ __forceinline__ void st_v8u(void* p, const uint32_t* v) {
                "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
-__device__ __forceinline__ void st_v8(float* p, const float* v) {
-  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
-               "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
-}
-
 // `left`: the tiles of the CTA's range from tile t0 of the item on.
 __device__ __forceinline__ Unit unit_of(const AttnArgs& a, const Item& it, int t0, long long left) {
   Unit x;
@@ -396,21 +390,6 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       }
       __syncwarp();
       if (n > 0) {
-#pragma unroll 1
-        for (int k = 0; k < (two(x) ? 2 : 1); ++k) {
-          const int qb = two(x) ? k : qsel, before = qb ? qn1 : qn0;
-          if (before > 0 && !(alive = warp_wait(&bars->q_empty[qb], (before - 1) & 1, &s_abort))) break;
-          if (elect_one()) {
-            mbar_expect_tx(&bars->q_full[qb], (uint32_t)(C::halves * a.tile_tok * a.G * 128));
-            for (int h = 0; h < C::halves; ++h)
-              tma_load_3d(smem + qb * C::q_step + h * kHalf, &tm_q, &bars->q_full[qb], 64 * h, x.kvh * a.G, x.row0 + k * a.tile_tok);
-          }
-          __syncwarp();
-          qn0 += qb == 0;
-          qn1 += qb == 1;
-        }
-        if (!alive) break;
-        if (!two(x)) qsel ^= 1;
         Box b{-1, 0};
 #pragma unroll 1
         for (int t = x.t0 - 1; t < x.t1; ++t) {
@@ -426,6 +405,24 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 used[k] |= 1u << sl;
               }
             ++c;
+            // Q behind the unit's first K, whose slot was freed a tile before the Q buffers were.
+            if (t == x.t0) {
+#pragma unroll 1
+              for (int k = 0; k < (two(x) ? 2 : 1); ++k) {
+                const int qb = two(x) ? k : qsel, before = qb ? qn1 : qn0;
+                if (before > 0 && !(alive = warp_wait(&bars->q_empty[qb], (before - 1) & 1, &s_abort))) break;
+                if (elect_one()) {
+                  mbar_expect_tx(&bars->q_full[qb], (uint32_t)(C::halves * a.tile_tok * a.G * 128));
+                  for (int h = 0; h < C::halves; ++h)
+                    tma_load_3d(smem + qb * C::q_step + h * kHalf, &tm_q, &bars->q_full[qb], 64 * h, x.kvh * a.G, x.row0 + k * a.tile_tok);
+                }
+                __syncwarp();
+                qn0 += qb == 0;
+                qn1 += qb == 1;
+              }
+              if (!alive) break;
+              if (!two(x)) qsel ^= 1;
+            }
           }
           b = next;
         }
@@ -760,7 +757,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           w0 *= inv;
           w1 *= inv;
           const size_t orow = ((size_t)x.row0 + tok) * a.Hq + x.kvh * a.G + mh;
-          const size_t prow = (size_t)(2 * blockIdx.x + (x.t0 == 0 ? 1 : 0)) * a.R + rt * 128 + m;
+          const int slot = 2 * blockIdx.x + (x.t0 == 0 ? 1 : 0), prow = rt * 128 + m;
 #pragma unroll 1
           for (int q = 0; q < DH / 32; ++q) {
             float o[32];
@@ -798,14 +795,15 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
               }
             } else {
-              float* dst = a.part_o + prow * a.d + 32 * q;
+              float* dst = part_at(a, slot, prow, 8 * q);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (32 * q + 8 * i < a.d) st_v8(dst + 8 * i, o + 8 * i);
+              for (int i = 0; i < 8; ++i)
+                if (32 * q + 4 * i < a.d)
+                  *reinterpret_cast<float4*>(dst + i * (4 * part_rows(NARROW ? 64 : 256))) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
           }
           if (row_ok) {
-            if (!whole) a.part_ml[prow] = make_float2(mu, sum);
+            if (!whole) a.part_ml[(size_t)slot * a.R + prow] = make_float2(mu, sum);
             else if (a.lse) a.lse[orow] = lse_of(mu, sum);
           }
           tc_fence_before();

@@ -47,7 +47,7 @@ struct AttnArgs {
   const uint32_t* mask;  // [N][W]
   void* out;
   float* lse;
-  float* part_o;    // [slot][R][d] unnormalised sums of shared items
+  float* part_o;    // [slot][R / rows of a group][d / 4][row][4]: unnormalised sums of shared items
   float2* part_ml;  // [slot][R] their row maxima (log2 domain) and row sums
   Shared* shared;   // [CTA] the boundary its range starts at
   int32_t* d_status;
@@ -79,6 +79,17 @@ __device__ __forceinline__ Row row_of(const AttnArgs& a, const Item& it, int r) 
 // Index of the row in q, out ([nl * T] tokens, Hq heads) and lse.
 __device__ __forceinline__ size_t out_row(const AttnArgs& a, const Item& it, const Row& x) {
   return ((size_t)(it.lg / a.w.nh) * a.w.T + it.s.q0 + x.tok) * a.Hq + x.h;
+}
+
+// Rows whose fours of columns take turns in a partial slot.  Of a big slot a warp's
+// worth: lanes that hold a row each then write and read neighbouring words (a
+// store of 32 separate lines takes 32 clocks).  Of a small one, in which few rows
+// may exist, a row lies by itself.
+__host__ __device__ constexpr int part_rows(int R) { return R > 64 ? 32 : 1; }
+// Where columns 4 c .. + 3 of row r of a slot lie.
+__device__ __forceinline__ float* part_at(const AttnArgs& a, int slot, int r, int c) {
+  const int n = part_rows(a.R), g = r / n;
+  return a.part_o + ((size_t)slot * a.R + g * n) * a.d + ((size_t)c * n + (r - g * n)) * 4;
 }
 
 // One thread of every CTA: what its boundary's merge has to do (`any`: the CTA
