@@ -9,12 +9,16 @@ projections, RoPE at the tree positions) and between tree_attention and
 typical_accept (output projection, MLP, LM head) is not part of this library:
 the caller supplies the verify pass's q / tree k,v and the base logits at the
 tree nodes.
+
+PagedVerifyStep is the same step with the cache in pages, and brings prompts
+and decoded tokens into it.
 """
 from __future__ import annotations
 
 import torch
 
 from . import binding as B_
+from . import paged as P_
 
 
 class VerifyStep:
@@ -41,11 +45,15 @@ class VerifyStep:
         L = B_.lib()
         dt = B_.MEDUSA_BF16 if dtype == torch.bfloat16 else B_.MEDUSA_F32
         self.ws_heads = B_._ws(L.medusa_heads_workspace_size(B, H, V, K, topk), device)
-        self.ws_attn = B_._ws(L.medusa_tree_attention_workspace_size(nl, B, N, Hq, Hkv, d, Lmax, dt), device)
+        self.ws_attn = B_._ws(self._attention_workspace_size(L, dt), device)
         self.ws_acc = B_._ws(L.medusa_typical_accept_workspace_size(B, N, V), device)
         # one attention launch when the library asks for no workspace; a workspace holds
         # the partials of split key ranges, merged by a second launch
         self.attn_launches = 1 if self.ws_attn is None else 2
+
+    def _attention_workspace_size(self, L, dt) -> int:
+        c = self.dims
+        return L.medusa_tree_attention_workspace_size(c["nl"], c["B"], self.N, c["Hq"], c["Hkv"], c["d"], c["Lmax"], dt)
 
     def heads(self, h, w1, w2, stream=None):
         B_.medusa_heads(h, w1, w2, self.dims["topk"], self.topk_idx, self.topk_logit, ws=self.ws_heads,
@@ -120,6 +128,54 @@ class VerifyStep:
 
     def check(self, stream=None) -> int:
         return B_.medusa_status_check(self.status, stream)
+
+
+class PagedVerifyStep(VerifyStep):
+    """A verify step whose cache lies in pages: where VerifyStep takes kc and vc
+    [nl, B, Lmax, Hkv, d], this one takes k_pages and v_pages [nl, n_pages,
+    page_size, Hkv, d], and `page_table` [B, max_pages] int32 says which pages a
+    row has.  The table stays the caller's: a server that gives a row another page
+    writes it there between steps (a captured step reads it on the device).
+    `rope` (RopeSpec) is how the backbone turns queries and keys; without one they
+    come turned already."""
+
+    def __init__(self, *, page_table, page_size, rope: P_.RopeSpec | None = None, **kw):
+        if page_table.dim() != 2 or page_table.shape[0] != kw["B"]:
+            raise ValueError(f"PagedVerifyStep: page_table must be [B, max_pages], B = {kw['B']}, not {list(page_table.shape)}")
+        self.page_table, self.page_size, self.rope_spec = page_table, int(page_size), rope
+        super().__init__(Lmax=page_table.shape[1] * self.page_size, **kw)
+
+    def _attention_workspace_size(self, L, dt) -> int:
+        c = self.dims
+        return L.medusa_paged_attention_workspace_size(c["nl"], c["B"] * self.N, c["B"], c["Hq"], c["Hkv"], c["d"],
+                                                       self.page_size, dt)
+
+    def chunk(self, q, k, v, k_pages, v_pages, q_start, prefix_len, pos=None, scale=None, out=None, ws=None, stream=None):
+        """Tokens before the step: prompts, one decoded token per row, any mix.  Their
+        keys and values enter the pages behind prefix_len [B] rows, and each attends
+        to its row's tokens up to itself.  q [nl, T, Hq, d], k and v [nl, T, Hkv, d]
+        as they come out of the projections (slices of one output will do); returns
+        the attention's output like q.  nl may be one layer of the pages."""
+        turned = P_.medusa_paged_append(k, v, k_pages, v_pages, self.page_table, q_start, prefix_len, q=q, pos=pos,
+                                        rope=self.rope_spec, d_status=self.status, stream=stream)
+        return P_.medusa_paged_attention(turned, k_pages, v_pages, self.page_table, q_start, prefix_len, scale=scale,
+                                         out=out, ws=ws, d_status=self.status, stream=stream)[0]
+
+    def rope(self, q, kt, stream=None):
+        """Rotary embedding of the verify pass's q and tree K at this step's tree
+        positions (in place), between tree() and attention()."""
+        if self.rope_spec is None:
+            raise ValueError("PagedVerifyStep.rope: the step was made without a RopeSpec")
+        rows = [x.view(x.shape[0], -1, *x.shape[3:]) for x in (q, kt)]
+        P_.medusa_rope(*rows, self.pos.view(-1), self.rope_spec, q_out=rows[0], k_out=rows[1], stream=stream)
+
+    def attention(self, q, k_pages, v_pages, kt, vt, prefix_len, stream=None):
+        P_.medusa_paged_tree_attention(q, k_pages, v_pages, self.page_table, kt, vt, self.mask, prefix_len,
+                                       out=self.attn_out, ws=self.ws_attn, d_status=self.status, stream=stream)
+
+    def compact(self, k_pages, v_pages, kt, vt, prefix_len, stream=None):
+        P_.medusa_paged_compact(k_pages, v_pages, self.page_table, kt, vt, self.path_nodes, self.accept_len, prefix_len,
+                                self.new_len, d_status=self.status, stream=stream)
 
 
 class PipelinedSteps:

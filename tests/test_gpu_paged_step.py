@@ -1,0 +1,268 @@
+"""The paged calls as a server uses them: prompts entered and attended to, tokens
+decoded one by one, a tree verified over the pages, its path compacted, and on;
+and calls of many and of mixed sequences.  Bounds as in tests/paged.py."""
+import numpy as np
+import pytest
+
+from oracle import paged as ref
+from oracle import topology as otopo
+import workloads as wl
+from tests.helpers import TOL, bf16_to_f64, rel_err, to_dev, to_host
+from tests.paged import attention_bound, dev_ints, lse_bound, pool, starts, values
+from tests.step import lib_topology, make_step_inputs, run_gpu_step, run_oracle_step
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mg():
+    import medusa_head_speculative_heads_gb300 as m
+    m.build()
+    return m
+
+
+def host64(t):
+    a = to_host(t)
+    return bf16_to_f64(a) if a.dtype == np.uint16 else a.astype(np.float64)
+
+
+def within(out, lse, want, q, kp, dtype, n, rounded_p, extra_keys=None):
+    """out, lse against want = (out, lse, mag) of the definition on the same inputs."""
+    o, z, mag = want
+    d = q.shape[-1]
+    k64 = ref.f64(kp)
+    norms = [np.nanmax(np.nansum(k64 * k64, -1))]
+    if extra_keys is not None:
+        norms.append(np.max(np.sum(ref.f64(extra_keys) ** 2, -1)))
+    k_norm = np.sqrt(max(norms))
+    live = ~np.isnan(z)
+    bound = attention_bound(q, k_norm, d, d ** -0.5, n, mag, o, dtype, rounded_p)
+    assert np.all(np.abs(host64(out) - o)[live] <= bound[live])
+    if lse is not None:
+        assert np.all(np.abs(host64(lse) - z)[live] <= lse_bound(q, k_norm, d, d ** -0.5, n, np.where(live, z, 0))[live])
+
+
+def paged_like(kc, page, max_pages, rng):
+    """An empty pool for caches [nl, B, Lmax, Hkv, d], pages in random order."""
+    nl, B, _, hkv, d = kc.shape
+    n_pages = B * max_pages
+    table = rng.permutation(n_pages).reshape(B, max_pages).astype(np.int32)
+    nan = np.uint16(0x7FC0) if kc.dtype == np.uint16 else np.float32(np.nan)
+    return np.full((nl, n_pages, page, hkv, d), nan), table
+
+
+def gathered(pages, table, b, n):
+    """Rows 0 .. n - 1 of sequence b: [nl, n, Hkv, d]."""
+    p = to_host(pages)
+    at = ref.rows_of(table, b, 0, n, p.shape[2])
+    return p.reshape(p.shape[0], -1, *p.shape[3:])[:, at]
+
+
+def paged_step(mg, c, inp, table, page, rope=None):
+    from medusa_head_speculative_heads_gb300.step import PagedVerifyStep
+    dtype = torch.bfloat16 if c["dtype"] == "bf16" else torch.float32
+    return PagedVerifyStep(B=len(inp["rows"]), H=c["H"], V=c["V"], K=c["K"], topk=c["topk"], nl=inp["q"].shape[0], Hq=c["Hq"],
+                           Hkv=c["Hkv"], d=c["d"], dtype=dtype, topology=lib_topology(mg, c), temperature=c["T"], eps=c["eps"],
+                           delta=c["delta"], page_table=dev_ints(table), page_size=page, rope=rope)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("dtype,page", [("f32", 8), ("bf16", 16), ("bf16", 128)])
+def test_the_step_over_pages_is_the_step_over_rows(mg, dtype, page, captured):
+    """The whole verify step with the cache in pages against the contiguous one and the
+    oracle's: the same tokens, decisions and cache rows, attention within bounds."""
+    c = wl.config("tiny", dtype=dtype, B=3, nl=2)
+    inp = make_step_inputs(c)
+    want, flat = run_oracle_step(c, inp), run_gpu_step(mg, c, inp)
+    rng = np.random.default_rng(5)
+    B, nl, L = len(inp["rows"]), inp["q"].shape[0], int(inp["prefix_len"][0])
+    empty, table = paged_like(inp["kc"], page, -(-(L + 64) // page), rng)
+    vs = paged_step(mg, c, inp, table, page)
+    kp, vp = to_dev(empty), to_dev(empty)
+    # the prefix enters through the step itself
+    rows = [to_dev(np.ascontiguousarray(x[:, :, :L]).reshape(nl, B * L, *x.shape[3:])) for x in (inp["kc"], inp["vc"])]
+    zero = dev_ints([0] * B)
+    vs.chunk(torch.zeros((nl, B * L, c["Hq"], c["d"]), dtype=kp.dtype, device="cuda"), *rows, kp, vp, dev_ints(starts([L] * B)), zero)
+    d = {k: to_dev(inp[k]) for k in ("h", "w1", "w2", "root_tok", "prefix_len", "q", "kt", "vt", "logits")}
+    args = (d["h"], d["w1"], d["w2"], d["root_tok"], d["prefix_len"], d["q"], kp, vp, d["kt"], d["vt"], d["logits"])
+    if captured:
+        g = vs.capture(*args)
+        for t in (vs.attn_out, vs.accept_len, vs.new_len, vs.tokens):
+            t.zero_()
+        g.replay()
+    else:
+        vs.run(*args)
+    assert vs.check() == 0
+    assert np.array_equal(to_host(vs.tokens), flat["tokens"]) and np.array_equal(to_host(vs.pos), flat["pos"])
+    assert np.array_equal(to_host(vs.accept_len), flat["accept_len"]) and np.array_equal(to_host(vs.new_len), flat["new_len"])
+    assert rel_err(host64(vs.attn_out), want["attn_out"]) <= TOL[dtype]
+    for b in range(B):
+        n = int(flat["new_len"][b])
+        assert np.array_equal(gathered(kp, table, b, n), flat["kc"][:, b, :n]) and np.array_equal(gathered(vp, table, b, n), flat["vc"][:, b, :n])
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("f32", 4, 2, 64), ("bf16", 8, 2, 128), ("bf16", 4, 4, 64)])
+def test_prompt_decode_verify_compact_decode(mg, dtype, hq, hkv, d):
+    """Ragged prompts in one call, two tokens decoded one by one, a tree turned, verified
+    and compacted, one more token: every attention against its definition on what the
+    cache then holds, the cache against rotations of what entered it, and the decoded
+    tokens against the same tokens entered as one chunk."""
+    from medusa_head_speculative_heads_gb300.step import PagedVerifyStep
+    rng = np.random.default_rng(d + hq)
+    nl, page, prompts = 2, 16, [37, 1, 130]
+    B, rc = len(prompts), dtype == "bf16"
+    t = otopo.dense([2, 2])
+    N, W = t.n_nodes, (t.n_nodes + 31) // 32
+    max_pages = 14
+    table = rng.permutation(B * max_pages).reshape(B, max_pages).astype(np.int32)
+    spec = mg.RopeSpec(d, base=500000.0)
+    freq = ref.rope_frequencies(d, 500000.0)
+    tt = torch.bfloat16 if rc else torch.float32
+    vs = PagedVerifyStep(B=B, H=64, V=64, K=2, topk=2, nl=nl, Hq=hq, Hkv=hkv, d=d, dtype=tt, topology=mg.Topology.from_paths([list(p) for p in t.paths[1:]]),
+                         temperature=0.7, eps=0.1, delta=0.3, page_table=dev_ints(table), page_size=page, rope=spec)
+    nan = torch.full((nl, B * max_pages, page, hkv, d), float("nan"), dtype=tt, device="cuda")
+    kp, vp, kp2, vp2 = nan.clone(), nan.clone(), nan.clone(), nan.clone()
+
+    def tokens(n):
+        qkv = to_dev(values(rng, (nl, n, hq + 2 * hkv, d), dtype))
+        return qkv[:, :, :hq], qkv[:, :, hq:hq + hkv], qkv[:, :, hq + hkv:]
+
+    def chunk_checked(q, k, v, lens, prefix):
+        q0 = starts(lens)
+        out = vs.chunk(q, k, v, kp, vp, dev_ints(q0), dev_ints(prefix))
+        pos = np.concatenate([np.arange(p, p + n) for p, n in zip(prefix, lens)])
+        turned = mg.medusa_rope(q, None, dev_ints(pos), spec)[0]
+        held = [to_host(kp), to_host(vp)]
+        qh = to_host(turned)
+        want = ref.paged_attention(qh, *held, table, q0, prefix)
+        within(out, None, want, qh, held[0], dtype, 200, rc)
+        for b in range(B):  # what entered: values as they were, keys turned at their rows
+            rows = gathered(vp, table, b, prefix[b] + lens[b])[:, prefix[b]:]
+            assert np.array_equal(rows, to_host(v[:, q0[b]:q0[b + 1]]))
+            kw = ref.rope(to_host(k[:, q0[b]:q0[b + 1]]), np.arange(prefix[b], prefix[b] + lens[b]), freq)
+            got = ref.f64(gathered(kp, table, b, prefix[b] + lens[b])[:, prefix[b]:])
+            assert np.all(np.abs(got - kw) <= 8 * 2.0 ** -24 * 11 + (2.0 ** -8 if rc else 2.0 ** -24) * np.abs(kw) + 1e-30)
+        return out
+
+    lens = list(prompts)
+    prompt = tokens(sum(prompts))
+    chunk_checked(*prompt, prompts, [0] * B)
+    one = [tokens(B) for _ in range(2)]
+    outs = []
+    for x in one:
+        outs.append(chunk_checked(*x, [1] * B, lens))
+        lens = [n + 1 for n in lens]
+    # the same two tokens of each sequence as one chunk behind the same prompts
+    vs.chunk(*prompt, kp2, vp2, dev_ints(starts(prompts)), dev_ints([0] * B))
+    two = [torch.stack((a, b), 2).reshape(nl, 2 * B, a.shape[2], d) for a, b in zip(*one)]
+    both = vs.chunk(*two, kp2, vp2, dev_ints(starts([2] * B)), dev_ints(prompts))
+    assert torch.equal(kp.view(torch.int16 if rc else torch.int32), kp2.view(torch.int16 if rc else torch.int32))
+    apart = torch.stack(outs, 2).reshape(both.shape)
+    assert rel_err(host64(apart), host64(both)) <= TOL[dtype]
+
+    q, kt, vt = (to_dev(values(rng, (nl, B, N, h, d), dtype)) for h in (hq, hkv, hkv))
+    depth = np.array([len(p) for p in t.paths])
+    bits = np.zeros((N, W), np.uint32)
+    for i, p in enumerate(t.paths):
+        for j, o in enumerate(t.paths):
+            if list(o) == list(p)[:len(o)]:
+                bits[i, j // 32] |= np.uint32(1 << (j % 32))
+    vs.mask.copy_(to_dev(bits.view(np.int32)))
+    vs.pos.copy_(dev_ints(np.array(lens)[:, None] + depth[None]))
+    before = to_host(kt.view(nl, B * N, hkv, d))
+    vs.rope(q, kt)
+    kw = ref.rope(before, (np.array(lens)[:, None] + depth[None]).reshape(-1), freq).reshape(nl, B, N, hkv, d)
+    assert np.all(np.abs(host64(kt) - kw) <= 8 * 2.0 ** -24 * 11 + (2.0 ** -8 if rc else 2.0 ** -24) * np.abs(kw) + 1e-30)
+    vs.attention(q, kp, vp, kt, vt, dev_ints(lens))
+    want = ref.paged_tree_attention(to_host(q), to_host(kp), to_host(vp), table, to_host(kt), to_host(vt), bits, lens)
+    within(vs.attn_out, None, want, to_host(q), to_host(kp), dtype, 200, rc, to_host(kt))
+    path, acc = np.zeros((B, vs.topo.max_depth + 1), np.int32), [1, 3, 2]
+    deep = next(i for i, p in enumerate(t.paths) if len(p) == 2)
+    chain = [next(i for i, o in enumerate(t.paths) if list(o) == list(t.paths[deep])[:n]) for n in range(3)]
+    path[:] = chain
+    vs.path_nodes.copy_(dev_ints(path))
+    vs.accept_len.copy_(dev_ints(acc))
+    k3, v3, n3 = ref.paged_compact(to_host(kp), to_host(vp), table, to_host(kt), to_host(vt), path, acc, lens)
+    vs.compact(kp, vp, kt, vt, dev_ints(lens))
+    assert np.array_equal(to_host(kp), k3, equal_nan=not rc) and np.array_equal(to_host(vp), v3, equal_nan=not rc)
+    assert np.array_equal(to_host(vs.new_len), n3)
+    chunk_checked(*tokens(B), [1] * B, n3.tolist())
+    assert vs.check() == 0
+
+
+MIXED = [
+    # more sequences than a CTA has threads, some without a token
+    dict(dtype="bf16", nl=1, hq=4, hkv=4, d=64, page=16, B=420, prefix=90, chunk=lambda r, b: int(r.integers(0, 2))),
+    dict(dtype="f32", nl=1, hq=2, hkv=1, d=32, page=16, B=300, prefix=70, chunk=lambda r, b: int(r.integers(0, 2))),
+    # many single tokens and one chunk (blocks of 64 rows), one long chunk and a few single tokens (of 256)
+    dict(dtype="bf16", nl=1, hq=8, hkv=2, d=128, page=16, B=40, prefix=400, chunk=lambda r, b: 90 if b == 17 else 1),
+    dict(dtype="bf16", nl=1, hq=8, hkv=8, d=128, page=64, B=6, prefix=260, chunk=lambda r, b: [1, 300, 0, 1, 5, 129][b]),
+    # many blocks a CTA, and one sequence's rows over every CTA
+    dict(dtype="bf16", nl=12, hq=16, hkv=4, d=64, page=8, B=9, prefix=130, chunk=lambda r, b: int(r.integers(1, 60))),
+    dict(dtype="bf16", nl=1, hq=20, hkv=1, d=104, page=32, B=1, prefix=9000, chunk=lambda r, b: 14),
+    dict(dtype="f32", nl=1, hq=3, hkv=1, d=96, page=7, B=1, prefix=5000, chunk=lambda r, b: 30),
+]
+
+
+@pytest.mark.parametrize("c", MIXED, ids=lambda c: f"{c['dtype']}-{c['hq']}-{c['hkv']}-d{c['d']}-B{c['B']}")
+def test_many_and_mixed_sequences(mg, c):
+    rng = np.random.default_rng(c["B"] + c["d"])
+    prefix = rng.integers(0, c["prefix"] + 1, c["B"]).tolist()
+    if c["B"] == 1:
+        prefix = [c["prefix"]]
+    chunk = [c["chunk"](rng, b) for b in range(c["B"])]
+    kp, vp, table = pool(rng, [p + n for p, n in zip(prefix, chunk)], nl=c["nl"], page=c["page"], hkv=c["hkv"], d=c["d"], dtype=c["dtype"])
+    q0 = starts(chunk)
+    q = values(rng, (c["nl"], int(q0[-1]), c["hq"], c["d"]), c["dtype"])
+    want = ref.paged_attention(q, kp, vp, table, q0, prefix)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    first = None
+    for _ in range(3):  # on memory of its own each time
+        dev = [to_dev(x) for x in (q, kp, vp)] + [dev_ints(x) for x in (table, q0, prefix)]
+        out, lse = mg.medusa_paged_attention(*dev, want_lse=True, d_status=st)
+        assert mg.medusa_status_check(st) == 0
+        if first is None:
+            first = out.clone()
+            rc = c["dtype"] == "bf16"
+            within(out, lse, want, q, kp, c["dtype"], max(p + n for p, n in zip(prefix, chunk)), rc)
+        assert torch.equal(out, first)
+        del dev, out, lse
+        torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("N,hq,hkv,d,B,nl", [(64, 4, 4, 128, 2, 10), (100, 6, 3, 64, 3, 5), (33, 8, 1, 96, 5, 3)])
+def test_trees_of_many_layers(mg, N, hq, hkv, d, B, nl):
+    rng = np.random.default_rng(N)
+    prefix = rng.integers(0, 300, B).tolist()
+    kp, vp, table = pool(rng, prefix, nl=nl, page=16, hkv=hkv, d=d, dtype="bf16")
+    q, kt, vt = (values(rng, (nl, B, N, h, d), "bf16") for h in (hq, hkv, hkv))
+    see = np.tril(rng.random((N, N)) < 0.3)
+    bits = np.zeros((N, (N + 31) // 32), np.uint32)
+    for i, j in zip(*np.nonzero(see)):
+        bits[i, j // 32] |= np.uint32(1 << (j % 32))
+    want = ref.paged_tree_attention(q, kp, vp, table, kt, vt, bits, prefix)
+    first = None
+    for _ in range(3):
+        dev = [to_dev(x) for x in (q, kp, vp)] + [dev_ints(table), to_dev(kt), to_dev(vt), to_dev(bits.view(np.int32)), dev_ints(prefix)]
+        out, lse = mg.medusa_paged_tree_attention(*dev, want_lse=True)
+        if first is None:
+            first = out.clone()
+            sees = ~np.isneginf(want[1])
+            bare = np.where(sees, want[1], np.nan)
+            within(out, lse, (want[0], bare, want[2]), q, kp, "bf16", 300 + N, True, kt)
+            assert np.all(host64(out)[~sees] == 0) and np.all(np.isneginf(host64(lse)[~sees]))
+        assert torch.equal(out, first)
+        del dev, out, lse
+        torch.cuda.empty_cache()
+
+
+def test_a_step_refuses_what_does_not_fit(mg):
+    c = wl.config("tiny")
+    inp = make_step_inputs(c)
+    B = len(inp["rows"])
+    with pytest.raises(ValueError, match="page_table"):
+        paged_step(mg, c, inp, np.zeros((B + 1, 4), np.int32), 16)
+    vs = paged_step(mg, c, inp, np.zeros((B, 40), np.int32), 16)
+    with pytest.raises(ValueError, match="RopeSpec"):
+        vs.rope(to_dev(inp["q"]), to_dev(inp["kt"]))
