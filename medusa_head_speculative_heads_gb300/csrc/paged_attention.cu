@@ -40,10 +40,15 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v) {
 // memory between threads of one half warp.  K and V have one buffer each, filled by
 // asynchronous copies: the next K under the products with V, V under the scores.
 // A warp none of whose rows exists takes part in the copies only.
-// Issue slots bound it, so products are taken two at a time (fma.rn.f32x2: over even
-// and odd columns in the scores, over pairs of columns in the sums).  Measured, fp32,
-// 5 ragged sequences of up to 331 tokens behind up to 1338 rows, 8 + 4 heads of 64: 91
-// us, 22 TFLOP/s (with single products and loads between two barriers 114 us).
+// Products are taken two at a time (fma.rn.f32x2: over even and odd columns in the
+// scores, over pairs of columns in the sums).  Measured, fp32, 5 ragged sequences of
+// up to 331 tokens behind up to 1338 rows, 8 + 4 heads of 64: the kernel 85 us, with the
+// merge 93 us, 21 TFLOP/s (with single products and loads between two barriers 114 us).
+// Shared memory's pipe bounds it, busy for 64 % of the clocks (the FMA pipe for 47 %): a
+// 16-byte load takes four of them when lanes read several rows and two as a broadcast,
+// 24 for the 64 products of four columns.  A warp of 8 rows x 64 keys, each K row
+// read once and Q as broadcasts, takes as many and measured 101 us; fewer would need
+// more scores a thread than two CTAs' registers hold.
 template <int DC>
 __host__ __device__ constexpr int simt_pitch() { return 16 * DC + 4; }
 template <typename T, int DC, int RM>
