@@ -27,7 +27,7 @@ __device__ __forceinline__ int pool_row(const Cache& c, int b, int r) {
 // An item is (layer, head group, sequence, block of `ctok` tokens); its cost is
 // its number of KT-key tiles.  All items' tiles are laid end to end, layer and
 // head group outermost (CTAs that run together then read the same head's rows),
-// and CTA c of C takes tiles [c Q, (c + 1) Q), Q = max(ceil(U / C), min_tiles).
+// and CTA c of C takes tiles [c Q, (c + 1) Q), Q = ceil(U / C).
 // Each CTA has at most two items that it shares with others: the one its range
 // starts inside (partial slot 0) and the one its range ends inside (slot 1).
 struct Work {
@@ -37,7 +37,7 @@ struct Work {
   int nl, nh, cap;            // nh: head groups per layer; cap: rows a sequence can hold
   int ctok, KT;               // tokens per block and keys per tile
   int ctok_log2, KT_log2;     // both are powers of two
-  int ctas, min_tiles;
+  int ctas;
   unsigned long long ctas_inv;  // 2^64 / ctas, rounded up
 };
 
@@ -163,7 +163,6 @@ __device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, lon
       pl.per = per;
       pl.U = per * ((long long)w.nl * w.nh);
       pl.Q = (long long)__umul64hi((unsigned long long)(pl.U + w.ctas - 1), w.ctas_inv);
-      if (pl.Q < w.min_tiles) pl.Q = w.min_tiles;
       u = pl.Q * cta;
       if (u >= pl.U) return false;
       lg = (int)((float)u / (float)per);  // to within a few
