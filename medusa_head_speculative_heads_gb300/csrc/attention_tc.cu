@@ -99,7 +99,11 @@ struct Params {
 };
 
 struct Bars {
-  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  // A wait tells phases apart by their parity, so a waiter may skip none.  A slot holds K tiles
+  // and V tiles in turn, and each MMA warp waits for one kind only: each kind's arrivals have a
+  // barrier of their own (full[0] K, full[1] V).  On a shared one, the S warp could wait for a K
+  // behind a V still in flight, whose phase it had not seen, and go on at once.
+  uint64_t full[2][kMaxSlots], empty[kMaxSlots];
   uint64_t q_full, q_empty, s_full[2], s_free[2], p_full[2], pv_done[2], o_free, drain, drain_pv;
   uint64_t mx[2][4];  // SPLIT = 2: partial row maxima of a tile exchanged (tile parity, lane quarter)
   uint64_t lx[4];     // SPLIT = 2: partial row sums of an item exchanged (lane quarter)
@@ -229,7 +233,7 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   if (threadIdx.x == 0) {
     s_abort = 0;
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&bars->full[s], 1);
+      for (int kv = 0; kv < 2; ++kv) mbar_init(&bars->full[kv][s], 1);
       mbar_init(&bars->empty[s], 1);
     }
     mbar_init(&bars->q_full, 1);
@@ -286,7 +290,8 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int g = 0, n = 0, issued = 0;
+      int g = 0, n = 0;
+      uint32_t used[2] = {0, 0}, odd[2] = {0, 0};  // bit: full[kv][slot] has been used, an odd number of times
       bool alive = true;
       for (int u = blockIdx.x; u < p.units && alive; u += gridDim.x) {
         const Unit w = decode_unit(p, u);
@@ -318,12 +323,15 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
               break;
             const CUtensorMap* mp = kv ? (tree ? &tm_vt : &tm_vc) : (tree ? &tm_kt : &tm_kc);
             uint8_t* dst = smem + kOffRing + sl * kSlotBytes;
-            mbar_expect_tx(&bars->full[sl], kSlotBytes);
+            uint64_t* full = &bars->full[kv][sl];
+            mbar_expect_tx(full, kSlotBytes);
             for (int dh = 0; dh < 2; ++dh)
               for (int cb = 0; cb < 2; ++cb)
-                tma_load_4d(dst + dh * kHalf + cb * kBox, mp, &bars->full[sl], 64 * dh,
+                tma_load_4d(dst + dh * kHalf + cb * kBox, mp, full, 64 * dh,
                             PACKED ? x.h0 + cb : x.h0, PACKED ? j0 : j0 + 64 * cb, x.lb);
-            issued = ++c;
+            used[kv] |= 1u << sl;
+            odd[kv] ^= 1u << sl;
+            ++c;
           }
         }
         g += cnt;
@@ -332,8 +340,10 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         // Drain: wait (bounded, regardless of the abort flag) for the last
         // phase issued on every load barrier, so no copy lands after exit.
         if (n > 0) mbar_wait_bounded(&bars->q_full, (n - 1) & 1, nullptr, kDrainNs);
-        for (int c = issued - 1; c >= 0 && c >= issued - kSlots; --c)
-          mbar_wait_bounded(&bars->full[slot_of<kSlots>(c)], use_parity<kSlots>(c), nullptr, kDrainNs);
+        for (int kv = 0; kv < 2; ++kv)
+          for (int sl = 0; sl < kSlots; ++sl)
+            if ((used[kv] >> sl) & 1u)
+              mbar_wait_bounded(&bars->full[kv][sl], ((odd[kv] >> sl) & 1u) ^ 1u, nullptr, kDrainNs);
       }
     }
   } else if (warp == 1 || warp == 2) {
@@ -344,6 +354,12 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     // both streams.  Both warps walk the same load sequence to find their slots.
     const bool s_role = warp == 1;
     int g = 0, n = 0;
+    uint32_t odd = 0;  // bit: phases of this warp's kind seen on the slot, modulo 2
+    auto came = [&](int sl) {
+      const bool ok = warp_wait(&bars->full[s_role ? 0 : 1][sl], (odd >> sl) & 1u, &s_abort);
+      odd ^= 1u << sl;
+      return ok;
+    };
     bool alive = true;
     for (int u = blockIdx.x; u < p.units && alive; u += gridDim.x) {
       const Unit w = decode_unit(p, u);
@@ -364,7 +380,7 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         if (j < cnt) {
           const int gj = g0 + j, ck = c++, sb = gj & 1;
           if (s_role) {
-            if (!(alive = warp_wait(&bars->full[slot_of<kSlots>(ck)], use_parity<kSlots>(ck), &s_abort))) break;
+            if (!(alive = came(slot_of<kSlots>(ck)))) break;
             if (gj >= 2 && !(alive = warp_wait(&bars->s_free[sb], ((gj >> 1) - 1) & 1, &s_abort))) break;
             tc_fence_after();
             if (lane == 0) {
@@ -389,7 +405,7 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
           if (!s_role) {
             if (tt == 0 && n > 0 && !(alive = warp_wait(&bars->o_free, (n - 1) & 1, &s_abort))) break;
             if (!(alive = warp_wait(&bars->p_full[gt & 1], (gt >> 1) & 1, &s_abort))) break;
-            if (!(alive = warp_wait(&bars->full[slot_of<kSlots>(cv)], use_parity<kSlots>(cv), &s_abort))) break;
+            if (!(alive = came(slot_of<kSlots>(cv)))) break;
             uint8_t* vb = smem + kOffRing + slot_of<kSlots>(cv) * kSlotBytes;
             // The last prefix tile may run past prefix_len: zero those V rows
             // (stale cache rows may hold anything, and 0 * NaN is NaN).
