@@ -409,7 +409,7 @@ medusa_status medusa_head_loss(const void* logits, const int32_t* tokens, int K,
  *   q_start[b] .. q_start[b+1]-1 (none, one or many; q_start[0] = 0 and the
  *   last entry at most T; tokens at and past it are left alone)
  * Lengths, starts and pages are read on the device only.  A sequence whose
- * starts decrease or leave [0, T], or whose prefix_len is outside
+ * starts decrease or leave [0, T], or that has tokens and a prefix_len outside
  * [0, max_pages * page_size], sets BAD_LENGTH and nothing of it is written.
  * Entries of page_table behind a sequence's last row are never read.  Pools,
  * outputs and inputs must not overlap one another (ALIAS), except where a call
@@ -518,7 +518,8 @@ medusa_status medusa_paged_attention(const void* q, int64_t ldq, const void* k_p
  * with mask bit (i, j) set.
  *   q, out [n_layers][B][N][Hq][d]; kt, vt [n_layers][B][N][Hkv][d];
  *   mask [N][ceil(N/32)]; lse [n_layers][B][N][Hq] or NULL.
- * A node that sees nothing gets zeros, and -inf as lse.  N <= MEDUSA_MAX_NODES;
+ * A node that sees nothing gets zeros, and -inf as lse.  Tree rows must be
+ * finite, visible or not.  N <= MEDUSA_MAX_NODES;
  * other limits, kernels and errors as in medusa_paged_attention (kt and vt
  * 16-byte aligned); the workspace is medusa_paged_attention_workspace_size(
  * n_layers, B * N, B, ...) bytes. */

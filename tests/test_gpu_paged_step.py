@@ -257,6 +257,58 @@ def test_trees_of_many_layers(mg, N, hq, hkv, d, B, nl):
         torch.cuda.empty_cache()
 
 
+def test_pipelined_steps_over_pages(mg):
+    """The step under PipelinedSteps: inputs from pinned memory, results read back, the
+    page table changed between steps (a captured step reads it on the device)."""
+    from medusa_head_speculative_heads_gb300.step import PipelinedSteps
+    c = wl.config("tiny", dtype="bf16", B=3, nl=2)
+    inp = make_step_inputs(c)
+    flat = run_gpu_step(mg, c, inp)
+    rng = np.random.default_rng(6)
+    page, L, B = 16, int(inp["prefix_len"][0]), 3
+    empty, table = paged_like(inp["kc"], page, -(-(L + 64) // page), rng)
+    vs = paged_step(mg, c, inp, table, page)
+
+    def pools(t):
+        out = []
+        for x in (inp["kc"], inp["vc"]):
+            p = empty.copy()
+            for b in range(B):
+                p.reshape(p.shape[0], -1, *p.shape[3:])[:, ref.rows_of(t, b, 0, L, page)] = x[:, b, :L]
+            out.append(to_dev(p))
+        return out
+
+    kp, vp = pools(table)
+    names = ("h", "root_tok", "prefix_len", "q", "kt", "vt", "logits")
+    dev = {k: to_dev(inp[k]) for k in names}
+    outs = [vs.accept_len, vs.next_tok, vs.new_len, vs.attn_out]
+    hosts = [torch.empty(o.shape, dtype=o.dtype).pin_memory() for o in outs]
+    resident = dict(w1=to_dev(inp["w1"]), w2=to_dev(inp["w2"]), kc=kp, vc=vp)  # the graphs hold addresses only
+    ps = PipelinedSteps(vs, dev, resident, outs, hosts)
+    staged, views = ps.host_staging()
+    for k in names:
+        views[k].copy_(dev[k])
+    torch.cuda.synchronize()
+    for turn in range(4):
+        if turn == 2:  # other pages for every row
+            table = table[:, ::-1][[1, 2, 0]].copy()
+            vs.page_table.copy_(dev_ints(table))
+            for p, x in zip((kp, vp), pools(table)):
+                p.copy_(x)
+            torch.cuda.synchronize()
+        for h in hosts:
+            h.zero_()
+        ps.step(staged)
+        torch.cuda.synchronize()
+        assert np.array_equal(to_host(hosts[0]), flat["accept_len"]) and np.array_equal(to_host(hosts[2]), flat["new_len"])
+        assert np.array_equal(to_host(hosts[1]), flat["next_tok"])
+        assert rel_err(host64(hosts[3]), flat["attn_out"]) <= TOL["bf16"]
+        for b in range(B):
+            n = int(flat["new_len"][b])
+            assert np.array_equal(gathered(kp, table, b, n), flat["kc"][:, b, :n])
+    assert vs.check() == 0
+
+
 def test_a_step_refuses_what_does_not_fit(mg):
     c = wl.config("tiny")
     inp = make_step_inputs(c)
