@@ -411,10 +411,10 @@ medusa_status medusa_head_loss(const void* logits, const int32_t* tokens, int K,
  * Lengths, starts and pages are read on the device only.  A sequence whose
  * starts decrease or leave [0, T], or that has tokens and a prefix_len outside
  * [0, max_pages * page_size], sets BAD_LENGTH and nothing of it is written.
- * Entries of page_table behind a sequence's last row are never read.  Pools,
- * outputs and inputs must not overlap one another (ALIAS), except where a call
- * says so.  page_size >= 1, max_pages >= 1, n_layers * n_pages * page_size
- * and n_layers * T < 2^31, max_pages * page_size < 2^31 - 2^16.
+ * Entries of page_table behind a sequence's last row are never read.  What a
+ * call writes (pools, outputs, workspace) must overlap nothing else (ALIAS),
+ * except where it says so.  T, B, page_size and max_pages >= 1, n_layers *
+ * n_pages * page_size and n_layers * T < 2^31, max_pages * page_size < 2^31 - 2^16.
  *
  * medusa_rope_plan: how a rotary embedding turns.  The leading rotary_dim
  * elements of a head are pairs (i, i + rotary_dim/2), or (2i, 2i+1) when
@@ -494,10 +494,10 @@ medusa_status medusa_paged_append(const void* q, int64_t ldq, const void* k, int
  * result, whatever they hold; rows it has must be finite.  A page outside
  * [0, n_pages) among a sequence's rows sets BAD_INDEX and counts as zero rows;
  * prefix_len + chunk past max_pages * page_size sets BAD_LENGTH (unwritten).
- * bf16 with d <= 128 a multiple of 8, page_size a multiple of 8, G <= 128 and
- * ldq a multiple of 8 runs on tcgen05 tensor cores; everything else on CUDA
- * cores (fp32 never uses TF32).  d a multiple of 4 up to MEDUSA_MAX_HEAD_DIM,
- * q, pools and out 16-byte aligned, ldq a multiple of 4, scale > 0.
+ * bf16 with d <= 128 a multiple of 8, page_size a multiple of 8 and G <= 128
+ * runs on tcgen05 tensor cores; everything else on CUDA cores (fp32 never uses
+ * TF32).  d a multiple of 4 up to MEDUSA_MAX_HEAD_DIM, q, pools and out 16-byte
+ * aligned, ldq a multiple of 4 (of 8 on tensor cores), scale > 0.
  * The key tiles of all (layer, kv head, sequence, row block) items are laid end
  * to end and divided evenly over the SMs; an item shared by several CTAs leaves
  * partial results in the workspace, added in a fixed order by a second kernel

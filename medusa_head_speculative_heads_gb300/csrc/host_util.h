@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "medusa.h"
 
 namespace medusa {
@@ -20,6 +22,18 @@ inline size_t dtype_bytes(medusa_dtype dt) { return dt == MEDUSA_BF16 ? 2 : 4; }
 inline bool dtype_ok(int dt) { return dt == MEDUSA_F32 || dt == MEDUSA_BF16; }
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// A buffer a call reads or writes.
+struct Region {
+  const void* p;  // may be NULL
+  size_t n;
+};
+// Whether `out` overlaps one of the others.
+inline bool overlaps_any(Region out, std::initializer_list<Region> others) {
+  for (const Region& r : others)
+    if (out.p && r.p && overlaps(out.p, out.n, r.p, r.n)) return true;
+  return false;
+}
 
 // Sizes of a paged cache: pool rows and a sequence's rows stay inside int32,
 // with room for a tile behind the last row.

@@ -480,6 +480,15 @@ static medusa_status attend(AttnArgs& a, int n_layers, int T, int B, int Hq, int
   a.ldq = ldq;
   a.scale_log2 = scale * 1.4426950408889634f;
   if (!ws || !aligned16(ws) || ws_bytes < ws_bytes_of(v, d)) return MEDUSA_ERR_WORKSPACE;
+  // The entry points have compared out and lse with the big inputs.
+  const size_t es = dtype_bytes(dt), tokens = (size_t)n_layers * T, pool = (size_t)n_layers * n_pages * page_size * Hkv * d * es;
+  const size_t tree = a.w.N ? tokens * Hkv * d * es : 0, nb = (size_t)B * 4;
+  const Region small[] = {{a.cache.page_table, nb * max_pages}, {a.w.q_start, nb + 4}, {a.w.prefix_len, nb}, {a.mask, (size_t)a.w.N * a.W * 4}};
+  const Region out{a.out, tokens * Hq * d * es}, lse{a.lse, tokens * Hq * 4}, scratch{ws, ws_bytes_of(v, d)};
+  for (const Region& r : small)
+    if (overlaps_any(r, {out, lse, scratch})) return MEDUSA_ERR_ALIAS;
+  if (overlaps_any(scratch, {out, lse, {a.q, ((tokens - 1) * (size_t)ldq + (size_t)Hq * d) * es}, {a.k_pages, pool}, {a.v_pages, pool}, {a.kt, tree}, {a.vt, tree}}))
+    return MEDUSA_ERR_ALIAS;
   a.part_o = static_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)v.ctas * 2 * v.R * d);
   a.shared = reinterpret_cast<Shared*>(a.part_ml + (size_t)v.ctas * 2 * v.R);

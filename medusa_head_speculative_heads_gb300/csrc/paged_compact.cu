@@ -125,6 +125,9 @@ extern "C" medusa_status medusa_paged_compact(void* k_pages, void* v_pages, cons
   for (const void* pool : {(const void*)k_pages, (const void*)v_pages})
     if (overlaps(pool, np, kt, nt) || overlaps(pool, np, vt, nt)) return MEDUSA_ERR_ALIAS;
   const size_t nb = (size_t)B * 4;
+  if (overlaps_any({new_len, nb}, {{k_pages, np}, {v_pages, np}, {kt, nt}, {vt, nt}})) return MEDUSA_ERR_ALIAS;
+  for (const Region& r : {Region{page_table, nb * max_pages}, Region{path_nodes, nb * (Dmax + 1)}, Region{accept_len, nb}, Region{prefix_len, nb}})
+    if (overlaps_any(r, {{k_pages, np}, {v_pages, np}})) return MEDUSA_ERR_ALIAS;
   if (overlaps(new_len, nb, accept_len, nb) || overlaps(new_len, nb, path_nodes, nb * (Dmax + 1)) ||
       overlaps(new_len, nb, page_table, nb * max_pages) || (new_len != prefix_len && overlaps(new_len, nb, prefix_len, nb)))
     return MEDUSA_ERR_ALIAS;

@@ -425,6 +425,9 @@ extern "C" medusa_status medusa_paged_append(const void* q, int64_t ldq, const v
     if (!(q_out == q && ldq == (int64_t)Hq * d) && overlaps(q, nq, q_out, oq)) return MEDUSA_ERR_ALIAS;
     if (overlaps(q_out, oq, k, nk) || overlaps(q_out, oq, v, nv)) return MEDUSA_ERR_ALIAS;
   }
+  const size_t nb = (size_t)B * 4;
+  for (const Region& r : {Region{page_table, nb * max_pages}, Region{q_start, nb + 4}, Region{prefix_len, nb}, Region{pos, (size_t)T * 4}})
+    if (overlaps_any(r, {{q_out, oq}, {k_pages, np}, {v_pages, np}})) return MEDUSA_ERR_ALIAS;
   RopeArgs a{};
   a.q = q;
   a.k = k;

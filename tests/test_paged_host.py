@@ -159,6 +159,15 @@ def test_compaction_refuses_overlaps(o):
     assert compact(**o) == ALIAS
 
 
+@pytest.mark.parametrize("call,o", [
+    (append, dict(qo=at(3))), (append, dict(q0=at(7) + 64)), (append, dict(pl=at(8))), (append, dict(pos=at(6) + 4)), (append, dict(table=at(7))),
+    (attn, dict(out=at(3))), (attn, dict(lse=at(4))), (attn, dict(out=at(5))), (attn, dict(ws=at(0))), (attn, dict(ws=at(1) + 64)), (attn, dict(ws=at(6))),
+    (attn, dict(ws=at(7))), (attn, dict(table=at(8) + 256)), (tree, dict(out=at(6))), (tree, dict(ws=at(5))), (tree, dict(ws=at(7))), (tree, dict(lse=at(9))),
+    (compact, dict(nl_=at(0))), (compact, dict(nl_=at(4) + 8)), (compact, dict(path=at(1))), (compact, dict(pl=at(0), nl_=at(0))), (compact, dict(table=at(1) + 16))])
+def test_tables_lengths_and_workspaces_may_not_overlap_what_is_written(call, o):
+    assert call(**o) == ALIAS
+
+
 def test_the_binding_refuses_other_shapes_types_and_places():
     i32, bf = torch.int32, torch.bfloat16
     z = lambda *s, dt=bf: torch.zeros(*s, dtype=dt)  # noqa: E731
