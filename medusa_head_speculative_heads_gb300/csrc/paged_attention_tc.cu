@@ -180,6 +180,24 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
+// Every lane with `need` waits for a phase of a barrier of its own, all at once: a wait costs some
+// 200 clocks even when its phase is long over, and an issuing warp that made its five one after the
+// other came to the probabilities 500 clocks after they were there.
+__device__ __forceinline__ bool lanes_wait(uint64_t* bar, uint32_t parity, bool need, volatile int* abort) {
+  bool ok = !need;
+#pragma unroll 1
+  for (int n = kTries; n > 0; --n) {
+    if (!ok) ok = mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) {
+      __syncwarp();  // what one lane has seen to be there, all have
+      return true;
+    }
+    if ((n & 15) == 0 && __any_sync(0xffffffffu, *abort)) return false;
+  }
+  *abort = 1;
+  return false;
+}
+
 // All lanes, whose work so far the arrival of one of them announces.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
@@ -487,9 +505,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll 1
     for (int n = 0; (alive = read_unit(tail, n, x, &s_abort)) && x.t1 > 0; ++n) {
       const int qb = two(x) ? s : qsel, end = stream_end(x, s);
-      if (!(alive = warp_wait(&bars->q_full[qb], (qb ? qn1 : qn0) & 1, &s_abort))) break;
+      if (!(alive = lanes_wait(&bars->q_full[lane & 1], ((lane & 1) ? qn1 : qn0) & 1, two(x) ? lane < 2 : lane == qb, &s_abort))) break;
       if (two(x)) {  // the other stream's rows
-        if (!(alive = warp_wait(&bars->q_full[1 - qb], (qb ? qn0 : qn1) & 1, &s_abort))) break;
         if (lane == 0) mbar_arrive(&bars->q_empty[1 - qb]);
         __syncwarp();
       }
@@ -504,23 +521,16 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         else alone ^= 1u << sl;
         return ok;
       };
-      // What P V of tile t needs but P: O read out by the unit before, and V, its rows behind the last one zeros.
-      auto v_ready = [&](int t) {
-        const int cv = slot_v(t);
-        if (t == first && n > 0 && !warp_wait(&bars->o_free[s], (n - 1) & 1, &s_abort)) return false;
-        if (!came(cv)) return false;
-        const int steps = (tile_keys(a, x, s, t) + 15) >> 4, have = tile_rows_loaded(a, x, t);
-        if (have < steps * 16) {
-          uint8_t* vb = smem + C::off_ring + cv * C::slot;
+      // Rows of V behind the last one of tile t, up to what P V reads: zeros.
+      auto clear_rest = [&](int cv, int steps, int have) {
+        uint8_t* vb = smem + C::off_ring + cv * C::slot;
 #pragma unroll 1
-          for (int i = lane; i < (steps * 16 - have) * 8 * C::halves; i += 32) {
-            const int r = have + i / (8 * C::halves), cc = i % (8 * C::halves);
-            *reinterpret_cast<uint4*>(vb + (cc >> 3) * kHalf + r * 128 + (cc & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
+        for (int i = lane; i < (steps * 16 - have) * 8 * C::halves; i += 32) {
+          const int r = have + i / (8 * C::halves), cc = i % (8 * C::halves);
+          *reinterpret_cast<uint4*>(vb + (cc >> 3) * kHalf + r * 128 + (cc & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
-        return true;
+        fence_proxy_async_smem();
+        __syncwarp();
       };
       // Step by step: P V of tile t - step, then S of tile t, back to back.  Of a block of two row
       // tiles the streams take turns.  The tensor pipe takes products in the order of their issue:
@@ -530,9 +540,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll 1
       for (int t = first;; t += step) {
         const bool had = t > first && t - step < end, has = t < end;
-        if (had) {
-          if (!(alive = v_ready(t - step))) break;
-        } else if (two(x) && t > first) {  // a tile of the other stream's alone
+        if (!had && two(x) && t > first) {  // a tile of the other stream's alone
           if (!(alive = came(slot_k(t - 1)) && came(slot_v(t - 1)))) break;
           if (lane == 0) {
             mbar_arrive(&bars->empty[slot_k(t - 1)]);
@@ -540,23 +548,25 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           }
           __syncwarp();
         }
-        // Of one row tile the next K may still be far: P V does not wait for it.
-        bool k_came = false;
-        if (has && (two(x) || !had)) {
-          if (!(alive = came(slot_k(t)))) break;
-          k_came = true;
-        }
-        const int cv = slot_v(t - step), ck = slot_k(t), steps = had ? (tile_keys(a, x, s, t - step) + 15) >> 4 : 0;
+        // Lane 0: V; 1: K (of one row tile the next K may still be far, and P V does not wait for it);
+        // 2: the turn; 3: P; 4: O, read out by the unit before.
+        const int cv = slot_v(t - step), ck = slot_k(t);
+        const bool k_too = has && (two(x) || !had), turn = two(x) && (s || turns);
+        const uint32_t mine = two(x) ? shared : alone;
+        uint64_t* const rows = bars->full[two(x) ? 2 : s];
+        uint64_t* const bar = lane == 0 ? rows + cv : lane == 1 ? rows + ck : lane == 2 ? &bars->turn[s] : lane == 3 ? &bars->p_full[s] : &bars->o_free[s];
+        const uint32_t phase = lane == 0 ? mine >> cv : lane == 1 ? mine >> ck : lane == 2 ? turns - (s == 0) : lane == 3 ? np : n - 1;
+        const bool need = lane == 0 || lane == 3 ? had : lane == 1 ? k_too : lane == 2 ? turn : lane == 4 && had && t - step == first && n > 0;
+        const int steps = had ? (tile_keys(a, x, s, t - step) + 15) >> 4 : 0, have = had ? tile_rows_loaded(a, x, t - step) : 0;
         const uint32_t uv = uniform(smem_u32(smem + C::off_ring + cv * C::slot)), uk = uniform(smem_u32(smem + C::off_ring + ck * C::slot));
         const uint32_t uq = uniform(qa), ut = uniform(ts), uo = uniform(to);
-        if (two(x)) {  // before P, which comes last as a rule
-          if ((s || turns) && !(alive = warp_wait(&bars->turn[s], (turns - (s == 0)) & 1, &s_abort))) break;
-          ++turns;
-        }
-        if (had) {
-          if (!(alive = warp_wait(&bars->p_full[s], np & 1, &s_abort))) break;
-          ++np;
-        }
+        if (!(alive = lanes_wait(bar, phase & 1u, need, &s_abort))) break;
+        const uint32_t seen = (had ? 1u << cv : 0u) | (k_too ? 1u << ck : 0u);
+        if (two(x)) shared ^= seen;
+        else alone ^= seen;
+        turns += two(x);
+        np += had;
+        if (had && have < steps * 16) clear_rest(cv, steps, have);
         tc_fence_after();
         if (two(x)) {
           if (elect_one()) {
@@ -584,7 +594,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           }
           __syncwarp();
           if (!has) break;
-          if (!k_came) {
+          if (had) {
             if (!(alive = came(ck))) break;
             tc_fence_after();
           }
@@ -749,8 +759,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         ++nb;
       }
       if (two(x) || s == 0) {
-        if (!(alive = warp_wait(&bars->o_full[s], n & 1, &s_abort))) break;
-        if (!two(x) && !(alive = warp_wait(&bars->o_full[1], n & 1, &s_abort))) break;
+        // Of one row tile both streams' (stream 1's phases of units with two are over: ml_full comes later).
+        if (!(alive = lanes_wait(&bars->o_full[two(x) ? s : lane & 1], n & 1, lane < (two(x) ? 1 : 2), &s_abort))) break;
         if (busy) {
           tc_fence_after();
           const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
