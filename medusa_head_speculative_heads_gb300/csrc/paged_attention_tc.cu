@@ -63,7 +63,7 @@ struct Bars {
   // they need them or not.  Every slot and Q buffer is released twice.
   uint64_t full[3][kMaxSlots], empty[kMaxSlots];  // K's slots, then V's
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_full[2];
+  uint64_t s_full[2], p_half[2], p_full[2];    // P's first 64 columns, and the others
   uint64_t turn[2];                            // a stream may issue its products of the next tile
   uint64_t o_full[2], o_free[2], ml_full, drain[2];  // o_full, o_free: one phase a unit
   uint64_t u_full[kUnits], u_free[kUnits];
@@ -151,11 +151,12 @@ __device__ __forceinline__ void issue_scores(uint32_t ts, uint32_t qa, uint32_t 
     mma_bf16(ts, desc_of(q + off), desc_of(k + off), idesc, kk > 0);
   }
 }
-// The first `steps` 16-key steps; `add`: to what O holds.
+// 16-key steps of the first (H = 0) or second half of the keys, up to `steps`; `add`: to what O holds.
+template <int H>
 __device__ __forceinline__ void issue_sums(uint32_t to, uint32_t tp, uint32_t va, uint32_t idesc, int steps, bool add) {
   const uint32_t v = (va >> 4) | ((kHalf >> 4) << 16);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 4 * H; i < 4 * H + 4; ++i)
     if (i < steps) mma_bf16_ts(to, tp + 8 * i, desc_of(v + 128 * i), idesc, i > 0 || add);
 }
 
@@ -336,6 +337,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       mbar_init(&bars->q_empty[s], 2);
       mbar_init(&bars->s_full[s], 1);
       mbar_init(&bars->turn[s], 1);
+      mbar_init(&bars->p_half[s], 4);
       mbar_init(&bars->p_full[s], 4);
       mbar_init(&bars->o_full[s], 1);
       mbar_init(&bars->o_free[s], 4);
@@ -549,12 +551,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           __syncwarp();
         }
         // Lane 0: V; 1: K (of one row tile the next K may still be far, and P V does not wait for it);
-        // 2: the turn; 3: P; 4: O, read out by the unit before.
+        // 2: the turn; 3: P's first half; 4: O, read out by the unit before.
         const int cv = slot_v(t - step), ck = slot_k(t);
         const bool k_too = has && (two(x) || !had), turn = two(x) && (s || turns);
         const uint32_t mine = two(x) ? shared : alone;
         uint64_t* const rows = bars->full[two(x) ? 2 : s];
-        uint64_t* const bar = lane == 0 ? rows + cv : lane == 1 ? rows + ck : lane == 2 ? &bars->turn[s] : lane == 3 ? &bars->p_full[s] : &bars->o_free[s];
+        uint64_t* const bar = lane == 0 ? rows + cv : lane == 1 ? rows + ck : lane == 2 ? &bars->turn[s] : lane == 3 ? &bars->p_half[s] : &bars->o_free[s];
         const uint32_t phase = lane == 0 ? mine >> cv : lane == 1 ? mine >> ck : lane == 2 ? turns - (s == 0) : lane == 3 ? np : n - 1;
         const bool need = lane == 0 || lane == 3 ? had : lane == 1 ? k_too : lane == 2 ? turn : lane == 4 && had && t - step == first && n > 0;
         const int steps = had ? (tile_keys(a, x, s, t - step) + 15) >> 4 : 0, have = had ? tile_rows_loaded(a, x, t - step) : 0;
@@ -565,12 +567,18 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (two(x)) shared ^= seen;
         else alone ^= seen;
         turns += two(x);
-        np += had;
-        if (had && have < steps * 16) clear_rest(cv, steps, have);
+        if (had) {
+          if (have < steps * 16) clear_rest(cv, steps, have);
+          tc_fence_after();
+          if (elect_one()) issue_sums<0>(uo, ut, uv, C::idesc_pv, steps, t - step > first);
+          __syncwarp();
+          if (!(alive = warp_wait(&bars->p_full[s], np & 1, &s_abort))) break;
+          ++np;
+        }
         tc_fence_after();
         if (two(x)) {
           if (elect_one()) {
-            if (had) issue_sums(uo, ut, uv, C::idesc_pv, steps, t - step > first);
+            if (had) issue_sums<1>(uo, ut, uv, C::idesc_pv, steps, true);
             if (has) issue_scores<DH, 0>(ut, uq, uk, C::idesc_qk);
             mbar_arrive(&bars->turn[1 - s]);
             if (has) {
@@ -587,7 +595,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           if (t == x.t1) break;
         } else {
           if (had && elect_one()) {
-            issue_sums(uo, ut, uv, C::idesc_pv, steps, t - step > first);
+            issue_sums<1>(uo, ut, uv, C::idesc_pv, steps, true);
             if (!has) mma_commit(&bars->o_full[s]);
             mma_commit(&bars->empty[cv]);
             mma_commit(&bars->empty[cv]);
@@ -659,6 +667,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const bool tree = t >= x.pre, masked = tree || keys < kKeys || t * kKeys + kKeys > all_see;
         if (!(alive = warp_wait(&bars->s_full[s], ns & 1, &s_abort))) break;
         if (!busy) {
+          warp_arrive(&bars->p_half[s]);
           warp_arrive(&bars->p_full[s]);
           continue;
         }
@@ -714,18 +723,24 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             pk[i] = bf16x2_rn(e0, e1);
           }
           tmem_st16u(ts + 16 * q, pk);
-        }
-        if (t > first && __any_sync(0xffffffffu, need)) {
-          sum *= f;
+          if (q == 1) {
+            if (t > first && __any_sync(0xffffffffu, need)) {
+              sum *= f;
 #pragma unroll 1
-          for (int q = 0; q < DH / 32; ++q) {
-            float o[32];
-            __syncwarp();
-            tmem_ld32(to + 128 * s + 32 * q, o);
-            tmem_wait_ld();
+              for (int q = 0; q < DH / 32; ++q) {
+                float o[32];
+                __syncwarp();
+                tmem_ld32(to + 128 * s + 32 * q, o);
+                tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= f;
-            tmem_st32(to + 128 * s + 32 * q, o);
+                for (int i = 0; i < 32; ++i) o[i] *= f;
+                tmem_st32(to + 128 * s + 32 * q, o);
+              }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(&bars->p_half[s]);
+            __syncwarp();
           }
         }
         tmem_wait_st();
