@@ -181,14 +181,27 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Every lane with `need` waits for a phase of a barrier of its own, all at once: a wait costs some
 // 200 clocks even when its phase is long over, and an issuing warp that made its five one after the
-// other came to the probabilities 500 clocks after they were there.
+// other came to the probabilities 500 clocks after they were there.  The lanes ask again and again
+// (40 clocks or more a time: over a second in all) and do not sleep on a barrier, which woke them
+// some 100 clocks late; for the eight softmax warps that would take issue slots from one another
+// (8192 tokens over 8192 rows: 1051 us so, with sleeping waits 1079, with all waits so 1094).
 __device__ __forceinline__ bool lanes_wait(uint64_t* bar, uint32_t parity, bool need, volatile int* abort) {
   bool ok = !need;
 #pragma unroll 1
-  for (int n = kTries; n > 0; --n) {
-    if (!ok) ok = mbar_try_wait(bar, parity);
+  for (int n = 8 * kTries; n > 0; --n) {
+    if (!ok) ok = mbar_test_wait(bar, parity);
     if (__all_sync(0xffffffffu, ok)) {
       __syncwarp();  // what one lane has seen to be there, all have
       return true;
@@ -572,7 +585,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           tc_fence_after();
           if (elect_one()) issue_sums<0>(uo, ut, uv, C::idesc_pv, steps, t - step > first);
           __syncwarp();
-          if (!(alive = warp_wait(&bars->p_full[s], np & 1, &s_abort))) break;
+          if (!(alive = lanes_wait(&bars->p_full[s], np & 1, true, &s_abort))) break;
           ++np;
         }
         tc_fence_after();
