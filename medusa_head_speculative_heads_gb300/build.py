@@ -3,6 +3,9 @@
 Each translation unit is compiled in parallel to an object file, then linked
 into one shared library with the CUDA runtime linked statically, so the library
 loads on a machine without a GPU (entry points then return MEDUSA_ERR_CUDA).
+
+Where torch is installed, the compiled binding of the paged-cache calls
+(csrc/python) is built beside it, against that torch's headers.
 """
 from __future__ import annotations
 
@@ -11,6 +14,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -37,15 +41,47 @@ def _deps() -> list:
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+def _newer(target: str, deps: list) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in deps)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _newer(LIB, _deps())
+
+
+def binding_path() -> str:
+    """The compiled binding for the installed torch."""
+    import torch
+    return os.path.join(BUILD, f"paged_binding-{torch.__version__}.so")
+
+
+def build_binding(force: bool = False) -> None:
+    """Compiles csrc/python against the installed torch (nothing without one) and
+    links it to the library, which lies beside it."""
+    try:
+        import torch
+    except ImportError:
+        return
+    src, out = os.path.join(CSRC, "python", "paged_binding.cpp"), binding_path()
+    if not force and _newer(out, [src, os.path.join(INCLUDE, "medusa.h")]):
+        return
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = out + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", src, "-o", tmp]
+    for d in (INCLUDE, f"{t}/include", f"{t}/include/torch/csrc/api/include", f"{cuda}/include", sysconfig.get_paths()["include"]):
+        cmd += ["-I", d]
+    cmd += [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-L{t}/lib", "-ltorch_python", "-ltorch_cpu",
+            "-lc10_cuda", "-lc10", f"-L{BUILD}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the binding does not build:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list | None = None) -> str:
     if not force and up_to_date():
+        build_binding()
         return LIB
     os.makedirs(os.path.join(BUILD, "obj"), exist_ok=True)
     cc = nvcc()
@@ -71,6 +107,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list | None =
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    build_binding(force)
     return LIB
 
 
