@@ -135,16 +135,17 @@ __device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, lon
     }
     inc = v;
 #pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
+    for (int o = 1; o < 32 && o < w.B; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
     __syncthreads();  // the round before is read
-    if (lane == 31) sh[wp] = inc;
+    if (lane == min(31, w.B - 1)) sh[wp] = inc;  // fewer than 32 sequences: lanes behind them hold no sums
     __syncthreads();
     before = total = 0;
+    const int busy = min(nw, (w.B - k * nt + 31) >> 5);  // warps that have sequences
 #pragma unroll 1
-    for (int j = 0; j < nw; ++j) {
+    for (int j = 0; j < busy; ++j) {
       const long long y = sh[j];
       if (j < wp) before += y;
       total += y;

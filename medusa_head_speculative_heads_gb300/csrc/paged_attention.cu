@@ -511,6 +511,8 @@ static medusa_status attend(AttnArgs& a, int n_layers, int T, int B, int Hq, int
   a.w.T = T;
   const medusa_status st = v.tc ? paged_attention_tc(a, s) : dt == MEDUSA_BF16 ? simt_launch<uint16_t>(a, s) : simt_launch<float>(a, s);
   if (st != MEDUSA_OK) return st;
+  // Sequences that can hold one tile of keys at most leave no item to share (2 to 3 us of a call's 10 to 13).
+  if (!a.w.N && a.w.cap <= v.KT) return launch_status();
   if (v.R > 64) launch_pdl(paged_attn_merge_wide_kernel, dim3(v.ctas - 1, v.R / 32), dim3(256), 0, s, a);
   else if (dt == MEDUSA_BF16) launch_pdl(paged_attn_merge_kernel<uint16_t>, dim3(v.ctas - 1, v.R / 8), dim3(256), 0, s, a);
   else launch_pdl(paged_attn_merge_kernel<float>, dim3(v.ctas - 1, v.R / 8), dim3(256), 0, s, a);

@@ -198,6 +198,10 @@ MIXED = [
     # many single tokens and one chunk (blocks of 64 rows), one long chunk and a few single tokens (of 256)
     dict(dtype="bf16", nl=1, hq=8, hkv=2, d=128, page=16, B=40, prefix=400, chunk=lambda r, b: 90 if b == 17 else 1),
     dict(dtype="bf16", nl=1, hq=8, hkv=8, d=128, page=64, B=6, prefix=260, chunk=lambda r, b: [1, 300, 0, 1, 5, 129][b]),
+    # sequences that hold one tile of keys at most, and just more
+    dict(dtype="bf16", nl=2, hq=8, hkv=2, d=64, page=64, B=70, prefix=60, chunk=lambda r, b: int(r.integers(1, 60)), cap=128),
+    dict(dtype="f32", nl=1, hq=8, hkv=2, d=64, page=16, B=30, prefix=40, chunk=lambda r, b: int(r.integers(0, 25)), cap=64),
+    dict(dtype="bf16", nl=1, hq=4, hkv=2, d=128, page=8, B=30, prefix=70, chunk=lambda r, b: int(r.integers(0, 60)), cap=136),
     # many blocks a CTA, and one sequence's rows over every CTA
     dict(dtype="bf16", nl=12, hq=16, hkv=4, d=64, page=8, B=9, prefix=130, chunk=lambda r, b: int(r.integers(1, 60))),
     dict(dtype="bf16", nl=1, hq=20, hkv=1, d=104, page=32, B=1, prefix=9000, chunk=lambda r, b: 14),
@@ -205,7 +209,7 @@ MIXED = [
 ]
 
 
-@pytest.mark.parametrize("c", MIXED, ids=lambda c: f"{c['dtype']}-{c['hq']}-{c['hkv']}-d{c['d']}-B{c['B']}")
+@pytest.mark.parametrize("c", MIXED, ids=lambda c: f"{c['dtype']}-{c['hq']}-{c['hkv']}-d{c['d']}-B{c['B']}-{c['prefix']}")
 def test_many_and_mixed_sequences(mg, c):
     rng = np.random.default_rng(c["B"] + c["d"])
     prefix = rng.integers(0, c["prefix"] + 1, c["B"]).tolist()
@@ -213,6 +217,9 @@ def test_many_and_mixed_sequences(mg, c):
         prefix = [c["prefix"]]
     chunk = [c["chunk"](rng, b) for b in range(c["B"])]
     kp, vp, table = pool(rng, [p + n for p, n in zip(prefix, chunk)], nl=c["nl"], page=c["page"], hkv=c["hkv"], d=c["d"], dtype=c["dtype"])
+    if "cap" in c:  # the table is as wide as `cap` rows need
+        assert table.shape[1] * c["page"] <= c["cap"]
+        table = np.pad(table, ((0, 0), (0, c["cap"] // c["page"] - table.shape[1])), constant_values=-1)
     q0 = starts(chunk)
     q = values(rng, (c["nl"], int(q0[-1]), c["hq"], c["d"]), c["dtype"])
     want = ref.paged_attention(q, kp, vp, table, q0, prefix)
