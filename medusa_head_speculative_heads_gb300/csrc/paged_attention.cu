@@ -47,8 +47,8 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v) {
 // Shared memory's pipe bounds it, busy for 64 % of the clocks (the FMA pipe for 47 %): a
 // 16-byte load takes four of them when lanes read several rows and two as a broadcast,
 // 24 for the 64 products of four columns.  A warp of 8 rows x 64 keys, each K row
-// read once and Q as broadcasts, takes as many and measured 101 us; fewer would need
-// more scores a thread than two CTAs' registers hold.
+// read once and Q as broadcasts, takes as many and measured 101 us; 128 threads with 8 x
+// 4 scores each take 16 and measured 98 to 101 (too few warps, or registers spilled).
 template <int DC>
 __host__ __device__ constexpr int simt_pitch() { return 16 * DC + 4; }
 template <typename T, int DC, int RM>
