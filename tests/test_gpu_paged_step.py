@@ -325,3 +325,45 @@ def test_a_step_refuses_what_does_not_fit(mg):
     vs = paged_step(mg, c, inp, np.zeros((B, 40), np.int32), 16)
     with pytest.raises(ValueError, match="RopeSpec"):
         vs.rope(to_dev(inp["q"]), to_dev(inp["kt"]))
+
+
+def test_the_binding_refuses_tensors_that_do_not_fit(mg):
+    """Types, shapes, strides and places, each named in the error; what is not refused runs."""
+    i32, bf, f32 = torch.int32, torch.bfloat16, torch.float32
+    z = lambda *s, dt=bf, dev="cuda": torch.zeros(s, dtype=dt, device=dev)  # noqa: E731
+    attn = dict(q=z(2, 5, 4, 64), k_pages=z(2, 6, 16, 2, 64), v_pages=z(2, 6, 16, 2, 64), page_table=z(2, 3, dt=i32), q_start=dev_ints([0, 2, 5]), prefix_len=dev_ints([0, 4]))
+    tree = dict(q=z(2, 2, 3, 4, 64), k_pages=attn["k_pages"], v_pages=attn["v_pages"], page_table=attn["page_table"], kt=z(2, 2, 3, 2, 64), vt=z(2, 2, 3, 2, 64),
+                mask=z(3, 1, dt=i32), prefix_len=attn["prefix_len"])
+    entry = dict(k=z(2, 5, 2, 64), v=z(2, 5, 2, 64), k_pages=attn["k_pages"], v_pages=attn["v_pages"], page_table=attn["page_table"], q_start=attn["q_start"],
+                 prefix_len=attn["prefix_len"])
+    pack = dict(k_pages=attn["k_pages"], v_pages=attn["v_pages"], page_table=attn["page_table"], kt=tree["kt"], vt=tree["vt"], path_nodes=z(2, 3, dt=i32),
+                accept_len=dev_ints([1, 2]), prefix_len=attn["prefix_len"])
+    turn = dict(q=z(2, 5, 4, 64), k=z(2, 5, 2, 64), pos=z(5, dt=i32), rope=mg.RopeSpec(64))
+    calls = {mg.medusa_paged_attention: attn, mg.medusa_paged_tree_attention: tree, mg.medusa_paged_append: entry, mg.medusa_paged_compact: pack, mg.medusa_rope: turn}
+    for call, args in calls.items():
+        call(**args)
+    bad = [(mg.medusa_paged_attention, dict(q=z(2, 5, 4, 64, dt=f32)), "k_pages"), (mg.medusa_paged_attention, dict(q=z(1, 5, 4, 64)), "q"),
+           (mg.medusa_paged_attention, dict(v_pages=z(2, 6, 16, 2, 32)), "v_pages"), (mg.medusa_paged_attention, dict(k_pages=z(2, 6, 16, 64)), "k_pages"),
+           (mg.medusa_paged_attention, dict(k_pages=z(2, 6, 16, 4, 64)[:, :, :, :2]), "k_pages"), (mg.medusa_paged_attention, dict(page_table=z(2, 3, dt=torch.int64)), "page_table"),
+           (mg.medusa_paged_attention, dict(page_table=z(2, 3, dt=i32, dev="cpu")), "page_table"), (mg.medusa_paged_attention, dict(q_start=dev_ints([0, 5])), "q_start"),
+           (mg.medusa_paged_attention, dict(prefix_len=dev_ints([0, 1, 2])), "prefix_len"), (mg.medusa_paged_attention, dict(out=z(2, 5, 4, 64, dt=f32)), "out"),
+           (mg.medusa_paged_attention, dict(lse=z(2, 5, 4)), "lse"), (mg.medusa_paged_attention, dict(ws=z(8, dt=torch.uint8)), "workspace"),
+           (mg.medusa_paged_attention, dict(d_status=z(1)), "d_status"), (mg.medusa_paged_attention, dict(q=z(2, 4, 5, 64).transpose(1, 2)), "q"),
+           (mg.medusa_paged_tree_attention, dict(q=z(2, 2, 3, 64)), "q"), (mg.medusa_paged_tree_attention, dict(kt=z(2, 2, 4, 2, 64)), "kt"),
+           (mg.medusa_paged_tree_attention, dict(mask=z(3, 2, dt=i32)), "mask"), (mg.medusa_paged_append, dict(v=z(2, 4, 2, 64)), "v"),
+           (mg.medusa_paged_append, dict(q_out=z(2, 5, 4, 64)), "q_out"), (mg.medusa_paged_append, dict(pos=z(4, dt=i32)), "pos"), (mg.medusa_paged_append, dict(q=z(2, 5, 4, 32)), "q"),
+           (mg.medusa_paged_compact, dict(path_nodes=z(3, 3, dt=i32)), "path_nodes"), (mg.medusa_paged_compact, dict(new_len=z(2)), "new_len"),
+           (mg.medusa_paged_compact, dict(vt=z(2, 2, 3, 2, 64, dt=f32)), "vt"), (mg.medusa_rope, dict(k=None, k_out=z(2, 5, 2, 64)), "k_out"),
+           (mg.medusa_rope, dict(pos=z(5)), "pos"), (mg.medusa_rope, dict(q_out=z(2, 5, 6, 64)[:, :, :4]), "q_out"), (mg.medusa_rope, dict(k=z(2, 6, 2, 64)), "k")]
+    for call, change, name in bad:
+        with pytest.raises(ValueError, match=f"{call.__name__}.*{name}"):
+            call(**{**calls[call], **change})
+    with pytest.raises(TypeError, match="float16"):
+        mg.medusa_paged_attention(**{**attn, "q": z(2, 5, 4, 64, dt=torch.float16)})
+    with pytest.raises(TypeError, match="prefix_len"):
+        mg.medusa_paged_attention(**{**attn, "prefix_len": [0, 4]})
+    with pytest.raises(mg.MedusaError):  # the library's own: 3 q heads over 2 kv heads
+        mg.medusa_paged_attention(**{**attn, "q": z(2, 5, 3, 64)})
+    with pytest.raises(mg.MedusaError):  # and no tokens
+        mg.medusa_paged_attention(**{**attn, "k_pages": z(1, 6, 16, 2, 64), "v_pages": z(1, 6, 16, 2, 64), "q": z(1, 0, 4, 64)})
+    torch.cuda.synchronize()
