@@ -505,17 +505,22 @@ static medusa_status attend(AttnArgs& a, int n_layers, int T, int B, int Hq, int
   a.w.KT = v.KT;
   a.w.ctok_log2 = log2_of(v.ctok);
   a.w.KT_log2 = log2_of(v.KT);
-  a.w.ctas = v.ctas;
-  a.w.ctas_inv = ~0ull / v.ctas + 1;
+  // No more CTAs than there can be tiles (but two, for the reciprocal): idle ones delay a small call
+  // (3 heads x 10 nodes of 4 sequences 12.7 us, on all SMs 14.1; fp32, 21 short sequences 9.0 and 11.7).
+  const long long blocks = a.w.N ? (long long)B * ((a.w.N + v.ctok - 1) / v.ctok) : B + T / v.ctok;
+  const long long tiles = (a.w.cap + v.KT - 1) / v.KT + (a.w.N + v.KT - 1) / v.KT;
+  const double most = (double)a.w.nl * a.w.nh * blocks * tiles;
+  a.w.ctas = most >= v.ctas ? v.ctas : most <= 2 ? 2 : (int)most;
+  a.w.ctas_inv = ~0ull / a.w.ctas + 1;
   a.w.B = B;
   a.w.T = T;
   const medusa_status st = v.tc ? paged_attention_tc(a, s) : dt == MEDUSA_BF16 ? simt_launch<uint16_t>(a, s) : simt_launch<float>(a, s);
   if (st != MEDUSA_OK) return st;
   // Sequences that can hold one tile of keys at most leave no item to share (2 to 3 us of a call's 10 to 13).
   if (!a.w.N && a.w.cap <= v.KT) return launch_status();
-  if (v.R > 64) launch_pdl(paged_attn_merge_wide_kernel, dim3(v.ctas - 1, v.R / 32), dim3(256), 0, s, a);
-  else if (dt == MEDUSA_BF16) launch_pdl(paged_attn_merge_kernel<uint16_t>, dim3(v.ctas - 1, v.R / 8), dim3(256), 0, s, a);
-  else launch_pdl(paged_attn_merge_kernel<float>, dim3(v.ctas - 1, v.R / 8), dim3(256), 0, s, a);
+  if (v.R > 64) launch_pdl(paged_attn_merge_wide_kernel, dim3(a.w.ctas - 1, v.R / 32), dim3(256), 0, s, a);
+  else if (dt == MEDUSA_BF16) launch_pdl(paged_attn_merge_kernel<uint16_t>, dim3(a.w.ctas - 1, v.R / 8), dim3(256), 0, s, a);
+  else launch_pdl(paged_attn_merge_kernel<float>, dim3(a.w.ctas - 1, v.R / 8), dim3(256), 0, s, a);
   return launch_status();
 }
 
