@@ -19,7 +19,8 @@
 // their way.  Measured, 10782 prompt tokens with 32 + 8 + 8 heads entered into
 // the cache: 44 us (6.0 TB/s); with 256 threads 56 us, with two, three or four
 // tasks in flight 49 to 52 us, with the next task's loads ahead of the turn 48 us
-// (registers: fewer CTAs on an SM).  32 layers of 64 tokens with 32 + 32 heads: 13.5
+// (registers: fewer CTAs on an SM), with a thread's angles kept in registers over its
+// heads 51 us (the same).  32 layers of 64 tokens with 32 + 32 heads: 13.5
 // us; 16384 fp32 tokens with 32 + 8 heads: 99 us (6.8 TB/s).
 #include <cmath>
 
