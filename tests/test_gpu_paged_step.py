@@ -367,3 +367,44 @@ def test_the_binding_refuses_tensors_that_do_not_fit(mg):
     with pytest.raises(mg.MedusaError):  # and no tokens
         mg.medusa_paged_attention(**{**attn, "k_pages": z(1, 6, 16, 2, 64), "v_pages": z(1, 6, 16, 2, 64), "q": z(1, 0, 4, 64)})
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype,nl,hkv,d", [("bf16", 1, 64, 128), ("f32", 1, 64, 128), ("bf16", 3, 24, 128), ("bf16", 1, 40, 256)])
+def test_pools_whose_offsets_pass_32_bits(mg, dtype, nl, hkv, d):
+    """The same calls on a small pool and on one of 2.6e9 elements with the pages at its end
+    (the second layer of three passes 2^31 by itself): the same bits."""
+    rng = np.random.default_rng(hkv)
+    tt, page, B, G, N = (torch.bfloat16 if dtype == "bf16" else torch.float32), 16, 2, 2, 9
+    if torch.cuda.mem_get_info()[0] < 40e9:
+        pytest.skip("two pools of up to 10 GB")
+    big_pages = int(2.6e9) // (nl * page * hkv * d)
+    assert nl * big_pages * page * hkv * d > 2 ** 31
+    few = 10
+    small_table = rng.permutation(few).reshape(B, few // B).astype(np.int32)
+    big_table = small_table + np.int32(big_pages - few)
+    prefix, chunk = [0, 33], [37, 3]
+    q0 = starts(chunk)
+    T = int(q0[-1])
+    q, k, v = (to_dev(values(rng, (nl, T, h, d), dtype)) for h in (G * hkv, hkv, hkv))
+    kt, vt, tq = (to_dev(values(rng, (nl, B, N, h, d), dtype)) for h in (hkv, hkv, G * hkv))
+    mask = dev_ints(np.array([[(2 << i) - 1] for i in range(N)]))
+    first = [to_dev(values(rng, (nl, few, page, hkv, d), dtype)) for _ in range(2)]
+    spec = mg.RopeSpec(d)
+    results = []
+    for n_pages, table in ((few, small_table), (big_pages, big_table)):
+        pools = [torch.empty((nl, n_pages, page, hkv, d), dtype=tt, device="cuda") for _ in range(2)]
+        for p, f in zip(pools, first):
+            p[:, n_pages - few:] = f
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        tab, lens = dev_ints(table), dev_ints(prefix)
+        turned = mg.medusa_paged_append(k, v, *pools, tab, dev_ints(q0), lens, q=q, rope=spec, d_status=st)
+        out, lse = mg.medusa_paged_attention(turned, *pools, tab, dev_ints(q0), lens, want_lse=True, d_status=st)
+        held = dev_ints(np.add(prefix, chunk))
+        tree, tree_lse = mg.medusa_paged_tree_attention(tq, *pools, tab, kt, vt, mask, held, want_lse=True, d_status=st)
+        new = mg.medusa_paged_compact(*pools, tab, kt, vt, dev_ints([[0, 2, 5], [0, 1, 8]]), dev_ints([3, 2]), held, d_status=st)
+        assert mg.medusa_status_check(st) == 0
+        results.append([turned, out, lse, tree, tree_lse, new] + [p[:, n_pages - few:].clone() for p in pools])
+        del pools
+        torch.cuda.empty_cache()
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
