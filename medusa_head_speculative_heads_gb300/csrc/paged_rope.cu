@@ -24,6 +24,7 @@
 // us; 16384 fp32 tokens with 32 + 8 heads: 99 us (6.8 TB/s).
 #include <cmath>
 
+#include "divide.h"
 #include "host_util.h"
 #include "paged.cuh"
 
@@ -43,7 +44,8 @@ struct RopeArgs {
   Cache cache;
   int nl, T, B, Hq, Hkv, d, rotary, inverse;
   int tokens;  // per CTA
-  unsigned per_tok_inv, per_head_inv;  // floor(2^32 / n) + 1: the high word of a product divides by n
+  unsigned per_tok_inv;   // the reciprocal of a token's tasks; 0 where a CTA has one token
+  unsigned per_head_inv;  // floor(2^32 / n) + 1: the high word of a product divides by n > 1
   float magnitude;
   unsigned long long turn[MEDUSA_MAX_HEAD_DIM / 2];
 };
@@ -140,7 +142,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   };
   auto find = [&](unsigned id) {
     Task t;
-    t.tok = a.tokens == 1 ? 0u : __umulhi(id, a.per_tok_inv);
+    t.tok = quotient(id, a.per_tok_inv);
     const unsigned r = id - t.tok * per_tok;
     t.head = per_head == 1 ? r : __umulhi(r, a.per_head_inv);
     t.c = r - t.head * per_head;
@@ -286,11 +288,11 @@ static medusa_status rope_launch(RopeArgs& a, const medusa_rope_plan* plan, medu
   const long long spread = all / (2 * device_sm_count());
   if (n > spread) n = spread;
   a.tokens = n < 1 ? 1 : n > kRopeMaxTokens ? kRopeMaxTokens : (int)n;
-  // Exact: with several tokens there are at most kRopeThreads tasks, and a vector's
-  // number within its token times the vectors of a head stays below 2^32 (3 x 65535
-  // heads of at most 128 vectors).
+  // Exact: with several tokens there are at most kRopeThreads tasks, of one or more to a
+  // token; a vector's number within its token times the vectors of a head stays below 2^32
+  // (3 x 65535 heads of at most 128 vectors).
   const unsigned per_head = (unsigned)(a.d / (2 * w));
-  a.per_tok_inv = (unsigned)((1ull << 32) / (unsigned long long)per_tok) + 1;
+  a.per_tok_inv = a.tokens == 1 ? 0u : reciprocal((unsigned)per_tok);
   a.per_head_inv = (unsigned)((1ull << 32) / per_head) + 1;
   const unsigned grid = (unsigned)((all + a.tokens - 1) / a.tokens);
   const bool inter = plan && plan->interleaved;
