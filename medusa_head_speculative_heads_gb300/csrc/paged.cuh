@@ -22,6 +22,18 @@ __device__ __forceinline__ int pool_row(const Cache& c, int b, int r) {
   return id >= 0 && id < c.n_pages ? id * c.page_size + (r - pg * c.page_size) : -1;
 }
 
+// Whether a sequence with tokens [q0, q1) has one that an earlier sequence's starts hold too,
+// which takes starts that decrease somewhere between them.  The token is the first one's, and
+// the later sequence as bad as the one whose own starts decrease.
+__device__ __forceinline__ bool shares_tokens(const int32_t* q_start, int T, int b, int q0, int q1) {
+#pragma unroll 1
+  for (int j = 0; j < b; ++j) {
+    const int a = q_start[j], e = q_start[j + 1];
+    if (a >= 0 && a < e && e <= T && a < q1 && q0 < e) return true;
+  }
+  return false;
+}
+
 // ------------------------------------------------------------------ attention work
 //
 // An item is (layer, head group, sequence, block of `ctok` tokens); its cost is
@@ -60,6 +72,11 @@ __device__ __forceinline__ Seq seq_of(const Work& w, int b) {
     s.len = s.ok ? w.N : 0;
   }
   return s;
+}
+
+// Some sequence is bad: s is left out where it shares tokens with one before it.
+__device__ __forceinline__ void leave_shared_out(const Work& w, int b, Seq& s) {
+  if (w.q_start && s.len > 0 && shares_tokens(w.q_start, w.T, b, s.q0, s.q0 + s.len)) s.len = 0;
 }
 
 __device__ __forceinline__ int n_blocks(const Work& w, const Seq& s) { return (s.len + w.ctok - 1) >> w.ctok_log2; }
@@ -118,6 +135,7 @@ struct Item {
 // fetched cold.
 struct Plan {
   long long per, U, Q;  // tiles per layer-head, in all, per CTA
+  bool odd;             // some sequence is bad
 };
 
 __device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, long long* sh, int cta) {
@@ -125,31 +143,39 @@ __device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, lon
   const int rounds = (w.B + nt - 1) / nt;
   Seq s{};
   long long v = 0, inc = 0, before = 0, total = 0;
+  pl.odd = false;
   // This thread's sequence of a round, and the tiles of the round's sequences up to it and in all.
+  // Whether one is bad comes with a warp's sum, at no cost where none is; then the round is made
+  // again, and from there on sequences that share tokens are left out.
   auto round = [&](int k) {
     const int b = k * nt + tid;
-    v = 0;
-    if (b < w.B) {
-      s = seq_of(w, b);
-      v = seq_tiles(w, s);
-    }
-    inc = v;
+    bool again;
 #pragma unroll 1
-    for (int o = 1; o < 32 && o < w.B; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    __syncthreads();  // the round before is read
-    if (lane == min(31, w.B - 1)) sh[wp] = inc;  // fewer than 32 sequences: lanes behind them hold no sums
-    __syncthreads();
-    before = total = 0;
-    const int busy = min(nw, (w.B - k * nt + 31) >> 5);  // warps that have sequences
+    do {
+      s = b < w.B ? seq_of(w, b) : Seq{0, 0, 0, true};
+      if (pl.odd) leave_shared_out(w, b, s);
+      v = inc = seq_tiles(w, s);
 #pragma unroll 1
-    for (int j = 0; j < busy; ++j) {
-      const long long y = sh[j];
-      if (j < wp) before += y;
-      total += y;
-    }
+      for (int o = 1; o < 32 && o < w.B; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const bool bad = __any_sync(0xffffffffu, !s.ok) && !pl.odd;
+      __syncthreads();  // the round before is read
+      if (lane == min(31, w.B - 1)) sh[wp] = bad ? -1 : inc;  // fewer than 32 sequences: lanes behind them hold no sums
+      __syncthreads();
+      before = total = 0;
+      again = false;
+      const int busy = min(nw, (w.B - k * nt + 31) >> 5);  // warps that have sequences
+#pragma unroll 1
+      for (int j = 0; j < busy; ++j) {
+        const long long y = sh[j];
+        again |= y < 0;
+        if (j < wp) before += y;
+        total += y;
+      }
+      pl.odd |= again;
+    } while (again);
   };
   // First the sums of all rounds, then, the last round first being the one in hand, the search.
   long long per = 0, u = -1, off = 0, base = 0;
@@ -174,6 +200,7 @@ __device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, lon
       off = u - lg * per;
       continue;
     }
+    if (tid == 0) sh[63] = pl.odd;
     const long long lo = base + before + inc - v;
     if (v > 0 && off >= lo && off < lo + v) {  // one thread
       int i0 = 0, i1 = n_blocks(w, s);
@@ -203,8 +230,8 @@ __device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, lon
   return true;
 }
 
-// The next item in order; false behind the last one.
-__device__ __forceinline__ bool next_item(const Work& w, Item& it) {
+// The next item in order (`odd`: the plan's); false behind the last one.
+__device__ __forceinline__ bool next_item(const Work& w, bool odd, Item& it) {
   it.first += it.tiles;
   ++it.i;
 #pragma unroll 1
@@ -215,6 +242,7 @@ __device__ __forceinline__ bool next_item(const Work& w, Item& it) {
       if (++it.lg == w.nl * w.nh) return false;
     }
     it.s = seq_of(w, it.b);
+    if (odd) leave_shared_out(w, it.b, it.s);
   }
   it.tiles = block_tiles(w, it.s, it.i);
   return true;

@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kSimtThreads, simt_ctas(DC, RM)) paged_attn_si
       }
     }
     u = end;
-    if (u < u1 && !next_item(a.w, it)) break;
+    if (u < u1 && !next_item(a.w, sh[63] != 0, it)) break;
   }
 }
 

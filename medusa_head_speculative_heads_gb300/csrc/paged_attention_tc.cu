@@ -424,7 +424,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         y = unit_of(a, it, t0, left);
         left -= y.t1 - y.t0;
         t0 = 0;
-        if (left > 0 && !next_item(a.w, it)) left = 0;
+        if (left > 0 && !next_item(a.w, pl.odd, it)) left = 0;
       }
       if (lane == 0) {
         tail->units[k] = y;

@@ -117,8 +117,10 @@ __device__ __forceinline__ float2 turn_of(int p, unsigned long long turn, int in
   return make_float2(cc * m, ss * m);
 }
 
+// Sixteen CTAs an SM (32 registers, none spilled): with 40, which the look for a token's sequence
+// would take, the prompts' 44 us are 48.
 template <typename T, int W, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 16) rope_kernel(const __grid_constant__ RopeArgs a) {
   using C = Chunk<T, W>;
   // Angle e of the W that vector c needs lies at (e / 2, c, e % 2): lanes with
   // neighbouring vectors then read neighbouring words.
@@ -168,27 +170,33 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   if (threadIdx.x < tasks) load(threadIdx.x);  // in flight while the angles are formed
 
   if (a.k_pages) {
-    // Token tok: its sequence is the number of starts q_start[1 .. B] at or before it.
+    // Token tok's sequence is the first whose starts hold it.
     for (int tk = warp; tk < n_tok; tk += kRopeThreads / 32) {
       const int t = (int)((tok0 + tk) % a.T);
-      int b = 0;
-      for (int j = lane; j < a.B; j += 32) b += __ldg(a.q_start + 1 + j) <= t;
-      b = __reduce_add_sync(0xffffffffu, b);
+      int b = a.B;
+      bool odd = false;  // some starts decrease or lie outside the tokens
+#pragma unroll 1
+      for (int j = lane; j < a.B; j += 32) {
+        const int q0 = __ldg(a.q_start + j), q1 = __ldg(a.q_start + j + 1);
+        if (q0 < 0 || q1 < q0 || q1 > a.T) odd = true;
+        else if (q0 <= t && t < q1) b = min(b, j);
+      }
+      b = __reduce_min_sync(0xffffffffu, b);
       int slot = -2, p = 0;
+      int err = __any_sync(0xffffffffu, odd) ? MEDUSA_DEV_BAD_LENGTH : MEDUSA_DEV_OK;
       if (b < a.B) {
-        const int q0 = __ldg(a.q_start + b), q1 = __ldg(a.q_start + b + 1), L = __ldg(a.prefix_len + b);
-        int err = MEDUSA_DEV_OK;
-        if (q0 < 0 || q0 > t || q1 > a.T || L < 0 || L > a.cache.rows()) {
+        const int q0 = __ldg(a.q_start + b), n = __ldg(a.q_start + b + 1) - q0, L = __ldg(a.prefix_len + b);
+        if (L < 0 || L > a.cache.rows() || (err && shares_tokens(a.q_start, a.T, b, q0, q0 + n))) {
           err = MEDUSA_DEV_BAD_LENGTH;
         } else {
           const int row = L + (t - q0);
           p = row;
           slot = -1;
-          if (L > a.cache.rows() - (q1 - q0)) err = MEDUSA_DEV_CACHE_OVERFLOW;
+          if (L > a.cache.rows() - n) err = MEDUSA_DEV_CACHE_OVERFLOW;
           else if ((slot = pool_row(a.cache, b, row)) < 0) err = MEDUSA_DEV_BAD_INDEX;
         }
-        if (err && lane == 0) set_status(a.d_status, err);
       }
+      if (err && lane == 0) set_status(a.d_status, err);
       if (lane == 0) {
         s_slot[tk] = slot;
         s_pos[tk] = a.pos ? __ldg(a.pos + t) : p;
