@@ -25,6 +25,17 @@ extern "C" {
 medusa_status medusa_linear_test_stall(const void* x, const void* w, void* y, int T, int K, int Nout, void* ws,
                                        size_t ws_bytes, int32_t* d_status, medusa_stream_t stream);
 
+/* medusa_paged_attention_test_stall: medusa_paged_attention, of a shape that runs on
+ * tensor cores (INVALID_ARG otherwise), whose values are never loaded, so that
+ * its waits run out after one to two seconds: the kernel ends as described above and
+ * sets MEDUSA_DEV_TIMEOUT; out and lse are not meaningful. */
+medusa_status medusa_paged_attention_test_stall(const void* q, int64_t ldq, const void* k_pages, const void* v_pages,
+                                                const int32_t* page_table, const int32_t* q_start,
+                                                const int32_t* prefix_len, int n_layers, int T, int B, int Hq, int Hkv,
+                                                int d, int n_pages, int page_size, int max_pages, float scale,
+                                                medusa_dtype dt, void* out, float* lse, void* ws, size_t ws_bytes,
+                                                int32_t* d_status, medusa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -33,7 +33,7 @@ EXPORTS = (
     "medusa_topology_greedy_device", "medusa_linear_workspace_size", "medusa_linear", "medusa_linear_test_stall",
     "medusa_head_loss_workspace_size", "medusa_head_loss", "medusa_rope_plan_init", "medusa_rope",
     "medusa_paged_append", "medusa_paged_attention_workspace_size", "medusa_paged_attention",
-    "medusa_paged_tree_attention", "medusa_paged_compact",
+    "medusa_paged_tree_attention", "medusa_paged_compact", "medusa_paged_attention_test_stall",
 )
 
 
@@ -105,6 +105,7 @@ def lib():
             "medusa_paged_append": (I, [P, LL, P, LL, P, LL, P, P, P, P, P] + [I] * 10 + [P] * 5),
             "medusa_paged_attention_workspace_size": (Z, [I] * 8),
             "medusa_paged_attention": (I, [P, LL, P, P, P, P, P] + [I] * 9 + [F, I, P, P, P, Z, P, P]),
+            "medusa_paged_attention_test_stall": (I, [P, LL, P, P, P, P, P] + [I] * 9 + [F, I, P, P, P, Z, P, P]),
             "medusa_paged_tree_attention": (I, [P] * 8 + [I] * 9 + [F, I, P, P, P, Z, P, P]),
             "medusa_paged_compact": (I, [P] * 9 + [I] * 10 + [P, P]),
             "medusa_acc_update": (I, [P, P, P, I, I, ctypes.c_double, P]),

@@ -13,6 +13,7 @@
 // s in the log2 domain (scale log2 e folded in); at the end O / l.  Two parts
 // of a row combine the same way.
 #include "host_util.h"
+#include "medusa_test_hooks.h"
 #include "paged_attn.cuh"
 
 namespace medusa {
@@ -545,12 +546,12 @@ extern "C" size_t medusa_paged_attention_workspace_size(int n_layers, int T, int
   return ws_bytes_of(divide(T, B, Hq, Hkv, d, page_size, dt), d);
 }
 
-extern "C" medusa_status medusa_paged_attention(const void* q, int64_t ldq, const void* k_pages, const void* v_pages,
-                                                const int32_t* page_table, const int32_t* q_start,
-                                                const int32_t* prefix_len, int n_layers, int T, int B, int Hq, int Hkv,
-                                                int d, int n_pages, int page_size, int max_pages, float scale,
-                                                medusa_dtype dt, void* out, float* lse, void* ws, size_t ws_bytes,
-                                                int32_t* d_status, medusa_stream_t stream) {
+static medusa_status chunk_attention(const void* q, int64_t ldq, const void* k_pages, const void* v_pages,
+                                     const int32_t* page_table, const int32_t* q_start,
+                                     const int32_t* prefix_len, int n_layers, int T, int B, int Hq, int Hkv,
+                                     int d, int n_pages, int page_size, int max_pages, float scale,
+                                     medusa_dtype dt, void* out, float* lse, void* ws, size_t ws_bytes,
+                                     int32_t* d_status, medusa_stream_t stream, int withhold) {
   if (!q || !k_pages || !v_pages || !page_table || !q_start || !prefix_len || !out) return MEDUSA_ERR_INVALID_ARG;
   if (!sizes_ok(n_layers, T, B, Hq, Hkv, d, n_pages, page_size, max_pages, scale, dt)) return MEDUSA_ERR_INVALID_ARG;
   if (ldq < (int64_t)Hq * d || ldq % 4 || !aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
@@ -574,8 +575,30 @@ extern "C" medusa_status medusa_paged_attention(const void* q, int64_t ldq, cons
   a.cache.page_table = page_table;
   a.w.q_start = q_start;
   a.w.prefix_len = prefix_len;
+  a.withhold = withhold;
   return attend(a, n_layers, T, B, Hq, Hkv, d, n_pages, page_size, max_pages, ldq, scale, dt, ws, ws_bytes,
                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" medusa_status medusa_paged_attention(const void* q, int64_t ldq, const void* k_pages, const void* v_pages,
+                                                const int32_t* page_table, const int32_t* q_start,
+                                                const int32_t* prefix_len, int n_layers, int T, int B, int Hq, int Hkv,
+                                                int d, int n_pages, int page_size, int max_pages, float scale,
+                                                medusa_dtype dt, void* out, float* lse, void* ws, size_t ws_bytes,
+                                                int32_t* d_status, medusa_stream_t stream) {
+  return chunk_attention(q, ldq, k_pages, v_pages, page_table, q_start, prefix_len, n_layers, T, B, Hq, Hkv, d, n_pages, page_size, max_pages, scale,
+                         dt, out, lse, ws, ws_bytes, d_status, stream, 0);
+}
+
+extern "C" medusa_status medusa_paged_attention_test_stall(const void* q, int64_t ldq, const void* k_pages, const void* v_pages,
+                                                           const int32_t* page_table, const int32_t* q_start,
+                                                           const int32_t* prefix_len, int n_layers, int T, int B, int Hq, int Hkv,
+                                                           int d, int n_pages, int page_size, int max_pages, float scale,
+                                                           medusa_dtype dt, void* out, float* lse, void* ws, size_t ws_bytes,
+                                                           int32_t* d_status, medusa_stream_t stream) {
+  if (Hkv < 1 || page_size < 1 || !tc_shape(Hq / Hkv, d, page_size, dt)) return MEDUSA_ERR_INVALID_ARG;
+  return chunk_attention(q, ldq, k_pages, v_pages, page_table, q_start, prefix_len, n_layers, T, B, Hq, Hkv, d, n_pages, page_size, max_pages, scale,
+                         dt, out, lse, ws, ws_bytes, d_status, stream, 1);
 }
 
 extern "C" medusa_status medusa_paged_tree_attention(const void* q, const void* k_pages, const void* v_pages,

@@ -59,7 +59,8 @@ namespace tc {
 constexpr int kThreads = 384;          // items and K, two MMA issuers, V; 2 x 4 softmax warps
 constexpr int kKeys = 128;             // keys of a tile
 constexpr uint32_t kHalf = 16384;      // 128 rows x 128 bytes (64 columns)
-constexpr int kTries = 1 << 23;
+constexpr int kTries = 1 << 20;        // of a wait that sleeps: 1.3 us each (measured), 1.4 s in all
+constexpr int kPolls = 1 << 23;        // of one that does not: 110 ns (measured), 0.9 s in all
 constexpr uint64_t kDrainNs = 100000000ull;
 constexpr uint32_t kTmemCols = 512;    // S0, S1, O0, O1
 constexpr int kMaxSlots = 12;
@@ -105,6 +106,17 @@ struct Tail {
   };
   uint32_t tmem;
   volatile int abort;
+  // What the loading warps (K, V) leave: loads into each Q buffer; the slots whose barriers full[k] they have
+  // used, and an odd number of times.
+  int q_loads[2];
+  uint32_t loads[2][3], odd[2][3];
+  __device__ void note_loads(int kv, const uint32_t* used, const uint32_t* flips) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      loads[kv][k] = used[k];
+      odd[kv][k] = flips[k];
+    }
+  }
 };
 
 // DH: columns computed, 64 or 128.  NARROW: blocks of one tile of at most 64 rows, whose Q buffers
@@ -169,10 +181,9 @@ __device__ __forceinline__ void issue_sums(uint32_t to, uint32_t tp, uint32_t va
     if (i < steps) mma_bf16_ts(to, tp + 8 * i, desc_of(v + 128 * i), idesc, i > 0 || add);
 }
 
-// Waits for a phase, at most kTries tries (each takes 100 clocks or more: half a second at the
-// least); false when they have run out or *abort is set.  Short on purpose: there are some fifty
-// waits, and with a timer in each of them the kernel's code was 150 KB, of which every warp fetched
-// its share anew.
+// Waits for a phase, at most kTries tries (about a second, 50 ms should each come back at once);
+// false when they have run out or *abort is set.  Short on purpose: there are some fifty waits, and
+// with a timer in each of them the kernel's code was 150 KB, of which every warp fetched its share anew.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort) {
 #pragma unroll 1
   for (int n = kTries; n > 0; --n) {
@@ -203,13 +214,13 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 // Every lane with `need` waits for a phase of a barrier of its own, all at once: a wait costs some
 // 200 clocks even when its phase is long over, and an issuing warp that made its five one after the
 // other came to the probabilities 500 clocks after they were there.  The lanes ask again and again
-// (40 clocks or more a time: over a second in all) and do not sleep on a barrier, which woke them
+// (kPolls times at most, about a second) and do not sleep on a barrier, which woke them
 // some 100 clocks late; for the eight softmax warps that would take issue slots from one another
 // (8192 tokens over 8192 rows: 1051 us so, with sleeping waits 1079, with all waits so 1094).
 __device__ __forceinline__ bool lanes_wait(uint64_t* bar, uint32_t parity, bool need, volatile int* abort) {
   bool ok = !need;
 #pragma unroll 1
-  for (int n = 8 * kTries; n > 0; --n) {
+  for (int n = kPolls; n > 0; --n) {
     if (!ok) ok = mbar_test_wait(bar, parity);
     if (__all_sync(0xffffffffu, ok)) {
       __syncwarp();  // what one lane has seen to be there, all have
@@ -473,14 +484,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       if (y.t1 <= 0) break;
       x = y;
     }
-    if (!alive) {
-      // No copy may land after exit: wait (bounded) for the last phase of every load barrier.
-      if (qn0 > 0) mbar_wait_bounded(&bars->q_full[0], (qn0 - 1) & 1, nullptr, kDrainNs);
-      if (qn1 > 0) mbar_wait_bounded(&bars->q_full[1], (qn1 - 1) & 1, nullptr, kDrainNs);
-#pragma unroll 1
-      for (int i = 0; i < C::nk; ++i)
-        for (int k = 0; k < 3; ++k)
-          if ((used[k] >> i) & 1) mbar_wait_bounded(&bars->full[k][i], ((flips[k] >> i) & 1) ^ 1, nullptr, kDrainNs);
+    if (lane == 0) {
+      tail->q_loads[0] = qn0;
+      tail->q_loads[1] = qn1;
+      tail->note_loads(0, used, flips);
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------ V
@@ -489,7 +496,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     bool alive = true;
     Unit x;
 #pragma unroll 1
-    for (int n = 0; (alive = read_unit(tail, n, x, &s_abort)) && x.t1 > 0; ++n) {
+    for (int n = 0; !a.withhold && (alive = read_unit(tail, n, x, &s_abort)) && x.t1 > 0; ++n) {
       Box b{-1, 0};
 #pragma unroll 1
       for (int t = x.t0 - 1; t < x.t1; ++t) {
@@ -510,12 +517,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       }
       if (!alive) break;
     }
-    if (!alive) {
-#pragma unroll 1
-      for (int i = C::nk; i < C::slots; ++i)
-        for (int k = 0; k < 3; ++k)
-          if ((used[k] >> i) & 1) mbar_wait_bounded(&bars->full[k][i], ((flips[k] >> i) & 1) ^ 1, nullptr, kDrainNs);
-    }
+    if (lane == 0) tail->note_loads(1, used, flips);
   } else {
     // ------------------------------------------------------------ MMA issuer of stream s
     const int s = warp - 1;
@@ -865,7 +867,18 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (threadIdx.x == 0 && s_abort) set_status(a.d_status, MEDUSA_DEV_TIMEOUT);
+  if (threadIdx.x == 0 && s_abort) {
+    set_status(a.d_status, MEDUSA_DEV_TIMEOUT);
+    // No copy may land after exit: wait (bounded) for the last phase of every load barrier.
+    for (int q = 0; q < 2; ++q)
+      if (tail->q_loads[q] > 0) mbar_wait_bounded(&bars->q_full[q], (tail->q_loads[q] - 1) & 1, nullptr, kDrainNs);
+#pragma unroll 1
+    for (int i = 0; i < 3 * C::slots; ++i) {
+      const int k = i / C::slots, sl = i - k * C::slots;
+      if (((tail->loads[0][k] | tail->loads[1][k]) >> sl) & 1)
+        mbar_wait_bounded(&bars->full[k][sl], (((tail->odd[0][k] | tail->odd[1][k]) >> sl) & 1) ^ 1, nullptr, kDrainNs);
+    }
+  }
   if (warp == 1) {
     __syncwarp();  // the lanes may come out of the barrier apart, and the warp frees once
     tmem_dealloc(tmem, kTmemCols);

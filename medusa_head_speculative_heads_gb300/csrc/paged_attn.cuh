@@ -57,6 +57,7 @@ struct AttnArgs {
   int R;          // rows of a partial slot
   int tile_rows, tile_tok;  // a block is tiles of tile_rows rows: tile_tok tokens x sub heads each
   int W;
+  int withhold;  // failure test: the tensor-core kernel brings no V
   int out32;  // rows of out start on 32 bytes
   float scale_log2;
 };
