@@ -145,37 +145,31 @@ __device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, lon
   long long v = 0, inc = 0, before = 0, total = 0;
   pl.odd = false;
   // This thread's sequence of a round, and the tiles of the round's sequences up to it and in all.
-  // Whether one is bad comes with a warp's sum, at no cost where none is; then the round is made
-  // again, and from there on sequences that share tokens are left out.
+  // A bad one makes its warp's sum -1 and the total negative.
   auto round = [&](int k) {
     const int b = k * nt + tid;
-    bool again;
+    s = b < w.B ? seq_of(w, b) : Seq{0, 0, 0, true};
+    if (pl.odd) leave_shared_out(w, b, s);
+    v = inc = seq_tiles(w, s);
 #pragma unroll 1
-    do {
-      s = b < w.B ? seq_of(w, b) : Seq{0, 0, 0, true};
-      if (pl.odd) leave_shared_out(w, b, s);
-      v = inc = seq_tiles(w, s);
+    for (int o = 1; o < 32 && o < w.B; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const bool bad = __any_sync(0xffffffffu, !s.ok) && !pl.odd;
+    __syncthreads();  // the round before is read
+    if (lane == min(31, w.B - 1)) sh[wp] = bad ? -1 : inc;  // fewer than 32 sequences: lanes behind them hold no sums
+    __syncthreads();
+    before = total = 0;
+    const int busy = min(nw, (w.B - k * nt + 31) >> 5);  // warps that have sequences
 #pragma unroll 1
-      for (int o = 1; o < 32 && o < w.B; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      const bool bad = __any_sync(0xffffffffu, !s.ok) && !pl.odd;
-      __syncthreads();  // the round before is read
-      if (lane == min(31, w.B - 1)) sh[wp] = bad ? -1 : inc;  // fewer than 32 sequences: lanes behind them hold no sums
-      __syncthreads();
-      before = total = 0;
-      again = false;
-      const int busy = min(nw, (w.B - k * nt + 31) >> 5);  // warps that have sequences
-#pragma unroll 1
-      for (int j = 0; j < busy; ++j) {
-        const long long y = sh[j];
-        again |= y < 0;
-        if (j < wp) before += y;
-        total += y;
-      }
-      pl.odd |= again;
-    } while (again);
+    for (int j = 0; j < busy; ++j) {
+      const long long y = sh[j];
+      if (y < 0) total = y;
+      if (total < 0) break;
+      if (j < wp) before += y;
+      total += y;
+    }
   };
   // First the sums of all rounds, then, the last round first being the one in hand, the search.
   long long per = 0, u = -1, off = 0, base = 0;
@@ -184,6 +178,11 @@ __device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, lon
 #pragma unroll 1
   for (int k = 0; k < 2 * rounds && !found; ++k) {
     if (k < rounds || rounds > 1) round(k < rounds ? k : k - rounds);
+    if (total < 0) {  // a bad sequence: from here on those that share tokens are left out
+      pl.odd = true;
+      --k;
+      continue;
+    }
     if (k < rounds) {
       per += total;
       if (k + 1 < rounds) continue;
