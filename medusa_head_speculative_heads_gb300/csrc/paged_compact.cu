@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(256) paged_compact_kernel(const __grid_constan
     const long long b = blockIdx.x * (long long)blockDim.x + threadIdx.x;
     if (b < a.B) a.new_len[b] = new_len_of(a, (int)b);
   }
-  for (int row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    int r = row;
+  for (unsigned row = blockIdx.x; row < (unsigned)a.rows; row += gridDim.x) {  // a sum past 2^31 is no row
+    int r = (int)row;
     const int kv = r & 1;
     r >>= 1;
     const int i = r % a.D1;
