@@ -416,7 +416,8 @@ medusa_status medusa_head_loss(const void* logits, const int32_t* tokens, int K,
  * Entries of page_table behind a sequence's last row are never read.  What a
  * call writes (pools, outputs, workspace) must overlap nothing else (ALIAS),
  * except where it says so.  T, B, page_size and max_pages >= 1, n_layers *
- * n_pages * page_size and n_layers * T < 2^31, max_pages * page_size < 2^31 - 2^16.
+ * n_pages * page_size and n_layers * T < 2^31, B and max_pages * page_size <
+ * 2^31 - 2^16.
  *
  * medusa_rope_plan: how a rotary embedding turns.  The leading rotary_dim
  * elements of a head are pairs (i, i + rotary_dim/2), or (2i, 2i+1) when

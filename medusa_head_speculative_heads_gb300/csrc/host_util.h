@@ -35,10 +35,10 @@ inline bool overlaps_any(Region out, std::initializer_list<Region> others) {
   return false;
 }
 
-// Sizes of a paged cache: pool rows and a sequence's rows stay inside int32,
-// with room for a tile behind the last row.
-inline bool cache_sizes_ok(int n_layers, int n_pages, int page_size, int max_pages) {
-  if (n_pages < 1 || page_size < 1 || max_pages < 1) return false;
+// Sizes of a paged cache: pool rows, a sequence's rows and the sequences stay inside
+// int32, with room for a tile behind the last row and a block's threads behind the last sequence.
+inline bool cache_sizes_ok(int n_layers, int B, int n_pages, int page_size, int max_pages) {
+  if (B < 1 || B >= 0x7fffffff - 65536 || n_pages < 1 || page_size < 1 || max_pages < 1) return false;
   const long long pool = (long long)n_pages * page_size;
   return pool <= 0x7fffffffll / n_layers && (long long)max_pages * page_size < 0x7fffffffll - 65536;
 }

@@ -508,7 +508,7 @@ static medusa_status attend(AttnArgs& a, int n_layers, int T, int B, int Hq, int
   a.w.KT_log2 = log2_of(v.KT);
   // No more CTAs than there can be tiles (but two, for the reciprocal): idle ones delay a small call
   // (3 heads x 10 nodes of 4 sequences 12.7 us, on all SMs 14.1; fp32, 21 short sequences 9.0 and 11.7).
-  const long long blocks = a.w.N ? (long long)B * ((a.w.N + v.ctok - 1) / v.ctok) : B + T / v.ctok;
+  const long long blocks = a.w.N ? (long long)B * ((a.w.N + v.ctok - 1) / v.ctok) : (long long)B + T / v.ctok;
   const long long tiles = (a.w.cap + v.KT - 1) / v.KT + (a.w.N + v.KT - 1) / v.KT;
   const double most = (double)a.w.nl * a.w.nh * blocks * tiles;
   a.w.ctas = most >= v.ctas ? v.ctas : most <= 2 ? 2 : (int)most;
@@ -530,7 +530,7 @@ static bool sizes_ok(int n_layers, int T, int B, int Hq, int Hkv, int d, int n_p
   if (n_layers < 1 || T < 1 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq > 65535) return false;
   if (d < 4 || d % 4 || d > MEDUSA_MAX_HEAD_DIM || !(scale > 0.f) || !(scale < INFINITY) || !dtype_ok(dt)) return false;
   if ((long long)n_layers * T > 0x7fffffffll || (long long)n_layers * Hq > 0x7fffffffll) return false;
-  return cache_sizes_ok(n_layers, n_pages, page_size, max_pages);
+  return cache_sizes_ok(n_layers, B, n_pages, page_size, max_pages);
 }
 
 }  // namespace paged

@@ -112,7 +112,7 @@ extern "C" medusa_status medusa_paged_compact(void* k_pages, void* v_pages, cons
     return MEDUSA_ERR_INVALID_ARG;
   if (n_layers < 1 || B < 1 || N < 1 || N > MEDUSA_MAX_NODES || Hkv < 1 || Hkv > 65535 || d < 1 || d > MEDUSA_MAX_HEAD_DIM)
     return MEDUSA_ERR_INVALID_ARG;
-  if (Dmax < 0 || Dmax > MEDUSA_MAX_DEPTH || !dtype_ok(dt) || !cache_sizes_ok(n_layers, n_pages, page_size, max_pages))
+  if (Dmax < 0 || Dmax > MEDUSA_MAX_DEPTH || !dtype_ok(dt) || !cache_sizes_ok(n_layers, B, n_pages, page_size, max_pages))
     return MEDUSA_ERR_INVALID_ARG;
   const long long rows = (long long)n_layers * B * (Dmax + 1) * 2;
   if (rows > INT_MAX) return MEDUSA_ERR_INVALID_ARG;

@@ -418,7 +418,7 @@ extern "C" medusa_status medusa_paged_append(const void* q, int64_t ldq, const v
     return MEDUSA_ERR_INVALID_ARG;
   if (!dtype_ok(dt) || n_layers < 1 || T < 1 || B < 1 || (q && Hq < 1) || Hkv < 1 || d < 2 || d % 2 || d > MEDUSA_MAX_HEAD_DIM)
     return MEDUSA_ERR_INVALID_ARG;
-  if (!cache_sizes_ok(n_layers, n_pages, page_size, max_pages) || (long long)n_layers * T > 0x7fffffffll) return MEDUSA_ERR_INVALID_ARG;
+  if (!cache_sizes_ok(n_layers, B, n_pages, page_size, max_pages) || (long long)n_layers * T > 0x7fffffffll) return MEDUSA_ERR_INVALID_ARG;
   if (Hq > 65535 || Hkv > 65535 || (plan && !plan_ok(plan, d))) return MEDUSA_ERR_INVALID_ARG;
   if ((q && ldq < (int64_t)Hq * d) || ldk < (int64_t)Hkv * d || ldv < (int64_t)Hkv * d) return MEDUSA_ERR_INVALID_ARG;
   const size_t es = dtype_bytes(dt);
