@@ -494,7 +494,8 @@ medusa_status medusa_paged_append(const void* q, int64_t ldq, const void* k, int
  *   logarithm of the sum of exp(scale q.k) over the visible keys.
  * One token per sequence is a decoding step, a whole prompt a prefill, any mix
  * of lengths one call.  Rows behind a sequence's last one are never part of a
- * result, whatever they hold; rows it has must be finite.  A page outside
+ * result, whatever they hold; rows it has must be finite.  A query whose scores
+ * are NaN, or one +inf, or all -inf, gets NaN.  A page outside
  * [0, n_pages) among a sequence's rows sets BAD_INDEX and counts as zero rows;
  * prefix_len + chunk past max_pages * page_size sets BAD_LENGTH (unwritten).
  * bf16 with d <= 128 a multiple of 8, page_size a multiple of 8 and G <= 128

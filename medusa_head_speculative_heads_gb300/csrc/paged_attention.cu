@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kSimtThreads, simt_ctas(DC, RM)) paged_attn_si
       for (int e = 8; e; e >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, e);
       if (!row[i].ok) continue;
       const size_t at = whole ? out_row(a, it, row[i]) : (size_t)slot * a.R + ty * RM + i;  // in lse or part_ml
-      const float f = !whole ? 1.f : ls > 0.f ? 1.f / ls : 0.f;
+      const float f = whole ? row_scale(a, it.s.L, row[i].tok, ls) : 1.f;
 #pragma unroll
       for (int c = 0; c < DC / 4; ++c) {
         const int col = 4 * tx + 64 * c;
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(256) paged_attn_merge_kernel(const __grid_cons
       l = fmaf(exp2f(q.x - off), q.y, l);
     }
     l = warp_sum(l);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = row_scale(a, it.s.L, x.tok, l);
     const size_t to = out_row(a, it, x);
     for (int col = 4 * lane; col < a.d; col += 128) {
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -326,9 +326,9 @@ __global__ void __launch_bounds__(256) paged_attn_merge_kernel(const __grid_cons
       for (int p = first; p <= last; ++p) {
         const size_t w = at(p);
         const float2 ml = a.part_ml[w];
-        const float f = ml.y > 0.f ? exp2f(ml.x - off) : 0.f;
+        const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - off);
         const float4 v = *reinterpret_cast<const float4*>(a.part_o + w * a.d + col);  // as part_at
-        if (f > 0.f) {  // a part that saw no key may hold anything
+        if (f != 0.f) {  // a part that saw no key may hold anything
           o.x = fmaf(f, v.x, o.x);
           o.y = fmaf(f, v.y, o.y);
           o.z = fmaf(f, v.z, o.z);
@@ -369,12 +369,12 @@ __global__ void __launch_bounds__(256) paged_attn_merge_wide_kernel(const __grid
       if (4 * (c0 + k) < a.d) v[k] = from[k * part_rows(256)];
     const float2 q = x.ok ? a.part_ml[(size_t)slot * a.R + r] : make_float2(-INFINITY, 0.f);
     const float m = fmaxf(M, q.x), off = m == -INFINITY ? 0.f : m;
-    const float f = exp2f(M - off), g = q.y > 0.f ? exp2f(q.x - off) : 0.f;
+    const float f = exp2f(M - off), g = q.y == 0.f ? 0.f : exp2f(q.x - off);
     M = m;
     l = fmaf(l, f, g * q.y);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (!(g > 0.f) || 4 * (c0 + k) >= a.d) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);  // a part that saw no key may hold anything
+      if (g == 0.f || 4 * (c0 + k) >= a.d) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);  // a part that saw no key may hold anything
       o[k].x = fmaf(o[k].x, f, g * v[k].x);
       o[k].y = fmaf(o[k].y, f, g * v[k].y);
       o[k].z = fmaf(o[k].z, f, g * v[k].z);
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(256) paged_attn_merge_wide_kernel(const __grid
     }
   }
   if (!x.ok) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = row_scale(a, sd.it.s.L, x.tok, l);
   const size_t to = out_row(a, sd.it, x);
 #pragma unroll
   for (int k = 0; k < 4; ++k)

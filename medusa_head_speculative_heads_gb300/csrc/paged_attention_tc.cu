@@ -802,7 +802,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (!(alive = lanes_wait(&bars->o_full[two(x) ? s : lane & 1], n & 1, lane < (two(x) ? 1 : 2), &s_abort))) break;
         if (busy) {
           tc_fence_after();
-          const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+          const float inv = !whole ? 1.f : row_ok ? row_scale(a, x.L, x.tok0 + tok, sum) : 0.f;
           w0 *= inv;
           w1 *= inv;
           const size_t orow = ((size_t)x.row0 + tok) * a.Hq + x.kvh * a.G + mh;
@@ -815,13 +815,13 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
               tmem_ld32(to + 128 * s + 32 * q, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = w0 > 0.f ? o[i] * w0 : 0.f;
+              for (int i = 0; i < 32; ++i) o[i] = w0 == 0.f ? 0.f : o[i] * w0;
               if (o1) {
                 float p[32];
                 tmem_ld32(to + 128 + 32 * q, p);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = w1 > 0.f ? fmaf(p[i], w1, o[i]) : o[i];
+                for (int i = 0; i < 32; ++i) o[i] = w1 == 0.f ? o[i] : fmaf(p[i], w1, o[i]);
               }
             } else {
 #pragma unroll

@@ -110,7 +110,22 @@ __device__ __forceinline__ void note_shared(const AttnArgs& a, const Plan& pl, c
 
 // Natural logarithm of the softmax's sum from its maximum (log2 domain) and scaled sum.
 __device__ __forceinline__ float lse_of(float m, float l) {
-  return l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// What a row's sums of products are multiplied by: 1 / l.  A maximum passes over NaN, so that a row whose
+// scores are NaN, or one of them infinite, has a NaN as its sum, and keeps it.  l = 0: zeros for a row
+// that sees no key (of a tree: a node with no mask bit before an empty prefix), and NaN for one whose
+// every score was -inf.
+__device__ __forceinline__ float row_scale(const AttnArgs& a, int L, int tok, float l) {
+  if (l != 0.f) return 1.f / l;
+  bool sees = !a.w.N || L > 0;
+#pragma unroll 1
+  for (int w = 0; !sees && w < a.W; ++w) {
+    const int n = a.w.N - 32 * w;
+    sees = a.mask[(size_t)tok * a.W + w] & (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+  }
+  return sees ? __int_as_float(0x7fffffff) : 0.f;
 }
 
 // Tensor-core kernel (paged_attention_tc.cu): bf16, d <= 128 a multiple of 8,

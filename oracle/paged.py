@@ -68,13 +68,14 @@ def paged_append(k, v, k_pages, v_pages, page_table, q_start, prefix_len, turn=l
 
 
 def _softmax_rows(q, k, v, see, scale):
-    """q [n, d], k, v [m, d], see [n, m] -> (out, lse, sum of p |v|); nothing seen: zeros and -inf."""
+    """q [n, d], k, v [m, d], see [n, m] -> (out, lse, sum of p |v|); nothing seen: zeros and -inf;
+    a score seen that is NaN or +inf, or none that is more than -inf: NaN."""
     with np.errstate(divide="ignore", invalid="ignore"):
         s = np.where(see, scale * (q @ k.T), -np.inf)
         m = s.max(-1, initial=-np.inf, keepdims=True)
         p = np.exp(s - np.where(np.isfinite(m), m, 0.0))
         l = p.sum(-1, keepdims=True)
-        w = np.where(l > 0, p / np.where(l > 0, l, 1.0), 0.0)
+        w = np.where(see.any(-1, keepdims=True), p / l, 0.0)
         return w @ v, (np.log(l) + m)[:, 0], w @ np.abs(v)
 
 
