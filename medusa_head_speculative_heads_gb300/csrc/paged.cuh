@@ -18,7 +18,7 @@ struct Cache {
 // the pool.  0 <= r < rows().
 __device__ __forceinline__ int pool_row(const Cache& c, int b, int r) {
   const int pg = r / c.page_size;
-  const int id = __ldg(c.page_table + (size_t)b * c.max_pages + pg);
+  const int id = c.page_table[(size_t)b * c.max_pages + pg];
   return id >= 0 && id < c.n_pages ? id * c.page_size + (r - pg * c.page_size) : -1;
 }
 
@@ -60,9 +60,9 @@ struct Seq {
 
 __device__ __forceinline__ Seq seq_of(const Work& w, int b) {
   Seq s;
-  s.L = __ldg(w.prefix_len + b);
+  s.L = w.prefix_len[b];
   if (w.q_start) {
-    const int a = __ldg(w.q_start + b), e = __ldg(w.q_start + b + 1);
+    const int a = w.q_start[b], e = w.q_start[b + 1];
     s.q0 = a;
     s.ok = a >= 0 && e >= a && e <= w.T && (e == a || (s.L >= 0 && s.L <= w.cap - (e - a)));
     s.len = s.ok ? e - a : 0;

@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kSimtThreads, simt_ctas(DC, RM)) paged_attn_si
         for (int j = 0; j < 4; ++j) {
           const int key = (t < pre ? t : t - pre) * kSimtKeys + tx + 16 * j;
           bool see;
-          if (t >= pre) see = row[i].ok && key < a.w.N && ((__ldg(a.mask + (size_t)row[i].tok * a.W + (key >> 5)) >> (key & 31)) & 1u);
+          if (t >= pre) see = row[i].ok && key < a.w.N && ((a.mask[(size_t)row[i].tok * a.W + (key >> 5)] >> (key & 31)) & 1u);
           else see = row[i].ok && key < (a.w.N ? it.s.L : it.s.L + row[i].tok + 1);
           const float2 z = unpack2(s2[i][j]);
           s[i][j] = see ? (z.x + z.y) * a.scale_log2 : -INFINITY;

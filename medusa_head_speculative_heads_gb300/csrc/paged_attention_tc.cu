@@ -300,7 +300,7 @@ __device__ __forceinline__ Box box_of(const AttnArgs& a, const Unit& x, int t, i
   if (t < x.pre && lane < kKeys / box_rows && r < x.rows_end) {
     const int pg = r / a.cache.page_size;
     b.off = r - pg * a.cache.page_size;
-    b.id = __ldg(a.cache.page_table + (size_t)x.b * a.cache.max_pages + pg);
+    b.id = a.cache.page_table[(size_t)x.b * a.cache.max_pages + pg];
   }
   return b;
 }
@@ -706,7 +706,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           for (int q = 0; q < 4; ++q) {
             const int c = lim - 32 * q;
             uint32_t w = !row_ok || c <= 0 ? 0u : c >= 32 ? 0xffffffffu : (1u << c) - 1u;
-            if (tree && w) w &= __ldg(a.mask + (size_t)(x.tok0 + tok) * a.W + (j >> 5) + q);
+            if (tree && w) w &= a.mask[(size_t)(x.tok0 + tok) * a.W + (j >> 5) + q];
             float z[32];
             __syncwarp();
             tmem_ld32(ts + 32 * q, z);

@@ -32,14 +32,14 @@ struct CompactArgs {
 
 // Why sequence b cannot be entered (MEDUSA_DEV_OK: it can), from its lengths alone.
 __device__ __forceinline__ int length_error(const CompactArgs& a, int b, int& L, int& A) {
-  L = __ldg(a.prefix_len + b);
-  A = __ldg(a.accept_len + b);
+  L = a.prefix_len[b];
+  A = a.accept_len[b];
   if (L < 0) return MEDUSA_DEV_BAD_LENGTH;
   if (A < 1 || A > a.D1) return MEDUSA_DEV_BAD_INDEX;
   return L > a.cache.rows() - A ? MEDUSA_DEV_CACHE_OVERFLOW : MEDUSA_DEV_OK;
 }
 __device__ __forceinline__ bool slot_ok(const CompactArgs& a, int b, int L, int j) {
-  const int n = __ldg(a.path_nodes + (size_t)b * a.D1 + j);
+  const int n = a.path_nodes[(size_t)b * a.D1 + j];
   return n >= 0 && n < a.N && pool_row(a.cache, b, L + j) >= 0;
 }
 
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(256) paged_compact_kernel(const __grid_constan
       if (l == 0 && i == 0 && kv == 0 && threadIdx.x == 0) set_status(a.d_status, err);
       continue;
     }
-    const int node = __ldg(a.path_nodes + (size_t)b * a.D1 + i);
+    const int node = a.path_nodes[(size_t)b * a.D1 + i];
     const WORD* from = static_cast<const WORD*>(kv ? a.vt : a.kt) + (((size_t)l * a.B + b) * a.N + node) * a.words;
     const size_t to_row = (size_t)l * a.cache.n_pages * a.cache.page_size + pool_row(a.cache, b, L + i);
     WORD* to = static_cast<WORD*>(kv ? a.v_pages : a.k_pages) + to_row * a.words;

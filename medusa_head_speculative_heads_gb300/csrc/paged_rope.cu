@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kRopeThreads, 16) rope_kernel(const __grid_con
       bool odd = false;  // some starts decrease or lie outside the tokens
 #pragma unroll 1
       for (int j = lane; j < a.B; j += 32) {
-        const int q0 = __ldg(a.q_start + j), q1 = __ldg(a.q_start + j + 1);
+        const int q0 = a.q_start[j], q1 = a.q_start[j + 1];
         if (q0 < 0 || q1 < q0 || q1 > a.T) odd = true;
         else if (q0 <= t && t < q1) b = min(b, j);
       }
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kRopeThreads, 16) rope_kernel(const __grid_con
       int slot = -2, p = 0;
       int err = __any_sync(0xffffffffu, odd) ? MEDUSA_DEV_BAD_LENGTH : MEDUSA_DEV_OK;
       if (b < a.B) {
-        const int q0 = __ldg(a.q_start + b), n = __ldg(a.q_start + b + 1) - q0, L = __ldg(a.prefix_len + b);
+        const int q0 = a.q_start[b], n = a.q_start[b + 1] - q0, L = a.prefix_len[b];
         if (L < 0 || L > a.cache.rows() || (err && shares_tokens(a.q_start, a.T, b, q0, q0 + n))) {
           err = MEDUSA_DEV_BAD_LENGTH;
         } else {
@@ -199,14 +199,14 @@ __global__ void __launch_bounds__(kRopeThreads, 16) rope_kernel(const __grid_con
       if (err && lane == 0) set_status(a.d_status, err);
       if (lane == 0) {
         s_slot[tk] = slot;
-        s_pos[tk] = a.pos ? __ldg(a.pos + t) : p;
+        s_pos[tk] = a.pos ? a.pos[t] : p;
       }
     }
     __syncthreads();
   }
   for (unsigned j = threadIdx.x; j < half * n_tok; j += kRopeThreads) {
     const unsigned tk = j / half, i = j - tk * half;
-    const int p = a.k_pages ? s_pos[tk] : __ldg(a.pos + (tok0 + tk) % a.T);
+    const int p = a.k_pages ? s_pos[tk] : a.pos[(tok0 + tk) % a.T];
     const unsigned c = i / W, e = i % W;
     cs[tk][W == 1 ? c : ((e >> 1) * turned + c) * 2 + (e & 1)] = turn_of(p, a.turn[i], a.inverse, a.magnitude);
   }
