@@ -171,6 +171,11 @@ float number(const Call& c, PyObject* o, double otherwise) {
   if (x == -1.0 && PyErr_Occurred()) throw python_error();
   return (float)x;
 }
+bool flag(PyObject* o) {
+  const int yes = PyObject_IsTrue(o);
+  if (yes < 0) throw python_error();
+  return yes == 1;
+}
 int small(const Call& c, int64_t n, const char* name) {
   if (n < 0 || n > 0x7fffffff) c.refuse(std::string(name) + " is out of range");
   return (int)n;
@@ -219,6 +224,7 @@ medusa_status enqueue(F&& f) {
 PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 7, [&]() -> PyObject* {
     Call c{"medusa_rope"};
+    const bool inverse = flag(a[6]);
     const Tensor& q = c.tensor(a[0], "q");
     const int dt = c.lead(q, "q");
     c.dims(q, "q", 4, "[nl, T, Hq, d]");
@@ -238,7 +244,6 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* pos = c.words(a[2], "pos", T);
     c10::DeviceGuard on(c.dev);
     const Out qo(c, a[4], "q_out", {nl, T, hq, d}, c.ty), ko(c, a[5], "k_out", {nl, T, hkv, d}, c.ty, k != nullptr);
-    const int inverse = PyObject_IsTrue(a[6]);
     const medusa_rope_plan* plan = plan_at(a[3]);
     const medusa_status st = enqueue([&] {
       return medusa_rope(q.data_ptr(), ldq, k, ldk, pos, plan, inverse, small(c, nl, "nl"), small(c, T, "T"), small(c, hq, "Hq"),
@@ -291,6 +296,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 12, [&]() -> PyObject* {
     Call c{"medusa_paged_attention"};
+    const bool want_lse = flag(a[9]);
     const Tensor& q = c.tensor(a[0], "q");
     const int dt = c.lead(q, "q");
     const Pools p(c, a[1], a[2], a[3]);
@@ -301,7 +307,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t* status = status_word(c, a[11]);
     c10::DeviceGuard on(c.dev);
     const Out out(c, a[7], "out", {p.nl, T, hq, p.d}, c.ty);
-    const Out lse(c, a[8], "lse", {p.nl, T, hq}, ScalarType::Float, PyObject_IsTrue(a[9]) == 1);
+    const Out lse(c, a[8], "lse", {p.nl, T, hq}, ScalarType::Float, want_lse);
     const int nl = small(c, p.nl, "nl"), t = small(c, T, "T"), b = small(c, p.B, "B"), h = small(c, hq, "Hq"), hk = small(c, p.hkv, "Hkv"),
               d = small(c, p.d, "d"), np = small(c, p.n_pages, "n_pages"), ps = small(c, p.ps, "page_size"), mp = small(c, p.max_pages, "max_pages");
     const float scale = number(c, a[6], 1.0 / std::sqrt((double)(d > 0 ? d : 1)));
@@ -319,6 +325,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 14, [&]() -> PyObject* {
     Call c{"medusa_paged_tree_attention"};
+    const bool want_lse = flag(a[11]);
     const Tensor &q = c.tensor(a[0], "q"), &kt = c.tensor(a[4], "kt"), &vt = c.tensor(a[5], "vt");
     const int dt = c.lead(q, "q");
     const Pools p(c, a[1], a[2], a[3]);
@@ -334,7 +341,7 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t* status = status_word(c, a[13]);
     c10::DeviceGuard on(c.dev);
     const Out out(c, a[9], "out", {p.nl, p.B, N, hq, p.d}, c.ty);
-    const Out lse(c, a[10], "lse", {p.nl, p.B, N, hq}, ScalarType::Float, PyObject_IsTrue(a[11]) == 1);
+    const Out lse(c, a[10], "lse", {p.nl, p.B, N, hq}, ScalarType::Float, want_lse);
     const int nl = small(c, p.nl, "nl"), b = small(c, p.B, "B"), nn = small(c, N, "N"), t = small(c, p.B * N, "B * N"), h = small(c, hq, "Hq"),
               hk = small(c, p.hkv, "Hkv"), d = small(c, p.d, "d"), np = small(c, p.n_pages, "n_pages"), ps = small(c, p.ps, "page_size"),
               mp = small(c, p.max_pages, "max_pages");

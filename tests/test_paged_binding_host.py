@@ -1,0 +1,29 @@
+"""What the compiled binding of the paged calls does before it looks for a GPU."""
+import pytest
+
+import medusa_head_speculative_heads_gb300 as mg
+
+torch = pytest.importorskip("torch")
+
+
+class Neither:
+    def __bool__(self):
+        raise RuntimeError("neither true nor false")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    mg.build()
+
+
+def test_a_flag_that_is_neither_true_nor_false_is_its_own_error():
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt)  # noqa: E731
+    i32 = torch.int32
+    pools = (z(1, 3, 8, 2, 32), z(1, 3, 8, 2, 32), z(1, 2, dt=i32))
+    for flag in (Neither(), torch.zeros(2)):
+        with pytest.raises(RuntimeError, match="neither|ambiguous"):
+            mg.medusa_rope(z(1, 2, 4, 32), None, z(2, dt=i32), mg.RopeSpec(32), inverse=flag)
+        with pytest.raises(RuntimeError, match="neither|ambiguous"):
+            mg.medusa_paged_attention(z(1, 2, 4, 32), *pools, z(2, dt=i32), z(1, dt=i32), want_lse=flag)
+        with pytest.raises(RuntimeError, match="neither|ambiguous"):
+            mg.medusa_paged_tree_attention(z(1, 1, 2, 4, 32), *pools, z(1, 1, 2, 2, 32), z(1, 1, 2, 2, 32), z(2, 1, dt=i32), z(1, dt=i32), want_lse=flag)
