@@ -3,7 +3,8 @@ marshals their arguments: a decoding step makes these calls once per layer and
 their kernels run for a few microseconds.
 
 Everywhere: what is not given (outputs, workspace) is allocated, on the stream that
-the call runs on: the current one of the tensors' device, or `stream`.
+the call runs on: the current one of the tensors' device, or `stream`.  Gradients are
+recorded by medusa_rope where it makes its outputs, and by no other call.
 """
 from __future__ import annotations
 
@@ -70,13 +71,37 @@ class RopeSpec:
     interleaved = property(lambda self: bool(self.st.interleaved))
 
 
+class _Rope(torch.autograd.Function if torch is not None else object):
+    """medusa_rope of tensors that require grad: its gradient is the turn by the opposite angle."""
+
+    @staticmethod
+    def forward(ctx, q, k, pos, rope, inverse):
+        outs = medusa_rope(q, k, pos, rope, inverse=inverse)
+        ctx.save_for_backward(pos)
+        ctx.rope, ctx.inverse = rope, inverse
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(*(o for o, need in zip(outs, ctx.needs_input_grad) if o is not None and not need))
+        return outs
+
+    @staticmethod
+    def backward(ctx, *grads):
+        pos, = ctx.saved_tensors
+        back = [g.contiguous() for g, need in zip(grads, ctx.needs_input_grad) if g is not None and need]
+        back = iter(medusa_rope(back[0], back[1] if len(back) > 1 else None, pos, ctx.rope, inverse=not ctx.inverse) if back else ())
+        return *(next(back) if g is not None and need else None for g, need in zip(grads, ctx.needs_input_grad)), None, None, None
+
+
 def medusa_rope(q, k, pos, rope: RopeSpec, q_out=None, k_out=None, inverse: bool = False, stream=None):
     """Rotary embedding of q [nl, T, Hq, d] and k [nl, T, Hkv, d] (or None) at pos
     [T] int32; returns (q_out, k_out), new tensors unless given (q_out may be q,
     k_out may be k).  inverse=True maps gradients of the outputs to those of the
-    inputs."""
+    inputs; new outputs of inputs that require grad do so by themselves (given ones
+    record nothing)."""
     if stream is not None:
         return _on(stream, q, medusa_rope, q, k, pos, rope, q_out, k_out, inverse)
+    if q_out is None and k_out is None and torch.is_grad_enabled() and (
+            getattr(q, "requires_grad", False) or getattr(k, "requires_grad", False)):
+        return _Rope.apply(q, k, pos, rope, inverse)
     r = (_native or _load()).rope(q, k, pos, rope.addr, q_out, k_out, inverse)
     if type(r) is int:
         raise B_.MedusaError("medusa_rope", r)

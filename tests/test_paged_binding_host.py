@@ -27,3 +27,12 @@ def test_a_flag_that_is_neither_true_nor_false_is_its_own_error():
             mg.medusa_paged_attention(z(1, 2, 4, 32), *pools, z(2, dt=i32), z(1, dt=i32), want_lse=flag)
         with pytest.raises(RuntimeError, match="neither|ambiguous"):
             mg.medusa_paged_tree_attention(z(1, 1, 2, 4, 32), *pools, z(1, 1, 2, 2, 32), z(1, 1, 2, 2, 32), z(2, 1, dt=i32), z(1, dt=i32), want_lse=flag)
+
+
+def test_a_rotation_that_would_record_a_gradient_refuses_alike():
+    z = torch.zeros(1, 2, 4, 32, requires_grad=True)
+    for q, k in ((z, None), (z, z), (z.detach(), z)):
+        with pytest.raises(ValueError, match="on a GPU"):
+            mg.medusa_rope(q, k, torch.zeros(2, dtype=torch.int32), mg.RopeSpec(32))
+    with pytest.raises(TypeError, match="must be a tensor"):
+        mg.medusa_rope(3, None, torch.zeros(2, dtype=torch.int32), mg.RopeSpec(32))
