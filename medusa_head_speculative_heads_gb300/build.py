@@ -50,9 +50,11 @@ def up_to_date() -> bool:
 
 
 def binding_path() -> str:
-    """The compiled binding for the installed torch."""
+    """The compiled binding for this Python (version, platform) and the installed
+    torch (version, C++ ABI)."""
     import torch
-    return os.path.join(BUILD, f"paged_binding-{torch.__version__}.so")
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(BUILD, f"paged_binding-{torch.__version__}-abi{abi}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def build_binding(force: bool = False) -> None:

@@ -36,3 +36,24 @@ def test_a_rotation_that_would_record_a_gradient_refuses_alike():
             mg.medusa_rope(q, k, torch.zeros(2, dtype=torch.int32), mg.RopeSpec(32))
     with pytest.raises(TypeError, match="must be a tensor"):
         mg.medusa_rope(3, None, torch.zeros(2, dtype=torch.int32), mg.RopeSpec(32))
+
+
+def test_the_compiled_file_is_of_one_python_torch_and_abi(monkeypatch):
+    """Another Python, torch or C++ ABI never takes this one's binding for its own."""
+    import sysconfig
+
+    from medusa_head_speculative_heads_gb300.build import binding_path
+    here = binding_path()
+    suffix = sysconfig.get_config_var("EXT_SUFFIX")
+    assert here.endswith(suffix) and torch.__version__ in here
+    others = {here}
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda name: suffix.replace("cpython-3", "cpython-9") if name == "EXT_SUFFIX" else None)
+        others.add(binding_path())
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.0")
+        others.add(binding_path())
+    with monkeypatch.context() as m:
+        m.setattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", not torch._C._GLIBCXX_USE_CXX11_ABI)
+        others.add(binding_path())
+    assert len(others) == 4
