@@ -411,8 +411,8 @@ medusa_status medusa_head_loss(const void* logits, const int32_t* tokens, int K,
  * Lengths, starts and pages are read on the device only.  A sequence whose
  * starts decrease or leave [0, T], or that has tokens and a prefix_len outside
  * [0, max_pages * page_size], sets BAD_LENGTH and nothing of it is written.  Starts
- * that decrease can give later sequences tokens of an earlier one: these stay the
- * earlier one's, and the later ones set BAD_LENGTH too.
+ * that decrease can bring a later sequence back before the end of an earlier one: it
+ * sets BAD_LENGTH too, and the tokens stay the earlier one's.
  * Entries of page_table behind a sequence's last row are never read.  What a
  * call writes (pools, outputs, workspace) must overlap nothing else (ALIAS),
  * except where it says so.  T, B, page_size and max_pages >= 1, n_layers *

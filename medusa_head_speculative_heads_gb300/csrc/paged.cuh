@@ -22,16 +22,12 @@ __device__ __forceinline__ int pool_row(const Cache& c, int b, int r) {
   return id >= 0 && id < c.n_pages ? id * c.page_size + (r - pg * c.page_size) : -1;
 }
 
-// Whether a sequence with tokens [q0, q1) has one that an earlier sequence's starts hold too,
-// which takes starts that decrease somewhere between them.  The token is the first one's, and
-// the later sequence as bad as the one whose own starts decrease.
-__device__ __forceinline__ bool shares_tokens(const int32_t* q_start, int T, int b, int q0, int q1) {
-#pragma unroll 1
-  for (int j = 0; j < b; ++j) {
-    const int a = q_start[j], e = q_start[j + 1];
-    if (a >= 0 && a < e && e <= T && a < q1 && q0 < e) return true;
-  }
-  return false;
+// Where sequence j ends, or -1 when its starts decrease or leave [0, T].  Starts that decrease can
+// bring a later sequence back among the tokens of earlier ones: one that begins before the largest
+// of their ends is as bad as the one whose own starts decrease, so that a token is one sequence's.
+__device__ __forceinline__ int end_of(const int32_t* q_start, int T, int j) {
+  const int a = q_start[j], e = q_start[j + 1];
+  return a >= 0 && a <= e && e <= T ? e : -1;
 }
 
 // ------------------------------------------------------------------ attention work
@@ -72,11 +68,6 @@ __device__ __forceinline__ Seq seq_of(const Work& w, int b) {
     s.len = s.ok ? w.N : 0;
   }
   return s;
-}
-
-// Some sequence is bad: s is left out where it shares tokens with one before it.
-__device__ __forceinline__ void leave_shared_out(const Work& w, int b, Seq& s) {
-  if (w.q_start && s.len > 0 && shares_tokens(w.q_start, w.T, b, s.q0, s.q0 + s.len)) s.len = 0;
 }
 
 __device__ __forceinline__ int n_blocks(const Work& w, const Seq& s) { return (s.len + w.ctok - 1) >> w.ctok_log2; }
@@ -125,6 +116,7 @@ struct Item {
   int lg, b, i, tiles;
   long long first;
   Seq s;
+  int top;  // the largest end of the sequences so far
 };
 
 // Block-wide set-up: every thread of the CTA calls plan_find() once.  It sums the
@@ -144,12 +136,23 @@ __device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, lon
   Seq s{};
   long long v = 0, inc = 0, before = 0, total = 0;
   pl.odd = false;
+  int top = -1;  // the largest end in the rounds before, where some sequence is bad
   // This thread's sequence of a round, and the tiles of the round's sequences up to it and in all.
   // A bad one makes its warp's sum -1 and the total negative.
   auto round = [&](int k) {
     const int b = k * nt + tid;
     s = b < w.B ? seq_of(w, b) : Seq{0, 0, 0, true};
-    if (pl.odd) leave_shared_out(w, b, s);
+    if (pl.odd && w.q_start) {
+      int mine = top;
+      const int last = min(w.B, (k + 1) * nt);
+#pragma unroll 1
+      for (int j = k * nt; j < last; ++j) {
+        const int e = end_of(w.q_start, w.T, j);
+        if (j < b) mine = max(mine, e);
+        top = max(top, e);
+      }
+      if (s.q0 < mine) s.len = 0;
+    }
     v = inc = seq_tiles(w, s);
 #pragma unroll 1
     for (int o = 1; o < 32 && o < w.B; o <<= 1) {
@@ -177,9 +180,11 @@ __device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, lon
   bool found = false;
 #pragma unroll 1
   for (int k = 0; k < 2 * rounds && !found; ++k) {
+    if (k == rounds) top = -1;
     if (k < rounds || rounds > 1) round(k < rounds ? k : k - rounds);
-    if (total < 0) {  // a bad sequence: from here on those that share tokens are left out
+    if (total < 0) {  // the first bad sequence: the round is made again, without those that begin too early
       pl.odd = true;
+      if (k > 0 && w.q_start) top = w.q_start[k * nt];  // none was bad before
       --k;
       continue;
     }
@@ -224,6 +229,7 @@ __device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, lon
   it.b = (int)sh[64];
   it.i = (int)sh[65];
   it.s = Seq{(int)sh[67], (int)sh[68], (int)sh[69], true};
+  it.top = it.s.q0 + it.s.len;
   it.first = lg * per + sh[66];
   it.tiles = block_tiles(w, it.s, it.i);
   return true;
@@ -241,7 +247,11 @@ __device__ __forceinline__ bool next_item(const Work& w, bool odd, Item& it) {
       if (++it.lg == w.nl * w.nh) return false;
     }
     it.s = seq_of(w, it.b);
-    if (odd) leave_shared_out(w, it.b, it.s);
+    if (odd && w.q_start) {
+      if (it.b == 0) it.top = -1;
+      if (it.s.q0 < it.top) it.s.len = 0;
+      it.top = max(it.top, end_of(w.q_start, w.T, it.b));
+    }
   }
   it.tiles = block_tiles(w, it.s, it.i);
   return true;

@@ -183,10 +183,16 @@ __global__ void __launch_bounds__(kRopeThreads, 16) rope_kernel(const __grid_con
       }
       b = __reduce_min_sync(0xffffffffu, b);
       int slot = -2, p = 0;
-      int err = __any_sync(0xffffffffu, odd) ? MEDUSA_DEV_BAD_LENGTH : MEDUSA_DEV_OK;
+      int err = MEDUSA_DEV_OK, top = -1;
+      if (__any_sync(0xffffffffu, odd)) {
+        if (lane == 0) set_status(a.d_status, MEDUSA_DEV_BAD_LENGTH);
+#pragma unroll 1
+        for (int j = lane; j < b; j += 32) top = max(top, end_of(a.q_start, a.T, j));
+        top = __reduce_max_sync(0xffffffffu, top);
+      }
       if (b < a.B) {
         const int q0 = a.q_start[b], n = a.q_start[b + 1] - q0, L = a.prefix_len[b];
-        if (L < 0 || L > a.cache.rows() || (err && shares_tokens(a.q_start, a.T, b, q0, q0 + n))) {
+        if (L < 0 || L > a.cache.rows() || q0 < top) {
           err = MEDUSA_DEV_BAD_LENGTH;
         } else {
           const int row = L + (t - q0);

@@ -1,6 +1,6 @@
 """Starts that decrease or leave [0, T]: a sequence is entered and attended to by its own
-starts and by them alone, tokens that two sequences' starts hold are the first one's, and
-nothing of a refused sequence is read or written."""
+starts, one that begins before the end of an earlier one is refused, so that a token is one
+sequence's, and nothing of a refused sequence is read or written."""
 import numpy as np
 import pytest
 
@@ -27,9 +27,9 @@ def host64(t):
 
 
 def holders(q0, T):
-    """The sequences whose starts are in order, and hold tokens that no earlier such sequence's do."""
+    """The sequences whose starts are in order and not before the end of an earlier such sequence."""
     fine = [b for b in range(len(q0) - 1) if 0 <= q0[b] <= q0[b + 1] <= T]
-    return [b for b in fine if not any(j < b and q0[j] < q0[j + 1] and q0[j] < q0[b + 1] and q0[b] < q0[j + 1] for j in fine)]
+    return [b for b in fine if all(j >= b or q0[j + 1] <= q0[b] for j in fine)]
 
 
 def many():
@@ -46,6 +46,8 @@ CASES = {
     "negative": (10, [0, -4, 3, 10], [1, 0, 2]),
     "inside another": (30, [0, 20, 6, 9, 9, 30], [0, 2, 4, 0, 5]),
     "many sequences": (900, many(), [1] * 900),
+    "back in a later round": (900, [*range(500), 450, *range(501, 901)], [1] * 900),
+    "before all others": (20, [0, 0, 9, 12, 3, 6, 12, 20], [2, 0, 1, 4, 0, 3, 5]),
 }
 
 
@@ -119,3 +121,26 @@ def test_a_token_behind_its_sequence_reaches_no_page(mg):
     assert mg.medusa_status_check(st) in (OVERFLOW, BAD_LENGTH)  # the first to be seen
     assert np.array_equal(to_host(dk), kp) and np.array_equal(to_host(dv), vp)
     assert np.array_equal(to_host(out)[:, :50], q[:, :50]) and torch.all(out[:, 50:] == 7.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_hundred_thousand_sequences_one_of_them_bad(mg, dtype):
+    """One token each, which sees its own row alone; sequence 7's starts decrease and 8 begins before 6's end."""
+    B, dt = 100000, torch.bfloat16 if dtype == "bf16" else torch.float32
+    q0 = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    q0[8] = 6
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v, q = (torch.randn((1, B, 1, 64), generator=g, device="cuda").to(dt) for _ in range(3))
+    kp, vp = (torch.full((1, B, 8, 1, 64), 3.0, dtype=dt, device="cuda") for _ in range(2))
+    table, prefix = torch.arange(B, dtype=torch.int32, device="cuda").flip(0).view(B, 1).contiguous(), torch.zeros(B, dtype=torch.int32, device="cuda")
+    st, out = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full_like(q, 7.0)
+    mg.medusa_paged_append(k, v, kp, vp, table, q0, prefix, d_status=st)
+    assert mg.medusa_status_check(st) == BAD_LENGTH
+    mg.medusa_paged_attention(q, kp, vp, table, q0, prefix, out=out, d_status=st)
+    assert mg.medusa_status_check(st) == BAD_LENGTH
+    live = torch.ones(B, dtype=torch.bool, device="cuda")
+    live[7:9] = False
+    assert torch.equal(out[:, live], v[:, live]) and torch.all(out[:, ~live] == 7.0)
+    rows = kp.flip(1)[0, :, 0], vp.flip(1)[0, :, 0]
+    assert torch.equal(rows[0][live], k[0][live]) and torch.equal(rows[1][live], v[0][live])
+    assert torch.all(rows[0][~live] == 3.0) and torch.all(kp[:, :, 1:] == 3.0)
