@@ -235,13 +235,17 @@ __device__ __forceinline__ bool plan_find(const Work& w, Plan& pl, Item& it, lon
   return true;
 }
 
-// The next item in order (`odd`: the plan's); false behind the last one.
+// The next item in order (`odd`: the plan's); false behind the last one.  Whole warps.  Behind a few
+// sequences without tokens, 32 at a time are passed over: other warps wait for the item meanwhile,
+// and a million of them, one by one, took longer than a wait may.
 __device__ __forceinline__ bool next_item(const Work& w, bool odd, Item& it) {
   it.first += it.tiles;
   ++it.i;
 #pragma unroll 1
-  while (it.s.len == 0 || it.i >= n_blocks(w, it.s)) {
+  for (int n = 0; it.s.len == 0 || it.i >= n_blocks(w, it.s); ++n) {
     it.i = 0;
+    if (n >= 8 && !odd)
+      while (it.b + 33 < w.B && !__any_sync(0xffffffffu, seq_of(w, it.b + 1 + (threadIdx.x & 31)).len)) it.b += 32;
     if (++it.b == w.B) {
       it.b = 0;
       if (++it.lg == w.nl * w.nh) return false;
