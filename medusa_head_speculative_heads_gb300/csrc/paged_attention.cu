@@ -556,7 +556,7 @@ static medusa_status chunk_attention(const void* q, int64_t ldq, const void* k_p
   if (!sizes_ok(n_layers, T, B, Hq, Hkv, d, n_pages, page_size, max_pages, scale, dt)) return MEDUSA_ERR_INVALID_ARG;
   if (ldq < (int64_t)Hq * d || ldq % 4 || !aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
     return MEDUSA_ERR_INVALID_ARG;
-  const uintptr_t words = (uintptr_t)page_table | (uintptr_t)q_start | (uintptr_t)prefix_len | (uintptr_t)lse;
+  const uintptr_t words = (uintptr_t)page_table | (uintptr_t)q_start | (uintptr_t)prefix_len | (uintptr_t)lse | (uintptr_t)d_status;
   if (words & 3) return MEDUSA_ERR_INVALID_ARG;
   if (tc_shape(Hq / Hkv, d, page_size, dt) && ldq % 8) return MEDUSA_ERR_INVALID_ARG;
   const size_t es = dtype_bytes(dt), tokens = (size_t)n_layers * T;
@@ -613,7 +613,7 @@ extern "C" medusa_status medusa_paged_tree_attention(const void* q, const void* 
   const void* rows[] = {q, k_pages, v_pages, kt, vt, out};
   for (const void* p : rows)
     if (!aligned16(p)) return MEDUSA_ERR_INVALID_ARG;
-  const uintptr_t words = (uintptr_t)page_table | (uintptr_t)mask | (uintptr_t)prefix_len | (uintptr_t)lse;
+  const uintptr_t words = (uintptr_t)page_table | (uintptr_t)mask | (uintptr_t)prefix_len | (uintptr_t)lse | (uintptr_t)d_status;
   if (words & 3) return MEDUSA_ERR_INVALID_ARG;
   const size_t es = dtype_bytes(dt), tokens = (size_t)n_layers * B * N;
   const size_t no = tokens * Hq * d * es, nt = tokens * Hkv * d * es, nl = tokens * Hq * 4;

@@ -118,7 +118,8 @@ extern "C" medusa_status medusa_paged_compact(void* k_pages, void* v_pages, cons
   if (rows > INT_MAX) return MEDUSA_ERR_INVALID_ARG;
   const size_t es = dtype_bytes(dt), row_bytes = (size_t)Hkv * d * es;
   const uintptr_t all = (uintptr_t)k_pages | (uintptr_t)v_pages | (uintptr_t)kt | (uintptr_t)vt;
-  const uintptr_t ints = (uintptr_t)page_table | (uintptr_t)path_nodes | (uintptr_t)accept_len | (uintptr_t)prefix_len | (uintptr_t)new_len;
+  const uintptr_t ints = (uintptr_t)page_table | (uintptr_t)path_nodes | (uintptr_t)accept_len | (uintptr_t)prefix_len |
+                         (uintptr_t)new_len | (uintptr_t)d_status;
   if ((all & (es - 1)) || (ints & 3)) return MEDUSA_ERR_INVALID_ARG;
   const size_t np = (size_t)n_layers * n_pages * page_size * row_bytes, nt = (size_t)n_layers * B * N * row_bytes;
   if (overlaps(k_pages, np, v_pages, np)) return MEDUSA_ERR_ALIAS;

@@ -429,7 +429,7 @@ extern "C" medusa_status medusa_paged_append(const void* q, int64_t ldq, const v
   if ((q && ldq < (int64_t)Hq * d) || ldk < (int64_t)Hkv * d || ldv < (int64_t)Hkv * d) return MEDUSA_ERR_INVALID_ARG;
   const size_t es = dtype_bytes(dt);
   const uintptr_t all = (uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out | (uintptr_t)k_pages | (uintptr_t)v_pages;
-  const uintptr_t words = (uintptr_t)pos | (uintptr_t)page_table | (uintptr_t)q_start | (uintptr_t)prefix_len;
+  const uintptr_t words = (uintptr_t)pos | (uintptr_t)page_table | (uintptr_t)q_start | (uintptr_t)prefix_len | (uintptr_t)d_status;
   if ((all & (es - 1)) || (words & 3)) return MEDUSA_ERR_INVALID_ARG;
   const size_t np = (size_t)n_layers * n_pages * page_size * Hkv * d * es;
   const size_t nk = span(n_layers, T, ldk, Hkv, d, es), nv = span(n_layers, T, ldv, Hkv, d, es);
