@@ -488,7 +488,8 @@ medusa_status medusa_paged_append(const void* q, int64_t ldq, const void* k, int
 /* medusa_paged_attention: causal attention of the chunk over the cache, the
  * chunk's own rows included (enter them first): token i of sequence b sees rows
  * 0 .. prefix_len[b] + i.  For q head h and kv head h / G, G = Hq / Hkv:
- *   out = softmax(scale q K^T) V   (fp32 scores, softmax and accumulation)
+ *   out = softmax(scale q K^T) V   (fp32 scores, softmax and accumulation; on tensor
+ *   cores the probabilities are rounded to bf16 for the product with V, their sum is not)
  *   q   [n_layers][T][Hq][d] with ldq as in medusa_rope
  *   out [n_layers][T][Hq][d] dt;  lse [n_layers][T][Hq] fp32 or NULL: the natural
  *   logarithm of the sum of exp(scale q.k) over the visible keys.

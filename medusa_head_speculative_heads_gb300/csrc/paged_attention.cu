@@ -43,8 +43,8 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v) {
 // A warp none of whose rows exists takes part in the copies only.
 // Products are taken two at a time (fma.rn.f32x2: over even and odd columns in the
 // scores, over pairs of columns in the sums).  Measured, fp32, 5 ragged sequences of
-// up to 331 tokens behind up to 1338 rows, 8 + 4 heads of 64: the kernel 85 us, with the
-// merge 93 us, 21 TFLOP/s (with single products and loads between two barriers 114 us).
+// up to 331 tokens behind up to 1338 rows, 8 + 4 heads of 64: the kernel 86 us, with the
+// merge 90 to 98 us, 21 TFLOP/s (with single products and loads between two barriers 114 us).
 // Shared memory's pipe bounds it, busy for 64 % of the clocks (the FMA pipe for 47 %): a
 // 16-byte load takes four of them when lanes read several rows and two as a broadcast,
 // 24 for the 64 products of four columns.  A warp of 8 rows x 64 keys, each K row
@@ -421,9 +421,12 @@ static Division divide(int T, int B, int Hq, int Hkv, int d, int page_size, medu
   v.tc = tc_shape(G, d, page_size, dt);
   if (v.tc) {
     // Blocks of up to 64 rows where a sequence has no more on average (decoding, trees), else of
-    // two tiles of 128: right for any lengths, but the first streams keys faster (a decoding token
-    // of 64 sequences 194 us, in the wide blocks 200; a 64-node verify pass of 32 layers 113 and 120)
-    // and the second reads them less often (a prompt's block 4 times).
+    // two tiles of 128.  The first streams keys faster (a decoding token of 64 sequences 194 us, in the
+    // wide blocks 200; a 64-node verify pass of 32 layers 113 and 120), the second reads a
+    // prompt's keys a quarter as often.  The mean decides for the whole call: a prompt among so many
+    // decoding sequences that it stays low runs in narrow blocks, which fill half of each product
+    // (32 + 8 heads; 60 sequences 106 us and 512 tokens 23, in one call 139; with 2048 tokens, 70 us,
+    // the wide blocks take both: 193).
     const bool narrow = (long long)T * G <= 64ll * B && G <= 64;
     v.R = narrow ? 64 : 256;
     v.tile_rows = narrow ? 64 : 128;

@@ -35,8 +35,9 @@
 // stale row holds could be NaN), and the products stop there.
 //
 // What bounds it: decoding, memory (64 sequences of up to 8192 rows 188 to 194 us, 6.3 to 6.5
-// TB/s).  A long prompt (8192 tokens over 8192 rows, 32 + 8 heads of 128: 1051 to 1094 us,
-// 1510 to 1570 TFLOP/s), a stream's chain of softmax (1160 clocks a tile), hand-over of P (250),
+// TB/s).  A long prompt (8192 tokens over 8192 rows, 32 + 8 heads of 128: 1053 to 1105 us captured
+// one after the other, 1490 to 1565 TFLOP/s; 1130 to 1142, 1445 to 1460, called one by one on
+// other data each time), a stream's chain of softmax (1160 clocks a tile), hand-over of P (250),
 // products (768 behind the second half) and hand-over of S (330), half of which the other
 // stream's products fill.  Prompts of a few thousand tokens, also the hand-over between blocks
 // (some 6000 clocks: the last products, the output of 256 rows, Q, the first scores).
@@ -216,7 +217,7 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 // other came to the probabilities 500 clocks after they were there.  The lanes ask again and again
 // (kPolls times at most, about a second) and do not sleep on a barrier, which woke them
 // some 100 clocks late; for the eight softmax warps that would take issue slots from one another
-// (8192 tokens over 8192 rows: 1051 us so, with sleeping waits 1079, with all waits so 1094).
+// (8192 tokens over 8192 rows, in turn on one box: 1051 us so, with sleeping waits 1079, with all waits so 1094).
 __device__ __forceinline__ bool lanes_wait(uint64_t* bar, uint32_t parity, bool need, volatile int* abort) {
   bool ok = !need;
 #pragma unroll 1

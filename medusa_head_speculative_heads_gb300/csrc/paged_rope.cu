@@ -17,10 +17,10 @@
 // (more when a token has fewer than 128 tasks of two vectors), one task in flight a
 // thread, its angles formed once into shared memory while the first loads are on
 // their way.  Measured, 10782 prompt tokens with 32 + 8 + 8 heads entered into
-// the cache: 44 us (6.0 TB/s); with 256 threads 56 us, with two, three or four
+// the cache: 44 us (6.0 TB/s), in sixteen CTAs an SM (32 registers); with 256 threads 56 us, with two, three or four
 // tasks in flight 49 to 52 us, with the next task's loads ahead of the turn 48 us
 // (registers: fewer CTAs on an SM), with a thread's angles kept in registers over its
-// heads 51 us (the same).  32 layers of 64 tokens with 32 + 32 heads: 13.5
+// heads 51 us (the same).  32 layers of 64 tokens with 32 + 32 heads: 13.1
 // us; 16384 fp32 tokens with 32 + 8 heads: 99 us (6.8 TB/s).
 #include <cmath>
 
@@ -117,8 +117,8 @@ __device__ __forceinline__ float2 turn_of(int p, unsigned long long turn, int in
   return make_float2(cc * m, ss * m);
 }
 
-// Sixteen CTAs an SM (32 registers, none spilled): with 40, which the look for a token's sequence
-// would take, the prompts' 44 us are 48.
+// Sixteen CTAs an SM, 32 registers: with 40, which the look for a token's sequence would take,
+// the prompts' 44 us are 48.
 template <typename T, int W, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 16) rope_kernel(const __grid_constant__ RopeArgs a) {
   using C = Chunk<T, W>;
