@@ -95,8 +95,8 @@ def medusa_rope(q, k, pos, rope: RopeSpec, q_out=None, k_out=None, inverse: bool
     """Rotary embedding of q [nl, T, Hq, d] and k [nl, T, Hkv, d] (or None) at pos
     [T] int32; returns (q_out, k_out), new tensors unless given (q_out may be q,
     k_out may be k).  inverse=True maps gradients of the outputs to those of the
-    inputs; new outputs of inputs that require grad do so by themselves (given ones
-    record nothing)."""
+    inputs; outputs of inputs that require grad do so by themselves, unless q_out or
+    k_out is given (nothing is recorded then)."""
     if stream is not None:
         return _on(stream, q, medusa_rope, q, k, pos, rope, q_out, k_out, inverse)
     if q_out is None and k_out is None and torch.is_grad_enabled() and (
