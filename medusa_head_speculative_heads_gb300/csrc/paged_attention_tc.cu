@@ -217,7 +217,7 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 // other came to the probabilities 500 clocks after they were there.  The lanes ask again and again
 // (kPolls times at most, about a second) and do not sleep on a barrier, which woke them
 // some 100 clocks late; for the eight softmax warps that would take issue slots from one another
-// (8192 tokens over 8192 rows, in turn on one box: 1051 us so, with sleeping waits 1079, with all waits so 1094).
+// (8192 tokens over 8192 rows, in turn on one machine: 1051 us so, with sleeping waits 1079, with all waits so 1094).
 __device__ __forceinline__ bool lanes_wait(uint64_t* bar, uint32_t parity, bool need, volatile int* abort) {
   bool ok = !need;
 #pragma unroll 1
