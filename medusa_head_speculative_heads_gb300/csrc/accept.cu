@@ -135,7 +135,7 @@ node_partial_kernel(const float* __restrict__ logits, int N, int V, int C, float
           const float a = (x[j] - mv) * inv_t;
           const float w = expf(a);
           s2 += w;
-          e2 = fmaf(w, a, e2);
+          if (w > 0.f) e2 = fmaf(w, a, e2);  // a logit of -inf: 0 times -inf
         }
       }
       s2 = warp_sum(s2);
@@ -183,7 +183,7 @@ node_partial_kernel(const float* __restrict__ logits, int N, int V, int C, float
           const float a = (x[j] - mv) * inv_t;
           const float w = expf(a);
           s += w;
-          e = fmaf(w, a, e);
+          if (w > 0.f) e = fmaf(w, a, e);
         }
       }
     } else {
@@ -191,7 +191,7 @@ node_partial_kernel(const float* __restrict__ logits, int N, int V, int C, float
         const float a = (z[v] - mv) * inv_t;
         const float w = expf(a);
         s += w;
-        e = fmaf(w, a, e);
+        if (w > 0.f) e = fmaf(w, a, e);
       }
     }
     S = block_sum(s, sv);
@@ -327,7 +327,7 @@ select_path_kernel(const float* __restrict__ logits, const int32_t* __restrict__
         ok = 0;
         p = 0.f;
       } else if (T > 0.f) {
-        p = expf((z_px - zmax[pc]) / T) / ssum[pc];
+        p = ssum[pc] == 0.f ? 0.f : expf((z_px - zmax[pc]) / T) / ssum[pc];  // 0: the parent's logits are all -inf
         ok = p > t;
       } else {
         ok = x == amax[pc];
