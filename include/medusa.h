@@ -550,6 +550,94 @@ medusa_status medusa_paged_compact(void* k_pages, void* v_pages, const int32_t* 
                                    int Hkv, int d, int n_pages, int page_size, int max_pages, int Dmax,
                                    medusa_dtype dt, int32_t* d_status, medusa_stream_t stream);
 
+/* ------------------------------------------------------- (k) 4-bit weights
+ * The verify pass's linear layers with weights kept in 4 bits: decoding is bound by
+ * the bytes of the weights (paper review, roofline in "实验设计与结果"), and 4 bits and
+ * a scale a group are a quarter of them.
+ *   qweight [Nout][K/8] 32-bit words: elements 8j .. 8j+7 of a row in word j, element
+ *           8j + 2i in bits 4i .. 4i+3 and element 8j + 2i + 1 in bits 16+4i .. 19+4i
+ *   scales  [K/group][Nout] bf16, zeros [K/group][Nout] bytes 0 .. 127 (their top bit is
+ *           ignored) or NULL (8 everywhere)
+ * Element (n, k) stands for the bf16 nearest to scale * (q - zero), scale and zero
+ * those of group k / group: a matrix of bf16 weights, as medusa_linear takes it.
+ * group is 32, 64 or 128, K a multiple of it; K, Nout and T < 2^31 - 2^16.
+ *
+ * medusa_w4_quantize: words, scales and zeros of w [Nout][K] (dt), set-up work.
+ *   symmetric == 0: lo = min(w, 0), hi = max(w, 0) over the group, scale = bf16((hi - lo) / 15),
+ *     zero = rint(-lo / scale), q = rint(w / scale) + zero, both clamped to 0 .. 15
+ *   symmetric != 0: scale = bf16(max |w| / 7), q = rint(w / scale) + 8 clamped to 0 .. 15;
+ *     zeros may be NULL (else 8 is written)
+ * fp32 arithmetic, each operation rounded on its own, halves to even.  A group whose
+ * scale would be 0 gets scale 1 and stands for zeros; one that holds NaN or an infinity, or whose
+ * scale would be one, gets the scale NaN. */
+medusa_status medusa_w4_quantize(const void* w, int Nout, int K, int group, int symmetric, medusa_dtype dt,
+                                 uint32_t* qweight, void* scales, uint8_t* zeros, medusa_stream_t stream);
+
+/* medusa_linear_w4: y = x W^T, W in 4 bits.
+ *   x [T][K] bf16, ldx elements from one row to the next (>= K, a multiple of 8);
+ *   y [T][Nout], bf16 or fp32 (y_dt), rounded once from fp32 sums.
+ * T >= 0 (nothing is launched for 0).  x and qweight 16-byte aligned.  y must
+ * overlap no other buffer (ALIAS).  A row of x with NaN or infinities changes that
+ * row of y alone.  Sums are made in a fixed order (deterministic on a given device).
+ * Workspace: medusa_linear_w4_workspace_size() bytes for the current device (0: none
+ * needed), 16-byte aligned, its contents before the call do not matter; calls that
+ * may run at the same time need one each. */
+size_t medusa_linear_w4_workspace_size(int T, int K, int Nout, int group);
+medusa_status medusa_linear_w4(const void* x, int64_t ldx, const uint32_t* qweight, const void* scales,
+                               const uint8_t* zeros, int T, int K, int Nout, int group, void* y, medusa_dtype y_dt,
+                               void* ws, size_t ws_bytes, int32_t* d_status, medusa_stream_t stream);
+
+/* ------------------------------------------- (l) what requests ask of logits
+ * Between the output head and medusa_typical_accept: penalties for tokens that
+ * were said, biases, and the tokens a grammar leaves.  In a tree each node has a context
+ * of its own, the sequence and then the tokens on the path from the root to it
+ * (guide, "树形验证": every candidate is verified in its own context).
+ *   logits [B][N][V] (dt), ld elements from one row to the next (>= V; node n of row b is
+ *   row b * N + n); out [B][N][V] fp32, dense; out may be logits when those are fp32
+ *   and dense.  For z = logits[b][n][v]:
+ *     c = counts[b][v] + the times v occurs among tokens[b][j], j on the path root .. n
+ *     c > 0 or prompt bit v of row b:  z = z > 0 ? z / repetition[b] : z * repetition[b]
+ *     z = z - frequency[b] * c - presence[b] (the latter where c > 0)
+ *     z = z + bias[v]
+ *     -inf, whatever z is, where bit v of the node's mask row is 0
+ *   in fp32.  A part whose pointer is NULL is left out (counts: 0).
+ * t NULL: the rows have no tokens of their own (N >= 1 of any size, tokens ignored);
+ * else N = t->n_nodes, tokens [B][N] as from medusa_tree_build.
+ * A token outside [0, V) on a path sets BAD_INDEX and is passed over; a parent that is
+ * not an earlier node sets BAD_TOPOLOGY and ends the path there; a mask_row outside
+ * [-1, n_masks) sets BAD_INDEX and leaves the node without a mask.  A mask that
+ * leaves nothing makes a row of -inf.  out must overlap nothing else (ALIAS).
+ * V < 2^31 - 2^16, B * N < 2^31; pointers are aligned to their element size. */
+typedef struct medusa_logits_rules {
+  const int32_t* counts;       /* [B][V] tokens said so far, the prompt's left out */
+  const uint32_t* prompt_bits; /* [B][ceil(V/32)] bit v % 32 of word v / 32: v is in the prompt */
+  const float* repetition;     /* [B] > 0 */
+  const float* frequency;      /* [B] */
+  const float* presence;       /* [B] */
+  const float* bias;           /* [bias_rows][V] */
+  const uint32_t* mask;        /* [n_masks][ceil(V/32)] 1: the token may follow */
+  const int32_t* mask_row;     /* [B][N] row of mask, -1: none; NULL: row b * N + n (n_masks = B * N) */
+  int32_t bias_rows;           /* 1 or B */
+  int32_t n_masks;
+} medusa_logits_rules;
+medusa_status medusa_logits_process(const void* logits, int64_t ld, medusa_dtype dt, const medusa_logits_rules* rules,
+                                    const int32_t* tokens, const medusa_dev_topology* t, int B, int N, int V,
+                                    float* out, int32_t* d_status, medusa_stream_t stream);
+
+/* medusa_count_tokens: enters tokens [B][S] (negative: padding) into counts [B][V]
+ * (one more each) and / or prompt_bits [B][ceil(V/32)] (their bits set); either may be NULL, not both.
+ * A token >= V sets BAD_INDEX and is passed over.  S >= 0.
+ * medusa_count_accepted: the tokens of the accepted path, counts[b][tokens[b][path_nodes[b][i]]]
+ * + 1 for i < accept_len[b] (tokens [B][N], path_nodes [B][Dmax+1]).  An accept_len outside
+ * 1 .. Dmax+1, a path node outside [0, N) or a token outside [0, V) on the path sets
+ * BAD_INDEX and nothing of that row is counted.
+ * What a call writes must overlap nothing else (ALIAS). */
+medusa_status medusa_count_tokens(const int32_t* tokens, int B, int S, int V, int32_t* counts, uint32_t* prompt_bits,
+                                  int32_t* d_status, medusa_stream_t stream);
+medusa_status medusa_count_accepted(const int32_t* tokens, const int32_t* path_nodes, const int32_t* accept_len,
+                                    int B, int N, int Dmax, int V, int32_t* counts, int32_t* d_status,
+                                    medusa_stream_t stream);
+
 /* ------------------------------------------------------------------ status
  * Synchronises `stream`, copies the device status word to *host_code and
  * resets it to 0.  Returns CUDA_ERROR if the stream holds a failed launch. */

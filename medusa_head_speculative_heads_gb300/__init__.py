@@ -2,8 +2,8 @@
 typical acceptance and KV compaction as hand-written sm_103a CUDA kernels
 behind the C ABI of include/medusa.h (libmedusa_gb300.so).
 
-The Python names mirror the C entry points; see ``binding`` and ``paged`` for
-the argument marshalling.
+The Python names mirror the C entry points; see ``binding``, ``paged`` and ``verify``
+for the argument marshalling.
 """
 from .binding import (  # noqa: F401
     DEV_CODES, EXPORTS, MEDUSA_BF16, MEDUSA_F32, DevTopology, MedusaError, Topology, lib, lib_path,
@@ -14,4 +14,7 @@ from .binding import (  # noqa: F401
 from .build import build  # noqa: F401
 from .paged import (  # noqa: F401
     RopeSpec, medusa_paged_append, medusa_paged_attention, medusa_paged_compact, medusa_paged_tree_attention, medusa_rope,
+)
+from .verify import (  # noqa: F401
+    medusa_count_accepted, medusa_count_tokens, medusa_linear_w4, medusa_logits_process, medusa_w4_quantize,
 )

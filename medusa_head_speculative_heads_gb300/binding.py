@@ -34,6 +34,8 @@ EXPORTS = (
     "medusa_head_loss_workspace_size", "medusa_head_loss", "medusa_rope_plan_init", "medusa_rope",
     "medusa_paged_append", "medusa_paged_attention_workspace_size", "medusa_paged_attention",
     "medusa_paged_tree_attention", "medusa_paged_compact", "medusa_paged_attention_test_stall",
+    "medusa_w4_quantize", "medusa_linear_w4_workspace_size", "medusa_linear_w4", "medusa_logits_process",
+    "medusa_count_tokens", "medusa_count_accepted",
 )
 
 
@@ -108,6 +110,12 @@ def lib():
             "medusa_paged_attention_test_stall": (I, [P, LL, P, P, P, P, P] + [I] * 9 + [F, I, P, P, P, Z, P, P]),
             "medusa_paged_tree_attention": (I, [P] * 8 + [I] * 9 + [F, I, P, P, P, Z, P, P]),
             "medusa_paged_compact": (I, [P] * 9 + [I] * 10 + [P, P]),
+            "medusa_w4_quantize": (I, [P, I, I, I, I, I, P, P, P, P]),
+            "medusa_linear_w4_workspace_size": (Z, [I] * 4),
+            "medusa_linear_w4": (I, [P, LL, P, P, P, I, I, I, I, P, I, P, Z, P, P]),
+            "medusa_logits_process": (I, [P, LL, I, P, P, P, I, I, I, P, P, P]),
+            "medusa_count_tokens": (I, [P, I, I, I, P, P, P, P]),
+            "medusa_count_accepted": (I, [P, P, P, I, I, I, I, P, P, P]),
             "medusa_acc_update": (I, [P, P, P, I, I, ctypes.c_double, P]),
             "medusa_topology_greedy_device_elems": (Z, [I, I]),
             "medusa_topology_greedy_device": (I, [P, I, I, I, P, Z, P, P, P, P]),
@@ -220,6 +228,11 @@ class Topology:
 class medusa_rope_plan(ctypes.Structure):
     _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float),
                 ("reserved", ctypes.c_int32), ("turn", ctypes.c_uint64 * 128)]
+
+
+class medusa_logits_rules(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("counts", "prompt_bits", "repetition", "frequency", "presence", "bias", "mask",
+                                               "mask_row")] + [("bias_rows", ctypes.c_int32), ("n_masks", ctypes.c_int32)]
 
 
 class DevTopology:

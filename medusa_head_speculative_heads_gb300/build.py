@@ -4,13 +4,15 @@ Each translation unit is compiled in parallel to an object file, then linked
 into one shared library with the CUDA runtime linked statically, so the library
 loads on a machine without a GPU (entry points then return MEDUSA_ERR_CUDA).
 
-Where torch is installed, the compiled binding of the paged-cache calls
-(csrc/python) is built beside it, against that torch's headers.
+Where torch is installed, the compiled bindings of the calls that are made once per
+layer (csrc/python) are built beside it, against that torch's headers.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.machinery
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -49,12 +51,26 @@ def up_to_date() -> bool:
     return _newer(LIB, _deps())
 
 
-def binding_path() -> str:
+BINDINGS = ("paged_binding", "verify_binding")
+
+
+def binding_path(name: str = BINDINGS[0]) -> str:
     """The compiled binding for this Python (version, platform) and the installed
     torch (version, C++ ABI)."""
     import torch
     abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
-    return os.path.join(BUILD, f"paged_binding-{torch.__version__}-abi{abi}{sysconfig.get_config_var('EXT_SUFFIX')}")
+    return os.path.join(BUILD, f"{name}-{torch.__version__}-abi{abi}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def load_binding(name: str):
+    """The compiled binding as a module (raises if it has not been built)."""
+    path = binding_path(name)
+    if not os.path.exists(path):
+        raise FileNotFoundError(f"{path} does not exist: run medusa_head_speculative_heads_gb300.build.build() first")
+    spec = importlib.util.spec_from_loader(name, importlib.machinery.ExtensionFileLoader(name, path))
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
 
 
 def build_binding(force: bool = False) -> None:
@@ -64,21 +80,27 @@ def build_binding(force: bool = False) -> None:
         import torch
     except ImportError:
         return
-    src, out = os.path.join(CSRC, "python", "paged_binding.cpp"), binding_path()
-    if not force and _newer(out, [src, os.path.join(INCLUDE, "medusa.h")]):
-        return
     t = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    tmp = out + f".{os.getpid()}.tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", src, "-o", tmp]
-    for d in (INCLUDE, f"{t}/include", f"{t}/include/torch/csrc/api/include", f"{cuda}/include", sysconfig.get_paths()["include"]):
-        cmd += ["-I", d]
-    cmd += [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-L{t}/lib", "-ltorch_python", "-ltorch_cpu",
-            "-lc10_cuda", "-lc10", f"-L{BUILD}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"the binding does not build:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, out)
+    deps = glob.glob(os.path.join(CSRC, "python", "*.h")) + [os.path.join(INCLUDE, "medusa.h")]
+
+    def compile_one(name):
+        src, out = os.path.join(CSRC, "python", f"{name}.cpp"), binding_path(name)
+        if not force and _newer(out, [src] + deps):
+            return
+        tmp = out + f".{os.getpid()}.tmp"
+        cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", src, "-o", tmp]
+        for d in (INCLUDE, f"{t}/include", f"{t}/include/torch/csrc/api/include", f"{cuda}/include", sysconfig.get_paths()["include"]):
+            cmd += ["-I", d]
+        cmd += [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-L{t}/lib", "-ltorch_python", "-ltorch_cpu",
+                "-lc10_cuda", "-lc10", f"-L{BUILD}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{name} does not build:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, out)
+
+    with cf.ThreadPoolExecutor(len(BINDINGS)) as ex:
+        list(ex.map(compile_one, BINDINGS))
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list | None = None) -> str:

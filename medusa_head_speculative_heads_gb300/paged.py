@@ -9,12 +9,9 @@ recorded by medusa_rope where it makes its outputs, and by no other call.
 from __future__ import annotations
 
 import ctypes
-import importlib.machinery
-import importlib.util
-import os
 
 from . import binding as B_
-from .build import binding_path
+from .build import load_binding
 
 try:
     import torch
@@ -27,12 +24,7 @@ _native = None
 def _load():
     """The compiled binding (raises if it has not been built)."""
     global _native
-    path = binding_path()
-    if not os.path.exists(path):
-        raise FileNotFoundError(f"{path} does not exist: run medusa_head_speculative_heads_gb300.build.build() first")
-    spec = importlib.util.spec_from_loader("paged_binding", importlib.machinery.ExtensionFileLoader("paged_binding", path))
-    _native = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(_native)
+    _native = load_binding("paged_binding")
     return _native
 
 

@@ -19,6 +19,7 @@ import torch
 
 from . import binding as B_
 from . import paged as P_
+from . import verify as V_
 
 
 class VerifyStep:
@@ -42,6 +43,7 @@ class VerifyStep:
         self.next_tok = torch.empty(B, **i32)
         self.new_len = torch.empty(B, **i32)
         self.status = torch.zeros(1, **i32)
+        self.processed = None  # logits as constrain() leaves them, where they need a place
         L = B_.lib()
         dt = B_.MEDUSA_BF16 if dtype == torch.bfloat16 else B_.MEDUSA_F32
         self.ws_heads = B_._ws(L.medusa_heads_workspace_size(B, H, V, K, topk), device)
@@ -77,6 +79,22 @@ class VerifyStep:
         B_.medusa_typical_accept(logits, self.tokens, self.topo, self.T, self.eps, self.delta, self.accept_len,
                                  self.path_nodes, self.next_tok, ws=self.ws_acc, d_status=self.status,
                                  stream=stream)
+
+    def constrain(self, logits, stream=None, **rules):
+        """The base logits [B, N, V] as the requests want them, each node with its path as
+        context (the rules of medusa_logits_process), for accept(): in place where the logits are
+        fp32 and dense, else in a buffer that the step keeps.  Between tree() and accept()."""
+        if logits.dtype == torch.float32 and logits.is_contiguous():
+            out = logits
+        else:
+            if self.processed is None:
+                self.processed = torch.empty(logits.shape, dtype=torch.float32, device=logits.device)
+            out = self.processed
+        return V_.medusa_logits_process(logits, tokens=self.tokens, topo=self.topo, out=out, d_status=self.status, stream=stream, **rules)
+
+    def count(self, counts, stream=None):
+        """Counts the accepted path's tokens into counts [B, V]; after accept()."""
+        return V_.medusa_count_accepted(counts, self.tokens, self.path_nodes, self.accept_len, d_status=self.status, stream=stream)
 
     def compact(self, kc, vc, kt, vt, prefix_len, stream=None):
         B_.medusa_kv_compact(kc, vc, kt, vt, self.path_nodes, self.accept_len, prefix_len, self.new_len,
