@@ -6,49 +6,12 @@
 // logic operation unpack a pair.
 #include <math.h>
 
-#include "common.cuh"
 #include "host_util.h"
+#include "linear_w4.h"
+#include "medusa_test_hooks.h"
 
 namespace medusa {
 namespace w4 {
-
-struct Args {
-  const uint16_t* x;
-  long long ldx;
-  const uint32_t* q;
-  const uint16_t* scales;
-  const uint8_t* zeros;
-  int T, K, Nout, glog;  // glog: log2 of the group
-  void* y;
-  int y32;
-};
-
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// What a group's weights are made of: 128 + zero and the scale, twice each.
-struct Group {
-  uint32_t base, scale;
-};
-__device__ __forceinline__ Group group_at(const Args& a, int g, int n) {
-  const size_t i = (size_t)g * a.Nout + n;
-  const uint32_t s = a.scales[i];
-  const uint32_t b = 0x4300u | (a.zeros ? a.zeros[i] & 127u : 8u);
-  return {b | b << 16, s | s << 16};
-}
-// The four pairs of a word.
-__device__ __forceinline__ void unpack(uint32_t w, const Group& g, uint32_t* p) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) p[i] = mul2(sub2(((w >> (4 * i)) & 0x000f000fu) | 0x43004300u, g.base), g.scale);
-}
 
 // 16 bytes of weights, which are read once.
 __device__ __forceinline__ uint4 load_once(const void* p) {
@@ -61,12 +24,6 @@ __device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uin
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void store_y(const Args& a, int t, int n, float v) {
-  const size_t i = (size_t)t * a.Nout + n;
-  if (a.y32) static_cast<float*>(a.y)[i] = v;
-  else static_cast<uint16_t*>(a.y)[i] = (uint16_t)f32_to_bf16_bits(v);
 }
 
 // ------------------------------------------------------------------ few tokens
@@ -84,7 +41,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(const __grid_constant_
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int mtiles = (a.Nout + 15) / 16, mt = blockIdx.x % mtiles, t0 = blockIdx.x / mtiles * (8 * NT);
+  const int mt = blockIdx.x;
   const int n_lo = min(mt * 16 + g, a.Nout - 1), n_hi = min(mt * 16 + g + 8, a.Nout - 1);  // rows past the last: computed, not stored
   const uint8_t *w_lo = reinterpret_cast<const uint8_t*>(a.q) + (size_t)n_lo * (a.K / 2), *w_hi = reinterpret_cast<const uint8_t*>(a.q) + (size_t)n_hi * (a.K / 2);
   float acc[NT][4] = {};
@@ -104,8 +61,8 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(const __grid_constant_
       g_hi = group_at(a, k >> a.glog, n_hi);
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        if (t0 + 8 * j + g < a.T) {
-          const uint4* p = reinterpret_cast<const uint4*>(a.x + (t0 + 8 * j + g) * a.ldx + k);
+        if (8 * j + g < a.T) {
+          const uint4* p = reinterpret_cast<const uint4*>(a.x + (8 * j + g) * a.ldx + k);
 #pragma unroll
           for (int i = 0; i < 4; ++i) xv[j][i] = p[i];
         }
@@ -135,7 +92,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(const __grid_constant_
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) v += part[w][tok >> 3][m][tok & 7];
-    if (t0 + tok < a.T && mt * 16 + m < a.Nout) store_y(a, t0 + tok, mt * 16 + m, v);
+    if (tok < a.T && mt * 16 + m < a.Nout) store_y(a, tok, mt * 16 + m, v);
   }
 }
 
@@ -214,18 +171,28 @@ extern "C" medusa_status medusa_w4_quantize(const void* w, int Nout, int K, int 
   return launch_status();
 }
 
-extern "C" size_t medusa_linear_w4_workspace_size(int T, int K, int Nout, int group) { return 0; }
+// Up to 16 tokens the warps' own product instructions, fed from registers; more on tensor memory.
+static bool on_tc(int T) { return T > 16; }
 
-extern "C" medusa_status medusa_linear_w4(const void* x, int64_t ldx, const uint32_t* qweight, const void* scales, const uint8_t* zeros, int T,
-                                          int K, int Nout, int group, void* y, medusa_dtype y_dt, void* ws, size_t ws_bytes, int32_t* d_status,
-                                          medusa_stream_t stream) {
+extern "C" size_t medusa_linear_w4_workspace_size(int T, int K, int Nout, int group) {
+  return T < 1 || T >= 0x7fffffff - 65536 || !sizes_ok(K, Nout, group) || !on_tc(T) ? 0 : tc_workspace(T, K, Nout);
+}
+
+static medusa_status linear_call(const void* x, int64_t ldx, const uint32_t* qweight, const void* scales, const uint8_t* zeros, int T, int K,
+                                 int Nout, int group, void* y, medusa_dtype y_dt, void* ws, size_t ws_bytes, int32_t* d_status,
+                                 medusa_stream_t stream, int withhold) {
   if (T < 0 || !sizes_ok(K, Nout, group) || !dtype_ok(y_dt)) return MEDUSA_ERR_INVALID_ARG;
   if (T == 0) return MEDUSA_OK;
-  if (!x || !qweight || !scales || !y || ldx < K || ldx % 8 || ldx > (1ll << 40) || T >= 0x7fffffff - 65536) return MEDUSA_ERR_INVALID_ARG;
+  if (!x || !qweight || !scales || !y || ldx < K || ldx % 8 || ldx >= (1ll << 38) || T >= 0x7fffffff - 65536) return MEDUSA_ERR_INVALID_ARG;
   const size_t es = dtype_bytes(y_dt);
-  if (!aligned16(x) || !aligned16(qweight) || ((uintptr_t)scales & 1) || ((uintptr_t)y & (es - 1))) return MEDUSA_ERR_INVALID_ARG;
-  const size_t ny = (size_t)T * Nout * es, ns = (size_t)Nout * (K / group);
-  if (overlaps_any({y, ny}, {{x, ((size_t)(T - 1) * ldx + K) * 2}, {qweight, (size_t)Nout * K / 2}, {scales, 2 * ns}, {zeros, ns}, {d_status, 4}}))
+  if (!aligned16(x) || !aligned16(qweight) || ((uintptr_t)scales & 1) || ((uintptr_t)y & (es - 1)) || ((uintptr_t)d_status & 3))
+    return MEDUSA_ERR_INVALID_ARG;
+  const size_t need = medusa_linear_w4_workspace_size(T, K, Nout, group);
+  if (need && (!ws || ws_bytes < need || !aligned16(ws))) return MEDUSA_ERR_WORKSPACE;
+  const size_t ny = (size_t)T * Nout * es, ns = (size_t)Nout * (K / group), nx = ((size_t)(T - 1) * ldx + K) * 2;
+  const Region nothing{nullptr, 0}, part = need ? Region{ws, need} : nothing;
+  if (overlaps_any({y, ny}, {{x, nx}, {qweight, (size_t)Nout * K / 2}, {scales, 2 * ns}, {zeros, ns}, {d_status, 4}, part}) ||
+      overlaps_any(part, {{x, nx}, {qweight, (size_t)Nout * K / 2}, {scales, 2 * ns}, {zeros, ns}, {d_status, 4}}))
     return MEDUSA_ERR_ALIAS;
   Args a{};
   a.x = static_cast<const uint16_t*>(x);
@@ -239,13 +206,25 @@ extern "C" medusa_status medusa_linear_w4(const void* x, int64_t ldx, const uint
   a.glog = group_log2(group);
   a.y = y;
   a.y32 = y_dt == MEDUSA_F32;
+  a.d_status = d_status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int nt = T <= 8 ? 1 : T <= 16 ? 2 : 4;
-  const long long grid = (long long)((Nout + 15) / 16) * ((T + 8 * nt - 1) / (8 * nt));
-  if (grid > 0x7fffffffll) return MEDUSA_ERR_INVALID_ARG;
-  const dim3 gd((unsigned)grid), bd(kWarps * 32);
+  if (on_tc(T)) return tc_launch(a, static_cast<float*>(ws), withhold, s);
+  if (withhold) return MEDUSA_ERR_INVALID_ARG;
+  const int nt = T <= 8 ? 1 : 2;
+  const dim3 gd((Nout + 15) / 16), bd(kWarps * 32);
   if (nt == 1) launch_pdl(few_kernel<1>, gd, bd, 0, s, a);
-  else if (nt == 2) launch_pdl(few_kernel<2>, gd, bd, 0, s, a);
-  else launch_pdl(few_kernel<4>, gd, bd, 0, s, a);
+  else launch_pdl(few_kernel<2>, gd, bd, 0, s, a);
   return launch_status();
+}
+
+extern "C" medusa_status medusa_linear_w4(const void* x, int64_t ldx, const uint32_t* qweight, const void* scales, const uint8_t* zeros, int T,
+                                          int K, int Nout, int group, void* y, medusa_dtype y_dt, void* ws, size_t ws_bytes, int32_t* d_status,
+                                          medusa_stream_t stream) {
+  return linear_call(x, ldx, qweight, scales, zeros, T, K, Nout, group, y, y_dt, ws, ws_bytes, d_status, stream, 0);
+}
+
+extern "C" medusa_status medusa_linear_w4_test_stall(const void* x, int64_t ldx, const uint32_t* qweight, const void* scales,
+                                                     const uint8_t* zeros, int T, int K, int Nout, int group, void* y, medusa_dtype y_dt,
+                                                     void* ws, size_t ws_bytes, int32_t* d_status, medusa_stream_t stream) {
+  return linear_call(x, ldx, qweight, scales, zeros, T, K, Nout, group, y, y_dt, ws, ws_bytes, d_status, stream, 1);
 }

@@ -1,0 +1,61 @@
+// What the kernels of medusa_linear_w4 share.
+#pragma once
+
+#include "common.cuh"
+
+namespace medusa {
+namespace w4 {
+
+struct Args {
+  const uint16_t* x;
+  long long ldx;
+  const uint32_t* q;
+  const uint16_t* scales;
+  const uint8_t* zeros;
+  int T, K, Nout, glog;  // glog: log2 of the group
+  void* y;
+  int y32;
+  int32_t* d_status;
+};
+
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// What a group's weights are made of: 128 + zero and the scale, twice each.
+struct Group {
+  uint32_t base, scale;
+};
+__device__ __forceinline__ Group group_of(uint32_t scale, uint32_t zero) {
+  const uint32_t b = 0x4300u | (zero & 127u);
+  return {b | b << 16, scale | scale << 16};
+}
+__device__ __forceinline__ Group group_at(const Args& a, int g, int n) {
+  const size_t i = (size_t)g * a.Nout + n;
+  return group_of(a.scales[i], a.zeros ? a.zeros[i] : 8);
+}
+// The four pairs of a word.
+__device__ __forceinline__ void unpack(uint32_t w, const Group& g, uint32_t* p) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = mul2(sub2(((w >> (4 * i)) & 0x000f000fu) | 0x43004300u, g.base), g.scale);
+}
+
+__device__ __forceinline__ void store_y(const Args& a, int t, int n, float v) {
+  const size_t i = (size_t)t * a.Nout + n;
+  if (a.y32) static_cast<float*>(a.y)[i] = v;
+  else static_cast<uint16_t*>(a.y)[i] = (uint16_t)f32_to_bf16_bits(v);
+}
+
+// Tensor-core kernel (linear_w4_tc.cu).
+size_t tc_workspace(int T, int K, int Nout);
+medusa_status tc_launch(const Args& a, float* part, int withhold, cudaStream_t s);
+
+}  // namespace w4
+}  // namespace medusa
