@@ -29,18 +29,18 @@ namespace medusa {
 namespace w4 {
 using namespace sm100;
 
-constexpr int kThreads = 512;              // W, products, x, -; 2 x 4 unpacking; 4 reading out
+constexpr int kThreads = 768;              // W, products, x, products; 4 x 4 unpacking; 4 reading out
+constexpr int kUnpackers = 16;
 constexpr int kRows = 256;                 // features of a tile
 constexpr int kCols = 128;                 // columns of a block
 constexpr int kMaxTN = 192;
 constexpr int kSlotsW = 4;
-constexpr int kMaxSlotsX = 16;
+constexpr int kMaxSlotsX = 8;
 constexpr uint32_t kSlotW = kRows * kCols / 2;
 constexpr uint32_t kHalfW = kSlotW / 2;
 constexpr uint32_t kRing = 229376;         // 224 KB for both rings
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMinBlocks = 2;              // of a CTA
-constexpr int kPolls = 1 << 23;            // of a wait that does not sleep: some 100 ns each
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainNs = 100000000ull;
 
@@ -55,7 +55,7 @@ struct Tc {
 
 struct Tail {
   uint64_t w_full[kSlotsW], w_empty[kSlotsW], x_full[kMaxSlotsX], x_empty[kMaxSlotsX];
-  uint64_t a_full[2][4], a_empty[2][4], d_full[2], d_empty[2], drain;
+  uint64_t a_full[2][2], a_empty[2][2], d_full[2], d_empty[2], drain[2];
   uint32_t tmem;
   volatile int abort;
   int w_loads, x_loads;
@@ -66,81 +66,86 @@ static_assert(kSmem <= 232448, "shared memory of a CTA");
 __host__ __device__ __forceinline__ long long work_begin(long long work, int grid, int c) { return work * c / grid; }
 __device__ __forceinline__ int work_owner(long long work, int grid, long long w) { return (int)(((w + 1) * grid - 1) / work); }
 
-// A CTA's blocks, one after the other.
+// A CTA's blocks, one after the other: feature tile, token tile, block of columns.
 struct Walk {
-  int tile, kb, left;
+  int mt, nt, kb, left;
 };
 __device__ __forceinline__ Walk walk_of(const Tc& p) {
   const long long w0 = work_begin(p.work, p.grid, blockIdx.x), w1 = work_begin(p.work, p.grid, blockIdx.x + 1);
-  const int tile = (int)(w0 / p.kblocks);
-  return {tile, (int)(w0 - (long long)tile * p.kblocks), (int)(w1 - w0)};
+  const int tile = (int)(w0 / p.kblocks), mt = tile / p.ntiles;
+  return {mt, tile - mt * p.ntiles, (int)(w0 - (long long)tile * p.kblocks), (int)(w1 - w0)};
+}
+__device__ __forceinline__ void next_tile(const Tc& p, Walk& x) {
+  x.kb = 0;
+  if (++x.nt == p.ntiles) {
+    x.nt = 0;
+    ++x.mt;
+  }
 }
 __device__ __forceinline__ void step(const Tc& p, Walk& x) {
   --x.left;
-  if (++x.kb == p.kblocks) {
-    x.kb = 0;
-    ++x.tile;
-  }
+  if (++x.kb == p.kblocks) next_tile(p, x);
 }
 // Blocks of the tile the walk is in that are this CTA's.
 __device__ __forceinline__ int tile_blocks(const Tc& p, const Walk& x) { return min(x.left, p.kblocks - x.kb); }
+
+// A place in a ring and the parity of its present round.
+struct Ring {
+  int i = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) {
+      i = 0;
+      ++round;
+    }
+  }
+  // The phase that ends when this place is full; the one that ended when it was last emptied.
+  __device__ __forceinline__ uint32_t full() const { return round & 1u; }
+  __device__ __forceinline__ uint32_t empty() const { return (round - 1u) & 1u; }
+  __device__ __forceinline__ bool used() const { return round > 0; }
+};
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t ok;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(ok));
   return ok != 0;
 }
+// All lanes wait for a phase; true when all saw it end.  What follows a try that came back empty is kept out
+// of line: the roles' loops have to stay in the instruction caches next to one another.
+__device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_wait_bounded(bar, parity, abort, kWaitNs);
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const bool ok = mbar_wait_bounded(bar, parity, abort, kWaitNs);
+  bool ok = mbar_try_wait(bar, parity);
+  if (!__all_sync(0xffffffffu, ok)) ok = wait_longer(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
 }
-__device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-               : "=r"(ok)
-               : "r"(smem_u32(bar)), "r"(parity)
-               : "memory");
-  return ok != 0;
-}
-// Every lane with `need` waits for a phase of a barrier of its own, all at once.
-__device__ __forceinline__ bool lanes_wait(uint64_t* bar, uint32_t parity, bool need, volatile int* abort) {
-  bool ok = !need;
-#pragma unroll 1
-  for (int n = kPolls; n > 0; --n) {
-    if (!ok) ok = test_wait(bar, parity);
-    if (__all_sync(0xffffffffu, ok)) {
-      __syncwarp();
-      return true;
-    }
-    if ((n & 15) == 0 && __any_sync(0xffffffffu, *abort)) return false;
-  }
-  *abort = 1;
-  return false;
-}
+// A value that is the same in all lanes, known to be so by the compiler.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+// Descriptors of K-major operands with 128-byte swizzle are a constant half and an address in units of 16 bytes.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// The scales and zeros of a thread's row in a block of columns: GROUPS of them.
+// The scales and zeros of a row in a block of columns: GROUPS of them.
 template <int GROUPS>
 struct Raw {
-  uint16_t s[GROUPS];
-  uint8_t z[GROUPS];
+  uint32_t s[GROUPS], z[GROUPS];
 };
 template <int GROUPS>
 __device__ __forceinline__ Raw<GROUPS> load_groups(const Tc& p, const Walk& x, int row) {
   Raw<GROUPS> r;
-  const int n = min(x.tile / p.ntiles * kRows + row, p.a.Nout - 1);
-  const int g0 = x.kb * GROUPS, ng = p.a.K >> p.a.glog;
+  const size_t at = (size_t)(x.kb * GROUPS) * p.a.Nout + min(x.mt * kRows + row, p.a.Nout - 1);
 #pragma unroll
   for (int i = 0; i < GROUPS; ++i) {
     r.s[i] = 0;  // behind the last column: weights of 0
     r.z[i] = 8;
-    if (g0 + i < ng) {
-      const size_t at = (size_t)(g0 + i) * p.a.Nout + n;
-      r.s[i] = p.a.scales[at];
-      if (p.a.zeros) r.z[i] = p.a.zeros[at];
+    if (x.left > 0 && x.kb * kCols + kCols / GROUPS * i < p.a.K) {
+      r.s[i] = p.a.scales[at + (size_t)i * p.a.Nout];
+      if (p.a.zeros) r.z[i] = p.a.zeros[at + (size_t)i * p.a.Nout];
     }
   }
   return r;
@@ -162,21 +167,21 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     tail->abort = 0;
     for (int i = 0; i < kSlotsW; ++i) {
       mbar_init(&tail->w_full[i], 1);
-      mbar_init(&tail->w_empty[i], 8);
+      mbar_init(&tail->w_empty[i], kUnpackers / 2);
     }
     for (int i = 0; i < p.NX; ++i) {
       mbar_init(&tail->x_full[i], 1);
-      mbar_init(&tail->x_empty[i], 1);
+      mbar_init(&tail->x_empty[i], 2);
     }
     for (int h = 0; h < 2; ++h) {
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         mbar_init(&tail->a_full[h][i], 4);
         mbar_init(&tail->a_empty[h][i], 1);
       }
       mbar_init(&tail->d_full[h], 1);
+      mbar_init(&tail->drain[h], 1);
       mbar_init(&tail->d_empty[h], 4);
     }
-    mbar_init(&tail->drain, 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -198,143 +203,131 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 
   if (warp == 0) {
     // ------------------------------------------------------------ weights as they are kept
-    int i = 0;
-    for (; x.left > 0; step(p, x), ++i) {
-      const int s = i % kSlotsW;
-      if (i >= kSlotsW && !warp_wait(&tail->w_empty[s], (uint32_t)(i / kSlotsW - 1) & 1u, abort)) break;
+    int n = 0;
+    for (Ring w; x.left > 0; step(p, x), w.next(kSlotsW), ++n) {
+      if (w.used() && !warp_wait(&tail->w_empty[w.i], w.empty(), abort)) break;
       if (elect_one()) {
-        mbar_expect_tx(&tail->w_full[s], kSlotW);
+        mbar_expect_tx(&tail->w_full[w.i], kSlotW);
         for (int h = 0; h < 2; ++h)
-          tma_load_2d(smem + s * kSlotW + h * kHalfW, &tm_w, &tail->w_full[s], x.kb * (kCols / 2), x.tile / p.ntiles * kRows + h * 128);
+          tma_load_2d(smem + w.i * kSlotW + h * kHalfW, &tm_w, &tail->w_full[w.i], x.kb * (kCols / 2), x.mt * kRows + h * 128);
       }
       __syncwarp();
     }
-    if (lane == 0) tail->w_loads = i;
+    if (lane == 0) tail->w_loads = n;
   } else if (warp == 2) {
     // ------------------------------------------------------------ tokens
-    int j = 0;
+    int n = 0;
+    for (Ring t; x.left > 0; step(p, x), t.next(p.NX), ++n) {
+      if (t.used() && !warp_wait(&tail->x_empty[t.i], t.empty(), abort)) break;
+      if (elect_one()) {
+        mbar_expect_tx(&tail->x_full[t.i], (uint32_t)p.TN * 256);
+        for (int u = 0; u < 2; ++u)
+          if (!(p.withhold && n == 0 && u == 0))
+            tma_load_2d(ring_x + (2 * t.i + u) * (p.TN * 128), &tm_x, &tail->x_full[t.i], x.kb * kCols + u * 64, x.nt * p.TN);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) tail->x_loads = n;
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------------ products of half h
+    // Issued by an elected lane of the whole warp, their addresses known to be the same in all lanes: by a lane on
+    // its own a product took 80 clocks to issue, so 11.
+    const int h = warp >> 1;
+    const uint32_t idesc = uniform(idesc_bf16_f32(128, p.TN, false, false)), d = uniform(tmem + h * p.DN),
+                   a0 = uniform(tmem + 2 * p.DN + h * p.NA * 64), x0 = (smem_u32(ring_x) >> 4) | (1u << 16), half = uniform(p.TN * 8);
+    Ring t;
+    uint32_t i = 0;  // blocks
     bool alive = true;
-    for (; x.left > 0 && alive; step(p, x)) {
-      for (int u = 0; u < 2; ++u, ++j) {
-        const int s = j % p.NX;
-        if (j >= p.NX && !(alive = warp_wait(&tail->x_empty[s], (uint32_t)(j / p.NX - 1) & 1u, abort))) break;
+    for (int seg = 0; x.left > 0 && alive; ++seg) {
+      const int nb = tile_blocks(p, x);
+#pragma unroll 1
+      for (int k = 0; k < nb; ++k, ++i) {
+        const uint32_t xd = uniform(x0 + t.i * p.TN * 16), a = uniform(a0 + (i & (p.NA - 1)) * 64);
+        if (k == 0 && seg > 0 && !(alive = warp_wait(&tail->d_empty[h], (uint32_t)(seg - 1) & 1u, abort))) break;
+        if (!(alive = warp_wait(&tail->x_full[t.i], t.full(), abort) && warp_wait(&tail->a_full[h][i & 1], (i >> 1) & 1u, abort))) break;
+        tc_fence_after();
         if (elect_one()) {
-          mbar_expect_tx(&tail->x_full[s], (uint32_t)p.TN * 128);
-          if (!(p.withhold && j == 0))
-            tma_load_2d(ring_x + s * (p.TN * 128), &tm_x, &tail->x_full[s], x.kb * kCols + u * 64, x.tile % p.ntiles * p.TN);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(d, a + 8 * kk, desc_of(xd + (kk >> 2) * half + 2 * (kk & 3)), idesc, kk > 0 || k > 0);
+          mma_commit(&tail->a_empty[h][i & 1]);
+          mma_commit(&tail->x_empty[t.i]);
+          if (k == nb - 1) mma_commit(&tail->d_full[h]);
         }
         __syncwarp();
+        t.next(p.NX);
       }
-    }
-    if (lane == 0) tail->x_loads = j;
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ products
-    const uint32_t idesc = idesc_bf16_f32(128, p.TN, false, false);
-    const uint32_t a0 = tmem + 2 * p.DN;
-    int j = 0, seg = 0;
-    bool alive = true;
-    while (x.left > 0 && alive) {
-      const int nb = tile_blocks(p, x);
-      for (int k = 0; k < 2 * nb && alive; ++k, ++j) {
-        const int sx = j % p.NX, b = j & (p.NA - 1);
-        const uint32_t px = (uint32_t)(j / p.NX) & 1u, pa = (uint32_t)(j / p.NA) & 1u;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint64_t* bar = lane == 0 ? &tail->a_full[h][b] : lane == 1 ? &tail->x_full[sx] : &tail->d_empty[h];
-          const bool need = lane == 0 || (lane == 1 && h == 0) || (lane == 2 && k == 0 && seg > 0);
-          if (!(alive = lanes_wait(bar, lane == 0 ? pa : lane == 1 ? px : (uint32_t)(seg - 1) & 1u, need, abort))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t xd = smem_desc_sw128(smem_u32(ring_x + sx * (p.TN * 128)), 16, 1024);
-            const uint32_t at = a0 + (h * p.NA + b) * 32;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mma_bf16_ts(tmem + h * p.DN, at + 8 * kk, xd + 2 * kk, idesc, k > 0 || kk > 0);
-            mma_commit(&tail->a_empty[h][b]);
-            if (h == 1) mma_commit(&tail->x_empty[sx]);
-            if (k == 2 * nb - 1) mma_commit(&tail->d_full[h]);
-          }
-          __syncwarp();
-        }
-      }
-      ++seg;
       x.left -= nb;
-      x.kb = 0;
-      ++x.tile;
+      next_tile(p, x);
     }
     if (elect_one()) {
       // This warp's products and the arrivals they signal, before tensor and shared memory go away.
-      mma_commit(&tail->drain);
-      mbar_wait_bounded(&tail->drain, 0, nullptr, kDrainNs);
+      mma_commit(&tail->drain[h]);
+      mbar_wait_bounded(&tail->drain[h], 0, nullptr, kDrainNs);
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < 12) {
-    // ------------------------------------------------------------ unpacking: half h, rows 32 q4 ..
-    const int h = (warp - 4) >> 2, q4 = warp & 3, row = 32 * q4 + lane;
-    const uint32_t a0 = tmem + ((uint32_t)(32 * q4) << 16) + 2 * p.DN + h * p.NA * 32;
-    Walk ahead = x;
-    int i = 0;
-    bool alive = true;
-    // Scales two blocks ahead: they take a round trip to memory.
-    auto next = [&] {
-      Raw<GROUPS> r{};
-      if (ahead.left > 0) {
-        r = load_groups<GROUPS>(p, ahead, h * 128 + row);
-        step(p, ahead);
-      }
-      return r;
-    };
-    auto block = [&](Raw<GROUPS>& raw) {
+  } else if (warp >= 4 && warp < 4 + kUnpackers) {
+    // ------------------------------------------------------------ unpacking: half h, every second block, rows 32 q4 ..
+    // A set has the blocks of one parity, and so the same slots of the ring and the same barriers each time: it
+    // passes over no phase of them.
+    const int h = (warp >> 2) & 1, set = warp >= 4 + kUnpackers / 2, q4 = warp & 3, row = 32 * q4 + lane;
+    const uint32_t to = tmem + ((uint32_t)(32 * q4) << 16) + 2 * p.DN + (h * p.NA + (set & (p.NA - 1))) * 64;
+    const uint8_t* mine = smem + set * kSlotW + h * kHalfW + row * 64;
+    const int sw = 16 * ((row >> 1) & 3);  // 64-byte swizzle
+    // The buffer is free once the products of the block before it there are done: of two blocks ago, or,
+    // with one buffer, of the other set's.
+    uint64_t* const free = &tail->a_empty[h][p.NA == 2 ? set : set ^ 1];
+    uint32_t it = 0;  // this set's blocks
+    const uint32_t lag = p.NA == 1 && set == 1 ? 0 : 1;
+    if (set) step(p, x);
+    Raw<GROUPS> raw = load_groups<GROUPS>(p, x, h * 128 + row);
+#pragma unroll 1
+    for (; x.left > 0; ++it) {
       Group g[GROUPS];
 #pragma unroll
       for (int k = 0; k < GROUPS; ++k) g[k] = group_of(raw.s[k], raw.z[k]);
-      raw = next();
-      const int s = i % kSlotsW;
-      if (!warp_wait(&tail->w_full[s], (uint32_t)(i / kSlotsW) & 1u, abort)) return false;
-      const uint8_t* w = smem + s * kSlotW + h * kHalfW + row * 64;
+      step(p, x);
+      step(p, x);
+      raw = load_groups<GROUPS>(p, x, h * 128 + row);  // of the set's next block: they take a round trip to memory
+      uint64_t* const full = &tail->w_full[set + 2 * (it & 1)];
+      if (!warp_wait(full, (it >> 1) & 1u, abort)) break;
+      const uint8_t* w = mine + (it & 1) * (2 * kSlotW);
       uint4 v[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(w + 16 * (c ^ ((row >> 1) & 3)));  // 64-byte swizzle
-      warp_arrive(&tail->w_empty[s]);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int j = 2 * i + u, b = j & (p.NA - 1);
-        uint32_t r[32];
+      for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(w + ((16 * c) ^ sw));
+      uint32_t r[32];
+      auto half_block = [&](int u) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const uint4& t = v[2 * u + c];
           const Group& gr = g[(2 * u + c) * GROUPS / 4];
-          unpack(t.x, gr, r + 16 * c);
-          unpack(t.y, gr, r + 16 * c + 4);
-          unpack(t.z, gr, r + 16 * c + 8);
-          unpack(t.w, gr, r + 16 * c + 12);
+          unpack(v[2 * u + c].x, gr, r + 16 * c);
+          unpack(v[2 * u + c].y, gr, r + 16 * c + 4);
+          unpack(v[2 * u + c].z, gr, r + 16 * c + 8);
+          unpack(v[2 * u + c].w, gr, r + 16 * c + 12);
         }
-        if (j >= p.NA && !warp_wait(&tail->a_empty[h][b], (uint32_t)(j / p.NA - 1) & 1u, abort)) return false;
-        tc_fence_after();
-        tmem_st32u(a0 + 32 * b, r);
-        tmem_wait_st();
-        tc_fence_before();
-        warp_arrive(&tail->a_full[h][b]);
-      }
-      ++i;
-      return true;
-    };
-    Raw<GROUPS> r0 = next(), r1 = next();
-    const int n = x.left;
-    while (i < n && alive) {
-      alive = block(r0);
-      if (alive && i < n) alive = block(r1);
+      };
+      half_block(0);
+      warp_arrive(&tail->w_empty[set + 2 * (it & 1)]);
+      if (it >= lag && !warp_wait(free, (it - lag) & 1u, abort)) break;
+      tc_fence_after();
+      tmem_st32u(to, r);
+      half_block(1);
+      __syncwarp();
+      tmem_st32u(to + 32, r);
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(&tail->a_full[h][set]);
     }
-  } else if (warp >= 12) {
+  } else if (warp >= 4 + kUnpackers) {
     // ------------------------------------------------------------ reading out
-    const int q4 = warp & 3, m = 32 * q4 + lane, first = x.tile;
+    const int q4 = warp & 3, m = 32 * q4 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16);
-    int seg = 0;
     bool alive = true;
-    for (; x.left > 0 && alive; ++seg) {
+    for (int seg = 0; x.left > 0 && alive; ++seg) {
       const int nb = tile_blocks(p, x);
       const bool whole = nb == p.kblocks;
-      const int t0 = x.tile % p.ntiles * p.TN, f0 = x.tile / p.ntiles * kRows;
-      float* part = p.part + ((size_t)blockIdx.x * 2 + (x.tile == first ? 0 : 1)) * p.TN * kRows;
+      const int t0 = x.nt * p.TN, f0 = x.mt * kRows;
+      float* part = p.part + ((size_t)blockIdx.x * 2 + (seg ? 1 : 0)) * p.TN * kRows;
       for (int h = 0; h < 2; ++h) {
         if (!(alive = warp_wait(&tail->d_full[h], seg & 1, abort))) break;
         tc_fence_after();
@@ -361,8 +354,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
         warp_arrive(&tail->d_empty[h]);
       }
       x.left -= nb;
-      x.kb = 0;
-      ++x.tile;
+      next_tile(p, x);
     }
   }
 
@@ -451,8 +443,8 @@ static Tc plan(int T, int K, int Nout) {
   p.TN = ((T + p.ntiles - 1) / p.ntiles + 15) / 16 * 16;
   p.ntiles = (T + p.TN - 1) / p.TN;
   p.DN = (p.TN + 31) / 32 * 32;
-  p.NA = 2 * p.DN + 2 * 4 * 32 <= (int)kTmemCols ? 4 : 2;
-  p.NX = (int)((kRing - kSlotsW * kSlotW) / (p.TN * 128));
+  p.NA = 2 * p.DN + 2 * 2 * 64 <= (int)kTmemCols ? 2 : 1;
+  p.NX = (int)((kRing - kSlotsW * kSlotW) / (p.TN * 256));
   if (p.NX > kMaxSlotsX) p.NX = kMaxSlotsX;
   p.kblocks = (K + kCols - 1) / kCols;
   p.work = (long long)((Nout + kRows - 1) / kRows) * p.ntiles * p.kblocks;
