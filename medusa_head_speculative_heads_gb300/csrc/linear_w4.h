@@ -47,10 +47,16 @@ __device__ __forceinline__ void unpack(uint32_t w, const Group& g, uint32_t* p) 
   for (int i = 0; i < 4; ++i) p[i] = mul2(sub2(((w >> (4 * i)) & 0x000f000fu) | 0x43004300u, g.base), g.scale);
 }
 
+// To bf16, to nearest even, by the hardware's conversion.
+__device__ __forceinline__ uint16_t bf16_rn(float v) {
+  uint16_t r;
+  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(v));
+  return r;
+}
 __device__ __forceinline__ void store_y(const Args& a, int t, int n, float v) {
   const size_t i = (size_t)t * a.Nout + n;
   if (a.y32) static_cast<float*>(a.y)[i] = v;
-  else static_cast<uint16_t*>(a.y)[i] = (uint16_t)f32_to_bf16_bits(v);
+  else static_cast<uint16_t*>(a.y)[i] = bf16_rn(v);
 }
 
 // Tensor-core kernel (linear_w4_tc.cu).

@@ -110,24 +110,44 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(ok));
   return ok != 0;
 }
-// All lanes wait for a phase; true when all saw it end.  What follows a try that came back empty is kept out
-// of line: the roles' loops have to stay in the instruction caches next to one another.
-__device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return mbar_wait_bounded(bar, parity, abort, kWaitNs);
+// Barriers by their shared-memory addresses: what a wait costs in instructions, the unpacking warps have less for
+// their work.
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok != 0;
 }
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (!__all_sync(0xffffffffu, ok)) ok = wait_longer(bar, parity, abort);
+// What follows a try that came back empty, out of line: the roles' loops have to stay in the instruction caches next
+// to one another.
+__device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, volatile int* abort) {
+  const uint64_t t0 = global_timer_ns();
+  while (!try_wait(bar, parity)) {
+    if (*abort) return false;
+    if ((int64_t)(global_timer_ns() - t0) > (int64_t)kWaitNs) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+// All lanes wait for a phase; true when all saw it end.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
+  const bool ok = wait_longer(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
 }
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) { return warp_wait(smem_u32(bar), parity, abort); }
 // A value that is the same in all lanes, known to be so by the compiler.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 // Descriptors of K-major operands with 128-byte swizzle are a constant half and an address in units of 16 bytes.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
-__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // The scales and zeros of a row in a block of columns: GROUPS of them.
@@ -135,21 +155,42 @@ template <int GROUPS>
 struct Raw {
   uint32_t s[GROUPS], z[GROUPS];
 };
+// Those of the blocks a thread unpacks, which are two apart.
 template <int GROUPS>
-__device__ __forceinline__ Raw<GROUPS> load_groups(const Tc& p, const Walk& x, int row) {
-  Raw<GROUPS> r;
-  const size_t at = (size_t)(x.kb * GROUPS) * p.a.Nout + min(x.mt * kRows + row, p.a.Nout - 1);
-#pragma unroll
-  for (int i = 0; i < GROUPS; ++i) {
-    r.s[i] = 0;  // behind the last column: weights of 0
-    r.z[i] = 8;
-    if (x.left > 0 && x.kb * kCols + kCols / GROUPS * i < p.a.K) {
-      r.s[i] = p.a.scales[at + (size_t)i * p.a.Nout];
-      if (p.a.zeros) r.z[i] = p.a.zeros[at + (size_t)i * p.a.Nout];
+struct Scales {
+  Walk x;
+  int row;
+  size_t at, two;  // of the block; from it to the next but one of the same tile
+  __device__ __forceinline__ void start(const Tc& p) {
+    at = (size_t)(x.kb * GROUPS) * p.a.Nout + min(x.mt * kRows + row, p.a.Nout - 1);
+  }
+  __device__ __forceinline__ Scales(const Tc& p, const Walk& w, int r) : x(w), row(r), two((size_t)(2 * GROUPS) * p.a.Nout) { start(p); }
+  __device__ __forceinline__ void next(const Tc& p) {
+    x.left -= 2;
+    x.kb += 2;
+    at += two;
+    if (x.kb >= p.kblocks) {
+      x.kb -= 2;
+      x.left += 2;
+      step(p, x);
+      step(p, x);
+      start(p);
     }
   }
-  return r;
-}
+  __device__ __forceinline__ Raw<GROUPS> load(const Tc& p) const {
+    Raw<GROUPS> r;
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) {
+      r.s[i] = 0;  // behind the last column: weights of 0
+      r.z[i] = 8;
+      if (x.left > 0 && (GROUPS == 1 || x.kb * kCols + kCols / GROUPS * i < p.a.K)) {
+        r.s[i] = p.a.scales[at + (size_t)i * p.a.Nout];
+        if (p.a.zeros) r.z[i] = p.a.zeros[at + (size_t)i * p.a.Nout];
+      }
+    }
+    return r;
+  }
+};
 
 template <int GROUPS>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -272,29 +313,29 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     // passes over no phase of them.
     const int h = (warp >> 2) & 1, set = warp >= 4 + kUnpackers / 2, q4 = warp & 3, row = 32 * q4 + lane;
     const uint32_t to = tmem + ((uint32_t)(32 * q4) << 16) + 2 * p.DN + (h * p.NA + (set & (p.NA - 1))) * 64;
-    const uint8_t* mine = smem + set * kSlotW + h * kHalfW + row * 64;
-    const int sw = 16 * ((row >> 1) & 3);  // 64-byte swizzle
+    const uint32_t sw = 16 * ((row >> 1) & 3);  // 64-byte swizzle
     // The buffer is free once the products of the block before it there are done: of two blocks ago, or,
     // with one buffer, of the other set's.
-    uint64_t* const free = &tail->a_empty[h][p.NA == 2 ? set : set ^ 1];
-    uint32_t it = 0;  // this set's blocks
-    const uint32_t lag = p.NA == 1 && set == 1 ? 0 : 1;
+    const uint32_t free = smem_u32(&tail->a_empty[h][p.NA == 2 ? set : set ^ 1]), filled = smem_u32(&tail->a_full[h][set]);
+    uint32_t free_phase = 1, slot = set;
+    bool first = p.NA == 2 || set == 0;  // nothing was there before
+    uint32_t round = 0;
     if (set) step(p, x);
-    Raw<GROUPS> raw = load_groups<GROUPS>(p, x, h * 128 + row);
+    Scales<GROUPS> scales(p, x, h * 128 + row);
+    Raw<GROUPS> raw = scales.load(p);
 #pragma unroll 1
-    for (; x.left > 0; ++it) {
+    for (int left = x.left; left > 0; left -= 2) {
       Group g[GROUPS];
 #pragma unroll
       for (int k = 0; k < GROUPS; ++k) g[k] = group_of(raw.s[k], raw.z[k]);
-      step(p, x);
-      step(p, x);
-      raw = load_groups<GROUPS>(p, x, h * 128 + row);  // of the set's next block: they take a round trip to memory
-      uint64_t* const full = &tail->w_full[set + 2 * (it & 1)];
-      if (!warp_wait(full, (it >> 1) & 1u, abort)) break;
-      const uint8_t* w = mine + (it & 1) * (2 * kSlotW);
+      scales.next(p);
+      raw = scales.load(p);  // of the set's next block: they take a round trip to memory
+      if (!warp_wait(smem_u32(&tail->w_full[0]) + 8 * slot, round, abort)) break;
+      const uint32_t w = smem_u32(smem) + slot * kSlotW + h * kHalfW + row * 64;
       uint4 v[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(w + ((16 * c) ^ sw));
+      for (int c = 0; c < 4; ++c)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v[c].x), "=r"(v[c].y), "=r"(v[c].z), "=r"(v[c].w) : "r"(w + ((16 * c) ^ sw)) : "memory");
       uint32_t r[32];
       auto half_block = [&](int u) {
 #pragma unroll
@@ -307,8 +348,11 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
         }
       };
       half_block(0);
-      warp_arrive(&tail->w_empty[set + 2 * (it & 1)]);
-      if (it >= lag && !warp_wait(free, (it - lag) & 1u, abort)) break;
+      warp_arrive(smem_u32(&tail->w_empty[0]) + 8 * slot, lane);
+      slot ^= 2;
+      round ^= slot < 2;
+      if (first) first = false;
+      else if (!warp_wait(free, free_phase ^= 1, abort)) break;
       tc_fence_after();
       tmem_st32u(to, r);
       half_block(1);
@@ -316,7 +360,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
       tmem_st32u(to + 32, r);
       tmem_wait_st();
       tc_fence_before();
-      warp_arrive(&tail->a_full[h][set]);
+      warp_arrive(filled, lane);
     }
   } else if (warp >= 4 + kUnpackers) {
     // ------------------------------------------------------------ reading out
@@ -326,32 +370,39 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     for (int seg = 0; x.left > 0 && alive; ++seg) {
       const int nb = tile_blocks(p, x);
       const bool whole = nb == p.kblocks;
-      const int t0 = x.nt * p.TN, f0 = x.mt * kRows;
-      float* part = p.part + ((size_t)blockIdx.x * 2 + (seg ? 1 : 0)) * p.TN * kRows;
+      const int t0 = x.nt * p.TN, tokens = min(p.TN, p.a.T - t0);
       for (int h = 0; h < 2; ++h) {
         if (!(alive = warp_wait(&tail->d_full[h], seg & 1, abort))) break;
         tc_fence_after();
-        const int n = f0 + h * 128 + m;
+        const int n = x.mt * kRows + h * 128 + m;
+        float* part = p.part + ((size_t)blockIdx.x * 2 + (seg ? 1 : 0)) * p.TN * kRows + h * 128 + m;
+        size_t at = (size_t)t0 * p.a.Nout + n;
 #pragma unroll 1
-        for (int c = 0; c < p.TN; c += 32) {
-          float v[32];
+        for (int c = 0; c < p.TN; c += 16, part += 16 * kRows) {
+          float v[16];
           __syncwarp();
-          tmem_ld32(lanes + h * p.DN + c, v);
+          tmem_ld16(lanes + h * p.DN + c, v);
           tmem_wait_ld();
-          if (whole) {
-            if (n < p.a.Nout) {
+          if (!whole) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (t0 + c + e < p.a.T && c + e < p.TN) store_y(p.a, t0 + c + e, n, v[e]);
+            for (int e = 0; e < 16; ++e) part[e * kRows] = v[e];
+          } else if (n < p.a.Nout) {
+            const int more = tokens - c;
+            if (p.a.y32) {
+              float* y = static_cast<float*>(p.a.y);
+#pragma unroll
+              for (int e = 0; e < 16; ++e, at += p.a.Nout)
+                if (e < more) y[at] = v[e];
+            } else {
+              uint16_t* y = static_cast<uint16_t*>(p.a.y);
+#pragma unroll
+              for (int e = 0; e < 16; ++e, at += p.a.Nout)
+                if (e < more) y[at] = bf16_rn(v[e]);
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c + e < p.TN) part[(size_t)(c + e) * kRows + h * 128 + m] = v[e];
           }
         }
         tc_fence_before();
-        warp_arrive(&tail->d_empty[h]);
+        warp_arrive(smem_u32(&tail->d_empty[h]), lane);
       }
       x.left -= nb;
       next_tile(p, x);
