@@ -60,8 +60,7 @@ __device__ __forceinline__ void store_y(const Args& a, int t, int n, float v) {
 }
 
 // Tensor-core kernel (linear_w4_tc.cu).
-size_t tc_workspace(int T, int K, int Nout);
-medusa_status tc_launch(const Args& a, float* part, int withhold, cudaStream_t s);
+medusa_status tc_launch(const Args& a, int withhold, cudaStream_t s);
 
 }  // namespace w4
 }  // namespace medusa

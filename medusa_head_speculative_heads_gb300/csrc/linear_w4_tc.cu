@@ -1,19 +1,18 @@
 // medusa_linear_w4 on tcgen05 tensor cores: many tokens.
 //
-// y^T = W x^T in tiles of 256 features by up to 192 tokens.  Weights come as they are kept, 64 bytes a
-// row and 128 columns, by TMA; eight warps unpack them into tensor memory, where the matrix instruction reads its
-// first operand (a thread has a row and 64 columns of it: 32 words, four loads of 16 bytes from
-// shared memory), so that unpacked weights never pass through shared memory.  The tokens are the second
-// operand, by TMA in slots of 64 columns.  256 features share a tile of tokens: with weights this
-// small it is the tokens whose traffic counts.
+// y^T = W x^T in tiles of up to 256 features by up to 192 tokens.  Weights come as they are kept, 64 bytes a
+// row and 128 columns, by TMA; sixteen warps unpack them into tensor memory, where the matrix instruction reads its
+// first operand (a thread has a row's 128 columns: 16 words, four loads of 16 bytes from shared memory), so that
+// unpacked weights never pass through shared memory.  The tokens are the second operand, by TMA.  The features
+// share a tile of tokens: with weights this small it is the tokens whose traffic counts.
 //
-// The two halves of 128 features have a sum in tensor memory, buffers of unpacked weights and
-// four unpacking warps of their own; one warp issues their products in turn, so that a half's sum is read out
-// under the other's products.
+// The two halves of a tile's features, up to 128 each, have a sum and buffers of unpacked weights in tensor memory, a
+// warp that issues their products and two sets of four unpacking warps, which take blocks of 128 columns in turn.
 //
-// The blocks of 128 columns of all tiles, laid end to end (the token tiles of a feature tile
-// behind one another), are divided evenly over the CTAs, one an SM.  A tile that several CTAs share
-// leaves a partial sum each, at most two a CTA, which a second kernel adds in the CTAs' order.
+// The work is divided into equal tiles: their height is chosen so that they fill the SMs in whole rounds (a CTA takes
+// one after the other, without a pause in the rings).  Where there are too few of them, the CTAs of a
+// cluster share a tile's columns: each sums up its blocks, sends the other CTAs their tokens' sums through
+// distributed shared memory, and adds what it receives in the CTAs' order.
 //
 // Every wait is bounded: a timeout sets MEDUSA_DEV_TIMEOUT, all roles stop, copies and products in
 // flight are waited for and tensor memory is freed.
@@ -31,25 +30,26 @@ using namespace sm100;
 
 constexpr int kThreads = 768;              // W, products, x, products; 4 x 4 unpacking; 4 reading out
 constexpr int kUnpackers = 16;
-constexpr int kRows = 256;                 // features of a tile
+constexpr int kHalf = 128;                 // features of a half of a tile at most
 constexpr int kCols = 128;                 // columns of a block
 constexpr int kMaxTN = 192;
+constexpr int kMaxShare = 8;               // CTAs of a cluster
 constexpr int kSlotsW = 4;
 constexpr int kMaxSlotsX = 8;
-constexpr uint32_t kSlotW = kRows * kCols / 2;
-constexpr uint32_t kHalfW = kSlotW / 2;
+constexpr uint32_t kHalfW = kHalf * kCols / 2;
+constexpr uint32_t kSlotW = 2 * kHalfW;
 constexpr uint32_t kRing = 229376;         // 224 KB for both rings
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMinBlocks = 2;              // of a CTA
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainNs = 100000000ull;
 
 struct Tc {
   Args a;
   int TN, DN, NA, NX;  // tokens of a tile, columns of a sum, buffers of unpacked weights and slots of tokens
-  int ntiles, kblocks, grid;
-  long long work;
-  float* part;         // [grid][2][TN][256]
+  int halves, RH;      // halves of a tile and the features of one
+  int mtiles, ntiles, kblocks;
+  int share;           // CTAs of a cluster, which share a tile
+  int grid;
   int withhold;        // failure test: the first tokens are never loaded
 };
 
@@ -63,31 +63,36 @@ struct Tail {
 constexpr uint32_t kSmem = kRing + sizeof(Tail);
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
-__host__ __device__ __forceinline__ long long work_begin(long long work, int grid, int c) { return work * c / grid; }
-__device__ __forceinline__ int work_owner(long long work, int grid, long long w) { return (int)(((w + 1) * grid - 1) / work); }
-
 // A CTA's blocks, one after the other: feature tile, token tile, block of columns.
 struct Walk {
-  int mt, nt, kb, left;
+  int mt, nt, kb, left;  // left: blocks, this one included
+  int kb0, nb;           // the CTA's blocks of a tile
+  int tile, stride;
+  __device__ __forceinline__ void place(const Tc& p) {
+    mt = tile / p.ntiles;
+    nt = tile - mt * p.ntiles;
+    kb = kb0;
+  }
+  __device__ __forceinline__ void next_tile(const Tc& p) {
+    tile += stride;
+    place(p);
+  }
+  __device__ __forceinline__ void step(const Tc& p) {
+    --left;
+    if (++kb == kb0 + nb) next_tile(p);
+  }
 };
 __device__ __forceinline__ Walk walk_of(const Tc& p) {
-  const long long w0 = work_begin(p.work, p.grid, blockIdx.x), w1 = work_begin(p.work, p.grid, blockIdx.x + 1);
-  const int tile = (int)(w0 / p.kblocks), mt = tile / p.ntiles;
-  return {mt, tile - mt * p.ntiles, (int)(w0 - (long long)tile * p.kblocks), (int)(w1 - w0)};
+  Walk x;
+  const int tiles = p.mtiles * p.ntiles, rank = blockIdx.x % p.share;
+  x.tile = blockIdx.x / p.share;
+  x.stride = p.grid / p.share;
+  x.kb0 = (int)((long long)p.kblocks * rank / p.share);
+  x.nb = (int)((long long)p.kblocks * (rank + 1) / p.share) - x.kb0;
+  x.left = (tiles - x.tile + x.stride - 1) / x.stride * x.nb;
+  x.place(p);
+  return x;
 }
-__device__ __forceinline__ void next_tile(const Tc& p, Walk& x) {
-  x.kb = 0;
-  if (++x.nt == p.ntiles) {
-    x.nt = 0;
-    ++x.mt;
-  }
-}
-__device__ __forceinline__ void step(const Tc& p, Walk& x) {
-  --x.left;
-  if (++x.kb == p.kblocks) next_tile(p, x);
-}
-// Blocks of the tile the walk is in that are this CTA's.
-__device__ __forceinline__ int tile_blocks(const Tc& p, const Walk& x) { return min(x.left, p.kblocks - x.kb); }
 
 // A place in a ring and the parity of its present round.
 struct Ring {
@@ -161,19 +166,16 @@ struct Scales {
   Walk x;
   int row;
   size_t at, two;  // of the block; from it to the next but one of the same tile
-  __device__ __forceinline__ void start(const Tc& p) {
-    at = (size_t)(x.kb * GROUPS) * p.a.Nout + min(x.mt * kRows + row, p.a.Nout - 1);
-  }
+  __device__ __forceinline__ void start(const Tc& p) { at = (size_t)(x.kb * GROUPS) * p.a.Nout + min(x.mt * (p.halves * p.RH) + row, p.a.Nout - 1); }
   __device__ __forceinline__ Scales(const Tc& p, const Walk& w, int r) : x(w), row(r), two((size_t)(2 * GROUPS) * p.a.Nout) { start(p); }
   __device__ __forceinline__ void next(const Tc& p) {
-    x.left -= 2;
-    x.kb += 2;
-    at += two;
-    if (x.kb >= p.kblocks) {
-      x.kb -= 2;
-      x.left += 2;
-      step(p, x);
-      step(p, x);
+    if (x.kb + 2 < x.kb0 + x.nb) {
+      x.left -= 2;
+      x.kb += 2;
+      at += two;
+    } else {
+      x.step(p);
+      x.step(p);
       start(p);
     }
   }
@@ -192,6 +194,12 @@ struct Scales {
   }
 };
 
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 template <int GROUPS>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ Tc p) {
@@ -204,24 +212,25 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
   }
   uint8_t* ring_x = smem + kSlotsW * kSlotW;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quads = (p.RH + 31) / 32;  // warps that have rows of a half
   if (threadIdx.x == 0) {
     tail->abort = 0;
     for (int i = 0; i < kSlotsW; ++i) {
       mbar_init(&tail->w_full[i], 1);
-      mbar_init(&tail->w_empty[i], kUnpackers / 2);
+      mbar_init(&tail->w_empty[i], p.halves * quads);
     }
     for (int i = 0; i < p.NX; ++i) {
       mbar_init(&tail->x_full[i], 1);
-      mbar_init(&tail->x_empty[i], 2);
+      mbar_init(&tail->x_empty[i], p.halves);
     }
     for (int h = 0; h < 2; ++h) {
       for (int i = 0; i < 2; ++i) {
-        mbar_init(&tail->a_full[h][i], 4);
+        mbar_init(&tail->a_full[h][i], quads);
         mbar_init(&tail->a_empty[h][i], 1);
       }
       mbar_init(&tail->d_full[h], 1);
       mbar_init(&tail->drain[h], 1);
-      mbar_init(&tail->d_empty[h], 4);
+      mbar_init(&tail->d_empty[h], quads);
     }
     fence_mbar_init();
   }
@@ -231,6 +240,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     tmem_relinquish();
   }
   Walk x = walk_of(p);
+  const int mt0 = x.mt, x0t = x.nt * p.TN;  // the one tile of a cluster
   if (warp == 0 && lane == 0) {
     tma_prefetch(&tm_w);
     tma_prefetch(&tm_x);
@@ -245,12 +255,12 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
   if (warp == 0) {
     // ------------------------------------------------------------ weights as they are kept
     int n = 0;
-    for (Ring w; x.left > 0; step(p, x), w.next(kSlotsW), ++n) {
+    for (Ring w; x.left > 0; x.step(p), w.next(kSlotsW), ++n) {
       if (w.used() && !warp_wait(&tail->w_empty[w.i], w.empty(), abort)) break;
       if (elect_one()) {
-        mbar_expect_tx(&tail->w_full[w.i], kSlotW);
-        for (int h = 0; h < 2; ++h)
-          tma_load_2d(smem + w.i * kSlotW + h * kHalfW, &tm_w, &tail->w_full[w.i], x.kb * (kCols / 2), x.mt * kRows + h * 128);
+        mbar_expect_tx(&tail->w_full[w.i], (uint32_t)(p.halves * p.RH) * (kCols / 2));
+        for (int h = 0; h < p.halves; ++h)
+          tma_load_2d(smem + w.i * kSlotW + h * kHalfW, &tm_w, &tail->w_full[w.i], x.kb * (kCols / 2), (x.mt * p.halves + h) * p.RH);
       }
       __syncwarp();
     }
@@ -258,7 +268,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
   } else if (warp == 2) {
     // ------------------------------------------------------------ tokens
     int n = 0;
-    for (Ring t; x.left > 0; step(p, x), t.next(p.NX), ++n) {
+    for (Ring t; x.left > 0; x.step(p), t.next(p.NX), ++n) {
       if (t.used() && !warp_wait(&tail->x_empty[t.i], t.empty(), abort)) break;
       if (elect_one()) {
         mbar_expect_tx(&tail->x_full[t.i], (uint32_t)p.TN * 256);
@@ -269,7 +279,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
       __syncwarp();
     }
     if (lane == 0) tail->x_loads = n;
-  } else if (warp == 1 || warp == 3) {
+  } else if (warp == 1 || (warp == 3 && p.halves == 2)) {
     // ------------------------------------------------------------ products of half h
     // Issued by an elected lane of the whole warp, their addresses known to be the same in all lanes: by a lane on
     // its own a product took 80 clocks to issue, so 11.
@@ -279,8 +289,8 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     Ring t;
     uint32_t i = 0;  // blocks
     bool alive = true;
-    for (int seg = 0; x.left > 0 && alive; ++seg) {
-      const int nb = tile_blocks(p, x);
+    for (int seg = 0; x.left > 0 && alive; ++seg, x.left -= x.nb) {
+      const int nb = x.nb;
 #pragma unroll 1
       for (int k = 0; k < nb; ++k, ++i) {
         const uint32_t xd = uniform(x0 + t.i * p.TN * 16), a = uniform(a0 + (i & (p.NA - 1)) * 64);
@@ -298,8 +308,6 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
         __syncwarp();
         t.next(p.NX);
       }
-      x.left -= nb;
-      next_tile(p, x);
     }
     if (elect_one()) {
       // This warp's products and the arrivals they signal, before tensor and shared memory go away.
@@ -307,7 +315,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
       mbar_wait_bounded(&tail->drain[h], 0, nullptr, kDrainNs);
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < 4 + kUnpackers) {
+  } else if (warp >= 4 && warp < 4 + kUnpackers && ((warp >> 2) & 1) < p.halves && (warp & 3) < quads) {
     // ------------------------------------------------------------ unpacking: half h, every second block, rows 32 q4 ..
     // A set has the blocks of one parity, and so the same slots of the ring and the same barriers each time: it
     // passes over no phase of them.
@@ -320,8 +328,8 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     uint32_t free_phase = 1, slot = set;
     bool first = p.NA == 2 || set == 0;  // nothing was there before
     uint32_t round = 0;
-    if (set) step(p, x);
-    Scales<GROUPS> scales(p, x, h * 128 + row);
+    if (set) x.step(p);
+    Scales<GROUPS> scales(p, x, h * p.RH + row);
     Raw<GROUPS> raw = scales.load(p);
 #pragma unroll 1
     for (int left = x.left; left > 0; left -= 2) {
@@ -362,50 +370,43 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
       tc_fence_before();
       warp_arrive(filled, lane);
     }
-  } else if (warp >= 4 + kUnpackers) {
+  } else if (warp >= 4 + kUnpackers && p.share == 1 && (warp & 3) < quads) {
     // ------------------------------------------------------------ reading out
     const int q4 = warp & 3, m = 32 * q4 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16);
     bool alive = true;
-    for (int seg = 0; x.left > 0 && alive; ++seg) {
-      const int nb = tile_blocks(p, x);
-      const bool whole = nb == p.kblocks;
+    for (int seg = 0; x.left > 0 && alive; ++seg, x.left -= x.nb, x.next_tile(p)) {
       const int t0 = x.nt * p.TN, tokens = min(p.TN, p.a.T - t0);
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < p.halves; ++h) {
         if (!(alive = warp_wait(&tail->d_full[h], seg & 1, abort))) break;
         tc_fence_after();
-        const int n = x.mt * kRows + h * 128 + m;
-        float* part = p.part + ((size_t)blockIdx.x * 2 + (seg ? 1 : 0)) * p.TN * kRows + h * 128 + m;
+        const int n = (x.mt * p.halves + h) * p.RH + m;
+        const bool mine = m < p.RH && n < p.a.Nout;
         size_t at = (size_t)t0 * p.a.Nout + n;
 #pragma unroll 1
-        for (int c = 0; c < p.TN; c += 16, part += 16 * kRows) {
+        for (int c = 0; c < tokens; c += 16) {
           float v[16];
           __syncwarp();
           tmem_ld16(lanes + h * p.DN + c, v);
           tmem_wait_ld();
-          if (!whole) {
+          if (!mine) continue;
+          const int more = tokens - c;
+          if (p.a.y32) {
+            float* y = static_cast<float*>(p.a.y);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) part[e * kRows] = v[e];
-          } else if (n < p.a.Nout) {
-            const int more = tokens - c;
-            if (p.a.y32) {
-              float* y = static_cast<float*>(p.a.y);
+            for (int e = 0; e < 16; ++e, at += p.a.Nout)
+              if (e < more) y[at] = v[e];
+          } else {
+            uint16_t* y = static_cast<uint16_t*>(p.a.y);
 #pragma unroll
-              for (int e = 0; e < 16; ++e, at += p.a.Nout)
-                if (e < more) y[at] = v[e];
-            } else {
-              uint16_t* y = static_cast<uint16_t*>(p.a.y);
-#pragma unroll
-              for (int e = 0; e < 16; ++e, at += p.a.Nout)
-                if (e < more) y[at] = bf16_rn(v[e]);
-            }
+            for (int e = 0; e < 16; ++e, at += p.a.Nout)
+              if (e < more) y[at] = bf16_rn(v[e]);
           }
         }
+        __syncwarp();
         tc_fence_before();
         warp_arrive(smem_u32(&tail->d_empty[h]), lane);
       }
-      x.left -= nb;
-      next_tile(p, x);
     }
   }
 
@@ -421,44 +422,49 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     for (int j = max(0, tail->x_loads - p.NX); j < tail->x_loads; ++j)
       mbar_wait_bounded(&tail->x_full[j % p.NX], (uint32_t)(j / p.NX) & 1u, nullptr, kDrainNs);
   }
+  if (p.share > 1) {
+    // The tile's sums, of which each CTA of the cluster has a part: CTA r's tokens' sums go to CTA r, into the rings'
+    // place, [sender][token][feature].
+    const int rank = blockIdx.x % p.share, per = (p.TN + p.share - 1) / p.share, rows = p.halves * p.RH;
+    cluster_sync();  // all products of the cluster are done, and nobody reads from the rings
+    if (warp >= 4 && warp < 4 + kUnpackers) {
+      const int h = (warp >> 2) & 1, part = warp >= 4 + kUnpackers / 2, m = 32 * (warp & 3) + lane;
+      if (h < p.halves && (warp & 3) < quads) {
+        const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + h * p.DN, at = smem_u32(smem) + 4 * (h * p.RH + m);
+#pragma unroll 1
+        for (int c = 16 * part; c < p.TN; c += 32) {
+          float v[16];
+          __syncwarp();
+          tmem_ld16(from + c, v);
+          tmem_wait_ld();
+          if (m >= p.RH) continue;
+          int to = c / per, col = c - to * per;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            uint32_t there;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at + 4 * ((rank * per + col) * rows)), "r"(to));
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(v[e]) : "memory");
+            if (++col == per) {
+              col = 0;
+              ++to;
+            }
+          }
+        }
+      }
+    }
+    cluster_sync();
+    const float* sums = reinterpret_cast<const float*>(smem);
+    const int tokens = min(per, min(p.TN - rank * per, p.a.T - x0t - rank * per));
+    for (int i = threadIdx.x; i < tokens * rows; i += kThreads) {
+      const int t = i / rows, m = i - t * rows, n = mt0 * rows + m;
+      float v = 0.f;
+      for (int r = 0; r < p.share; ++r) v += sums[(r * per + t) * rows + m];
+      if (n < p.a.Nout) store_y(p.a, x0t + rank * per + t, n, v);
+    }
+  }
   if (warp == 1) {
     __syncwarp();
     tmem_dealloc(tmem, kTmemCols);
-  }
-}
-
-// The partial sums of shared tiles, in the CTAs' order.  Block x looks at the boundary in front of CTA x + 1:
-// when it lies inside a tile and no earlier boundary does, the block adds that tile's parts: a
-// thread has 4 features, blockIdx.y and the thread's row choose the tokens.
-__global__ void __launch_bounds__(256) tc_reduce_kernel(const __grid_constant__ Tc p) {
-  pdl_wait();
-  pdl_trigger();
-  const int c = blockIdx.x + 1;
-  const long long wc = work_begin(p.work, p.grid, c), wp = work_begin(p.work, p.grid, c - 1);
-  if (wc % p.kblocks == 0) return;
-  const int tile = (int)(wc / p.kblocks);
-  const long long base = (long long)tile * p.kblocks;
-  if (wp > base) return;
-  const int last = work_owner(p.work, p.grid, base + p.kblocks - 1);
-  const int row = (threadIdx.x & 63) * 4, n = tile / p.ntiles * kRows + row, t0 = tile % p.ntiles * p.TN;
-  if (n >= p.a.Nout) return;
-  const size_t slot = (size_t)p.TN * kRows;
-  const float* first = p.part + ((size_t)(c - 1) * 2 + (wp == base ? 0 : 1)) * slot;  // the tile is that CTA's first or its last
-  for (int col = blockIdx.y * 4 + (threadIdx.x >> 6); col < p.TN; col += gridDim.y * 4) {
-    if (t0 + col >= p.a.T) break;
-    const size_t off = (size_t)col * kRows + row;
-    float4 s = __ldcg(reinterpret_cast<const float4*>(first + off));
-    for (int k = c; k <= last; ++k) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part + (size_t)k * 2 * slot + off));
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
-    }
-    const float v[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n + i < p.a.Nout) store_y(p.a, t0 + col, n + i, v[i]);
   }
 }
 
@@ -487,48 +493,72 @@ static bool make_map(CUtensorMap* m, CUtensorMapDataType ty, const void* base, l
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The division of the work: shared by the workspace query and the call.
 static Tc plan(int T, int K, int Nout) {
-  Tc p{};
-  p.ntiles = (T + kMaxTN - 1) / kMaxTN;
-  p.TN = ((T + p.ntiles - 1) / p.ntiles + 15) / 16 * 16;
-  p.ntiles = (T + p.TN - 1) / p.TN;
-  p.DN = (p.TN + 31) / 32 * 32;
-  p.NA = 2 * p.DN + 2 * 2 * 64 <= (int)kTmemCols ? 2 : 1;
-  p.NX = (int)((kRing - kSlotsW * kSlotW) / (p.TN * 256));
-  if (p.NX > kMaxSlotsX) p.NX = kMaxSlotsX;
-  p.kblocks = (K + kCols - 1) / kCols;
-  p.work = (long long)((Nout + kRows - 1) / kRows) * p.ntiles * p.kblocks;
-  long long g = p.work / kMinBlocks;
-  if (g > device_sm_count()) g = device_sm_count();
-  p.grid = g < 1 ? 1 : (int)g;
-  return p;
-}
-static bool shared_tiles(const Tc& p) {
-  for (int c = 1; c < p.grid; ++c)
-    if (work_begin(p.work, p.grid, c) % p.kblocks != 0) return true;
-  return false;
+  Tc best{};
+  double least = 0;
+  const int sms = device_sm_count(), kblocks = (K + kCols - 1) / kCols;
+  for (int most = kMaxTN; most >= 128; most -= 64)
+    for (int share = 1; share <= kMaxShare && share <= kblocks; share *= 2) {
+      Tc p{};
+      p.ntiles = (T + most - 1) / most;
+      p.TN = ((T + p.ntiles - 1) / p.ntiles + 15) / 16 * 16;
+      p.ntiles = (T + p.TN - 1) / p.TN;
+      p.DN = (p.TN + 31) / 32 * 32;
+      p.NA = 2 * p.DN + 2 * 2 * 64 <= (int)kTmemCols ? 2 : 1;
+      p.NX = (int)((kRing - kSlotsW * kSlotW) / (p.TN * 256));
+      if (p.NX > kMaxSlotsX) p.NX = kMaxSlotsX;
+      p.kblocks = kblocks;
+      p.share = share;
+      // Rounds that the tiles need when they are as high as can be, then the tiles that fill these rounds.
+      const int at_once = share == 1 ? sms : sms * 7 / 8 / share;  // clusters do not fill every SM
+      const long long fewest = (long long)((Nout + 2 * kHalf - 1) / (2 * kHalf)) * p.ntiles, rounds = (fewest + at_once - 1) / at_once;
+      if (share > 1 && rounds > 1) break;
+      const long long high = rounds * at_once / p.ntiles;
+      int rows = (int)((Nout + high - 1) / high);
+      if (rows < 8) rows = 8;
+      p.halves = rows > kHalf ? 2 : 1;
+      p.RH = ((rows + p.halves - 1) / p.halves + 7) / 8 * 8;
+      p.mtiles = (Nout + p.halves * p.RH - 1) / (p.halves * p.RH);
+      const long long tiles = (long long)p.mtiles * p.ntiles;
+      p.grid = (int)(tiles < at_once ? tiles : at_once) * share;
+      // Clocks: a block's products, unpacking and bytes, whichever is most; what a tile's end costs.
+      const double products = 4.0 * p.TN * p.halves + (p.NA == 1 ? 200 : 0), unpacking = 330.0 * p.halves, bytes = p.halves * p.RH * 64 / 20.0;
+      double block = products > unpacking ? products : unpacking;
+      if (bytes > block) block = bytes;
+      const double cost = (double)rounds * ((kblocks + share - 1) / share * (block + 100) + 1500 + (share > 1 ? 2500 + p.TN * p.halves * p.RH / 10.0 : 0));
+      if (least == 0 || cost < least) {
+        least = cost;
+        best = p;
+      }
+    }
+  return best;
 }
 
-size_t tc_workspace(int T, int K, int Nout) {
-  const Tc p = plan(T, K, Nout);
-  return shared_tiles(p) ? (size_t)p.grid * 2 * p.TN * kRows * sizeof(float) : 0;
-}
-
-medusa_status tc_launch(const Args& a, float* part, int withhold, cudaStream_t s) {
+medusa_status tc_launch(const Args& a, int withhold, cudaStream_t s) {
   if (!encode_fn()) return MEDUSA_ERR_CUDA;
   Tc p = plan(a.T, a.K, a.Nout);
   p.a = a;
-  p.part = part;
   p.withhold = withhold;
   CUtensorMap mw, mx;
-  if (!make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q, a.K / 2, a.Nout, a.K / 2, kCols / 2, 128, CU_TENSOR_MAP_SWIZZLE_64B) ||
+  if (!make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q, a.K / 2, a.Nout, a.K / 2, kCols / 2, p.RH, CU_TENSOR_MAP_SWIZZLE_64B) ||
       !make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.K, a.T, a.ldx * 2, 64, p.TN, CU_TENSOR_MAP_SWIZZLE_128B))
     return MEDUSA_ERR_CUDA;
   auto kern = a.glog == 5 ? tc_kernel<4> : a.glog == 6 ? tc_kernel<2> : tc_kernel<1>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess) return MEDUSA_ERR_CUDA;
-  launch_pdl(kern, dim3(p.grid), dim3(kThreads), kSmem, s, mw, mx, p);
-  if (shared_tiles(p)) launch_pdl(tc_reduce_kernel, dim3(p.grid - 1, (p.TN + 15) / 16), dim3(256), 0, s, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.share;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaLaunchKernelEx(&cfg, kern, mw, mx, p);
   return launch_status();
 }
 
