@@ -37,7 +37,9 @@ constexpr int kMaxShare = 8;               // CTAs of a cluster
 constexpr int kSlotsW = 4;
 constexpr int kMaxSlotsX = 8;
 constexpr uint32_t kHalfW = kHalf * kCols / 2;
-constexpr uint32_t kSlotW = 2 * kHalfW;
+constexpr uint32_t kOffScales = 2 * kHalfW;  // of a slot: the weights, scales [group][feature], zeros likewise
+constexpr uint32_t kOffZeros = kOffScales + 2048;
+constexpr uint32_t kSlotW = kOffZeros + 1024;
 constexpr uint32_t kRing = 229376;         // 224 KB for both rings
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 1000000000ull;
@@ -50,6 +52,7 @@ struct Tc {
   int mtiles, ntiles, kblocks;
   int share;           // CTAs of a cluster, which share a tile
   int grid;
+  int slot_bytes;      // that come into a slot of weights
   int withhold;        // failure test: the first tokens are never loaded
 };
 
@@ -155,7 +158,8 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
   if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The scales and zeros of a row in a block of columns: GROUPS of them.
+// The scales and zeros of a row in a block of columns: GROUPS of them.  Where their rows lie on 16 bytes they come with
+// the weights by TMA (TILED); else a thread loads its own, a block ahead.
 template <int GROUPS>
 struct Raw {
   uint32_t s[GROUPS], z[GROUPS];
@@ -200,9 +204,10 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
-template <int GROUPS>
+template <int GROUPS, bool TILED>
 __global__ void __launch_bounds__(kThreads, 1)
-tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ Tc p) {
+tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_s,
+          const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ Tc p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Tail* tail = reinterpret_cast<Tail*>(smem + kRing);
   volatile int* abort = &tail->abort;
@@ -258,9 +263,13 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     for (Ring w; x.left > 0; x.step(p), w.next(kSlotsW), ++n) {
       if (w.used() && !warp_wait(&tail->w_empty[w.i], w.empty(), abort)) break;
       if (elect_one()) {
-        mbar_expect_tx(&tail->w_full[w.i], (uint32_t)(p.halves * p.RH) * (kCols / 2));
+        mbar_expect_tx(&tail->w_full[w.i], (uint32_t)p.slot_bytes);
         for (int h = 0; h < p.halves; ++h)
           tma_load_2d(smem + w.i * kSlotW + h * kHalfW, &tm_w, &tail->w_full[w.i], x.kb * (kCols / 2), (x.mt * p.halves + h) * p.RH);
+        if (TILED) {
+          tma_load_2d(smem + w.i * kSlotW + kOffScales, &tm_s, &tail->w_full[w.i], x.mt * p.halves * p.RH, x.kb * GROUPS);
+          if (p.a.zeros) tma_load_2d(smem + w.i * kSlotW + kOffZeros, &tm_z, &tail->w_full[w.i], x.mt * p.halves * p.RH, x.kb * GROUPS);
+        }
       }
       __syncwarp();
     }
@@ -328,17 +337,30 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     uint32_t free_phase = 1, slot = set;
     bool first = p.NA == 2 || set == 0;  // nothing was there before
     uint32_t round = 0;
+    const int rows = p.halves * p.RH;
     if (set) x.step(p);
+    int left = x.left;
     Scales<GROUPS> scales(p, x, h * p.RH + row);
-    Raw<GROUPS> raw = scales.load(p);
+    Raw<GROUPS> raw{};
+    if (!TILED) raw = scales.load(p);
 #pragma unroll 1
-    for (int left = x.left; left > 0; left -= 2) {
+    for (; left > 0; left -= 2) {
       Group g[GROUPS];
+      if (!TILED) {
 #pragma unroll
-      for (int k = 0; k < GROUPS; ++k) g[k] = group_of(raw.s[k], raw.z[k]);
-      scales.next(p);
-      raw = scales.load(p);  // of the set's next block: they take a round trip to memory
+        for (int k = 0; k < GROUPS; ++k) g[k] = group_of(raw.s[k], raw.z[k]);
+        scales.next(p);
+        raw = scales.load(p);  // of the set's next block: they take a round trip to memory
+      }
       if (!warp_wait(smem_u32(&tail->w_full[0]) + 8 * slot, round, abort)) break;
+      if (TILED) {
+        const uint8_t* at = smem + slot * kSlotW + kOffScales;
+#pragma unroll
+        for (int k = 0; k < GROUPS; ++k) {
+          const int i = k * rows + h * p.RH + row;
+          g[k] = group_of(reinterpret_cast<const uint16_t*>(at)[i], p.a.zeros ? at[kOffZeros - kOffScales + i] : 8);
+        }
+      }
       const uint32_t w = smem_u32(smem) + slot * kSlotW + h * kHalfW + row * 64;
       uint4 v[4];
 #pragma unroll
@@ -515,9 +537,8 @@ static Tc plan(int T, int K, int Nout) {
       if (share > 1 && rounds > 1) break;
       const long long high = rounds * at_once / p.ntiles;
       int rows = (int)((Nout + high - 1) / high);
-      if (rows < 8) rows = 8;
       p.halves = rows > kHalf ? 2 : 1;
-      p.RH = ((rows + p.halves - 1) / p.halves + 7) / 8 * 8;
+      p.RH = ((rows + p.halves - 1) / p.halves + 15) / 16 * 16;
       p.mtiles = (Nout + p.halves * p.RH - 1) / (p.halves * p.RH);
       const long long tiles = (long long)p.mtiles * p.ntiles;
       p.grid = (int)(tiles < at_once ? tiles : at_once) * share;
@@ -539,11 +560,20 @@ medusa_status tc_launch(const Args& a, int withhold, cudaStream_t s) {
   Tc p = plan(a.T, a.K, a.Nout);
   p.a = a;
   p.withhold = withhold;
-  CUtensorMap mw, mx;
+  const int per = kCols >> a.glog, ng = a.K >> a.glog, rows = p.halves * p.RH;
+  const bool tiled = a.Nout % 16 == 0 && aligned16(a.scales) && aligned16(a.zeros);
+  p.slot_bytes = rows * (kCols / 2 + (tiled ? per * (a.zeros ? 3 : 2) : 0));
+  CUtensorMap mw, mx, ms, mz;
   if (!make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q, a.K / 2, a.Nout, a.K / 2, kCols / 2, p.RH, CU_TENSOR_MAP_SWIZZLE_64B) ||
       !make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.K, a.T, a.ldx * 2, 64, p.TN, CU_TENSOR_MAP_SWIZZLE_128B))
     return MEDUSA_ERR_CUDA;
-  auto kern = a.glog == 5 ? tc_kernel<4> : a.glog == 6 ? tc_kernel<2> : tc_kernel<1>;
+  ms = mz = mw;
+  if (tiled && (!make_map(&ms, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.scales, a.Nout, ng, (long long)a.Nout * 2, rows, per, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+                (a.zeros && !make_map(&mz, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.zeros, a.Nout, ng, a.Nout, rows, per, CU_TENSOR_MAP_SWIZZLE_NONE))))
+    return MEDUSA_ERR_CUDA;
+  auto kern = a.glog == 5 ? (tiled ? tc_kernel<4, true> : tc_kernel<4, false>)
+              : a.glog == 6 ? (tiled ? tc_kernel<2, true> : tc_kernel<2, false>)
+                            : (tiled ? tc_kernel<1, true> : tc_kernel<1, false>);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess) return MEDUSA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.grid);
@@ -558,7 +588,7 @@ medusa_status tc_launch(const Args& a, int withhold, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaLaunchKernelEx(&cfg, kern, mw, mx, p);
+  cudaLaunchKernelEx(&cfg, kern, mw, mx, ms, mz, p);
   return launch_status();
 }
 
