@@ -2,12 +2,19 @@
 // of tokens that the penalties go by.
 //
 // The mathematics is elementwise: z' of (row b, node n, token v) needs z, what is known of
-// (b, v) (count, prompt bit, bias) and whether v lies on n's path or is masked.  What bounds it:
-// memory, z read and z' written once.  So a thread owns VEC neighbouring tokens of one row b, loads what is
-// known of them once and goes through the nodes, kNodes logit loads in flight at a time; the tokens on
-// the paths, at most 17 a node and hardly ever in a block's columns, are sorted out beforehand into a
-// list a node in shared memory.
+// (b, v) (count, prompt bit, bias) and whether v lies on n's path or is masked.  All but the last two is
+// z' = z f + s with f one of two factors, by z's sign, and s a sum, both of (b, v) alone: a thread works them
+// out once for the tokens that it has and goes through the nodes with one multiply-add each.  The tokens
+// on the paths, at most 17 a node and few of them among a block's, are sorted out beforehand into a
+// list a node in shared memory with their results, which are written last.
+//
+// What bounds it: memory, z read and z' written once.  A thread has several loads of logits in flight, those of the
+// next nodes while it writes the last ones': of one place in several nodes' rows, or, where there are few nodes, of
+// several places in one.  The rows of all chunks of tokens, laid end to end, are divided evenly over the blocks that
+// the SMs hold at once.
 #include <math.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "host_util.h"
@@ -16,7 +23,8 @@ namespace medusa {
 namespace logits {
 
 constexpr int kThreads = 256;
-constexpr int kGroup = 32;               // nodes of a block at most
+constexpr int kBlocks = 4;               // that an SM holds at once
+constexpr int kGroup = 32;               // nodes that a block takes together at most
 constexpr int kPath = MEDUSA_MAX_DEPTH + 1;
 
 struct Args {
@@ -25,129 +33,195 @@ struct Args {
   medusa_logits_rules r;
   const int32_t *tokens, *parent;  // parent NULL: no tree
   int B, N, V, W;                  // W: words of a bit row
-  int chunks, groups, group;       // column chunks, groups of nodes, nodes of a group
+  int chunks;                      // of a row's tokens
+  long long units;                 // rows of all chunks
   float* out;
   int32_t* d_status;
 };
 
+// VEC logits as they lie in memory.
 template <typename T, int VEC>
-__device__ __forceinline__ void load_z(const T* p, float* z) {
-  if constexpr (VEC == 1) {
-    z[0] = load_elem(p, 0);
-  } else if constexpr (sizeof(T) == 4) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    z[0] = v.x; z[1] = v.y; z[2] = v.z; z[3] = v.w;
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    z[0] = __uint_as_float(v.x << 16); z[1] = __uint_as_float(v.x & 0xffff0000u);
-    z[2] = __uint_as_float(v.y << 16); z[3] = __uint_as_float(v.y & 0xffff0000u);
+struct Raw {
+  using Word = std::conditional_t<VEC == 1, T, std::conditional_t<sizeof(T) == 4, float4, uint2>>;
+  Word w;
+  __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const Word*>(p); }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (VEC == 1) return load_elem(&w, 0);
+    else if constexpr (sizeof(T) == 4) return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+    else return __uint_as_float(i == 0 ? w.x << 16 : i == 1 ? w.x & 0xffff0000u : i == 2 ? w.y << 16 : w.y & 0xffff0000u);
   }
+};
+
+// The mask row of a node, -1 for none.
+__device__ __forceinline__ long long mask_row_of(const Args& a, size_t row) {
+  if (!a.r.mask) return -1;
+  const long long m = a.r.mask_row ? a.r.mask_row[row] : (long long)row;
+  if (m >= -1 && m < a.r.n_masks) return m;
+  set_status(a.d_status, MEDUSA_DEV_BAD_INDEX);
+  return -1;
 }
 
-// Grid (chunks * groups, B).
-template <typename T, int VEC, int NODES>
-__global__ void __launch_bounds__(kThreads) process_kernel(const __grid_constant__ Args a) {
+// The result of a token on a node's path, which occurs there and before it c times.
+template <typename T>
+__device__ __noinline__ float on_path(const Args& a, int b, size_t row, int v, int c) {
+  const long long m = mask_row_of(a, row);
+  if (m >= 0 && !((a.r.mask[(size_t)m * a.W + (v >> 5)] >> (v & 31)) & 1u)) return -INFINITY;
+  float x = load_elem(static_cast<const T*>(a.z), row * a.ld + v);
+  if (a.r.counts) c += a.r.counts[(size_t)b * a.V + v];
+  if (a.r.repetition) x = x > 0.f ? x / a.r.repetition[b] : x * a.r.repetition[b];
+  if (a.r.frequency) x -= a.r.frequency[b] * (float)c;
+  if (a.r.presence) x -= a.r.presence[b];
+  if (a.r.bias) x += a.r.bias[(a.r.bias_rows > 1 ? (size_t)b * a.V : 0) + v];
+  return x;
+}
+
+// A thread has COLS times VEC neighbouring tokens, and NODES nodes at a time.
+template <typename T, int VEC, int COLS, int NODES>
+__global__ void __launch_bounds__(kThreads, kBlocks) process_kernel(const __grid_constant__ Args a) {
+  constexpr int WIDE = kThreads * VEC * COLS;  // tokens of a chunk
   __shared__ int s_tok[MEDUSA_MAX_NODES], s_par[MEDUSA_MAX_NODES];
-  __shared__ int s_row[kGroup];            // mask row of a node, -1: none
-  __shared__ int s_n[kGroup];              // tokens of its path in this block's columns
+  __shared__ int s_row[kGroup];  // mask row of a node, -1: none
+  __shared__ int s_n[kGroup];    // tokens of a node's path among the chunk's
   __shared__ uint16_t s_col[kGroup][kPath];
+  __shared__ float s_y[kGroup][kPath];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, chunk = blockIdx.x % a.chunks, grp = blockIdx.x / a.chunks;
-  const int n0 = grp * a.group, nn = min(a.group, a.N - n0);
-  const int v_lo = chunk * (kThreads * VEC), v0 = v_lo + tid * VEC;
-  const bool in = v0 < a.V;
-  for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
+  const int tid = threadIdx.x;
+  long long u = a.units * blockIdx.x / gridDim.x;
+  const long long end = a.units * (blockIdx.x + 1) / gridDim.x;
+#pragma unroll 1
+  while (u < end) {
+    // Nodes n0 .. n0 + nn - 1 of row b, one chunk of their tokens.
+    const long long item = u / a.N;
+    const int n0 = (int)(u - item * a.N), b = (int)(item / a.chunks), v_lo = (int)(item - (long long)b * a.chunks) * WIDE, v0 = v_lo + tid * VEC;
+    const int nn = (int)min(min((long long)kGroup, end - u), (long long)(a.N - n0));
     const size_t row0 = (size_t)b * a.N + n0;
-    // The nodes' tokens on their way to the root that fall into the block's columns.
+    u += nn;
     if (a.parent)
       for (int j = tid; j < n0 + nn; j += kThreads) {
         s_tok[j] = a.tokens[(size_t)b * a.N + j];
         s_par[j] = a.parent[j];
       }
-    if (tid < nn) {
-      int m = -1;
-      if (a.r.mask) {
-        const long long x = a.r.mask_row ? a.r.mask_row[row0 + tid] : (long long)(row0 + tid);
-        if (x >= 0 && x < a.r.n_masks) m = (int)x;
-        else if (x != -1) set_status(a.d_status, MEDUSA_DEV_BAD_INDEX);
-      }
-      s_row[tid] = m;
-      s_n[tid] = 0;
-    }
-    __syncthreads();
-    if (a.parent && tid < nn) {
-      int k = 0, j = n0 + tid;
-      for (int steps = 0; j >= 0; ++steps) {
-        const int t = s_tok[j], up = s_par[j];
-        if (t < 0 || t >= a.V) set_status(a.d_status, MEDUSA_DEV_BAD_INDEX);
-        else if (t >= v_lo && t < v_lo + kThreads * VEC) s_col[tid][k++] = (uint16_t)(t - v_lo);
-        if (j == 0 ? up != -1 : up < 0 || up >= j || steps == kPath - 1) {
-          set_status(a.d_status, MEDUSA_DEV_BAD_TOPOLOGY);
-          break;
+    if (a.r.mask && tid < nn) s_row[tid] = (int)mask_row_of(a, row0 + tid);
+    // The first nodes' logits and what is known of this thread's tokens: all on their way at once.
+    Raw<T, VEC> z[NODES][COLS];
+    uint32_t allowed[NODES][COLS];
+    auto fetch = [&](int j0) {
+#pragma unroll
+      for (int j = 0; j < NODES; ++j)
+#pragma unroll
+        for (int q = 0; q < COLS; ++q) {
+          const int v = v0 + q * (kThreads * VEC);
+          if (j0 + j < nn && v < a.V) z[j][q].load(static_cast<const T*>(a.z) + (row0 + j0 + j) * a.ld + v);
         }
-        j = up;
-      }
-      s_n[tid] = k;
-    }
-    // What is known of this thread's tokens.
-    int cnt[VEC];
-    float bias[VEC];
-    uint32_t said = 0;  // bit i: in the prompt
-    const float rep = a.r.repetition ? a.r.repetition[b] : 1.f, fr = a.r.frequency ? a.r.frequency[b] : 0.f,
-                pr = a.r.presence ? a.r.presence[b] : 0.f;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      cnt[i] = 0;
-      bias[i] = 0.f;
-    }
-    if (in) {
-      if (a.r.counts)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) cnt[i] = a.r.counts[(size_t)b * a.V + v0 + i];
-      if (a.r.bias)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) bias[i] = a.r.bias[(a.r.bias_rows > 1 ? (size_t)b * a.V : 0) + v0 + i];
-      if (a.r.prompt_bits) said = a.r.prompt_bits[(size_t)b * a.W + (v0 >> 5)] >> (v0 & 31);
-    }
-    __syncthreads();
-    for (int j0 = 0; j0 < nn; j0 += NODES) {
-      float z[NODES][VEC];
-      uint32_t allowed[NODES];
+    };
+    auto fetch_masks = [&](int j0) {
 #pragma unroll
       for (int j = 0; j < NODES; ++j) {
-        allowed[j] = 0xffffffffu;
-        if (in && j0 + j < nn) {
-          load_z<T, VEC>(static_cast<const T*>(a.z) + (row0 + j0 + j) * a.ld + v0, z[j]);
-          const int m = s_row[j0 + j];
-          if (m >= 0) allowed[j] = a.r.mask[(size_t)m * a.W + (v0 >> 5)] >> (v0 & 31);
+        const int m = a.r.mask && j0 + j < nn ? s_row[j0 + j] : -1;
+#pragma unroll
+        for (int q = 0; q < COLS; ++q) {
+          const int v = v0 + q * (kThreads * VEC);
+          allowed[j][q] = m >= 0 && v < a.V ? a.r.mask[(size_t)m * a.W + (v >> 5)] >> (v & 31) : 0xffffffffu;
         }
       }
+    };
+    fetch(0);
+    // Factors for z > 0 and otherwise, and what is added.
+    float pos[COLS][VEC], neg[COLS][VEC], add[COLS][VEC];
+    {
+      int c[COLS][VEC];
+      uint32_t prompt[COLS];
 #pragma unroll
-      for (int j = 0; j < NODES; ++j) {
-        if (j0 + j >= nn || !in) break;
-        int c[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) c[i] = cnt[i];
-        for (int k = 0; k < s_n[j0 + j]; ++k) {
-          const int col = s_col[j0 + j][k] - tid * VEC;
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) c[i] += col == i;
-        }
-        float y[VEC];
+      for (int q = 0; q < COLS; ++q) {
+        const int v = v0 + q * (kThreads * VEC);
+        const bool in = v < a.V;
+        prompt[q] = in && a.r.prompt_bits ? a.r.prompt_bits[(size_t)b * a.W + (v >> 5)] >> (v & 31) : 0;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          float x = z[j][i];
-          if (c[i] > 0 || ((said >> i) & 1u)) x = x > 0.f ? x / rep : x * rep;
-          if (c[i] > 0) x = x - fr * (float)c[i] - pr;
-          y[i] = (allowed[j] >> i) & 1u ? x + bias[i] : -INFINITY;
+          c[q][i] = in && a.r.counts ? a.r.counts[(size_t)b * a.V + v + i] : 0;
+          add[q][i] = in && a.r.bias ? a.r.bias[(a.r.bias_rows > 1 ? (size_t)b * a.V : 0) + v + i] : 0.f;
         }
-        float* dst = a.out + (row0 + j0 + j) * a.V + v0;
-        if constexpr (VEC == 4) *reinterpret_cast<float4*>(dst) = make_float4(y[0], y[1], y[2], y[3]);
-        else dst[0] = y[0];
       }
+      const float rep = a.r.repetition ? a.r.repetition[b] : 1.f, inv = 1.f / rep, fr = a.r.frequency ? a.r.frequency[b] : 0.f,
+                  pr = a.r.presence ? a.r.presence[b] : 0.f;
+#pragma unroll
+      for (int q = 0; q < COLS; ++q)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const bool said = c[q][i] > 0 || ((prompt[q] >> i) & 1u);
+          pos[q][i] = said ? inv : 1.f;
+          neg[q][i] = said ? rep : 1.f;
+          if (c[q][i] > 0) add[q][i] -= fr * (float)c[q][i] + pr;
+        }
     }
-    __syncthreads();  // the lists are read
+    if (a.parent || a.r.mask) __syncthreads();
+    if (a.parent) {
+      if (tid < nn) {
+        int k = 0, j = n0 + tid;
+        for (int steps = 0; j >= 0; ++steps) {
+          const int t = s_tok[j], up = s_par[j];
+          if (t < 0 || t >= a.V) set_status(a.d_status, MEDUSA_DEV_BAD_INDEX);
+          else if (t >= v_lo && t < v_lo + WIDE) s_col[tid][k++] = (uint16_t)(t - v_lo);
+          if (j == 0 ? up != -1 : up < 0 || up >= j || steps == kPath - 1) {
+            set_status(a.d_status, MEDUSA_DEV_BAD_TOPOLOGY);
+            break;
+          }
+          j = up;
+        }
+        s_n[tid] = k;
+      }
+      __syncthreads();
+      for (int i = tid; i < nn * kPath; i += kThreads) {
+        const int j = i / kPath, k = i - j * kPath, listed = s_n[j];
+        if (k >= listed) continue;
+        int c = 0;
+        for (int h = 0; h < listed; ++h) c += s_col[j][h] == s_col[j][k];
+        s_y[j][k] = on_path<T>(a, b, row0 + j, v_lo + s_col[j][k], c);
+      }
+      __syncthreads();  // what is written below may be what was read here
+    }
+    fetch_masks(0);
+#pragma unroll 1
+    for (int j0 = 0; j0 < nn; j0 += NODES) {
+      Raw<T, VEC> now[NODES][COLS];
+      uint32_t may[NODES][COLS];
+#pragma unroll
+      for (int j = 0; j < NODES; ++j)
+#pragma unroll
+        for (int q = 0; q < COLS; ++q) {
+          now[j][q] = z[j][q];
+          may[j][q] = allowed[j][q];
+        }
+      if (j0 + NODES < nn) {
+        fetch(j0 + NODES);
+        fetch_masks(j0 + NODES);
+      }
+#pragma unroll
+      for (int j = 0; j < NODES; ++j)
+#pragma unroll
+        for (int q = 0; q < COLS; ++q) {
+          const int v = v0 + q * (kThreads * VEC);
+          if (j0 + j >= nn || v >= a.V) continue;
+          float y[VEC];
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            const float x = now[j][q].get(i);
+            y[i] = (may[j][q] >> i) & 1u ? fmaf(x, x > 0.f ? pos[q][i] : neg[q][i], add[q][i]) : -INFINITY;
+          }
+          float* dst = a.out + (row0 + j0 + j) * a.V + v;
+          if constexpr (VEC == 4) *reinterpret_cast<float4*>(dst) = make_float4(y[0], y[1], y[2], y[3]);
+          else dst[0] = y[0];
+        }
+    }
+    if (a.parent || a.r.mask) __syncthreads();  // the mask rows are read, and the results below go over others
+    if (a.parent) {
+      for (int i = tid; i < nn * kPath; i += kThreads) {
+        const int j = i / kPath, k = i - j * kPath;
+        if (k < s_n[j]) a.out[(row0 + j) * a.V + v_lo + s_col[j][k]] = s_y[j][k];
+      }
+      __syncthreads();  // the lists are read
+    }
   }
 }
 
@@ -188,9 +262,19 @@ count_accepted_kernel(const int32_t* tokens, const int32_t* path_nodes, const in
   if (mine) atomicAdd(counts + (size_t)b * V + t, 1);
 }
 
-template <typename T, int VEC, int NODES>
-static void launch(const Args& a, int rows, cudaStream_t s) {
-  launch_pdl(process_kernel<T, VEC, NODES>, dim3((unsigned)(a.chunks * a.groups), rows), dim3(kThreads), 0, s, a);
+template <typename T, int VEC, int COLS, int NODES>
+static void launch(Args a, cudaStream_t s) {
+  const long long wide = kThreads * VEC * COLS, most = (long long)kBlocks * device_sm_count();
+  a.chunks = (int)((a.V + wide - 1) / wide);
+  a.units = (long long)a.N * a.B * a.chunks;
+  launch_pdl(process_kernel<T, VEC, COLS, NODES>, dim3((unsigned)(a.units < most ? a.units : most)), dim3(kThreads), 0, s, a);
+}
+// Few nodes: a thread's loads are of several places in a row.
+template <typename T, int VEC>
+static void launch(const Args& a, cudaStream_t s) {
+  constexpr int kLoads = VEC == 4 ? 4 : 8;
+  if (a.N < kLoads) launch<T, VEC, kLoads, 1>(a, s);
+  else launch<T, VEC, 1, kLoads>(a, s);
 }
 
 }  // namespace logits
@@ -238,15 +322,9 @@ extern "C" medusa_status medusa_logits_process(const void* logits, int64_t ld, m
   a.out = out;
   a.d_status = d_status;
   const bool vec = V % 4 == 0 && ld % 4 == 0 && ((uintptr_t)logits & (4 * es - 1)) == 0 && aligned16(out);
-  const int cols = kThreads * (vec ? 4 : 1);
-  a.chunks = (V + cols - 1) / cols;
-  a.group = N < 8 ? N : 8;
-  a.groups = (N + a.group - 1) / a.group;
-  if ((long long)a.chunks * a.groups > 0x7fffffffll) return MEDUSA_ERR_INVALID_ARG;
-  const int gy = B < 65535 ? B : 65535;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dt == MEDUSA_F32) vec ? launch<float, 4, 4>(a, gy, s) : launch<float, 1, 8>(a, gy, s);
-  else vec ? launch<uint16_t, 4, 4>(a, gy, s) : launch<uint16_t, 1, 8>(a, gy, s);
+  if (dt == MEDUSA_F32) vec ? launch<float, 4>(a, s) : launch<float, 1>(a, s);
+  else vec ? launch<uint16_t, 4>(a, s) : launch<uint16_t, 1>(a, s);
   return launch_status();
 }
 
