@@ -5,13 +5,14 @@
 // (b, v) (count, prompt bit, bias) and whether v lies on n's path or is masked.  All but the last two is
 // z' = z f + s with f one of two factors, by z's sign, and s a sum, both of (b, v) alone: a thread works them
 // out once for the tokens that it has and goes through the nodes with one multiply-add each.  The tokens
-// on the paths, at most 17 a node and few of them among a block's, are sorted out beforehand into a
-// list a node in shared memory with their results, which are written last.
+// on the paths, at most 17 a node and few of them among a block's, are sorted out into a list a node in
+// shared memory with their results, which are written last.
 //
 // What bounds it: memory, z read and z' written once.  A thread has several loads of logits in flight, those of the
 // next nodes while it writes the last ones': of one place in several nodes' rows, or, where there are few nodes, of
 // several places in one.  The rows of all chunks of tokens, laid end to end, are divided evenly over the blocks that
-// the SMs hold at once.
+// the SMs hold at once.  The paths are a warp's own work, beside the others': what it finds out takes four trips to
+// memory one after the other, which all waited for when they shared it (16 trees 42 us).
 #include <math.h>
 
 #include <type_traits>
@@ -34,8 +35,9 @@ struct Args {
   const int32_t *tokens, *parent;  // parent NULL: no tree
   int B, N, V, W;                  // W: words of a bit row
   int chunks;                      // of a row's tokens
-  long long units;                 // rows of all chunks
+  uint32_t units;                  // rows of all chunks
   float* out;
+  int in_place;
   int32_t* d_status;
 };
 
@@ -53,20 +55,17 @@ struct Raw {
 };
 
 // The mask row of a node, -1 for none.
-__device__ __forceinline__ long long mask_row_of(const Args& a, size_t row) {
-  if (!a.r.mask) return -1;
-  const long long m = a.r.mask_row ? a.r.mask_row[row] : (long long)row;
+__device__ __forceinline__ int mask_row_of(const Args& a, size_t row) {
+  const int m = a.r.mask_row ? a.r.mask_row[row] : (int)row;
   if (m >= -1 && m < a.r.n_masks) return m;
   set_status(a.d_status, MEDUSA_DEV_BAD_INDEX);
   return -1;
 }
 
-// The result of a token on a node's path, which occurs there and before it c times.
-template <typename T>
-__device__ __noinline__ float on_path(const Args& a, int b, size_t row, int v, int c) {
-  const long long m = mask_row_of(a, row);
+// The result of a token on a node's path, which occurs there c times.
+__device__ __forceinline__ float on_path(const Args& a, int b, size_t row, int v, int c, float x) {
+  const int m = a.r.mask ? mask_row_of(a, row) : -1;
   if (m >= 0 && !((a.r.mask[(size_t)m * a.W + (v >> 5)] >> (v & 31)) & 1u)) return -INFINITY;
-  float x = load_elem(static_cast<const T*>(a.z), row * a.ld + v);
   if (a.r.counts) c += a.r.counts[(size_t)b * a.V + v];
   if (a.r.repetition) x = x > 0.f ? x / a.r.repetition[b] : x * a.r.repetition[b];
   if (a.r.frequency) x -= a.r.frequency[b] * (float)c;
@@ -75,57 +74,103 @@ __device__ __noinline__ float on_path(const Args& a, int b, size_t row, int v, i
   return x;
 }
 
-// A thread has COLS times VEC neighbouring tokens, and NODES nodes at a time.
-template <typename T, int VEC, int COLS, int NODES>
+// All warps of a block, from places of their own.
+__device__ __forceinline__ void block_sync() {
+  __syncwarp();
+  asm volatile("barrier.cta.sync.aligned 1, %0;" ::"n"(kThreads) : "memory");
+}
+
+// A thread has COLS times VEC neighbouring tokens, and NODES nodes at a time.  TREE: the last warp has the paths.
+template <typename T, int VEC, int COLS, int NODES, bool TREE>
 __global__ void __launch_bounds__(kThreads, kBlocks) process_kernel(const __grid_constant__ Args a) {
-  constexpr int WIDE = kThreads * VEC * COLS;  // tokens of a chunk
-  __shared__ int s_tok[MEDUSA_MAX_NODES], s_par[MEDUSA_MAX_NODES];
-  __shared__ int s_row[kGroup];  // mask row of a node, -1: none
-  __shared__ int s_n[kGroup];    // tokens of a node's path among the chunk's
-  __shared__ uint16_t s_col[kGroup][kPath];
-  __shared__ float s_y[kGroup][kPath];
+  constexpr int MAIN = TREE ? kThreads - 32 : kThreads, WIDE = MAIN * VEC * COLS;  // threads with tokens, tokens of a chunk
+  // The last warp's own.
+  __shared__ int s_tok[TREE ? MEDUSA_MAX_NODES : 1], s_par[TREE ? MEDUSA_MAX_NODES : 1];
+  __shared__ uint16_t s_col[TREE ? kGroup : 1][kPath];
+  __shared__ float s_y[TREE ? kGroup : 1][kPath];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
-  long long u = a.units * blockIdx.x / gridDim.x;
-  const long long end = a.units * (blockIdx.x + 1) / gridDim.x;
+  uint32_t u = (uint32_t)((uint64_t)a.units * blockIdx.x / gridDim.x);
+  const uint32_t end = (uint32_t)((uint64_t)a.units * (blockIdx.x + 1) / gridDim.x);
 #pragma unroll 1
   while (u < end) {
     // Nodes n0 .. n0 + nn - 1 of row b, one chunk of their tokens.
-    const long long item = u / a.N;
-    const int n0 = (int)(u - item * a.N), b = (int)(item / a.chunks), v_lo = (int)(item - (long long)b * a.chunks) * WIDE, v0 = v_lo + tid * VEC;
-    const int nn = (int)min(min((long long)kGroup, end - u), (long long)(a.N - n0));
+    const uint32_t item = u / (uint32_t)a.N;
+    const int n0 = (int)(u - item * a.N), b = (int)(item / (uint32_t)a.chunks), v_lo = (int)(item - (uint32_t)b * a.chunks) * WIDE;
+    const int nn = (int)min(min((uint32_t)kGroup, end - u), (uint32_t)(a.N - n0));
     const size_t row0 = (size_t)b * a.N + n0;
     u += nn;
-    if (a.parent)
-      for (int j = tid; j < n0 + nn; j += kThreads) {
+    if (TREE && tid >= MAIN) {
+      // A lane a node: its path's tokens in this chunk, then their results.
+      const int lane = tid - MAIN;
+      int listed = 0;
+#pragma unroll 1
+      for (int j = lane; j < n0 + nn; j += 32) {
         s_tok[j] = a.tokens[(size_t)b * a.N + j];
         s_par[j] = a.parent[j];
       }
-    if (a.r.mask && tid < nn) s_row[tid] = (int)mask_row_of(a, row0 + tid);
+      __syncwarp();
+      if (lane < nn) {
+        int j = n0 + lane;
+#pragma unroll 1
+        for (int steps = 0; j >= 0; ++steps) {
+          const int t = s_tok[j], up = s_par[j];
+          if (t < 0 || t >= a.V) {
+            set_status(a.d_status, MEDUSA_DEV_BAD_INDEX);
+          } else if (t >= v_lo && t < v_lo + WIDE) {
+            s_col[lane][listed] = (uint16_t)(t - v_lo);
+            s_y[lane][listed++] = load_elem(static_cast<const T*>(a.z), (row0 + lane) * a.ld + t);
+          }
+          if (j == 0 ? up != -1 : up < 0 || up >= j || steps == kPath - 1) {
+            set_status(a.d_status, MEDUSA_DEV_BAD_TOPOLOGY);
+            break;
+          }
+          j = up;
+        }
+      }
+      if (a.in_place) block_sync();  // these logits are read before their places are written
+#pragma unroll 1
+      for (int k = 0; k < listed; ++k) {
+        int c = 0;
+#pragma unroll 1
+        for (int h = 0; h < listed; ++h) c += s_col[lane][h] == s_col[lane][k];
+        s_y[lane][k] = on_path(a, b, row0 + lane, v_lo + s_col[lane][k], c, s_y[lane][k]);
+      }
+      block_sync();  // the other results are written
+#pragma unroll 1
+      for (int k = 0; k < listed; ++k) a.out[(row0 + lane) * a.V + v_lo + s_col[lane][k]] = s_y[lane][k];
+      __syncwarp();
+      continue;
+    }
     // The first nodes' logits and what is known of this thread's tokens: all on their way at once.
+    const int v0 = v_lo + tid * VEC;
     Raw<T, VEC> z[NODES][COLS];
     uint32_t allowed[NODES][COLS];
+    int rows[NODES];
     auto fetch = [&](int j0) {
 #pragma unroll
       for (int j = 0; j < NODES; ++j)
 #pragma unroll
         for (int q = 0; q < COLS; ++q) {
-          const int v = v0 + q * (kThreads * VEC);
+          const int v = v0 + q * (MAIN * VEC);
           if (j0 + j < nn && v < a.V) z[j][q].load(static_cast<const T*>(a.z) + (row0 + j0 + j) * a.ld + v);
         }
     };
-    auto fetch_masks = [&](int j0) {
+    auto fetch_rows = [&](int j0) {
 #pragma unroll
-      for (int j = 0; j < NODES; ++j) {
-        const int m = a.r.mask && j0 + j < nn ? s_row[j0 + j] : -1;
+      for (int j = 0; j < NODES; ++j) rows[j] = a.r.mask && j0 + j < nn ? mask_row_of(a, row0 + j0 + j) : -1;
+    };
+    auto fetch_masks = [&] {
+#pragma unroll
+      for (int j = 0; j < NODES; ++j)
 #pragma unroll
         for (int q = 0; q < COLS; ++q) {
-          const int v = v0 + q * (kThreads * VEC);
-          allowed[j][q] = m >= 0 && v < a.V ? a.r.mask[(size_t)m * a.W + (v >> 5)] >> (v & 31) : 0xffffffffu;
+          const int v = v0 + q * (MAIN * VEC);
+          allowed[j][q] = rows[j] >= 0 && v < a.V ? a.r.mask[(size_t)rows[j] * a.W + (v >> 5)] >> (v & 31) : 0xffffffffu;
         }
-      }
     };
+    fetch_rows(0);
     fetch(0);
     // Factors for z > 0 and otherwise, and what is added.
     float pos[COLS][VEC], neg[COLS][VEC], add[COLS][VEC];
@@ -134,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) process_kernel(const __grid
       uint32_t prompt[COLS];
 #pragma unroll
       for (int q = 0; q < COLS; ++q) {
-        const int v = v0 + q * (kThreads * VEC);
+        const int v = v0 + q * (MAIN * VEC);
         const bool in = v < a.V;
         prompt[q] = in && a.r.prompt_bits ? a.r.prompt_bits[(size_t)b * a.W + (v >> 5)] >> (v & 31) : 0;
 #pragma unroll
@@ -145,6 +190,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) process_kernel(const __grid
       }
       const float rep = a.r.repetition ? a.r.repetition[b] : 1.f, inv = 1.f / rep, fr = a.r.frequency ? a.r.frequency[b] : 0.f,
                   pr = a.r.presence ? a.r.presence[b] : 0.f;
+      fetch_masks();
+      fetch_rows(NODES);
 #pragma unroll
       for (int q = 0; q < COLS; ++q)
 #pragma unroll
@@ -155,33 +202,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) process_kernel(const __grid
           if (c[q][i] > 0) add[q][i] -= fr * (float)c[q][i] + pr;
         }
     }
-    if (a.parent || a.r.mask) __syncthreads();
-    if (a.parent) {
-      if (tid < nn) {
-        int k = 0, j = n0 + tid;
-        for (int steps = 0; j >= 0; ++steps) {
-          const int t = s_tok[j], up = s_par[j];
-          if (t < 0 || t >= a.V) set_status(a.d_status, MEDUSA_DEV_BAD_INDEX);
-          else if (t >= v_lo && t < v_lo + WIDE) s_col[tid][k++] = (uint16_t)(t - v_lo);
-          if (j == 0 ? up != -1 : up < 0 || up >= j || steps == kPath - 1) {
-            set_status(a.d_status, MEDUSA_DEV_BAD_TOPOLOGY);
-            break;
-          }
-          j = up;
-        }
-        s_n[tid] = k;
-      }
-      __syncthreads();
-      for (int i = tid; i < nn * kPath; i += kThreads) {
-        const int j = i / kPath, k = i - j * kPath, listed = s_n[j];
-        if (k >= listed) continue;
-        int c = 0;
-        for (int h = 0; h < listed; ++h) c += s_col[j][h] == s_col[j][k];
-        s_y[j][k] = on_path<T>(a, b, row0 + j, v_lo + s_col[j][k], c);
-      }
-      __syncthreads();  // what is written below may be what was read here
-    }
-    fetch_masks(0);
+    if (TREE && a.in_place) block_sync();
 #pragma unroll 1
     for (int j0 = 0; j0 < nn; j0 += NODES) {
       Raw<T, VEC> now[NODES][COLS];
@@ -195,13 +216,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks) process_kernel(const __grid
         }
       if (j0 + NODES < nn) {
         fetch(j0 + NODES);
-        fetch_masks(j0 + NODES);
+        fetch_masks();
+        fetch_rows(j0 + 2 * NODES);
       }
 #pragma unroll
       for (int j = 0; j < NODES; ++j)
 #pragma unroll
         for (int q = 0; q < COLS; ++q) {
-          const int v = v0 + q * (kThreads * VEC);
+          const int v = v0 + q * (MAIN * VEC);
           if (j0 + j >= nn || v >= a.V) continue;
           float y[VEC];
 #pragma unroll
@@ -214,14 +236,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) process_kernel(const __grid
           else dst[0] = y[0];
         }
     }
-    if (a.parent || a.r.mask) __syncthreads();  // the mask rows are read, and the results below go over others
-    if (a.parent) {
-      for (int i = tid; i < nn * kPath; i += kThreads) {
-        const int j = i / kPath, k = i - j * kPath;
-        if (k < s_n[j]) a.out[(row0 + j) * a.V + v_lo + s_col[j][k]] = s_y[j][k];
-      }
-      __syncthreads();  // the lists are read
-    }
+    if (TREE) block_sync();
   }
 }
 
@@ -262,19 +277,19 @@ count_accepted_kernel(const int32_t* tokens, const int32_t* path_nodes, const in
   if (mine) atomicAdd(counts + (size_t)b * V + t, 1);
 }
 
-template <typename T, int VEC, int COLS, int NODES>
+template <typename T, int VEC, int COLS, int NODES, bool TREE>
 static void launch(Args a, cudaStream_t s) {
-  const long long wide = kThreads * VEC * COLS, most = (long long)kBlocks * device_sm_count();
+  const long long wide = (TREE ? kThreads - 32 : kThreads) * VEC * COLS, most = (long long)kBlocks * device_sm_count();
   a.chunks = (int)((a.V + wide - 1) / wide);
-  a.units = (long long)a.N * a.B * a.chunks;
-  launch_pdl(process_kernel<T, VEC, COLS, NODES>, dim3((unsigned)(a.units < most ? a.units : most)), dim3(kThreads), 0, s, a);
+  a.units = (uint32_t)((long long)a.N * a.B * a.chunks);
+  launch_pdl(process_kernel<T, VEC, COLS, NODES, TREE>, dim3((unsigned)(a.units < most ? a.units : most)), dim3(kThreads), 0, s, a);
 }
 // Few nodes: a thread's loads are of several places in a row.
 template <typename T, int VEC>
 static void launch(const Args& a, cudaStream_t s) {
-  constexpr int kLoads = VEC == 4 ? 4 : 8;
-  if (a.N < kLoads) launch<T, VEC, kLoads, 1>(a, s);
-  else launch<T, VEC, 1, kLoads>(a, s);
+  constexpr int NODES = VEC == 4 ? (sizeof(T) == 4 ? 2 : 4) : 6, COLS = VEC == 4 ? 2 : 4;
+  if (a.parent) a.N < 4 ? launch<T, VEC, COLS, 1, true>(a, s) : launch<T, VEC, 1, NODES, true>(a, s);
+  else a.N < 4 ? launch<T, VEC, COLS, 1, false>(a, s) : launch<T, VEC, 1, NODES, false>(a, s);
 }
 
 }  // namespace logits
@@ -320,7 +335,9 @@ extern "C" medusa_status medusa_logits_process(const void* logits, int64_t ld, m
   a.N = N;
   a.V = V;
   a.out = out;
+  a.in_place = in_place;
   a.d_status = d_status;
+  if (rows * ((V + kThreads - 33) / (kThreads - 32)) > 0xffffffffll) return MEDUSA_ERR_INVALID_ARG;  // more than a GPU holds
   const bool vec = V % 4 == 0 && ld % 4 == 0 && ((uintptr_t)logits & (4 * es - 1)) == 0 && aligned16(out);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dt == MEDUSA_F32) vec ? launch<float, 4>(a, s) : launch<float, 1>(a, s);
