@@ -8,11 +8,12 @@
 // on the paths, at most 17 a node and few of them among a block's, are sorted out into a list a node in
 // shared memory with their results, which are written last.
 //
-// What bounds it: memory, z read and z' written once.  A thread has several loads of logits in flight, those of the
-// next nodes while it writes the last ones': of one place in several nodes' rows, or, where there are few nodes, of
-// several places in one.  The rows of all chunks of tokens, laid end to end, are divided evenly over the blocks that
-// the SMs hold at once.  The paths are a warp's own work, beside the others': what it finds out takes four trips to
-// memory one after the other, which all waited for when they shared it (16 trees 42 us).
+// What bounds it: memory, z read and z' written once; it takes care that instructions do not (the first form took 30
+// an element, of which 9 are left).  A thread has several loads of logits in flight, those of the next nodes while it
+// writes the last ones'; where there are few nodes and no tree, of several places in a row.  The rows of all chunks of
+// tokens, laid end to end, are divided evenly over the blocks that the SMs hold at once.  The paths are a warp's own
+// work, beside the others': what it finds out takes four trips to memory one after the other, which all waited for
+// when they shared it.
 #include <math.h>
 
 #include <type_traits>
@@ -80,10 +81,10 @@ __device__ __forceinline__ void block_sync() {
   asm volatile("barrier.cta.sync.aligned 1, %0;" ::"n"(kThreads) : "memory");
 }
 
-// A thread has COLS times VEC neighbouring tokens, and NODES nodes at a time.  TREE: the last warp has the paths.
-template <typename T, int VEC, int COLS, int NODES, bool TREE>
+// A thread has VEC neighbouring tokens, and NODES nodes at a time.  TREE: the last warp has the paths.
+template <typename T, int VEC, int NODES, bool TREE>
 __global__ void __launch_bounds__(kThreads, kBlocks) process_kernel(const __grid_constant__ Args a) {
-  constexpr int MAIN = TREE ? kThreads - 32 : kThreads, WIDE = MAIN * VEC * COLS;  // threads with tokens, tokens of a chunk
+  constexpr int MAIN = TREE ? kThreads - 32 : kThreads, WIDE = MAIN * VEC;  // threads with tokens, tokens of a chunk
   // The last warp's own.
   __shared__ int s_tok[TREE ? MEDUSA_MAX_NODES : 1], s_par[TREE ? MEDUSA_MAX_NODES : 1];
   __shared__ uint16_t s_col[TREE ? kGroup : 1][kPath];
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) process_kernel(const __grid
     // Nodes n0 .. n0 + nn - 1 of row b, one chunk of their tokens.
     const uint32_t item = u / (uint32_t)a.N;
     const int n0 = (int)(u - item * a.N), b = (int)(item / (uint32_t)a.chunks), v_lo = (int)(item - (uint32_t)b * a.chunks) * WIDE;
-    const int nn = (int)min(min((uint32_t)kGroup, end - u), (uint32_t)(a.N - n0));
+    const int nn = (int)min(TREE ? min((uint32_t)kGroup, end - u) : end - u, (uint32_t)(a.N - n0));
     const size_t row0 = (size_t)b * a.N + n0;
     u += nn;
     if (TREE && tid >= MAIN) {
@@ -143,100 +144,170 @@ __global__ void __launch_bounds__(kThreads, kBlocks) process_kernel(const __grid
       __syncwarp();
       continue;
     }
-    // The first nodes' logits and what is known of this thread's tokens: all on their way at once.
-    const int v0 = v_lo + tid * VEC;
-    Raw<T, VEC> z[NODES][COLS];
-    uint32_t allowed[NODES][COLS];
+    const int v0 = v_lo + tid * VEC, shift = v0 & 31;
+    const bool in = v0 < a.V;
+    int left = in ? nn : 0;  // nodes that this thread has still to write
+    const T* zp = static_cast<const T*>(a.z) + row0 * a.ld + v0;
+    float* yp = a.out + row0 * a.V + v0;
+    const int32_t* rp = a.r.mask_row ? a.r.mask_row + row0 : nullptr;
+    const uint32_t* mp = a.r.mask ? a.r.mask + (v0 >> 5) : nullptr;
+    int next_row = (int)row0;  // where no rows of masks are named
+    Raw<T, VEC> z[NODES];
+    uint32_t allowed[NODES];
     int rows[NODES];
-    auto fetch = [&](int j0) {
+    // The next `n` nodes' logits; their mask rows; the masks of rows fetched before.
+    auto fetch = [&](int n) {
 #pragma unroll
-      for (int j = 0; j < NODES; ++j)
-#pragma unroll
-        for (int q = 0; q < COLS; ++q) {
-          const int v = v0 + q * (MAIN * VEC);
-          if (j0 + j < nn && v < a.V) z[j][q].load(static_cast<const T*>(a.z) + (row0 + j0 + j) * a.ld + v);
-        }
+      for (int j = 0; j < NODES; ++j, zp += a.ld)
+        if (j < n) z[j].load(zp);
     };
-    auto fetch_rows = [&](int j0) {
+    auto fetch_rows = [&](int n) {
+      if (!mp) return;
 #pragma unroll
-      for (int j = 0; j < NODES; ++j) rows[j] = a.r.mask && j0 + j < nn ? mask_row_of(a, row0 + j0 + j) : -1;
+      for (int j = 0; j < NODES; ++j) {
+        rows[j] = -1;
+        if (j < n) rows[j] = rp ? rp[j] : next_row + j;
+      }
+      if (rp) rp += NODES;
+      next_row += NODES;
     };
     auto fetch_masks = [&] {
 #pragma unroll
-      for (int j = 0; j < NODES; ++j)
-#pragma unroll
-        for (int q = 0; q < COLS; ++q) {
-          const int v = v0 + q * (MAIN * VEC);
-          allowed[j][q] = rows[j] >= 0 && v < a.V ? a.r.mask[(size_t)rows[j] * a.W + (v >> 5)] >> (v & 31) : 0xffffffffu;
+      for (int j = 0; j < NODES; ++j) {
+        allowed[j] = 0xffffffffu;
+        if (mp) {
+          if (rows[j] < -1 || rows[j] >= a.r.n_masks) {
+            set_status(a.d_status, MEDUSA_DEV_BAD_INDEX);
+          } else if (rows[j] >= 0) {
+            allowed[j] = mp[(size_t)rows[j] * a.W] >> shift;
+          }
         }
+      }
     };
-    fetch_rows(0);
-    fetch(0);
+    fetch_rows(left);
+    fetch(left);
     // Factors for z > 0 and otherwise, and what is added.
-    float pos[COLS][VEC], neg[COLS][VEC], add[COLS][VEC];
+    float pos[VEC], neg[VEC], add[VEC];
     {
-      int c[COLS][VEC];
-      uint32_t prompt[COLS];
+      int c[VEC];
+      const uint32_t prompt = in && a.r.prompt_bits ? a.r.prompt_bits[(size_t)b * a.W + (v0 >> 5)] >> shift : 0;
 #pragma unroll
-      for (int q = 0; q < COLS; ++q) {
-        const int v = v0 + q * (MAIN * VEC);
-        const bool in = v < a.V;
-        prompt[q] = in && a.r.prompt_bits ? a.r.prompt_bits[(size_t)b * a.W + (v >> 5)] >> (v & 31) : 0;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          c[q][i] = in && a.r.counts ? a.r.counts[(size_t)b * a.V + v + i] : 0;
-          add[q][i] = in && a.r.bias ? a.r.bias[(a.r.bias_rows > 1 ? (size_t)b * a.V : 0) + v + i] : 0.f;
-        }
+      for (int i = 0; i < VEC; ++i) {
+        c[i] = in && a.r.counts ? a.r.counts[(size_t)b * a.V + v0 + i] : 0;
+        add[i] = in && a.r.bias ? a.r.bias[(a.r.bias_rows > 1 ? (size_t)b * a.V : 0) + v0 + i] : 0.f;
       }
       const float rep = a.r.repetition ? a.r.repetition[b] : 1.f, inv = 1.f / rep, fr = a.r.frequency ? a.r.frequency[b] : 0.f,
                   pr = a.r.presence ? a.r.presence[b] : 0.f;
       fetch_masks();
-      fetch_rows(NODES);
+      fetch_rows(left - NODES);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const bool said = c[i] > 0 || ((prompt >> i) & 1u);
+        pos[i] = said ? inv : 1.f;
+        neg[i] = said ? rep : 1.f;
+        if (c[i] > 0) add[i] -= fr * (float)c[i] + pr;
+      }
+    }
+    if (TREE && a.in_place) block_sync();
+    auto write = [&](const Raw<T, VEC>& x, uint32_t may) {
+      float y[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float e = x.get(i);
+        y[i] = may & (1u << i) ? fmaf(e, e > 0.f ? pos[i] : neg[i], add[i]) : -INFINITY;
+      }
+      if constexpr (VEC == 4) *reinterpret_cast<float4*>(yp) = make_float4(y[0], y[1], y[2], y[3]);
+      else *yp = y[0];
+      yp += a.V;
+    };
+#pragma unroll 1
+    for (; left > 0; left -= NODES) {
+      Raw<T, VEC> now[NODES];
+      uint32_t may[NODES];
+#pragma unroll
+      for (int j = 0; j < NODES; ++j) {
+        now[j] = z[j];
+        may[j] = allowed[j];
+      }
+      if (left >= 2 * NODES) {
+        fetch(NODES);
+        fetch_masks();
+        fetch_rows(left - 2 * NODES);
+      } else if (left > NODES) {
+        fetch(left - NODES);
+        fetch_masks();
+      }
+      if (left >= NODES) {
+#pragma unroll
+        for (int j = 0; j < NODES; ++j) write(now[j], may[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NODES; ++j)
+          if (j < left) write(now[j], may[j]);
+      }
+    }
+    if (TREE) block_sync();
+  }
+}
+
+// Few nodes and no tree: a thread has COLS times VEC tokens of a row, and nothing is worked out for other rows.
+template <typename T, int VEC, int COLS>
+__global__ void __launch_bounds__(kThreads, kBlocks) rows_kernel(const __grid_constant__ Args a) {
+  constexpr int STEP = kThreads * VEC, WIDE = STEP * COLS;
+  pdl_wait();
+  pdl_trigger();
+  uint32_t u = (uint32_t)((uint64_t)a.units * blockIdx.x / gridDim.x);
+  const uint32_t end = (uint32_t)((uint64_t)a.units * (blockIdx.x + 1) / gridDim.x);
+#pragma unroll 1
+  for (; u < end; ++u) {
+    const uint32_t row = u / (uint32_t)a.chunks;
+    const int v_lo = (int)(u - row * a.chunks) * WIDE, v0 = v_lo + threadIdx.x * VEC, shift = v0 & 31, b = (int)(row / (uint32_t)a.N);
+    const bool whole = v_lo + WIDE <= a.V;
+    const int m = a.r.mask ? mask_row_of(a, row) : -1;
+    const float rep = a.r.repetition ? a.r.repetition[b] : 1.f, fr = a.r.frequency ? a.r.frequency[b] : 0.f, pr = a.r.presence ? a.r.presence[b] : 0.f;
+    const T* zp = static_cast<const T*>(a.z) + (size_t)row * a.ld + v0;
+    const int32_t* cp = a.r.counts ? a.r.counts + (size_t)b * a.V + v0 : nullptr;
+    const float* ep = a.r.bias ? a.r.bias + (a.r.bias_rows > 1 ? (size_t)b * a.V : 0) + v0 : nullptr;
+    const uint32_t* pp = a.r.prompt_bits ? a.r.prompt_bits + (size_t)b * a.W + (v0 >> 5) : nullptr;
+    float* yp = a.out + (size_t)row * a.V + v0;
+    auto chunk = [&](auto here) {  // here(q): place q is inside the row
+      Raw<T, VEC> z[COLS];
+      int c[COLS][VEC];
+      float e[COLS][VEC];
+      uint32_t prompt[COLS], allowed[COLS];
+#pragma unroll
+      for (int q = 0; q < COLS; ++q)
+        if (here(q)) z[q].load(zp + q * STEP);
 #pragma unroll
       for (int q = 0; q < COLS; ++q)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          const bool said = c[q][i] > 0 || ((prompt[q] >> i) & 1u);
-          pos[q][i] = said ? inv : 1.f;
-          neg[q][i] = said ? rep : 1.f;
-          if (c[q][i] > 0) add[q][i] -= fr * (float)c[q][i] + pr;
+          c[q][i] = cp && here(q) ? cp[q * STEP + i] : 0;
+          e[q][i] = ep && here(q) ? ep[q * STEP + i] : 0.f;
         }
-    }
-    if (TREE && a.in_place) block_sync();
-#pragma unroll 1
-    for (int j0 = 0; j0 < nn; j0 += NODES) {
-      Raw<T, VEC> now[NODES][COLS];
-      uint32_t may[NODES][COLS];
 #pragma unroll
-      for (int j = 0; j < NODES; ++j)
+      for (int q = 0; q < COLS; ++q) prompt[q] = pp && here(q) ? pp[q * (STEP / 32)] >> shift : 0;
+      const uint32_t* mp = a.r.mask + (m >= 0 ? (size_t)m * a.W + (v0 >> 5) : 0);
 #pragma unroll
-        for (int q = 0; q < COLS; ++q) {
-          now[j][q] = z[j][q];
-          may[j][q] = allowed[j][q];
+      for (int q = 0; q < COLS; ++q) allowed[q] = m >= 0 && here(q) ? mp[q * (STEP / 32)] >> shift : 0xffffffffu;
+      const float inv = 1.f / rep;
+#pragma unroll
+      for (int q = 0; q < COLS; ++q) {
+        float y[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float x = z[q].get(i), f = c[q][i] > 0 || (prompt[q] & (1u << i)) ? (x > 0.f ? inv : rep) : 1.f;
+          const float s = c[q][i] > 0 ? e[q][i] - (fr * (float)c[q][i] + pr) : e[q][i];
+          y[i] = allowed[q] & (1u << i) ? fmaf(x, f, s) : -INFINITY;
         }
-      if (j0 + NODES < nn) {
-        fetch(j0 + NODES);
-        fetch_masks();
-        fetch_rows(j0 + 2 * NODES);
+        if (here(q)) {
+          if constexpr (VEC == 4) *reinterpret_cast<float4*>(yp + q * STEP) = make_float4(y[0], y[1], y[2], y[3]);
+          else yp[q * STEP] = y[0];
+        }
       }
-#pragma unroll
-      for (int j = 0; j < NODES; ++j)
-#pragma unroll
-        for (int q = 0; q < COLS; ++q) {
-          const int v = v0 + q * (MAIN * VEC);
-          if (j0 + j >= nn || v >= a.V) continue;
-          float y[VEC];
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const float x = now[j][q].get(i);
-            y[i] = (may[j][q] >> i) & 1u ? fmaf(x, x > 0.f ? pos[q][i] : neg[q][i], add[q][i]) : -INFINITY;
-          }
-          float* dst = a.out + (row0 + j0 + j) * a.V + v;
-          if constexpr (VEC == 4) *reinterpret_cast<float4*>(dst) = make_float4(y[0], y[1], y[2], y[3]);
-          else dst[0] = y[0];
-        }
-    }
-    if (TREE) block_sync();
+    };
+    if (whole) chunk([](int) { return true; });
+    else chunk([&](int q) { return v0 + q * STEP < a.V; });
   }
 }
 
@@ -277,19 +348,17 @@ count_accepted_kernel(const int32_t* tokens, const int32_t* path_nodes, const in
   if (mine) atomicAdd(counts + (size_t)b * V + t, 1);
 }
 
-template <typename T, int VEC, int COLS, int NODES, bool TREE>
+template <typename T, int VEC>
 static void launch(Args a, cudaStream_t s) {
-  const long long wide = (TREE ? kThreads - 32 : kThreads) * VEC * COLS, most = (long long)kBlocks * device_sm_count();
+  constexpr int NODES = VEC == 4 ? (sizeof(T) == 4 ? 2 : 4) : 6, COLS = VEC == 4 ? 2 : 8;
+  const bool few = !a.parent && a.N < 4;
+  const long long wide = few ? kThreads * VEC * COLS : (a.parent ? kThreads - 32 : kThreads) * VEC, most = (long long)kBlocks * device_sm_count();
   a.chunks = (int)((a.V + wide - 1) / wide);
   a.units = (uint32_t)((long long)a.N * a.B * a.chunks);
-  launch_pdl(process_kernel<T, VEC, COLS, NODES, TREE>, dim3((unsigned)(a.units < most ? a.units : most)), dim3(kThreads), 0, s, a);
-}
-// Few nodes: a thread's loads are of several places in a row.
-template <typename T, int VEC>
-static void launch(const Args& a, cudaStream_t s) {
-  constexpr int NODES = VEC == 4 ? (sizeof(T) == 4 ? 2 : 4) : 6, COLS = VEC == 4 ? 2 : 4;
-  if (a.parent) a.N < 4 ? launch<T, VEC, COLS, 1, true>(a, s) : launch<T, VEC, 1, NODES, true>(a, s);
-  else a.N < 4 ? launch<T, VEC, COLS, 1, false>(a, s) : launch<T, VEC, 1, NODES, false>(a, s);
+  const dim3 grid((unsigned)(a.units < most ? a.units : most));
+  if (few) launch_pdl(rows_kernel<T, VEC, COLS>, grid, dim3(kThreads), 0, s, a);
+  else if (a.parent) launch_pdl(process_kernel<T, VEC, NODES, true>, grid, dim3(kThreads), 0, s, a);
+  else launch_pdl(process_kernel<T, VEC, NODES, false>, grid, dim3(kThreads), 0, s, a);
 }
 
 }  // namespace logits
