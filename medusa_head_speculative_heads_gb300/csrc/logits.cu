@@ -26,6 +26,7 @@ namespace logits {
 
 constexpr int kThreads = 256;
 constexpr int kBlocks = 4;               // that an SM holds at once
+constexpr int kRowBlocks = 5;            // of few nodes
 constexpr int kGroup = 32;               // nodes that a block takes together at most
 constexpr int kPath = MEDUSA_MAX_DEPTH + 1;
 
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) process_kernel(const __grid
 
 // Few nodes and no tree: a thread has COLS times VEC tokens of a row, and nothing is worked out for other rows.
 template <typename T, int VEC, int COLS>
-__global__ void __launch_bounds__(kThreads, kBlocks) rows_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, kRowBlocks) rows_kernel(const __grid_constant__ Args a) {
   constexpr int STEP = kThreads * VEC, WIDE = STEP * COLS;
   pdl_wait();
   pdl_trigger();
@@ -350,9 +351,9 @@ count_accepted_kernel(const int32_t* tokens, const int32_t* path_nodes, const in
 
 template <typename T, int VEC>
 static void launch(Args a, cudaStream_t s) {
-  constexpr int NODES = VEC == 4 ? (sizeof(T) == 4 ? 2 : 4) : 6, COLS = VEC == 4 ? 2 : 8;
+  constexpr int NODES = VEC == 4 ? (sizeof(T) == 4 ? 2 : 4) : 6, COLS = VEC == 4 ? (sizeof(T) == 4 ? 1 : 2) : 7;
   const bool few = !a.parent && a.N < 4;
-  const long long wide = few ? kThreads * VEC * COLS : (a.parent ? kThreads - 32 : kThreads) * VEC, most = (long long)kBlocks * device_sm_count();
+  const long long wide = few ? kThreads * VEC * COLS : (a.parent ? kThreads - 32 : kThreads) * VEC, most = (long long)(few ? kRowBlocks : kBlocks) * device_sm_count();
   a.chunks = (int)((a.V + wide - 1) / wide);
   a.units = (uint32_t)((long long)a.N * a.B * a.chunks);
   const dim3 grid((unsigned)(a.units < most ? a.units : most));
