@@ -28,72 +28,116 @@ __device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uin
 
 // ------------------------------------------------------------------ few tokens
 //
-// A CTA has 16 rows of W and 8 NT tokens; its warps take blocks of 128 columns in turn and their sums
-// meet in shared memory.  Of a block, lane 4 g + t holds 32 columns, from 32 t on, of the rows g and g + 8 and of
-// the tokens g, g + 8, ...: two 16-byte loads of weights, whose group is one whatever its size.  The
-// products' columns may come in any order so long as both operands' do: word j of a lane's four gives
-// the operands of two 16-column products, of which each lane's elements are neighbours in memory.
-constexpr int kWarps = 8;
-
-template <int NT>
-__global__ void __launch_bounds__(kWarps * 32) few_kernel(const __grid_constant__ Args a) {
-  __shared__ float part[kWarps][NT][16][9];
+// A CTA has 16 MT rows of W and 8 NT tokens; its warps take blocks of 128 columns in turn and their sums
+// meet in shared memory.  Of a block, lane 4 g + t holds 32 columns, from 32 t on, of the rows g + 8 j and of
+// the tokens g + 8 j: 16-byte loads of weights, whose group is one whatever its size.  The product
+// instructions' columns may come in any order so long as both operands' do: word j of a lane's four gives the
+// operands of two 16-column products, of which each lane's elements are neighbours in memory.
+//
+// What bounds it: the instructions that unpack (15 a word, of which 7 at half rate), and memory next to them: a kernel
+// that only reads 65 MB in such pieces takes 13.5 us.  Rows that lie outside W are not asked for (the last CTA's rows
+// are moved up, what another CTA has too is not stored), tokens behind the last one repeat it, and the next block's
+// weights are on their way while one is unpacked.
+template <int NT, int MT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) few_kernel(const __grid_constant__ Args a) {
+  constexpr int R = 2 * MT, ROWS = 16 * MT;  // rows of a lane, of the CTA
+  __shared__ float part[WARPS][NT][ROWS][9];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int base = min((int)blockIdx.x * ROWS, a.Nout - ROWS);
+  const size_t pitch = (size_t)a.K / 2;
+  int k0 = warp * 128;
+  const uint8_t* w[R];
+#pragma unroll
+  for (int j = 0; j < R; ++j) w[j] = reinterpret_cast<const uint8_t*>(a.q) + (base + g + 8 * j) * pitch + (k0 + 32 * t) / 2;
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int mt = blockIdx.x;
-  const int n_lo = min(mt * 16 + g, a.Nout - 1), n_hi = min(mt * 16 + g + 8, a.Nout - 1);  // rows past the last: computed, not stored
-  const uint8_t *w_lo = reinterpret_cast<const uint8_t*>(a.q) + (size_t)n_lo * (a.K / 2), *w_hi = reinterpret_cast<const uint8_t*>(a.q) + (size_t)n_hi * (a.K / 2);
-  float acc[NT][4] = {};
-  for (int k0 = warp * 128; k0 < a.K; k0 += kWarps * 128) {
-    const int k = k0 + 32 * t;
-    uint32_t lo[4] = {}, hi[4] = {};
-    Group g_lo{0, 0}, g_hi{0, 0};
+  size_t at = (size_t)((k0 + 32 * t) >> a.glog) * a.Nout + base + g;
+  const size_t at_step = (size_t)((WARPS * 128) >> a.glog) * a.Nout;
+  const uint16_t* x[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) x[j] = a.x + (long long)min(g + 8 * j, a.T - 1) * a.ldx + k0 + 32 * t;
+  float acc[MT][NT][4] = {};
+  uint4 v[R];
+  auto load = [&](bool here) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      v[j] = make_uint4(0, 0, 0, 0);
+      if (here) v[j] = load_once(w[j]);
+      w[j] += WARPS * 64;
+    }
+  };
+  auto block = [&](bool here, bool more) {
+    uint32_t s[R], z[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      s[j] = here ? a.scales[at + 8 * j] : 0;
+      z[j] = here && a.zeros ? a.zeros[at + 8 * j] : 8;
+    }
     uint4 xv[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xv[j][i] = make_uint4(0, 0, 0, 0);
-    if (k < a.K) {
-      *reinterpret_cast<uint4*>(lo) = load_once(w_lo + k / 2);
-      *reinterpret_cast<uint4*>(hi) = load_once(w_hi + k / 2);
-      g_lo = group_at(a, k >> a.glog, n_lo);
-      g_hi = group_at(a, k >> a.glog, n_hi);
+      for (int i = 0; i < 4; ++i) {
+        xv[j][i] = make_uint4(0, 0, 0, 0);
+        if (here) xv[j][i] = reinterpret_cast<const uint4*>(x[j])[i];
+      }
+    uint4 now[R];
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        if (8 * j + g < a.T) {
-          const uint4* p = reinterpret_cast<const uint4*>(a.x + (8 * j + g) * a.ldx + k);
+    for (int j = 0; j < R; ++j) now[j] = v[j];
+    if (more) load(true);
+    at += at_step;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) xv[j][i] = p[i];
+    for (int j = 0; j < NT; ++j) x[j] += WARPS * 128;
+    Group gr[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) gr[j] = group_of(s[j], z[j]);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const uint32_t lo[4] = {now[2 * m].x, now[2 * m].y, now[2 * m].z, now[2 * m].w},
+                     hi[4] = {now[2 * m + 1].x, now[2 * m + 1].y, now[2 * m + 1].z, now[2 * m + 1].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t p[4], r[4];
+        unpack(lo[i], gr[2 * m], p);
+        unpack(hi[i], gr[2 * m + 1], r);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma16816(acc[m][j], p[0], r[0], p[1], r[1], xv[j][i].x, xv[j][i].y);
+          mma16816(acc[m][j], p[2], r[2], p[3], r[3], xv[j][i].z, xv[j][i].w);
         }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t p[4], r[4];
-      unpack(lo[i], g_lo, p);
-      unpack(hi[i], g_hi, r);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        mma16816(acc[j], p[0], r[0], p[1], r[1], xv[j][i].x, xv[j][i].y);
-        mma16816(acc[j], p[2], r[2], p[3], r[3], xv[j][i].z, xv[j][i].w);
       }
     }
+  };
+  if (k0 + 128 <= a.K) load(true);
+#pragma unroll 1
+  for (; k0 + 128 <= a.K; k0 += WARPS * 128) block(true, k0 + (WARPS + 1) * 128 <= a.K);
+  if (k0 < a.K) {  // the rest of K is this warp's
+    const bool here = k0 + 32 * t < a.K;
+    load(here);
+    block(here, false);
   }
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    part[warp][j][g][2 * t] = acc[j][0];
-    part[warp][j][g][2 * t + 1] = acc[j][1];
-    part[warp][j][g + 8][2 * t] = acc[j][2];
-    part[warp][j][g + 8][2 * t + 1] = acc[j][3];
-  }
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      part[warp][j][16 * m + g][2 * t] = acc[m][j][0];
+      part[warp][j][16 * m + g][2 * t + 1] = acc[m][j][1];
+      part[warp][j][16 * m + g + 8][2 * t] = acc[m][j][2];
+      part[warp][j][16 * m + g + 8][2 * t + 1] = acc[m][j][3];
+    }
   __syncthreads();
-  for (int i = threadIdx.x; i < NT * 128; i += kWarps * 32) {
-    const int m = i & 15, tok = i >> 4;
-    float v = 0.f;
+  for (int i = threadIdx.x; i < NT * 8 * ROWS; i += WARPS * 32) {
+    const int m = i % ROWS, tok = i / ROWS, n = base + m;
+    float y = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += part[w][tok >> 3][m][tok & 7];
-    if (tok < a.T && mt * 16 + m < a.Nout) store_y(a, tok, mt * 16 + m, v);
+    for (int k = 0; k < WARPS; ++k) y += part[k][tok >> 3][m][tok & 7];
+    if (tok < a.T && n >= (int)blockIdx.x * ROWS) store_y(a, tok, n, y);
   }
+}
+
+template <int NT, int MT, int WARPS>
+static void few(const Args& a, cudaStream_t s) {
+  launch_pdl(few_kernel<NT, MT, WARPS>, dim3((a.Nout + 16 * MT - 1) / (16 * MT)), dim3(WARPS * 32), 0, s, a);
 }
 
 // ------------------------------------------------------------------ making the weights
@@ -171,8 +215,13 @@ extern "C" medusa_status medusa_w4_quantize(const void* w, int Nout, int K, int 
   return launch_status();
 }
 
-// Up to 16 tokens the warps' own product instructions, fed from registers; more on tensor memory.
-static bool on_tc(int T) { return T > 16; }
+// Up to 16 tokens the warps' own product instructions, fed from registers; more on tensor memory (and fewer features
+// than a CTA's).
+static bool on_tc(int T, int Nout) { return T > 16 || Nout < 32; }
+// From here on there are CTAs enough of 32 rows, which share the tokens' loads among more weights (one token, 32000
+// features 20.0 us, with 16 rows 20.3; 7 tokens, 13825 features 13.0 and 15.6); below, 16 rows and twice the warps are
+// sooner done (4096 features 4.1 us, with 32 rows 4.9).
+constexpr int kWide = 8192;
 
 extern "C" size_t medusa_linear_w4_workspace_size(int T, int K, int Nout, int group) {
   return 0;
@@ -208,12 +257,10 @@ static medusa_status linear_call(const void* x, int64_t ldx, const uint32_t* qwe
   a.y32 = y_dt == MEDUSA_F32;
   a.d_status = d_status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (on_tc(T)) return tc_launch(a, withhold, s);
+  if (on_tc(T, Nout)) return tc_launch(a, withhold, s);
   if (withhold) return MEDUSA_ERR_INVALID_ARG;
-  const int nt = T <= 8 ? 1 : 2;
-  const dim3 gd((Nout + 15) / 16), bd(kWarps * 32);
-  if (nt == 1) launch_pdl(few_kernel<1>, gd, bd, 0, s, a);
-  else launch_pdl(few_kernel<2>, gd, bd, 0, s, a);
+  if (Nout >= kWide) T <= 8 ? few<1, 2, 8>(a, s) : few<2, 2, 8>(a, s);
+  else T <= 8 ? few<1, 1, 16>(a, s) : few<2, 1, 16>(a, s);
   return launch_status();
 }
 
