@@ -1,6 +1,6 @@
 // medusa_linear_w4 on tcgen05 tensor cores: many tokens.
 //
-// y^T = W x^T in tiles of up to 256 features by up to 192 tokens.  Weights come as they are kept, 64 bytes a
+// y^T = W x^T in tiles of up to 256 features by up to 128 tokens.  Weights come as they are kept, 64 bytes a
 // row and 128 columns, by TMA; sixteen warps unpack them into tensor memory, where the matrix instruction reads its
 // first operand (a thread has a row's 128 columns: 16 words, four loads of 16 bytes from shared memory), so that
 // unpacked weights never pass through shared memory.  The tokens are the second operand, by TMA.  The features
@@ -20,6 +20,8 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "host_util.h"
 #include "linear_w4.h"
 #include "sm100.cuh"
@@ -32,7 +34,7 @@ constexpr int kThreads = 768;              // W, products, x, products; 4 x 4 un
 constexpr int kUnpackers = 16;
 constexpr int kHalf = 128;                 // features of a half of a tile at most
 constexpr int kCols = 128;                 // columns of a block
-constexpr int kMaxTN = 192;
+constexpr int kMaxTN = 128;
 constexpr int kMaxShare = 8;               // CTAs of a cluster
 constexpr int kSlotsW = 4;
 constexpr int kMaxSlotsX = 8;
@@ -47,7 +49,7 @@ constexpr uint64_t kDrainNs = 100000000ull;
 
 struct Tc {
   Args a;
-  int TN, DN, NA, NX;  // tokens of a tile, columns of a sum, buffers of unpacked weights and slots of tokens
+  int TN, DN, NX;      // tokens of a tile, columns of a sum, slots of tokens (an even number)
   int halves, RH;      // halves of a tile and the features of one
   int mtiles, ntiles, kblocks;
   int share;           // CTAs of a cluster, which share a tile
@@ -291,33 +293,41 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
   } else if (warp == 1 || (warp == 3 && p.halves == 2)) {
     // ------------------------------------------------------------ products of half h
     // Issued by an elected lane of the whole warp, their addresses known to be the same in all lanes: by a lane on
-    // its own a product took 80 clocks to issue, so 11.
+    // its own a product took 80 clocks to issue, so 11.  What a block costs besides has to stay below what its products
+    // take: one wait (an unpacking warp has waited for the tokens), and blocks two by two, whose buffers are constants.
     const int h = warp >> 1;
     const uint32_t idesc = uniform(idesc_bf16_f32(128, p.TN, false, false)), d = uniform(tmem + h * p.DN),
-                   a0 = uniform(tmem + 2 * p.DN + h * p.NA * 64), x0 = (smem_u32(ring_x) >> 4) | (1u << 16), half = uniform(p.TN * 8);
-    Ring t;
-    uint32_t i = 0;  // blocks
-    bool alive = true;
-    for (int seg = 0; x.left > 0 && alive; ++seg, x.left -= x.nb) {
-      const int nb = x.nb;
-#pragma unroll 1
-      for (int k = 0; k < nb; ++k, ++i) {
-        const uint32_t xd = uniform(x0 + t.i * p.TN * 16), a = uniform(a0 + (i & (p.NA - 1)) * 64);
-        if (k == 0 && seg > 0 && !(alive = warp_wait(&tail->d_empty[h], (uint32_t)(seg - 1) & 1u, abort))) break;
-        if (!(alive = warp_wait(&tail->x_full[t.i], t.full(), abort) && warp_wait(&tail->a_full[h][i & 1], (i >> 1) & 1u, abort))) break;
-        tc_fence_after();
-        if (elect_one()) {
+                   a0 = uniform(tmem + 2 * p.DN + h * 128), x0 = uniform((smem_u32(ring_x) >> 4) | (1u << 16)), half = uniform(p.TN * 8);
+    const uint32_t full = smem_u32(&tail->a_full[h][0]);
+    uint32_t slot = 0, phase = 0;  // of the tokens' ring; of the weights' buffers
+    int k = 0, seg = 0;
+    auto block = [&](auto buffer) {
+      constexpr int B = decltype(buffer)::value;
+      const uint32_t s = uniform(slot);
+      if (k == 0 && seg > 0 && !warp_wait(&tail->d_empty[h], (uint32_t)(seg - 1) & 1u, abort)) return false;
+      if (!warp_wait(full + 8 * B, phase, abort)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t xd = x0 + s * 2 * half;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(d, a + 8 * kk, desc_of(xd + (kk >> 2) * half + 2 * (kk & 3)), idesc, kk > 0 || k > 0);
-          mma_commit(&tail->a_empty[h][i & 1]);
-          mma_commit(&tail->x_empty[t.i]);
-          if (k == nb - 1) mma_commit(&tail->d_full[h]);
-        }
-        __syncwarp();
-        t.next(p.NX);
+        for (int kk = 0; kk < 8; ++kk)
+          mma_bf16_ts(d, a0 + 64 * B + 8 * kk, desc_of(xd + (kk >> 2) * half + 2 * (kk & 3)), idesc, kk > 0 || k > 0);
+        mma_commit(&tail->a_empty[h][B]);
+        mma_commit(&tail->x_empty[s]);
+        if (k == x.nb - 1) mma_commit(&tail->d_full[h]);
       }
-    }
+      __syncwarp();
+      slot = slot + 1 == (uint32_t)p.NX ? 0 : slot + 1;
+      if (++k == x.nb) {
+        k = 0;
+        ++seg;
+      }
+      return true;
+    };
+    bool alive = true;
+#pragma unroll 1
+    for (int n = x.left; n > 0 && alive; n -= 2, phase ^= 1)
+      alive = block(std::integral_constant<int, 0>()) && (n == 1 || block(std::integral_constant<int, 1>()));
     if (elect_one()) {
       // This warp's products and the arrivals they signal, before tensor and shared memory go away.
       mma_commit(&tail->drain[h]);
@@ -329,13 +339,11 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     // A set has the blocks of one parity, and so the same slots of the ring and the same barriers each time: it
     // passes over no phase of them.
     const int h = (warp >> 2) & 1, set = warp >= 4 + kUnpackers / 2, q4 = warp & 3, row = 32 * q4 + lane;
-    const uint32_t to = tmem + ((uint32_t)(32 * q4) << 16) + 2 * p.DN + (h * p.NA + (set & (p.NA - 1))) * 64;
+    const uint32_t to = tmem + ((uint32_t)(32 * q4) << 16) + 2 * p.DN + h * 128 + set * 64;
     const uint32_t sw = 16 * ((row >> 1) & 3);  // 64-byte swizzle
-    // The buffer is free once the products of the block before it there are done: of two blocks ago, or,
-    // with one buffer, of the other set's.
-    const uint32_t free = smem_u32(&tail->a_empty[h][p.NA == 2 ? set : set ^ 1]), filled = smem_u32(&tail->a_full[h][set]);
-    uint32_t free_phase = 1, slot = set;
-    bool first = p.NA == 2 || set == 0;  // nothing was there before
+    const uint32_t free = smem_u32(&tail->a_empty[h][set]), filled = smem_u32(&tail->a_full[h][set]), tokens = smem_u32(&tail->x_full[0]);
+    uint32_t free_phase = 1, slot = set, x_slot = set, x_round = 0;
+    bool first = true;  // the buffer was never used
     uint32_t round = 0;
     const int rows = p.halves * p.RH;
     if (set) x.step(p);
@@ -390,6 +398,14 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
       tmem_st32u(to + 32, r);
       tmem_wait_st();
       tc_fence_before();
+      if (q4 == 0) {  // for the warp that issues the products
+        if (!warp_wait(tokens + 8 * x_slot, x_round, abort)) break;
+        x_slot += 2;
+        if (x_slot >= (uint32_t)p.NX) {
+          x_slot -= p.NX;
+          x_round ^= 1;
+        }
+      }
       warp_arrive(filled, lane);
     }
   } else if (warp >= 4 + kUnpackers && p.share == 1 && (warp & 3) < quads) {
@@ -519,39 +535,37 @@ static Tc plan(int T, int K, int Nout) {
   Tc best{};
   double least = 0;
   const int sms = device_sm_count(), kblocks = (K + kCols - 1) / kCols;
-  for (int most = kMaxTN; most >= 128; most -= 64)
-    for (int share = 1; share <= kMaxShare && share <= kblocks; share *= 2) {
-      Tc p{};
-      p.ntiles = (T + most - 1) / most;
-      p.TN = ((T + p.ntiles - 1) / p.ntiles + 15) / 16 * 16;
-      p.ntiles = (T + p.TN - 1) / p.TN;
-      p.DN = (p.TN + 31) / 32 * 32;
-      p.NA = 2 * p.DN + 2 * 2 * 64 <= (int)kTmemCols ? 2 : 1;
-      p.NX = (int)((kRing - kSlotsW * kSlotW) / (p.TN * 256));
-      if (p.NX > kMaxSlotsX) p.NX = kMaxSlotsX;
-      p.kblocks = kblocks;
-      p.share = share;
-      // Rounds that the tiles need when they are as high as can be, then the tiles that fill these rounds.
-      const int at_once = share == 1 ? sms : sms * 7 / 8 / share;  // clusters do not fill every SM
-      const long long fewest = (long long)((Nout + 2 * kHalf - 1) / (2 * kHalf)) * p.ntiles, rounds = (fewest + at_once - 1) / at_once;
-      if (share > 1 && rounds > 1) break;
-      const long long high = rounds * at_once / p.ntiles;
-      int rows = (int)((Nout + high - 1) / high);
-      p.halves = rows > kHalf ? 2 : 1;
-      p.RH = ((rows + p.halves - 1) / p.halves + 15) / 16 * 16;
-      p.mtiles = (Nout + p.halves * p.RH - 1) / (p.halves * p.RH);
-      const long long tiles = (long long)p.mtiles * p.ntiles;
-      p.grid = (int)(tiles < at_once ? tiles : at_once) * share;
-      // Clocks: a block's products, unpacking and bytes, whichever is most; what a tile's end costs.
-      const double products = 4.0 * p.TN * p.halves + (p.NA == 1 ? 200 : 0), unpacking = 330.0 * p.halves, bytes = p.halves * p.RH * 64 / 20.0;
-      double block = products > unpacking ? products : unpacking;
-      if (bytes > block) block = bytes;
-      const double cost = (double)rounds * ((kblocks + share - 1) / share * (block + 100) + 1500 + (share > 1 ? 2500 + p.TN * p.halves * p.RH / 10.0 : 0));
-      if (least == 0 || cost < least) {
-        least = cost;
-        best = p;
-      }
+  for (int share = 1; share <= kMaxShare && share <= kblocks; share *= 2) {
+    Tc p{};
+    p.ntiles = (T + kMaxTN - 1) / kMaxTN;
+    p.TN = ((T + p.ntiles - 1) / p.ntiles + 15) / 16 * 16;
+    p.ntiles = (T + p.TN - 1) / p.TN;
+    p.DN = (p.TN + 31) / 32 * 32;
+    p.NX = (int)((kRing - kSlotsW * kSlotW) / (p.TN * 256)) & ~1;
+    if (p.NX > kMaxSlotsX) p.NX = kMaxSlotsX;
+    p.kblocks = kblocks;
+    p.share = share;
+    // Rounds that the tiles need when they are as high as can be, then the tiles that fill these rounds.
+    const int at_once = share == 1 ? sms : sms * 7 / 8 / share;  // clusters do not fill every SM
+    const long long fewest = (long long)((Nout + 2 * kHalf - 1) / (2 * kHalf)) * p.ntiles, rounds = (fewest + at_once - 1) / at_once;
+    if (share > 1 && rounds > 1) break;
+    const long long high = rounds * at_once / p.ntiles;
+    int rows = (int)((Nout + high - 1) / high);
+    p.halves = rows > kHalf ? 2 : 1;
+    p.RH = ((rows + p.halves - 1) / p.halves + 15) / 16 * 16;
+    p.mtiles = (Nout + p.halves * p.RH - 1) / (p.halves * p.RH);
+    const long long tiles = (long long)p.mtiles * p.ntiles;
+    p.grid = (int)(tiles < at_once ? tiles : at_once) * share;
+    // Clocks: a block's products, unpacking and bytes, whichever is most; what a tile's end costs.
+    const double products = 4.0 * p.TN * p.halves, unpacking = 330.0 * p.halves, bytes = p.halves * p.RH * 64 / 20.0;
+    double block = products > unpacking ? products : unpacking;
+    if (bytes > block) block = bytes;
+    const double cost = (double)rounds * ((kblocks + share - 1) / share * (block + 100) + 1500 + (share > 1 ? 2500 + p.TN * p.halves * p.RH / 10.0 : 0));
+    if (least == 0 || cost < least) {
+      least = cost;
+      best = p;
     }
+  }
   return best;
 }
 
