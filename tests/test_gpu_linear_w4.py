@@ -55,6 +55,27 @@ def test_parity(mg, T, K, N, G, zeros, out):
     check_linear(got, x, m, out)
 
 
+MORE_SHAPES = [  # many tiles of few blocks, tiles shared by two to eight CTAs, parts of one block
+    (64, 128, 40000, 128, True, "bf16"),
+    (20, 256, 30000, 64, False, "f32"),
+    (64, 384, 20000, 128, True, "bf16"),
+    (33, 32, 1024, 32, True, "f32"),
+    (64, 1152, 22016, 128, True, "bf16"),
+    (48, 1408, 2064, 128, True, "f32"),
+    (17, 2048, 100, 64, True, "bf16"),
+    (64, 4096, 4096, 32, False, "bf16"),
+    (24, 640, 8193, 128, True, "bf16"),
+    (3, 640, 9, 128, True, "f32"),
+    (100, 256, 30000, 64, True, "bf16"),
+    (520, 384, 5000, 128, False, "bf16"),
+]
+
+
+@pytest.mark.parametrize("T,K,N,G,zeros,out", MORE_SHAPES, ids=["-".join(map(str, s)) for s in MORE_SHAPES])
+def test_parity_of_the_work_divided_otherwise(mg, T, K, N, G, zeros, out):
+    test_parity(mg, T, K, N, G, zeros, out)
+
+
 @pytest.mark.parametrize("T", [1, 5, 12, 30, 64, 300])
 def test_every_element_and_place_of_a_word(mg, T):
     """Whole-numbered weights and inputs: the result is exact, whatever was mixed up."""
