@@ -48,7 +48,16 @@ struct Plan {
   int withhold;         // failure test: the first tokens are never loaded
 };
 
+// A part of a tile: [0] is the part that a CTA's range begins with, [1] the one that it ends with.
+struct Part {
+  int there, tile, order;       // whether there is one; within the cluster; where the CTA's walk has it
+  int n, sender, per;           // CTAs that share the tile, which of them this is, tokens of each
+  int region;                   // where their sums arrive
+  uint2 to[kMaxTN / 4];         // of four tokens: the CTA of the cluster that adds them up, where in its shared memory
+};
+
 struct Tail {
+  Part part[2];
   uint64_t w_full[kSlots], w_empty[kSlots], x_full[kSlots], x_empty[kSlots];
   uint64_t a_full[kSets], a_empty[kSets], drain[2];
   // Of even and odd parts, by stream.  One barrier for both could be two phases ahead of who waits for it, which looks
@@ -175,6 +184,24 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
   Walk x{tile0 + (begin + first) / p.kpairs, 0, end - begin, tile0 + begin / p.kpairs, lead, first};
   x.to_first();
   const int parts = (first > 0) + (end - begin - first + p.kpairs - 1) / p.kpairs, tail_pairs = (end - begin - first) % p.kpairs;
+  if (warp == 2 && p.share > 1) {
+    // The divisions of the end, here where the kernel in front may still be running.
+    const int k = lane >> 4, tile = (k ? end - 1 : begin) / p.kpairs, f = (int)range.owner(tile * p.kpairs);
+    const int n = (int)range.owner((tile + 1) * p.kpairs - 1) - f + 1, per = (p.TN / 4 + n - 1) / n * 4;
+    const auto region = [&](int r) { return (int)range.begin(r) / p.kpairs == tile ? 0u : kRegion; };
+    Part& part = tail->part[k];
+    if ((lane & 15) == 0) {
+      part.there = k ? tail_pairs > 0 : first > 0;
+      part.tile = tile;
+      part.order = parts - 1 - (k && first ? 1 : 0);
+      part.n = n;
+      part.sender = rank - f;
+      part.per = per;
+      part.region = (int)region(rank);
+    }
+    const int t = 4 * (lane & 15), j = min(t / per, n - 1);  // tokens from p.TN on belong to nobody
+    part.to[lane & 15] = make_uint2(f + j, region(f + j) + 4 * ((rank - f) * per + t - j * per) * p.RH);
+  }
   if (warp == 0 && lane == 0) {
     tma_prefetch(&tm_w);
     tma_prefetch(&tm_x);
@@ -373,52 +400,29 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
       mbar_wait_bounded(&tail->x_full[i % kSlots], (uint32_t)(i / kSlots) & 1u, nullptr, kDrainNs);
   }
   if (p.share > 1) {
-    // Parts of tiles: those that this CTA's range begins and ends with.  A tile's CTAs f .. l take some tokens each, whose
-    // sums go into the rings' place, [sender][four tokens][feature][4] (a store of 16 bytes a lane takes no longer than one
-    // of 4), of the part that the receiver's range begins or ends with.
-    struct Part {
-      int tile, f, n, per, region;  // within the cluster; its first CTA, how many, their tokens; where this CTA's sums arrive
-      bool there;
-    } of[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      of[k].there = k ? tail_pairs > 0 : first > 0;
-      of[k].tile = (k ? end - 1 : begin) / p.kpairs;
-      of[k].f = (int)range.owner(of[k].tile * p.kpairs);
-      of[k].n = (int)range.owner((of[k].tile + 1) * p.kpairs - 1) - of[k].f + 1;
-      of[k].per = (p.TN / 4 + of[k].n - 1) / of[k].n * 4;
-      of[k].region = begin / p.kpairs == of[k].tile ? 0 : 1;
-    }
+    // Parts of tiles.  The sums go into the rings' place, [sender][four tokens][feature][4]: a store of 16 bytes a lane
+    // takes no longer than one of 4.
     const int m = 32 * (warp & 3) + lane, group = (warp - 4) >> 2;  // a feature, and which of the tokens
     const bool works = warp >= 4 && warp < 4 + 4 * kSets && m < p.RH;
     cluster_sync();  // all products of the cluster are done, and nobody reads from the rings
     if (warp >= 4 && warp < 4 + 4 * kSets && (warp & 3) < quads) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        if (!of[k].there) continue;
-        // In the order of the walk the part of the range's beginning is last, that of its end the one before.
-        const int order = parts - 1 - (k && first ? 1 : 0);
-        const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 2 * (order & 1) * p.DN;
+        const Part& part = tail->part[k];
+        if (!part.there) continue;
+        const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 2 * (part.order & 1) * p.DN;
 #pragma unroll 1
         for (int c = 16 * group; c < p.TN; c += 16 * kSets) {
           float v[16];
           read_sums(from + c, p.DN, v);
           if (!works) continue;
-          int to = c / of[k].per, col = c - to * of[k].per;
-          uint32_t there = 0;
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
-            if (e == 0 || col == of[k].per) {
-              if (e) ++to, col = 0;
-              const int region = (int)range.begin(of[k].f + to) / p.kpairs == of[k].tile ? 0 : 1;
-              asm("mapa.shared::cluster.u32 %0, %1, %2;"
-                  : "=r"(there)
-                  : "r"(smem_u32(smem) + region * kRegion + 4 * (((rank - of[k].f) * of[k].per + col) * p.RH + 4 * m)), "r"(of[k].f + to));
-            }
+            const uint2 to = part.to[(c + e) / 4];
+            uint32_t there;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(smem_u32(smem) + to.y + 16 * m), "r"(to.x));
             asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(there), "f"(v[e]), "f"(v[e + 1]), "f"(v[e + 2]), "f"(v[e + 3])
                          : "memory");
-            there += 16 * p.RH;
-            col += 4;
           }
         }
       }
@@ -427,14 +431,15 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
     if (works)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        if (!of[k].there) continue;
-        const int t0 = (rank - of[k].f) * of[k].per, tokens = min(of[k].per, p.a.T - t0), n = (tile0 + of[k].tile) * p.RH + m;
-        const float4* sums = reinterpret_cast<const float4*>(smem + of[k].region * kRegion) + m;
+        const Part& part = tail->part[k];
+        if (!part.there) continue;
+        const int t0 = part.sender * part.per, tokens = min(part.per, p.a.T - t0), n = (tile0 + part.tile) * p.RH + m;
+        const float4* sums = reinterpret_cast<const float4*>(smem + part.region) + m;
         for (int t = 4 * group; t < tokens; t += 4 * kSets) {
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-          for (int r = 0; r < of[k].n; ++r) {
-            const float4 w = sums[(r * of[k].per + t) / 4 * p.RH];
+          for (int r = 0; r < part.n; ++r) {
+            const float4 w = sums[(r * part.per + t) / 4 * p.RH];
             v.x += w.x;
             v.y += w.y;
             v.z += w.z;
