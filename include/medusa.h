@@ -579,13 +579,10 @@ medusa_status medusa_w4_quantize(const void* w, int Nout, int K, int group, int 
  * T >= 0 (nothing is launched for 0).  x and qweight 16-byte aligned.  y must
  * overlap no other buffer (ALIAS).  A row of x with NaN or infinities changes that
  * row of y alone.  Sums are made in a fixed order (deterministic on a given device).
- * Workspace: medusa_linear_w4_workspace_size() bytes for the current device (0: none
- * needed), 16-byte aligned, its contents before the call do not matter; calls that
- * may run at the same time need one each. */
-size_t medusa_linear_w4_workspace_size(int T, int K, int Nout, int group);
+ * No workspace. */
 medusa_status medusa_linear_w4(const void* x, int64_t ldx, const uint32_t* qweight, const void* scales,
                                const uint8_t* zeros, int T, int K, int Nout, int group, void* y, medusa_dtype y_dt,
-                               void* ws, size_t ws_bytes, int32_t* d_status, medusa_stream_t stream);
+                               int32_t* d_status, medusa_stream_t stream);
 
 /* ------------------------------------------- (l) what requests ask of logits
  * Between the output head and medusa_typical_accept: penalties for tokens that

@@ -41,8 +41,7 @@ medusa_status medusa_paged_attention_test_stall(const void* q, int64_t ldq, cons
  * after one to two seconds and it ends as medusa_linear_test_stall does. */
 medusa_status medusa_linear_w4_test_stall(const void* x, int64_t ldx, const uint32_t* qweight, const void* scales,
                                           const uint8_t* zeros, int T, int K, int Nout, int group, void* y,
-                                          medusa_dtype y_dt, void* ws, size_t ws_bytes, int32_t* d_status,
-                                          medusa_stream_t stream);
+                                          medusa_dtype y_dt, int32_t* d_status, medusa_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -34,7 +34,7 @@ EXPORTS = (
     "medusa_head_loss_workspace_size", "medusa_head_loss", "medusa_rope_plan_init", "medusa_rope",
     "medusa_paged_append", "medusa_paged_attention_workspace_size", "medusa_paged_attention",
     "medusa_paged_tree_attention", "medusa_paged_compact", "medusa_paged_attention_test_stall",
-    "medusa_w4_quantize", "medusa_linear_w4_workspace_size", "medusa_linear_w4", "medusa_logits_process",
+    "medusa_w4_quantize", "medusa_linear_w4", "medusa_logits_process",
     "medusa_count_tokens", "medusa_count_accepted", "medusa_linear_w4_test_stall",
 )
 
@@ -111,9 +111,8 @@ def lib():
             "medusa_paged_tree_attention": (I, [P] * 8 + [I] * 9 + [F, I, P, P, P, Z, P, P]),
             "medusa_paged_compact": (I, [P] * 9 + [I] * 10 + [P, P]),
             "medusa_w4_quantize": (I, [P, I, I, I, I, I, P, P, P, P]),
-            "medusa_linear_w4_workspace_size": (Z, [I] * 4),
-            "medusa_linear_w4": (I, [P, LL, P, P, P, I, I, I, I, P, I, P, Z, P, P]),
-            "medusa_linear_w4_test_stall": (I, [P, LL, P, P, P, I, I, I, I, P, I, P, Z, P, P]),
+            "medusa_linear_w4": (I, [P, LL, P, P, P, I, I, I, I, P, I, P, P]),
+            "medusa_linear_w4_test_stall": (I, [P, LL, P, P, P, I, I, I, I, P, I, P, P]),
             "medusa_logits_process": (I, [P, LL, I, P, P, P, I, I, I, P, P, P]),
             "medusa_count_tokens": (I, [P, I, I, I, P, P, P, P]),
             "medusa_count_accepted": (I, [P, P, P, I, I, I, I, P, P, P]),

@@ -215,34 +215,34 @@ extern "C" medusa_status medusa_w4_quantize(const void* w, int Nout, int K, int 
   return launch_status();
 }
 
-// Up to 16 tokens the warps' own product instructions, fed from registers; more on tensor memory (and fewer features
-// than a CTA's), up to 64 in the kernel that divides its work more evenly (64 tokens x 28672 features 20.6 us, in the other
-// 22.9; 17 x 4096 8.0 and 8.4).
-static bool on_tc(int T, int Nout) { return T > 16 || Nout < 32; }
-// From here on there are CTAs enough of 32 rows, which share the tokens' loads among more weights (one token, 32000
-// features 20.0 us, with 16 rows 20.3; 7 tokens, 13825 features 13.0 and 15.6); below, 16 rows and twice the warps are
-// sooner done (4096 features 4.1 us, with 32 rows 4.9).
-constexpr int kWide = 8192;
-
-extern "C" size_t medusa_linear_w4_workspace_size(int T, int K, int Nout, int group) {
-  return 0;
+// More than 64 tokens are the work of linear_w4_tc.cu, up to 64 of linear_w4_stream.cu, and of few tokens the warps' own
+// product instructions, fed from registers, where their CTAs are all there at once or the layer is small: the others
+// need some 2 us more to begin and to add up, and unpack faster.  Times for K = 4096, registers and tensor memory:
+//   one token    x  4096 features   5.0 and  7.1 us     9 tokens x 1024   4.5 and 5.4 us
+//                x 13825           10.1     12.2                 x 4096   6.5     7.1
+//                x 16384           14.2     12.1        16       x 4096   7.6     7.2
+//   8 tokens     x 28672           19.7     17.0        16       x 8192  10.9     9.1
+// Two CTAs of 16 rows and 16 warps are on an SM at once, three of 32 rows and 8 warps.  Those of 32 rows share the
+// tokens' loads among more weights, and are better from the second filling with the others on (K = 4096, 11008 features:
+// 9.8 us, with 16 rows 10.8; 8192 features: 9.6 and 8.4).
+static bool wide(int Nout) { return Nout > 64 * device_sm_count(); }
+static bool from_registers(int T, int K, int Nout) {
+  const long long n = (long long)K * Nout;
+  if (T > 16 || Nout < 32) return false;
+  if (T > 8) return n < 1 << 24 && !wide(Nout);
+  return n < 1 << 25 || Nout <= 32 * device_sm_count() || (wide(Nout) && Nout <= 96 * device_sm_count());
 }
 
 static medusa_status linear_call(const void* x, int64_t ldx, const uint32_t* qweight, const void* scales, const uint8_t* zeros, int T, int K,
-                                 int Nout, int group, void* y, medusa_dtype y_dt, void* ws, size_t ws_bytes, int32_t* d_status,
-                                 medusa_stream_t stream, int withhold) {
+                                 int Nout, int group, void* y, medusa_dtype y_dt, int32_t* d_status, medusa_stream_t stream, int withhold) {
   if (T < 0 || !sizes_ok(K, Nout, group) || !dtype_ok(y_dt)) return MEDUSA_ERR_INVALID_ARG;
   if (T == 0) return MEDUSA_OK;
   if (!x || !qweight || !scales || !y || ldx < K || ldx % 8 || ldx >= (1ll << 38) || T >= 0x7fffffff - 65536) return MEDUSA_ERR_INVALID_ARG;
   const size_t es = dtype_bytes(y_dt);
   if (!aligned16(x) || !aligned16(qweight) || ((uintptr_t)scales & 1) || ((uintptr_t)y & (es - 1)) || ((uintptr_t)d_status & 3))
     return MEDUSA_ERR_INVALID_ARG;
-  const size_t need = medusa_linear_w4_workspace_size(T, K, Nout, group);
-  if (need && (!ws || ws_bytes < need || !aligned16(ws))) return MEDUSA_ERR_WORKSPACE;
   const size_t ny = (size_t)T * Nout * es, ns = (size_t)Nout * (K / group), nx = ((size_t)(T - 1) * ldx + K) * 2;
-  const Region nothing{nullptr, 0}, part = need ? Region{ws, need} : nothing;
-  if (overlaps_any({y, ny}, {{x, nx}, {qweight, (size_t)Nout * K / 2}, {scales, 2 * ns}, {zeros, ns}, {d_status, 4}, part}) ||
-      overlaps_any(part, {{x, nx}, {qweight, (size_t)Nout * K / 2}, {scales, 2 * ns}, {zeros, ns}, {d_status, 4}}))
+  if (overlaps_any({y, ny}, {{x, nx}, {qweight, (size_t)Nout * K / 2}, {scales, 2 * ns}, {zeros, ns}, {d_status, 4}}))
     return MEDUSA_ERR_ALIAS;
   Args a{};
   a.x = static_cast<const uint16_t*>(x);
@@ -258,21 +258,22 @@ static medusa_status linear_call(const void* x, int64_t ldx, const uint32_t* qwe
   a.y32 = y_dt == MEDUSA_F32;
   a.d_status = d_status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (on_tc(T, Nout)) return T <= 64 ? stream_launch(a, withhold, s) : tc_launch(a, withhold, s);
+  if (T > 64) return tc_launch(a, withhold, s);
+  if (!from_registers(T, K, Nout)) return stream_launch(a, withhold, s);
   if (withhold) return MEDUSA_ERR_INVALID_ARG;
-  if (Nout >= kWide) T <= 8 ? few<1, 2, 8>(a, s) : few<2, 2, 8>(a, s);
-  else T <= 8 ? few<1, 1, 16>(a, s) : few<2, 1, 16>(a, s);
+  if (T > 8) few<2, 1, 16>(a, s);
+  else if (wide(Nout)) few<1, 2, 8>(a, s);
+  else few<1, 1, 16>(a, s);
   return launch_status();
 }
 
 extern "C" medusa_status medusa_linear_w4(const void* x, int64_t ldx, const uint32_t* qweight, const void* scales, const uint8_t* zeros, int T,
-                                          int K, int Nout, int group, void* y, medusa_dtype y_dt, void* ws, size_t ws_bytes, int32_t* d_status,
-                                          medusa_stream_t stream) {
-  return linear_call(x, ldx, qweight, scales, zeros, T, K, Nout, group, y, y_dt, ws, ws_bytes, d_status, stream, 0);
+                                          int K, int Nout, int group, void* y, medusa_dtype y_dt, int32_t* d_status, medusa_stream_t stream) {
+  return linear_call(x, ldx, qweight, scales, zeros, T, K, Nout, group, y, y_dt, d_status, stream, 0);
 }
 
 extern "C" medusa_status medusa_linear_w4_test_stall(const void* x, int64_t ldx, const uint32_t* qweight, const void* scales,
                                                      const uint8_t* zeros, int T, int K, int Nout, int group, void* y, medusa_dtype y_dt,
-                                                     void* ws, size_t ws_bytes, int32_t* d_status, medusa_stream_t stream) {
-  return linear_call(x, ldx, qweight, scales, zeros, T, K, Nout, group, y, y_dt, ws, ws_bytes, d_status, stream, 1);
+                                                     int32_t* d_status, medusa_stream_t stream) {
+  return linear_call(x, ldx, qweight, scales, zeros, T, K, Nout, group, y, y_dt, d_status, stream, 1);
 }

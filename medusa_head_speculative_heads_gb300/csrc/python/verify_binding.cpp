@@ -44,9 +44,9 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// x, qweight, scales, zeros, y, fp32 (a truth value; anything else: a type that y cannot have), ws, d_status
+// x, qweight, scales, zeros, y, fp32 (a truth value; anything else: a type that y cannot have), d_status
 PyObject* linear_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 8, [&]() -> PyObject* {
+  return guarded(n, 7, [&]() -> PyObject* {
     Call c{"medusa_linear_w4"};
     const Tensor &x = c.tensor(a[0], "x"), &q = c.tensor(a[1], "qweight"), &s = c.tensor(a[2], "scales");
     if (!PyBool_Check(a[5])) c.refuse("y is bfloat16 or float32", PyExc_TypeError);
@@ -62,7 +62,7 @@ PyObject* linear_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     c.dense(s, "scales", ScalarType::BFloat16, {ng, N});
     const uint8_t* zeros = nullptr;
     if (a[3] != Py_None) zeros = static_cast<uint8_t*>(c.dense(c.tensor(a[3], "zeros"), "zeros", ScalarType::Byte, {ng, N}).data_ptr());
-    int32_t* status = status_word(c, a[7]);
+    int32_t* status = status_word(c, a[6]);
     c10::DeviceGuard on(c.dev);
     ScalarType out = a[5] == Py_True ? ScalarType::Float : ScalarType::BFloat16;
     if (a[4] != Py_None) {
@@ -71,10 +71,9 @@ PyObject* linear_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const Out y(c, a[4], "y", {T, N}, out);
     const int t = small(c, T, "T"), k = small(c, K, "K"), nn = small(c, N, "Nout"), g = (int)(K / ng);
-    const Workspace ws(c, a[6], medusa_linear_w4_workspace_size(t, k, nn, g));
     const medusa_status st = enqueue([&] {
       return medusa_linear_w4(x.data_ptr(), ldx, static_cast<uint32_t*>(q.data_ptr()), s.data_ptr(), zeros, t, k, nn, g, y.ptr(),
-                              out == ScalarType::Float ? MEDUSA_F32 : MEDUSA_BF16, ws.n ? ws.t.data_ptr() : nullptr, ws.n, status, c.stream());
+                              out == ScalarType::Float ? MEDUSA_F32 : MEDUSA_BF16, status, c.stream());
     });
     return st != MEDUSA_OK ? PyLong_FromLong(st) : y.object();
   });

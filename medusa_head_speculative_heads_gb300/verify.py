@@ -2,7 +2,7 @@
 weights, the logits as requests want them, and the counts that go with them.
 csrc/python/verify_binding.cpp checks and marshals their arguments.
 
-Everywhere: what is not given (outputs, workspace) is allocated, on the stream that
+Everywhere: outputs that are not given are allocated, on the stream that
 the call runs on: the current one of the tensors' device, or `stream`.  No gradients
 are recorded.
 """
@@ -46,15 +46,13 @@ def medusa_w4_quantize(w, group: int = 128, symmetric: bool = False, stream=None
     return r
 
 
-def medusa_linear_w4(x, qweight, scales, zeros=None, y=None, out_dtype=None, ws=None, d_status=None, stream=None):
+def medusa_linear_w4(x, qweight, scales, zeros=None, y=None, out_dtype=None, d_status=None, stream=None):
     """y [T, Nout] = x [T, K] @ W^T with W in 4 bits (qweight, scales, zeros as
     medusa_w4_quantize makes them; zeros None: 8).  x is bf16, its rows may be spaced; y is
-    bf16, or fp32 with out_dtype=torch.float32 or a y of that type.  ws:
-    medusa_linear_w4_workspace_size() bytes."""
+    bf16, or fp32 with out_dtype=torch.float32 or a y of that type."""
     if stream is not None:
-        return _on(stream, x, medusa_linear_w4, x, qweight, scales, zeros, y, out_dtype, ws, d_status)
-    r = (_native or _load()).linear_w4(x, qweight, scales, zeros, y, out_dtype is torch.float32 if out_dtype in _OUT else out_dtype,
-                                       ws, d_status)
+        return _on(stream, x, medusa_linear_w4, x, qweight, scales, zeros, y, out_dtype, d_status)
+    r = (_native or _load()).linear_w4(x, qweight, scales, zeros, y, out_dtype is torch.float32 if out_dtype in _OUT else out_dtype, d_status)
     if type(r) is int:
         raise B_.MedusaError("medusa_linear_w4", r)
     return r

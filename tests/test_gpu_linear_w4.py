@@ -55,6 +55,25 @@ def test_parity(mg, T, K, N, G, zeros, out):
     check_linear(got, x, m, out)
 
 
+FEW_TOKENS = [  # layers that are large for their few tokens, and those just below
+    (1, 2304, 16384, 128, True, "bf16"),
+    (1, 2016, 16385, 32, False, "f32"),
+    (3, 8224, 5000, 32, True, "bf16"),
+    (8, 8192, 4865, 64, True, "f32"),
+    (8, 4096, 9729, 128, False, "bf16"),
+    (9, 4128, 4100, 32, True, "f32"),
+    (12, 1600, 10500, 64, True, "bf16"),
+    (16, 4096, 4097, 128, False, "f32"),
+    (16, 1024, 9728, 64, True, "bf16"),
+    (16, 128, 32768, 128, True, "bf16"),
+]
+
+
+@pytest.mark.parametrize("T,K,N,G,zeros,out", FEW_TOKENS, ids=["-".join(map(str, s)) for s in FEW_TOKENS])
+def test_parity_of_few_tokens(mg, T, K, N, G, zeros, out):
+    test_parity(mg, T, K, N, G, zeros, out)
+
+
 MORE_SHAPES = [  # many tiles of few blocks, tiles shared by two to eight CTAs, parts of one block
     (64, 128, 40000, 128, True, "bf16"),
     (20, 256, 30000, 64, False, "f32"),
@@ -133,20 +152,18 @@ def test_what_is_not_a_number_stays_in_its_row_or_column(mg, T):
 def test_calls_repeat_bit_for_bit_eager_captured_and_at_once(mg, T, K, N):
     rng = np.random.default_rng(N)
     x, m = to_dev(bf16(rng, T, K)), dev_matrix(matrix(rng, N, K, 128))
-    need = mg.lib().medusa_linear_w4_workspace_size(T, K, N, 128)
-    ws = [torch.full((max(1, need),), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]  # NaN, whatever it is read as
-    first = mg.medusa_linear_w4(x, *m, ws=ws[0])
+    first = mg.medusa_linear_w4(x, *m)
     assert torch.isfinite(first.float()).all()
     side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.graph(graph):
-        captured = mg.medusa_linear_w4(x, *m, ws=ws[0])
+        captured = mg.medusa_linear_w4(x, *m)
     outs = [torch.empty_like(first) for _ in range(2)]
     for _ in range(10):
         captured.zero_()
         graph.replay()
-        mg.medusa_linear_w4(x, *m, y=outs[1], ws=ws[1], stream=side)
-        mg.medusa_linear_w4(x, *m, y=outs[0], ws=ws[0])
+        mg.medusa_linear_w4(x, *m, y=outs[1], stream=side)
+        mg.medusa_linear_w4(x, *m, y=outs[0])
         torch.cuda.synchronize()
         assert torch.equal(captured, first) and torch.equal(outs[0], first) and torch.equal(outs[1], first)
 

@@ -24,9 +24,9 @@ def at(n):
 
 
 def linear(**o):
-    a = dict(x=at(0), ldx=512, q=at(1), s=at(2), z=at(3), T=9, K=512, N=100, G=64, y=at(4), dt=1, ws=at(5), n=1 << 31, st=None)
+    a = dict(x=at(0), ldx=512, q=at(1), s=at(2), z=at(3), T=9, K=512, N=100, G=64, y=at(4), dt=1, st=None)
     a.update(o)
-    return mg.lib().medusa_linear_w4(a["x"], a["ldx"], a["q"], a["s"], a["z"], a["T"], a["K"], a["N"], a["G"], a["y"], a["dt"], a["ws"], a["n"], a["st"], None)
+    return mg.lib().medusa_linear_w4(a["x"], a["ldx"], a["q"], a["s"], a["z"], a["T"], a["K"], a["N"], a["G"], a["y"], a["dt"], a["st"], None)
 
 
 @pytest.mark.parametrize("o", [dict(x=None), dict(q=None), dict(s=None), dict(y=None), dict(T=-1), dict(K=0), dict(K=500), dict(N=0), dict(G=16), dict(G=256), dict(G=96, K=96 * 4),
@@ -42,21 +42,8 @@ def test_linear_refuses_overlaps(o):
 
 
 def test_a_product_with_no_rows_launches_nothing():
-    assert linear(T=0, x=None, y=None, ws=None) == 0
+    assert linear(T=0, x=None, y=None) == 0
     assert linear(T=0, K=33) == INVALID
-    assert mg.lib().medusa_linear_w4_workspace_size(0, 512, 100, 64) == 0
-
-
-def test_workspaces_that_are_short_or_overlap():
-    T, K, N, G = 64, 4096, 4096, 128
-    need = mg.lib().medusa_linear_w4_workspace_size(T, K, N, G)
-    if need:
-        o = dict(T=T, K=K, ldx=K, N=N, G=G)
-        assert linear(**o, ws=None) == WORKSPACE and linear(**o, n=need - 1) == WORKSPACE and linear(**o, ws=at(5) + 8) == WORKSPACE
-        for other in range(5):
-            assert linear(**o, ws=at(other)) == ALIAS
-    for bad in ((-1, 512, 100, 64), (1, 500, 100, 64), (1, 512, 0, 64), (1, 512, 100, 65)):
-        assert mg.lib().medusa_linear_w4_workspace_size(*bad) == 0
 
 
 def quantize(**o):
