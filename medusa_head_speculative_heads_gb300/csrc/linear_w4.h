@@ -67,6 +67,8 @@ __device__ __forceinline__ void store_y(const Args& a, int t, int n, float v) {
   else static_cast<uint16_t*>(a.y)[i] = bf16_rn(v);
 }
 
+// Clusters of `share` CTAs of a tensor-memory kernel, one CTA an SM, that the current device holds at once.
+int clusters_at_once(int share);
 // Tensor-memory kernels: up to 64 tokens (linear_w4_stream.cu), any number (linear_w4_tc.cu).
 medusa_status stream_launch(const Args& a, int withhold, cudaStream_t s);
 medusa_status tc_launch(const Args& a, int withhold, cudaStream_t s);

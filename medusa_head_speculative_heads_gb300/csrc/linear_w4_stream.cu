@@ -459,36 +459,6 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
   }
 }
 
-// Clusters of `share` CTAs that the current device holds at once.
-static int clusters_at_once(int share) {
-  static std::atomic<int> known[16][4];
-  if (share == 1) return device_sm_count();
-  int dev = 0;
-  const int k = share == 2 ? 1 : share == 4 ? 2 : 3;
-  const int otherwise = device_sm_count() * 3 / 4 / share;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return otherwise;
-  int n = known[dev][k].load(std::memory_order_relaxed);
-  if (n) return n;
-  auto kern = stream_kernel<1, true>;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(share);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = share;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
-    cudaGetLastError();
-    n = otherwise;
-  }
-  known[dev][k].store(n, std::memory_order_relaxed);
-  return n;
-}
-
 static Plan plan(int T, int K, int Nout) {
   Plan best{};
   long long least = 0;
@@ -524,6 +494,35 @@ static bool make_slabs(CUtensorMap* m, const Args& a, int TN) {
 }
 
 }  // namespace
+
+int clusters_at_once(int share) {
+  static std::atomic<int> known[16][4];
+  if (share == 1) return device_sm_count();
+  int dev = 0;
+  const int k = share == 2 ? 1 : share == 4 ? 2 : 3;
+  const int otherwise = device_sm_count() * 3 / 4 / share;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return otherwise;
+  int n = known[dev][k].load(std::memory_order_relaxed);
+  if (n) return n;
+  auto kern = stream_kernel<1, true>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(share);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = share;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = otherwise;
+  }
+  known[dev][k].store(n, std::memory_order_relaxed);
+  return n;
+}
 
 medusa_status stream_launch(const Args& a, int withhold, cudaStream_t s) {
   if (!encode_fn()) return MEDUSA_ERR_CUDA;

@@ -46,6 +46,10 @@ struct Tc {
   int withhold;        // failure test: the first tokens are never loaded
 };
 
+// Tokens that each CTA of a cluster adds up.
+__host__ __device__ constexpr int per_cta(int TN, int share) { return (TN / 4 + share - 1) / share * 4; }
+static_assert((kMaxTN + 4 * kMaxShare) * 2 * kHalf * 4 <= kRing, "sums in the rings' place");
+
 struct Tail {
   uint64_t w_full[kSlotsW], w_empty[kSlotsW], x_full[kMaxSlotsX], x_empty[kMaxSlotsX];
   uint64_t a_full[2][2], a_empty[2][2], d_full[2], d_empty[2], drain[2];
@@ -181,8 +185,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
       if (w.used() && !warp_wait(&tail->w_empty[w.i], w.empty(), abort)) break;
       if (elect_one()) {
         mbar_expect_tx(&tail->w_full[w.i], (uint32_t)p.slot_bytes);
-        for (int h = 0; h < p.halves; ++h)
-          tma_load_2d(smem + w.i * kSlotW + h * kHalfW, &tm_w, &tail->w_full[w.i], x.kb * (kCols / 2), (x.mt * p.halves + h) * p.RH);
+        tma_load_2d(smem + w.i * kSlotW, &tm_w, &tail->w_full[w.i], x.kb * (kCols / 2), x.mt * p.halves * p.RH);
         if (TILED) {
           tma_load_2d(smem + w.i * kSlotW + kOffScales, &tm_s, &tail->w_full[w.i], x.mt * p.halves * p.RH, x.kb * GROUPS);
           if (p.a.zeros) tma_load_2d(smem + w.i * kSlotW + kOffZeros, &tm_z, &tail->w_full[w.i], x.mt * p.halves * p.RH, x.kb * GROUPS);
@@ -284,7 +287,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
           g[k] = group_of(reinterpret_cast<const uint16_t*>(at)[i], p.a.zeros ? at[kOffZeros - kOffScales + i] : 8);
         }
       }
-      const uint32_t w = smem_u32(smem) + slot * kSlotW + h * kHalfW + row * 64;
+      const uint32_t w = smem_u32(smem) + slot * kSlotW + (h * p.RH + row) * 64;
       uint4 v[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -377,43 +380,53 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
   }
   if (p.share > 1) {
     // The tile's sums, of which each CTA of the cluster has a part: CTA r's tokens' sums go to CTA r, into the rings'
-    // place, [sender][token][feature].
-    const int rank = blockIdx.x % p.share, per = (p.TN + p.share - 1) / p.share, rows = p.halves * p.RH;
+    // place, [sender][four tokens][feature][4].
+    const int rank = blockIdx.x % p.share, per = per_cta(p.TN, p.share), rows = p.halves * p.RH;
+    const int h = (warp >> 2) & 1, part = warp >= 4 + kUnpackers / 2, m = 32 * (warp & 3) + lane;
+    const bool works = warp >= 4 && warp < 4 + kUnpackers && h < p.halves && (warp & 3) < quads;
+    const uint32_t mine = 16 * (h * p.RH + m);
     cluster_sync();  // all products of the cluster are done, and nobody reads from the rings
-    if (warp >= 4 && warp < 4 + kUnpackers) {
-      const int h = (warp >> 2) & 1, part = warp >= 4 + kUnpackers / 2, m = 32 * (warp & 3) + lane;
-      if (h < p.halves && (warp & 3) < quads) {
-        const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + h * p.DN, at = smem_u32(smem) + 4 * (h * p.RH + m);
+    if (works) {
+      const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + h * p.DN, at = smem_u32(smem) + mine;
 #pragma unroll 1
-        for (int c = 16 * part; c < p.TN; c += 32) {
-          float v[16];
-          __syncwarp();
-          tmem_ld16(from + c, v);
-          tmem_wait_ld();
-          if (m >= p.RH) continue;
-          int to = c / per, col = c - to * per;
+      for (int c = 16 * part; c < p.TN; c += 32) {
+        float v[16];
+        __syncwarp();
+        tmem_ld16(from + c, v);
+        tmem_wait_ld();
+        if (m >= p.RH) continue;
+        int to = c / per, col = c - to * per;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            uint32_t there;
-            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at + 4 * ((rank * per + col) * rows)), "r"(to));
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(v[e]) : "memory");
-            if (++col == per) {
-              col = 0;
-              ++to;
-            }
+        for (int e = 0; e < 16; e += 4) {
+          uint32_t there;
+          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at + 4 * ((rank * per + col) * rows)), "r"(to));
+          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(there), "f"(v[e]), "f"(v[e + 1]), "f"(v[e + 2]), "f"(v[e + 3])
+                       : "memory");
+          col += 4;
+          if (col == per) {
+            col = 0;
+            ++to;
           }
         }
       }
     }
     cluster_sync();
-    const float* sums = reinterpret_cast<const float*>(smem);
-    const int tokens = min(per, min(p.TN - rank * per, p.a.T - x0t - rank * per));
-    for (int i = threadIdx.x; i < tokens * rows; i += kThreads) {
-      const int t = i / rows, m = i - t * rows, n = mt0 * rows + m;
-      float v = 0.f;
-      for (int r = 0; r < p.share; ++r) v += sums[(r * per + t) * rows + m];
-      if (n < p.a.Nout) store_y(p.a, x0t + rank * per + t, n, v);
-    }
+    const int tokens = min(per, min(p.TN - rank * per, p.a.T - x0t - rank * per)), n = mt0 * rows + h * p.RH + m;
+    if (works && m < p.RH && n < p.a.Nout)
+      for (int t = 4 * part; t < tokens; t += 8) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; r < p.share; ++r) {
+          const float4 w = *reinterpret_cast<const float4*>(smem + 4 * ((r * per + t) * rows) + mine);
+          v.x += w.x;
+          v.y += w.y;
+          v.z += w.z;
+          v.w += w.w;
+        }
+        const float y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (t + e < tokens) store_y(p.a, x0t + rank * per + t + e, n, y[e]);
+      }
   }
   if (warp == 1) {
     __syncwarp();
@@ -426,7 +439,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 static Tc plan(int T, int K, int Nout) {
   Tc best{};
   double least = 0;
-  const int sms = device_sm_count(), kblocks = (K + kCols - 1) / kCols;
+  const int kblocks = (K + kCols - 1) / kCols;
   for (int share = 1; share <= kMaxShare && share <= kblocks; share *= 2) {
     Tc p{};
     p.ntiles = (T + kMaxTN - 1) / kMaxTN;
@@ -438,7 +451,7 @@ static Tc plan(int T, int K, int Nout) {
     p.kblocks = kblocks;
     p.share = share;
     // Rounds that the tiles need when they are as high as can be, then the tiles that fill these rounds.
-    const int at_once = share == 1 ? sms : sms * 7 / 8 / share;  // clusters do not fill every SM
+    const int at_once = clusters_at_once(share);
     const long long fewest = (long long)((Nout + 2 * kHalf - 1) / (2 * kHalf)) * p.ntiles, rounds = (fewest + at_once - 1) / at_once;
     if (share > 1 && rounds > 1) break;
     const long long high = rounds * at_once / p.ntiles;
@@ -472,7 +485,7 @@ medusa_status tc_launch(const Args& a, int withhold, cudaStream_t s) {
   const bool tiled = a.Nout % 16 == 0 && aligned16(a.scales) && aligned16(a.zeros);
   p.slot_bytes = rows * (kCols / 2 + (tiled ? per * (a.zeros ? 3 : 2) : 0));
   CUtensorMap mw, mx, ms, mz;
-  if (!make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q, a.K / 2, a.Nout, a.K / 2, kCols / 2, p.RH, CU_TENSOR_MAP_SWIZZLE_64B) ||
+  if (!make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q, a.K / 2, a.Nout, a.K / 2, kCols / 2, rows, CU_TENSOR_MAP_SWIZZLE_64B) ||
       !make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.K, a.T, a.ldx * 2, 64, p.TN, CU_TENSOR_MAP_SWIZZLE_128B))
     return MEDUSA_ERR_CUDA;
   ms = mz = mw;
