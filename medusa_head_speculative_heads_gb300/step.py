@@ -43,7 +43,6 @@ class VerifyStep:
         self.next_tok = torch.empty(B, **i32)
         self.new_len = torch.empty(B, **i32)
         self.status = torch.zeros(1, **i32)
-        self.processed = None  # logits as constrain() leaves them, where they need a place
         L = B_.lib()
         dt = B_.MEDUSA_BF16 if dtype == torch.bfloat16 else B_.MEDUSA_F32
         self.ws_heads = B_._ws(L.medusa_heads_workspace_size(B, H, V, K, topk), device)
@@ -83,13 +82,8 @@ class VerifyStep:
     def constrain(self, logits, stream=None, **rules):
         """The base logits [B, N, V] as the requests want them, each node with its path as
         context (the rules of medusa_logits_process), for accept(): in place where the logits are
-        fp32 and dense, else in a buffer that the step keeps.  Between tree() and accept()."""
-        if logits.dtype == torch.float32 and logits.is_contiguous():
-            out = logits
-        else:
-            if self.processed is None:
-                self.processed = torch.empty(logits.shape, dtype=torch.float32, device=logits.device)
-            out = self.processed
+        fp32 and dense, else in a new tensor on the call's stream.  Between tree() and accept()."""
+        out = logits if logits.dtype == torch.float32 and logits.is_contiguous() else None
         return V_.medusa_logits_process(logits, tokens=self.tokens, topo=self.topo, out=out, d_status=self.status, stream=stream, **rules)
 
     def count(self, counts, stream=None):
