@@ -14,7 +14,10 @@
 //
 // Within a CTA four sets of four warps unpack a block each into a buffer of their own, and two warps issue the
 // products of every second block, each into sums of its own: what lies between a block's products and the next
-// one's (some 800 clocks) passes under the other's.  The two sums are added as they are read out.
+// one's (some 800 clocks) passes under the other's.  The sums are added as they are read out.  The tensor core cuts
+// a sum's last bits off, so that what is lost grows with the products that are added to it: of up to 16 tokens a
+// stream's blocks go to four sums in turn, of up to 32 to two (4096 columns, one token: an error of 2.9e-7 of the
+// result, with one sum each 1.4e-6).
 //
 // Every wait is bounded, as there.
 #include <atomic>
@@ -30,6 +33,7 @@ constexpr int kRows = 128;              // features of a tile at most
 constexpr int kMaxTN = 64;
 constexpr int kMaxShare = 8;            // CTAs of a cluster
 constexpr int kSets = 4, kSlots = 4;    // of both rings, of two blocks each
+constexpr uint32_t kSums = 64;           // columns of tensor memory that a part's sums of one stream have
 constexpr uint32_t kOffScales = kRows * kCols;  // of a slot: the weights, scales [group][feature], zeros likewise
 constexpr uint32_t kOffZeros = kOffScales + 2048;
 constexpr uint32_t kSlotW = kOffZeros + 1024;
@@ -40,6 +44,7 @@ static_assert(kSlots * (kSlotW + kMaxTN * 512) <= kRing && 2 * kRegion <= kRing,
 struct Plan {
   Args a;
   int TN, DN, RH;       // tokens, columns of a sum, features of a tile
+  int turns;            // sums of a stream, which take its blocks in turn
   int mtiles, kpairs;   // kpairs: pairs of blocks of K
   int slabs;            // 64 columns of tokens that a load brings: 4, or 1 if K has other columns than multiples of 64
   int share, each;      // CTAs of a cluster, tiles of one
@@ -50,7 +55,7 @@ struct Plan {
 
 // A part of a tile: [0] is the part that a CTA's range begins with, [1] the one that it ends with.
 struct Part {
-  int there, tile, order;       // whether there is one; within the cluster; where the CTA's walk has it
+  int there, tile, order, turns;  // whether there is one; within the cluster; where the CTA's walk has it
   int n, sender, per;           // CTAs that share the tile, which of them this is, tokens of each
   int region;                   // where their sums arrive
   uint2 to[kMaxTN / 4];         // of four tokens: the CTA of the cluster that adds them up, where in its shared memory
@@ -123,15 +128,25 @@ __device__ __forceinline__ Raw<GROUPS> load_groups(const Plan& p, const Walk& x,
   return r;
 }
 
-// 16 columns of a part's sum, that of both streams.
-__device__ __forceinline__ void read_sums(uint32_t at, int DN, float* v) {
+// 16 columns of a part's sum, that of all its sums: of both streams, `used` of each.
+__device__ __forceinline__ void read_sums(uint32_t at, int DN, int used, float* v) {
   float w[16];
   __syncwarp();
   tmem_ld16(at, v);
-  tmem_ld16(at + DN, w);
+  tmem_ld16(at + kSums, w);
   tmem_wait_ld();
 #pragma unroll
   for (int e = 0; e < 16; ++e) v[e] += w[e];
+#pragma unroll 1
+  for (int i = 1; i < used; ++i) {
+    float u[16];
+    __syncwarp();
+    tmem_ld16(at + i * DN, u);
+    tmem_ld16(at + kSums + i * DN, w);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] += u[e] + w[e];
+  }
 }
 
 template <int GROUPS, bool TILED>
@@ -194,6 +209,7 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
       part.there = k ? tail_pairs > 0 : first > 0;
       part.tile = tile;
       part.order = parts - 1 - (k && first ? 1 : 0);
+      part.turns = min(k ? tail_pairs : first, p.turns);
       part.n = n;
       part.sender = rank - f;
       part.per = per;
@@ -211,7 +227,7 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
   tc_fence_after();
   pdl_wait();
   pdl_trigger();
-  const uint32_t tmem = tail->tmem, weights = tmem + 4 * p.DN;  // sums: [part, even or odd][stream]; then unpacked weights
+  const uint32_t tmem = tail->tmem, weights = tmem + 4 * kSums;  // sums: [part, even or odd][stream][turn]; then unpacked weights
 
   if (warp == 0) {
     // ------------------------------------------------------------ weights as they are kept
@@ -259,19 +275,19 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
     bool alive = true;
     for (int part = 0; x.left > 0 && alive; ++part) {
       const int np = x.part(p.kpairs);
-      const uint32_t d = uniform(tmem + (2 * (part & 1) + s) * p.DN);
+      const uint32_t d = uniform(tmem + (2 * (part & 1) + s) * kSums);
       if (part > 1 && !(alive = warp_wait(&tail->d_empty[part & 1][s], (uint32_t)(part / 2 - 1) & 1u, abort))) break;  // the part before the last is read out
       const uint32_t last = i + np;
 #pragma unroll 1
-      for (uint32_t own = 0; i < last; ++i, own = 1) {
-        const uint32_t set = uniform(2 * (i & 1) + s), slot = uniform(i % kSlots);
+      for (uint32_t own = 0; i < last; ++i, ++own) {
+        const uint32_t set = uniform(2 * (i & 1) + s), slot = uniform(i % kSlots), sum = uniform(d + (own & (p.turns - 1)) * p.DN);
         if (!(alive = warp_wait(full + 8 * set, (i / 2) & 1u, abort))) break;
         tc_fence_after();
         if (elect_one()) {
           const uint32_t xd = x0 + (4 * slot + 2 * s) * half, a = a0 + 64 * set;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(d, a + 8 * kk, desc_of(xd + (kk >> 2) * half + 2 * (kk & 3)), idesc, kk > 0 || own);
+            mma_bf16_ts(sum, a + 8 * kk, desc_of(xd + (kk >> 2) * half + 2 * (kk & 3)), idesc, kk > 0 || own >= (uint32_t)p.turns);
           mma_commit(&tail->a_empty[set]);
           mma_commit(&tail->x_empty[slot]);
         }
@@ -359,13 +375,13 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
       uint64_t* const full = tail->d_full[part & 1];
       if (!(warp_wait(full, (uint32_t)(part / 2) & 1u, abort) && warp_wait(full + 1, (uint32_t)(part / 2) & 1u, abort))) break;
       tc_fence_after();
-      const uint32_t at = tmem + ((uint32_t)(32 * q4) << 16) + 2 * (part & 1) * p.DN;
+      const uint32_t at = tmem + ((uint32_t)(32 * q4) << 16) + 2 * (part & 1) * kSums;
       const bool mine = m < p.RH && n < p.a.Nout;
       size_t to = n;
 #pragma unroll 1
       for (int c = 0; c < p.a.T; c += 16) {
         float v[16];
-        read_sums(at + c, p.DN, v);
+        read_sums(at + c, p.DN, min(np, p.turns), v);
         if (!mine) continue;
         const int more = p.a.T - c;
         if (p.a.y32) {
@@ -410,11 +426,11 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
       for (int k = 0; k < 2; ++k) {
         const Part& part = tail->part[k];
         if (!part.there) continue;
-        const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 2 * (part.order & 1) * p.DN;
+        const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 2 * (part.order & 1) * kSums;
 #pragma unroll 1
         for (int c = 16 * group; c < p.TN; c += 16 * kSets) {
           float v[16];
-          read_sums(from + c, p.DN, v);
+          read_sums(from + c, p.DN, part.turns, v);
           if (!works) continue;
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
@@ -465,7 +481,8 @@ static Plan plan(int T, int K, int Nout) {
   for (int share = 1; share <= kMaxShare; share *= 2) {
     Plan p{};
     p.TN = (T + 15) / 16 * 16;
-    p.DN = (p.TN + 31) / 32 * 32;
+    p.DN = p.TN > 32 ? 64 : p.TN;
+    p.turns = kSums / p.DN;
     p.RH = Nout >= kRows ? kRows : (Nout + 15) / 16 * 16;
     p.mtiles = (Nout + p.RH - 1) / p.RH;
     p.kpairs = (K + 2 * kCols - 1) / (2 * kCols);
