@@ -608,7 +608,7 @@ medusa_status medusa_linear_w4(const void* x, int64_t ldx, const uint32_t* qweig
 typedef struct medusa_logits_rules {
   const int32_t* counts;       /* [B][V] tokens said so far, the prompt's left out */
   const uint32_t* prompt_bits; /* [B][ceil(V/32)] bit v % 32 of word v / 32: v is in the prompt */
-  const float* repetition;     /* [B] > 0 */
+  const float* repetition;     /* [B] > 0, 2^-126 .. 2^126 */
   const float* frequency;      /* [B] */
   const float* presence;       /* [B] */
   const float* bias;           /* [bias_rows][V] */

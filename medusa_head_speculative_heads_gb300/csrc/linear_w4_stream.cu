@@ -544,6 +544,7 @@ int clusters_at_once(int share) {
 medusa_status stream_launch(const Args& a, int withhold, cudaStream_t s) {
   if (!encode_fn()) return MEDUSA_ERR_CUDA;
   Plan p = plan(a.T, a.K, a.Nout);
+  if (!p.share) return MEDUSA_ERR_INVALID_ARG;  // more blocks than 31 bits count, and than memory holds
   p.a = a;
   p.withhold = withhold;
   const int per = kCols >> a.glog, ng = a.K >> a.glog;

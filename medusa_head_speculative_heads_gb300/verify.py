@@ -29,9 +29,14 @@ def _load():
     return _native
 
 
-def _topology(topo):
-    """The address of a device topology's description, or None."""
-    return None if topo is None else ctypes.addressof(topo.st)
+def _topology(topo, like):
+    """The address of a device topology's description, which must be on `like`'s device, or None."""
+    if topo is None:
+        return None
+    held = topo.buf if isinstance(topo.buf, torch.Tensor) else topo.buf[0]
+    if held.device != like.device:
+        raise ValueError(f"medusa_logits_process: topo is on {held.device}, logits are on {like.device}")
+    return ctypes.addressof(topo.st)
 
 
 def medusa_w4_quantize(w, group: int = 128, symmetric: bool = False, stream=None):
@@ -74,7 +79,7 @@ def medusa_logits_process(logits, counts=None, prompt_bits=None, repetition=None
         return _on(stream, logits, medusa_logits_process, logits, counts, prompt_bits, repetition, frequency, presence, bias, mask,
                    mask_row, tokens, topo, out, d_status)
     r = (_native or _load()).logits(logits, counts, prompt_bits, repetition, frequency, presence, bias, mask, mask_row, tokens,
-                                    _topology(topo), out, d_status)
+                                    _topology(topo, logits), out, d_status)
     if type(r) is int:
         raise B_.MedusaError("medusa_logits_process", r)
     return r

@@ -253,3 +253,15 @@ def test_quantizing_refuses(mg):
             mg.medusa_w4_quantize(w, group)
     with pytest.raises(ValueError, match="dense"):
         mg.medusa_w4_quantize(torch.zeros((4, 192), device="cuda")[:, ::2], 32)
+
+
+def test_outputs_past_32_bits(mg):
+    T, K, N = 70001, 64, 32016
+    rng = np.random.default_rng(2)
+    m, rows = matrix(rng, N, K, 64), [0, 35000, 67077, 67078, T - 1]
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device="cuda")
+    few = bf16(rng, len(rows), K)
+    x[rows] = to_dev(few)
+    y = mg.medusa_linear_w4(x, *dev_matrix(m))
+    check_linear(y[rows], few, m, "bf16")
+    assert not y[1:35000].any() and not y[67079:T - 1].any()

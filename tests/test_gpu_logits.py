@@ -278,3 +278,18 @@ def test_counting_accepted_paths(mg, B, N, D1, V):
                 tokens[4, path[4, 0]] = V
             assert run() == 1, what
             acc, path, tokens = a, p, t
+
+
+@pytest.mark.parametrize("N,V", [(64, 32016), (1, 32016), (64, 32001)])
+def test_logits_past_32_bits(mg, N, V):
+    B = 70400 // N
+    rng = np.random.default_rng(N + V)
+    rows = [0, 35000 // N, 67085 // N, B - 1]
+    part = wl.to_bf16_bits(rng.standard_normal((len(rows), N, V)).astype(np.float32))
+    counts, frequency = rng.integers(0, 3, (len(rows), V)).astype(np.int32), np.array([0.5, 1.0, -0.5, 0.25], np.float32)
+    z, c, f = torch.zeros((B, N, V), dtype=torch.bfloat16, device="cuda"), torch.zeros((B, V), dtype=torch.int32, device="cuda"), torch.zeros(B, device="cuda")
+    z[rows], c[rows], f[rows] = to_dev(part), to_dev(counts), to_dev(frequency)
+    got = mg.medusa_logits_process(z, c, frequency=f)
+    want, size = ov.process(ov.bf16_value(part), counts, frequency=frequency)
+    assert np.all(np.abs(value(got[rows]) - want) <= 6 * U * size)
+    assert not got[rows[1] + 1:rows[2]].any() and not got[rows[2] + 1:rows[3]].any()

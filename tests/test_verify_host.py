@@ -152,3 +152,9 @@ def test_the_binding_refuses_other_shapes_types_and_places():
         mg.medusa_count_tokens(z(1, 2, dt=i32), 9, counts=z(1, 9, dt=i32))
     with pytest.raises(ValueError, match="on a GPU"):
         mg.medusa_count_accepted(z(1, 9, dt=i32), z(1, 2, dt=i32), z(1, 2, dt=i32), z(1, dt=i32))
+
+
+def test_a_topology_of_another_device_is_refused():
+    topo = B_.DevTopology(topology(), torch.zeros(1))
+    with pytest.raises(ValueError, match="topo is on cpu, logits are on meta"):
+        mg.medusa_logits_process(torch.zeros(2, 7, 10, device="meta"), tokens=torch.zeros(2, 7, dtype=torch.int32), topo=topo)
