@@ -436,6 +436,8 @@ tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 
 // ------------------------------------------------------------------ host side
 
+static int log2_of(int n) { return n > 1 ? 1 + log2_of(n / 2) : 0; }
+
 static Tc plan(int T, int K, int Nout) {
   Tc best{};
   double least = 0;
@@ -461,11 +463,14 @@ static Tc plan(int T, int K, int Nout) {
     p.mtiles = (Nout + p.halves * p.RH - 1) / (p.halves * p.RH);
     const long long tiles = (long long)p.mtiles * p.ntiles;
     p.grid = (int)(tiles < at_once ? tiles : at_once) * share;
-    // Clocks: a block's products, unpacking and bytes, whichever is most; what a tile's end costs.
-    const double products = 4.0 * p.TN * p.halves, unpacking = 330.0 * p.halves, bytes = p.halves * p.RH * 64 / 20.0;
-    double block = products > unpacking ? products : unpacking;
+    // Clocks: a block's products, what its way through the two sets of unpacking warps takes, and its bytes, whichever is
+    // most (an SM gets some 36 bytes a clock when all do: 112 features x 96 tokens 864 clocks, 160 x 128 1240, 256 x 128
+    // 1380); what a tile's end costs, and the exchange of sums (171 tokens x 4096 features of 11008 columns: tiles of 256
+    // features that four CTAs share 20.7 us, of 112 that two share 23.0).
+    const double products = 4.0 * p.TN * p.halves, bytes = (p.halves * p.RH * 64 + p.TN * 256) / 36.0;
+    double block = products > 850 ? products : 850;
     if (bytes > block) block = bytes;
-    const double cost = (double)rounds * ((kblocks + share - 1) / share * (block + 100) + 1500 + (share > 1 ? 2500 + p.TN * p.halves * p.RH / 10.0 : 0));
+    const double cost = (double)rounds * ((kblocks + share - 1) / share * block + 1500 + (share > 1 ? 2000 * log2_of(share) + p.TN * p.halves * p.RH / 1.6 : 0));
     if (least == 0 || cost < least) {
       least = cost;
       best = p;
