@@ -215,7 +215,12 @@ extern "C" medusa_status medusa_w4_quantize(const void* w, int Nout, int K, int 
   return launch_status();
 }
 
-// More than 64 tokens are the work of linear_w4_tc.cu, up to 64 of linear_w4_stream.cu, and of few tokens the warps' own
+// More than 64 tokens are the work of linear_w4_tc.cu, unless the layer is so small that few blocks make a CTA of
+// linear_w4_stream.cu, whose evenly divided work then ends sooner (2048 features of 2048 columns, 128 tokens, 4 blocks: 6.9 and
+// 10.2 us; 4096 x 4096, 128 and 256 tokens, 16 and 32 blocks: 9.9 and 11.6, 12.2 and 15.1; 384 tokens, 48 blocks: 17.9 and
+// 17.4; 4096 features of 11008 columns, 65 tokens, 44 blocks: 16.6 and 15.4).
+constexpr int kSmall = 32;
+// Up to 64 tokens are the work of linear_w4_stream.cu, and of few tokens the warps' own
 // product instructions, fed from registers, where their CTAs are all there at once or the layer is small: the others
 // need some 2 us more to begin and to add up, and unpack faster.  Times for K = 4096, registers and tensor memory:
 //   one token    x  4096 features   5.0 and  7.1 us     9 tokens x 1024   4.5 and 5.4 us
@@ -258,7 +263,7 @@ static medusa_status linear_call(const void* x, int64_t ldx, const uint32_t* qwe
   a.y32 = y_dt == MEDUSA_F32;
   a.d_status = d_status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (T > 64) return tc_launch(a, withhold, s);
+  if (T > 64 && stream_blocks(T, K, Nout) > kSmall) return tc_launch(a, withhold, s);
   if (!from_registers(T, K, Nout)) return stream_launch(a, withhold, s);
   if (withhold) return MEDUSA_ERR_INVALID_ARG;
   if (T > 8) few<2, 1, 16>(a, s);

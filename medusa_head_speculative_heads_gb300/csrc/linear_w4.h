@@ -69,8 +69,10 @@ __device__ __forceinline__ void store_y(const Args& a, int t, int n, float v) {
 
 // Clusters of `share` CTAs of a tensor-memory kernel, one CTA an SM, that the current device holds at once.
 int clusters_at_once(int share);
-// Tensor-memory kernels: up to 64 tokens (linear_w4_stream.cu), any number (linear_w4_tc.cu).
+// Tensor-memory kernels: few tokens or a small layer (linear_w4_stream.cu), any number (linear_w4_tc.cu).
 medusa_status stream_launch(const Args& a, int withhold, cudaStream_t s);
+// Blocks of 128 features, 64 tokens and 128 columns that a CTA of the first one has at most.
+int stream_blocks(int T, int K, int Nout);
 medusa_status tc_launch(const Args& a, int withhold, cudaStream_t s);
 
 }  // namespace w4

@@ -1,9 +1,10 @@
-// medusa_linear_w4 on tcgen05 tensor cores: up to 64 tokens, bound by memory and by the unpacking of the weights.
+// medusa_linear_w4 on tcgen05 tensor cores: up to 64 tokens, and more of a small layer in tiles of up to 64, bound by memory and
+// by the unpacking of the weights.
 //
 // As in the kernel for many tokens (linear_w4_tc.cu) weights come as they are kept by TMA and sixteen warps unpack
 // them into tensor memory, the products' first operand.  A block of 128 columns of 128 features costs an SM's
 // schedulers some 350 clocks of unpacking each, so that what counts is that all of them have the same number of
-// blocks: the tiles of 128 features that a cluster of CTAs has, laid end to end, are divided evenly over its CTAs (64
+// blocks: the tiles of 128 features and up to 64 tokens that a cluster of CTAs has, laid end to end, are divided evenly over its CTAs (64
 // tokens, 22016 features of 4096 columns: 17.8 us, 2.8 TB/s; tiles of up to 256 features in whole rounds 22.4).  A CTA has its whole tiles first and
 // then the parts of tiles, whose sums stay in tensor memory until the end and then go through distributed shared
 // memory to the tile's CTAs, which add up some tokens each, in the CTAs' order.
@@ -44,19 +45,22 @@ static_assert(kSlots * (kSlotW + kMaxTN * 512) <= kRing && 2 * kRegion <= kRing,
 
 struct Plan {
   Args a;
-  int TN, DN, RH;       // tokens, columns of a sum, features of a tile
+  int TN, DN, RH;       // tokens of a tile, columns of a sum, features of a tile
   int turns;            // sums of a stream, which take its blocks in turn
-  int mtiles, kpairs;   // kpairs: pairs of blocks of K
+  int tiles, ntiles;    // all tiles; those of the same features, one after the other
+  int kpairs;           // pairs of blocks of K
   int slabs;            // 64 columns of tokens that a load brings: 4, or 1 if K has other columns than multiples of 64
   int share, each;      // CTAs of a cluster, tiles of one
   int clusters;
   int slot_bytes;       // that come into a slot of weights
+  long long cost;       // clocks
   int withhold;         // failure test: the first tokens are never loaded
 };
 
 // A part of a tile: [0] is the part that a CTA's range begins with, [1] the one that it ends with.
 struct Part {
-  int there, tile, order, turns;  // whether there is one; within the cluster; where the CTA's walk has it
+  int there, n0, t0;            // whether there is one; its features and tokens
+  int order, turns;             // where the CTA's walk has it; sums of a stream
   int n, sender, per;           // CTAs that share the tile, which of them this is, tokens of each
   int region;                   // where their sums arrive
   uint2 to[kMaxTN / 4];         // of four tokens: the CTA of the cluster that adds them up, where in its shared memory
@@ -86,28 +90,32 @@ struct Range {
 // A CTA's pairs of blocks, one after the other: whole tiles, the part of a tile that its range ends with, and last the part that it
 // begins with.  So the sums of both parts may stay where they are until the end.
 struct Walk {
-  int tile, kp, left;         // left: pairs, this one included
-  int tile0, kp0, first;      // the part that comes last: where it is, its pairs (0: none)
+  int mt, nt, kp, left;          // tile of features, of tokens, pair; left: pairs, this one included
+  int mt0, nt0, kp0, first;      // the part that comes last: where it is, its pairs (0: none)
   __device__ __forceinline__ void to_first() {
     if (left == first) {
-      tile = tile0;
+      mt = mt0;
+      nt = nt0;
       kp = kp0;
     }
   }
-  __device__ __forceinline__ void step(int kpairs) {
-    --left;
-    if (++kp == kpairs) {
-      kp = 0;
-      ++tile;
+  __device__ __forceinline__ void next_tile(int ntiles) {
+    kp = 0;
+    if (++nt == ntiles) {
+      nt = 0;
+      ++mt;
     }
+  }
+  __device__ __forceinline__ void step(const Plan& p) {
+    --left;
+    if (++kp == p.kpairs) next_tile(p.ntiles);
     to_first();
   }
   // Pairs of the tile that the walk is in, all of them if they are whole tiles'.
   __device__ __forceinline__ int part(int kpairs) const { return left <= first ? left : min(left - first, kpairs); }
-  __device__ __forceinline__ void next_part(int np) {
+  __device__ __forceinline__ void next_part(const Plan& p, int np) {
     left -= np;
-    kp = 0;
-    ++tile;
+    next_tile(p.ntiles);
     to_first();
   }
 };
@@ -116,7 +124,7 @@ template <int GROUPS>
 __device__ __forceinline__ Raw<GROUPS> load_groups(const Plan& p, const Walk& x, int odd, int row) {
   Raw<GROUPS> r;
   const int kb = 2 * x.kp + odd;
-  const size_t at = (size_t)kb * GROUPS * p.a.Nout + min(x.tile * p.RH + row, p.a.Nout - 1);
+  const size_t at = (size_t)kb * GROUPS * p.a.Nout + min(x.mt * p.RH + row, p.a.Nout - 1);
 #pragma unroll
   for (int i = 0; i < GROUPS; ++i) {
     r.s[i] = 0;  // behind the last column: weights of 0
@@ -193,11 +201,12 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
     tmem_relinquish();
   }
   const int rank = blockIdx.x % p.share, tile0 = blockIdx.x / p.share * p.each;
-  const Range range{tile0, (uint32_t)(min(p.each, p.mtiles - tile0) * p.kpairs), (uint32_t)p.share, (uint32_t)__ffs(p.share) - 1};
+  const Range range{tile0, (uint32_t)(min(p.each, p.tiles - tile0) * p.kpairs), (uint32_t)p.share, (uint32_t)__ffs(p.share) - 1};
   const int begin = (int)range.begin(rank), end = (int)range.begin(rank + 1);
   const int lead = begin % p.kpairs;  // pairs of the first tile that are another CTA's
   const int first = lead ? min(p.kpairs - lead, end - begin) : 0;
-  Walk x{tile0 + (begin + first) / p.kpairs, 0, end - begin, tile0 + begin / p.kpairs, lead, first};
+  const int whole = tile0 + (begin + first) / p.kpairs, last = tile0 + begin / p.kpairs;  // tiles that the walk begins and ends with
+  Walk x{whole / p.ntiles, whole % p.ntiles, 0, end - begin, last / p.ntiles, last % p.ntiles, lead, first};
   x.to_first();
   const int parts = (first > 0) + (end - begin - first + p.kpairs - 1) / p.kpairs, tail_pairs = (end - begin - first) % p.kpairs;
   if (warp == 2 && p.share > 1) {
@@ -208,7 +217,8 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
     Part& part = tail->part[k];
     if ((lane & 15) == 0) {
       part.there = k ? tail_pairs > 0 : first > 0;
-      part.tile = tile;
+      part.n0 = (tile0 + tile) / p.ntiles * p.RH;
+      part.t0 = (tile0 + tile) % p.ntiles * p.TN;
       part.order = parts - 1 - (k && first ? 1 : 0);
       part.turns = min(k ? tail_pairs : first, p.turns);
       part.n = n;
@@ -233,15 +243,16 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
   if (warp == 0) {
     // ------------------------------------------------------------ weights as they are kept
     int n = 0;
-    for (Ring w; x.left > 0; x.step(p.kpairs), w.next(kSlots), ++n) {
+    for (Ring w; x.left > 0; x.step(p), w.next(kSlots), ++n) {
       if (w.used() && !warp_wait(&tail->w_empty[w.i], w.empty(), abort)) break;
       if (elect_one()) {
         uint8_t* to = smem + w.i * kSlotW;
+        const int row = x.mt * p.RH;
         mbar_expect_tx(&tail->w_full[w.i], (uint32_t)p.slot_bytes);
-        tma_load_2d(to, &tm_w, &tail->w_full[w.i], x.kp * kCols, x.tile * p.RH);
+        tma_load_2d(to, &tm_w, &tail->w_full[w.i], x.kp * kCols, row);
         if (TILED) {
-          tma_load_2d(to + kOffScales, &tm_s, &tail->w_full[w.i], x.tile * p.RH, x.kp * (2 * GROUPS));
-          if (p.a.zeros) tma_load_2d(to + kOffZeros, &tm_z, &tail->w_full[w.i], x.tile * p.RH, x.kp * (2 * GROUPS));
+          tma_load_2d(to + kOffScales, &tm_s, &tail->w_full[w.i], row, x.kp * (2 * GROUPS));
+          if (p.a.zeros) tma_load_2d(to + kOffZeros, &tm_z, &tail->w_full[w.i], row, x.kp * (2 * GROUPS));
         }
       }
       __syncwarp();
@@ -250,17 +261,18 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
   } else if (warp == 2) {
     // ------------------------------------------------------------ tokens
     int n = 0;
-    for (Ring t; x.left > 0; x.step(p.kpairs), t.next(kSlots), ++n) {
+    for (Ring t; x.left > 0; x.step(p), t.next(kSlots), ++n) {
       if (t.used() && !warp_wait(&tail->x_empty[t.i], t.empty(), abort)) break;
       if (elect_one()) {
         mbar_expect_tx(&tail->x_full[t.i], (uint32_t)p.TN * 512);
         uint8_t* const to = ring_x + t.i * (p.TN * 512);
+        const int t0 = x.nt * p.TN;
         if (p.slabs == 4) {
-          if (!(p.withhold && n == 0)) tma_load_3d(to, &tm_x, &tail->x_full[t.i], 0, 0, x.kp * 4);
+          if (!(p.withhold && n == 0)) tma_load_3d(to, &tm_x, &tail->x_full[t.i], 0, t0, x.kp * 4);
         } else {
           for (int u = 0; u < 4; ++u)
             if (!(p.withhold && n == 0 && u == 0))
-              tma_load_2d(to + u * (p.TN * 128), &tm_x, &tail->x_full[t.i], x.kp * (2 * kCols) + u * 64, 0);
+              tma_load_2d(to + u * (p.TN * 128), &tm_x, &tail->x_full[t.i], x.kp * (2 * kCols) + u * 64, t0);
         }
       }
       __syncwarp();
@@ -297,7 +309,7 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
       if (!alive) break;
       if (elect_one()) mma_commit(&tail->d_full[part & 1][s]);
       __syncwarp();
-      x.next_part(np);
+      x.next_part(p, np);
     }
     if (elect_one()) {
       // This warp's products and the arrivals they signal, before tensor and shared memory go away.
@@ -314,7 +326,7 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
                    came = smem_u32(&tail->w_full[0]), left_empty = smem_u32(&tail->w_empty[0]);
     uint32_t phase = 0;  // of the set's blocks
     const int pairs = x.left;
-    if (set > 1) x.step(p.kpairs);
+    if (set > 1) x.step(p);
     Raw<GROUPS> raw{};
     if (!TILED) raw = load_groups<GROUPS>(p, x, odd, row);
 #pragma unroll 1
@@ -323,8 +335,8 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
       if (!TILED) {
 #pragma unroll
         for (int k = 0; k < GROUPS; ++k) g[k] = group_of(raw.s[k], raw.z[k]);
-        x.step(p.kpairs);
-        x.step(p.kpairs);
+        x.step(p);
+        x.step(p);
         raw = load_groups<GROUPS>(p, x, odd, row);  // of the set's next block: they take a round trip to memory
       }
       const uint32_t slot = (uint32_t)i % kSlots, round = (uint32_t)i / kSlots & 1u;
@@ -371,20 +383,20 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
     // ------------------------------------------------------------ whole tiles, read out
     const int q4 = warp & 3, m = 32 * q4 + lane;
     for (int part = 0; x.left > 0; ++part) {
-      const int np = x.part(p.kpairs), n = x.tile * p.RH + m;
+      const int np = x.part(p.kpairs), n = x.mt * p.RH + m, t0 = x.nt * p.TN, tokens = min(p.TN, p.a.T - t0);
       if (np < p.kpairs) break;  // what is left are parts
       uint64_t* const full = tail->d_full[part & 1];
       if (!(warp_wait(full, (uint32_t)(part / 2) & 1u, abort) && warp_wait(full + 1, (uint32_t)(part / 2) & 1u, abort))) break;
       tc_fence_after();
       const uint32_t at = tmem + ((uint32_t)(32 * q4) << 16) + 2 * (part & 1) * kSums;
       const bool mine = m < p.RH && n < p.a.Nout;
-      size_t to = n;
+      size_t to = (size_t)t0 * p.a.Nout + n;
 #pragma unroll 1
-      for (int c = 0; c < p.a.T; c += 16) {
+      for (int c = 0; c < tokens; c += 16) {
         float v[16];
         read_sums(at + c, p.DN, min(np, p.turns), v);
         if (!mine) continue;
-        const int more = p.a.T - c;
+        const int more = tokens - c;
         if (p.a.y32) {
           float* y = static_cast<float*>(p.a.y);
 #pragma unroll
@@ -400,7 +412,7 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
       __syncwarp();
       tc_fence_before();
       for (int s = 0; s < 2; ++s) warp_arrive(smem_u32(&tail->d_empty[part & 1][s]), lane);
-      x.next_part(np);
+      x.next_part(p, np);
     }
   }
 
@@ -450,7 +462,8 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
       for (int k = 0; k < 2; ++k) {
         const Part& part = tail->part[k];
         if (!part.there) continue;
-        const int t0 = part.sender * part.per, tokens = min(part.per, p.a.T - t0), n = (tile0 + part.tile) * p.RH + m;
+        const int skip = part.sender * part.per, t0 = part.t0 + skip;
+        const int tokens = min(min(part.per, p.TN - skip), p.a.T - t0), n = part.n0 + m;
         const float4* sums = reinterpret_cast<const float4*>(smem + part.region) + m;
         for (int t = 4 * group; t < tokens; t += 4 * kSets) {
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -478,27 +491,26 @@ stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
 
 static Plan plan(int T, int K, int Nout) {
   Plan best{};
-  long long least = 0;
   for (int share = 1; share <= kMaxShare; share *= 2) {
     Plan p{};
-    p.TN = (T + 15) / 16 * 16;
+    p.ntiles = (T + kMaxTN - 1) / kMaxTN;
+    p.TN = ((T + p.ntiles - 1) / p.ntiles + 15) / 16 * 16;
+    p.ntiles = (T + p.TN - 1) / p.TN;
     p.DN = p.TN > 32 ? 64 : p.TN;
     p.turns = kSums / p.DN;
     p.RH = Nout >= kRows ? kRows : (Nout + 15) / 16 * 16;
-    p.mtiles = (Nout + p.RH - 1) / p.RH;
     p.kpairs = (K + 2 * kCols - 1) / (2 * kCols);
     p.slabs = K % 64 ? 1 : 4;
     p.share = share;
-    if (share > p.kpairs || p.mtiles * (long long)p.kpairs * kMaxShare > 0x7fffffffll) break;
+    const long long tiles = (long long)((Nout + p.RH - 1) / p.RH) * p.ntiles;
+    if (share > p.kpairs || tiles * p.kpairs * kMaxShare > 0x7fffffffll) break;
+    p.tiles = (int)tiles;
     const int n = clusters_at_once(share);
-    p.each = (p.mtiles + n - 1) / n;
-    p.clusters = (p.mtiles + p.each - 1) / p.each;
+    p.each = (p.tiles + n - 1) / n;
+    p.clusters = (p.tiles + p.each - 1) / p.each;
     // Clocks: of a pair of blocks, and of the exchange of sums.
-    const long long cost = ((long long)p.each * p.kpairs + share - 1) / share * 900 + (share > 1 ? 3000 : 0);
-    if (least == 0 || cost < least) {
-      least = cost;
-      best = p;
-    }
+    p.cost = ((long long)p.each * p.kpairs + share - 1) / share * 900 + (share > 1 ? 3000 : 0);
+    if (best.tiles == 0 || p.cost < best.cost) best = p;
   }
   return best;
 }
@@ -540,6 +552,11 @@ int clusters_at_once(int share) {
   }
   known[dev][k].store(n, std::memory_order_relaxed);
   return n;
+}
+
+int stream_blocks(int T, int K, int Nout) {
+  const Plan p = plan(T, K, Nout);
+  return p.share ? 2 * (p.each * p.kpairs / p.share) : 0x7fffffff;
 }
 
 medusa_status stream_launch(const Args& a, int withhold, cudaStream_t s) {

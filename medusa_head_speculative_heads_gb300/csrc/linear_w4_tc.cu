@@ -15,9 +15,9 @@
 // distributed shared memory, and adds what it receives in the CTAs' order.
 //
 // What bounds it: for prompts the tensor cores and the power they take (2311 tokens, 11008 features of 4096 columns: 134 us,
-// 1550 TFLOP/s, tensor pipe 80 %); for a few hundred tokens the bytes that come into an SM, tokens most of all, some
-// 36 a clock, and what a shared tile's end costs (171 tokens, 4096 features of 11008 columns: 20.5 us, 750
-// TFLOP/s).  Tokens loaded once for two neighbouring CTAs made it no faster (21.4 us, prompts 137).
+// 1550 TFLOP/s, tensor pipe 80 %); for a few hundred tokens the unpacking, whose warps wait half of the time, and what a
+// shared tile's end costs (171 tokens, 4096 features of 11008 columns: 20.5 us, 750 TFLOP/s).  Tokens loaded once for
+// two neighbouring CTAs made it no faster (21.4 us, prompts 137).
 //
 // Every wait is bounded: a timeout sets MEDUSA_DEV_TIMEOUT, all roles stop, copies and products in
 // flight are waited for and tensor memory is freed.
@@ -469,7 +469,7 @@ static Tc plan(int T, int K, int Nout) {
     const long long tiles = (long long)p.mtiles * p.ntiles;
     p.grid = (int)(tiles < at_once ? tiles : at_once) * share;
     // Clocks: a block's products, what its way through the two sets of unpacking warps takes, and its bytes, whichever is
-    // most (an SM gets some 36 bytes a clock when all do: 112 features x 96 tokens 864 clocks, 160 x 128 1240, 256 x 128
+    // most (as measured these come to 36 a clock: 112 features x 96 tokens 864 clocks, 160 x 128 1240, 256 x 128
     // 1380); what a tile's end costs, and the exchange of sums (171 tokens x 4096 features of 11008 columns: tiles of 256
     // features that four CTAs share 20.7 us, of 112 that two share 23.0).
     const double products = 4.0 * p.TN * p.halves, bytes = (p.halves * p.RH * 64 + p.TN * 256) / 36.0;

@@ -55,6 +55,23 @@ def test_parity(mg, T, K, N, G, zeros, out):
     check_linear(got, x, m, out)
 
 
+SMALL_LAYERS = [  # of more than 64 tokens, in several tiles of tokens
+    (65, 64, 20, 64, True, "bf16"),
+    (70, 2080, 1000, 32, True, "f32"),
+    (128, 2048, 2048, 128, True, "bf16"),
+    (129, 1536, 2049, 64, False, "f32"),
+    (256, 4096, 4096, 128, True, "bf16"),
+    (333, 512, 3000, 64, True, "bf16"),
+    (1000, 2048, 512, 128, False, "f32"),
+    (2300, 256, 640, 32, True, "bf16"),
+]
+
+
+@pytest.mark.parametrize("T,K,N,G,zeros,out", SMALL_LAYERS, ids=["-".join(map(str, s)) for s in SMALL_LAYERS])
+def test_parity_of_small_layers(mg, T, K, N, G, zeros, out):
+    test_parity(mg, T, K, N, G, zeros, out)
+
+
 FEW_TOKENS = [  # layers that are large for their few tokens, and those just below
     (1, 2304, 16384, 128, True, "bf16"),
     (1, 2016, 16385, 32, False, "f32"),

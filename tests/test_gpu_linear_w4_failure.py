@@ -11,7 +11,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("T,K,N", [(64, 512, 300), (200, 2048, 256), (9, 4096, 4100), (40, 1088, 200)])
+@pytest.mark.parametrize("T,K,N", [(64, 512, 300), (200, 2048, 256), (9, 4096, 4100), (40, 1088, 200), (300, 8192, 4096)])
 def test_tokens_that_never_come(T, K, N):
     import medusa_head_speculative_heads_gb300 as mg
     from medusa_head_speculative_heads_gb300 import binding as B_
