@@ -232,7 +232,8 @@ medusa_status medusa_tree_attention(const void* q, const void* kc, const void* v
  *   tokens [B][N] int32 from tree_build; token ids must lie in [0, V) (else
  *   BAD_INDEX and the node fails its test).  temperature >= 0, eps >= 0,
  *   delta >= 0.  A logit of -inf has probability 0; where all of a node's are,
- *   its children fail (probability 0) and its argmax is token 0.  The workspace (16-byte aligned) holds per-chunk partial
+ *   its children fail at any temperature (probability 0), token 0 among them, although
+ *   that is its argmax, and its threshold at temperature > 0 is eps.  The workspace (16-byte aligned) holds per-chunk partial
  *   statistics of every node's logit row. */
 size_t medusa_typical_accept_workspace_size(int B, int N, int V);
 medusa_status medusa_typical_accept(const float* logits, const int32_t* tokens,

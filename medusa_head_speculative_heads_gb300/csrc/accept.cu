@@ -326,8 +326,11 @@ select_path_kernel(const float* __restrict__ logits, const int32_t* __restrict__
         set_status(d_status, MEDUSA_DEV_BAD_INDEX);
         ok = 0;
         p = 0.f;
+      } else if (zmax[pc] == -INFINITY) {  // all of the parent's logits: nothing follows, its argmax (token 0) neither
+        ok = 0;
+        p = 0.f;
       } else if (T > 0.f) {
-        p = ssum[pc] == 0.f ? 0.f : expf((z_px - zmax[pc]) / T) / ssum[pc];  // 0: the parent's logits are all -inf
+        p = ssum[pc] == 0.f ? 0.f : expf((z_px - zmax[pc]) / T) / ssum[pc];  // 0: NaN among the parent's logits
         ok = p > t;
       } else {
         ok = x == amax[pc];

@@ -223,6 +223,11 @@ static void orc_node_stats(const float* z, int V, double T, double eps, double d
     *thr = eps < delta ? eps : delta;
     return;
   }
+  if (z[a] == -INFINITY) { /* no distribution at all */
+    *sum = 0.0;
+    *thr = eps;
+    return;
+  }
   double S = 0.0;
   for (int v = 0; v < V; ++v) S += exp(((double)z[v] - *zmax) / T);
   double H = 0.0;
@@ -241,7 +246,8 @@ static void orc_node_stats(const float* z, int V, double T, double eps, double d
  * tokens [B][N]: node tokens (node 0 is the root).  parent [N]: parent index,
  * parent[0] = -1, parent[n] < n.
  * Node n >= 1 passes its test when p_parent(tokens[n]) > thr_parent (T > 0) or
- * tokens[n] == argmax of the parent's logits (T == 0).  The root is accepted
+ * tokens[n] == argmax of the parent's logits (T == 0); where all of the parent's
+ * logits are -inf it fails (p = 0, the threshold is eps for T > 0).  The root is accepted
  * unconditionally; accepted(n) = accepted(parent(n)) and test(n).  The best node
  * is the deepest accepted node (lowest index on ties); path_nodes[b] lists root
  * to best, padded with -1 up to Dmax + 1 entries; accept_len = depth(best) + 1;
@@ -285,7 +291,10 @@ int orc_typical_accept(const float* logits, const int32_t* tokens, const int32_t
       int x = tokens[(size_t)b * N + n];
       int test;
       double p;
-      if (T == 0.0) {
+      if (zmax[par] == -INFINITY) {
+        test = 0;
+        p = 0.0;
+      } else if (T == 0.0) {
         test = (x == amax[par]);
         p = test ? 1.0 : 0.0;
       } else {
