@@ -115,6 +115,7 @@ PyObject* logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
       const Tensor& m = c.tensor(a[7], "mask");
       c.dims(m, "mask", 2, "[M, ceil(V / 32)]");
       const int64_t M = given(8) ? m.size(0) : B * N;
+      if (M < 1) c.refuse("mask must have rows: one without any has no address, and would be none");
       r.mask = reinterpret_cast<uint32_t*>(ints(7, "mask", {M, W}));
       r.n_masks = small(c, M, "M");
       r.mask_row = ints(8, "mask_row", {B, N});
