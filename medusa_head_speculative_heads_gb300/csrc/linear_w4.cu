@@ -198,7 +198,7 @@ using namespace medusa;
 using namespace medusa::w4;
 
 static bool sizes_ok(int K, int Nout, int group) {
-  return group_log2(group) >= 0 && K >= group && K % group == 0 && K < 0x7fffffff - 65536 && Nout >= 1 && Nout < 0x7fffffff - 65536;
+  return group_log2(group) >= 0 && K >= group && K % group == 0 && K < 0x7fffffff - 65535 && Nout >= 1 && Nout < 0x7fffffff - 65535;
 }
 
 extern "C" medusa_status medusa_w4_quantize(const void* w, int Nout, int K, int group, int symmetric, medusa_dtype dt, uint32_t* qweight,

@@ -371,8 +371,8 @@ using namespace medusa;
 using namespace medusa::logits;
 
 static bool at4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-// Sizes whose last block's columns or threads stay inside int32.
-static bool fits(int n) { return n >= 1 && n < 0x7fffffff - 65536; }
+// Sizes whose last block's columns or threads, and a step of 65535 behind them, stay inside int32.
+static bool fits(int n) { return n >= 1 && n < 0x7fffffff - 65535; }
 
 extern "C" medusa_status medusa_logits_process(const void* logits, int64_t ld, medusa_dtype dt, const medusa_logits_rules* rules,
                                                const int32_t* tokens, const medusa_dev_topology* t, int B, int N, int V, float* out,
