@@ -624,7 +624,7 @@ medusa_status medusa_logits_process(const void* logits, int64_t ld, medusa_dtype
 
 /* medusa_count_tokens: enters tokens [B][S] (negative: padding) into counts [B][V]
  * (one more each) and / or prompt_bits [B][ceil(V/32)] (their bits set); either may be NULL, not both.
- * A token >= V sets BAD_INDEX and is passed over.  S >= 0.
+ * A token >= V sets BAD_INDEX and is passed over.  S >= 0; B, S and V < 2^31 - 2^16 in both calls.
  * medusa_count_accepted: the tokens of the accepted path, counts[b][tokens[b][path_nodes[b][i]]]
  * + 1 for i < accept_len[b] (tokens [B][N], path_nodes [B][Dmax+1]).  An accept_len outside
  * 1 .. Dmax+1, a path node outside [0, N) or a token outside [0, V) on the path sets

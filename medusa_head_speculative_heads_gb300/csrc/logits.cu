@@ -419,7 +419,7 @@ extern "C" medusa_status medusa_logits_process(const void* logits, int64_t ld, m
 
 extern "C" medusa_status medusa_count_tokens(const int32_t* tokens, int B, int S, int V, int32_t* counts, uint32_t* prompt_bits,
                                              int32_t* d_status, medusa_stream_t stream) {
-  if (B < 1 || S < 0 || (S > 0 && !fits(S)) || !fits(V) || (!counts && !prompt_bits) || (S > 0 && !tokens)) return MEDUSA_ERR_INVALID_ARG;
+  if (!fits(B) || S < 0 || (S > 0 && !fits(S)) || !fits(V) || (!counts && !prompt_bits) || (S > 0 && !tokens)) return MEDUSA_ERR_INVALID_ARG;
   if (!at4(tokens) || !at4(counts) || !at4(prompt_bits) || !at4(d_status)) return MEDUSA_ERR_INVALID_ARG;
   const size_t nt = (size_t)B * S * 4, nc = (size_t)B * V * 4, nb = (size_t)B * ((V + 31) / 32) * 4;
   if (overlaps_any({counts, nc}, {{tokens, nt}, {prompt_bits, nb}, {d_status, 4}}) || overlaps_any({prompt_bits, nb}, {{tokens, nt}, {d_status, 4}}))

@@ -36,3 +36,10 @@ def test_features_and_tokens_of_the_vocabulary(n):
     assert (L.medusa_count_tokens(at(0), 1, n, 1, at(1), at(2), None, None) == INVALID) == refused
     assert (L.medusa_count_accepted(at(0), at(1), at(2), n, 1, 0, 1, at(3), None, None) == INVALID) == refused
     assert (L.medusa_count_accepted(at(0), at(1), at(2), 1, 1, 0, n, at(3), None, None) == INVALID) == refused
+
+
+@pytest.mark.parametrize("B", SIZES)
+@pytest.mark.parametrize("S", [0, 1])
+def test_sequences_whose_tokens_are_counted(B, S):
+    """The kernel goes through sequences in steps of up to 65535: behind more than these an index would wrap below zero."""
+    assert (mg.lib().medusa_count_tokens(at(0), B, S, 1, at(1), at(2), None, None) == INVALID) == (B >= LIMIT)
