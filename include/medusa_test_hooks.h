@@ -43,6 +43,13 @@ medusa_status medusa_linear_w4_test_stall(const void* x, int64_t ldx, const uint
                                           const uint8_t* zeros, int T, int K, int Nout, int group, void* y,
                                           medusa_dtype y_dt, int32_t* d_status, medusa_stream_t stream);
 
+/* medusa_linear_w4_test_division: which kernel a layer of medusa_linear_w4 runs on, on the
+ * current device, and how it is divided: division[0] is 0 (product instructions fed
+ * from registers; the rest is 0), 1 (tensor memory, work divided evenly) or 2 (tensor
+ * memory, equal tiles), then the CTAs that share a tile, a tile's tokens and features, the
+ * tiles, the CTAs.  division is host memory; nothing is launched. */
+medusa_status medusa_linear_w4_test_division(int T, int K, int Nout, int32_t* division);
+
 #ifdef __cplusplus
 }
 #endif

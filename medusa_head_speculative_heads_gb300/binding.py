@@ -36,6 +36,7 @@ EXPORTS = (
     "medusa_paged_tree_attention", "medusa_paged_compact", "medusa_paged_attention_test_stall",
     "medusa_w4_quantize", "medusa_linear_w4", "medusa_logits_process",
     "medusa_count_tokens", "medusa_count_accepted", "medusa_linear_w4_test_stall",
+    "medusa_linear_w4_test_division",
 )
 
 
@@ -113,6 +114,7 @@ def lib():
             "medusa_w4_quantize": (I, [P, I, I, I, I, I, P, P, P, P]),
             "medusa_linear_w4": (I, [P, LL, P, P, P, I, I, I, I, P, I, P, P]),
             "medusa_linear_w4_test_stall": (I, [P, LL, P, P, P, I, I, I, I, P, I, P, P]),
+            "medusa_linear_w4_test_division": (I, [I, I, I, P]),
             "medusa_logits_process": (I, [P, LL, I, P, P, P, I, I, I, P, P, P]),
             "medusa_count_tokens": (I, [P, I, I, I, P, P, P, P]),
             "medusa_count_accepted": (I, [P, P, P, I, I, I, I, P, P, P]),

@@ -238,11 +238,17 @@ static bool from_registers(int T, int K, int Nout) {
   return n < 1 << 25 || Nout <= 32 * device_sm_count() || (wide(Nout) && Nout <= 96 * device_sm_count());
 }
 
+enum Kernel { kRegisters, kStream, kTiles };
+static Kernel kernel_of(int T, int K, int Nout) {
+  if (T > 64 && stream_blocks(T, K, Nout) > kSmall) return kTiles;
+  return from_registers(T, K, Nout) ? kRegisters : kStream;
+}
+
 static medusa_status linear_call(const void* x, int64_t ldx, const uint32_t* qweight, const void* scales, const uint8_t* zeros, int T, int K,
                                  int Nout, int group, void* y, medusa_dtype y_dt, int32_t* d_status, medusa_stream_t stream, int withhold) {
   if (T < 0 || !sizes_ok(K, Nout, group) || !dtype_ok(y_dt)) return MEDUSA_ERR_INVALID_ARG;
   if (T == 0) return MEDUSA_OK;
-  if (!x || !qweight || !scales || !y || ldx < K || ldx % 8 || ldx >= (1ll << 38) || T >= 0x7fffffff - 65536) return MEDUSA_ERR_INVALID_ARG;
+  if (!x || !qweight || !scales || !y || ldx < K || ldx % 8 || ldx >= (1ll << 38) || T >= 0x7fffffff - 65535) return MEDUSA_ERR_INVALID_ARG;
   const size_t es = dtype_bytes(y_dt);
   if (!aligned16(x) || !aligned16(qweight) || ((uintptr_t)scales & 1) || ((uintptr_t)y & (es - 1)) || ((uintptr_t)d_status & 3))
     return MEDUSA_ERR_INVALID_ARG;
@@ -263,8 +269,9 @@ static medusa_status linear_call(const void* x, int64_t ldx, const uint32_t* qwe
   a.y32 = y_dt == MEDUSA_F32;
   a.d_status = d_status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (T > 64 && stream_blocks(T, K, Nout) > kSmall) return tc_launch(a, withhold, s);
-  if (!from_registers(T, K, Nout)) return stream_launch(a, withhold, s);
+  const Kernel kernel = kernel_of(T, K, Nout);
+  if (kernel == kTiles) return tc_launch(a, withhold, s);
+  if (kernel == kStream) return stream_launch(a, withhold, s);
   if (withhold) return MEDUSA_ERR_INVALID_ARG;
   if (T > 8) few<2, 1, 16>(a, s);
   else if (wide(Nout)) few<1, 2, 8>(a, s);
@@ -281,4 +288,13 @@ extern "C" medusa_status medusa_linear_w4_test_stall(const void* x, int64_t ldx,
                                                      const uint8_t* zeros, int T, int K, int Nout, int group, void* y, medusa_dtype y_dt,
                                                      int32_t* d_status, medusa_stream_t stream) {
   return linear_call(x, ldx, qweight, scales, zeros, T, K, Nout, group, y, y_dt, d_status, stream, 1);
+}
+
+extern "C" medusa_status medusa_linear_w4_test_division(int T, int K, int Nout, int32_t* division) {
+  if (T < 1 || T >= 0x7fffffff - 65535 || !sizes_ok(K, Nout, 32) || !division) return MEDUSA_ERR_INVALID_ARG;
+  const Kernel kernel = kernel_of(T, K, Nout);
+  const Division d = kernel == kTiles ? tc_division(T, K, Nout) : kernel == kStream ? stream_division(T, K, Nout) : Division{};
+  const int32_t all[6] = {kernel, d.share, d.tokens, d.features, d.tiles, d.ctas};
+  for (int i = 0; i < 6; ++i) division[i] = all[i];
+  return MEDUSA_OK;
 }

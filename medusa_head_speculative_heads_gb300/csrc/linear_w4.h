@@ -74,6 +74,12 @@ medusa_status stream_launch(const Args& a, int withhold, cudaStream_t s);
 // Blocks of 128 features, 64 tokens and 128 columns that a CTA of the first one has at most.
 int stream_blocks(int T, int K, int Nout);
 medusa_status tc_launch(const Args& a, int withhold, cudaStream_t s);
+// How a kernel divides a layer, for tests.
+struct Division {
+  int share, tokens, features, tiles, ctas;  // CTAs that share a tile; of a tile; all of them
+};
+Division stream_division(int T, int K, int Nout);
+Division tc_division(int T, int K, int Nout);
 
 }  // namespace w4
 }  // namespace medusa

@@ -493,9 +493,9 @@ static Plan plan(int T, int K, int Nout) {
   Plan best{};
   for (int share = 1; share <= kMaxShare; share *= 2) {
     Plan p{};
-    p.ntiles = (T + kMaxTN - 1) / kMaxTN;
-    p.TN = ((T + p.ntiles - 1) / p.ntiles + 15) / 16 * 16;
-    p.ntiles = (T + p.TN - 1) / p.TN;
+    p.ntiles = ceil_div(T, kMaxTN);  // in 64 bits: T may be nearly 2^31
+    p.TN = (ceil_div(T, p.ntiles) + 15) / 16 * 16;
+    p.ntiles = ceil_div(T, p.TN);
     p.DN = p.TN > 32 ? 64 : p.TN;
     p.turns = kSums / p.DN;
     p.RH = Nout >= kRows ? kRows : (Nout + 15) / 16 * 16;
@@ -557,6 +557,11 @@ int clusters_at_once(int share) {
 int stream_blocks(int T, int K, int Nout) {
   const Plan p = plan(T, K, Nout);
   return p.share ? 2 * (p.each * p.kpairs / p.share) : 0x7fffffff;
+}
+
+Division stream_division(int T, int K, int Nout) {
+  const Plan p = plan(T, K, Nout);
+  return {p.share, p.TN, p.RH, p.tiles, p.clusters * p.share};
 }
 
 medusa_status stream_launch(const Args& a, int withhold, cudaStream_t s) {

@@ -449,9 +449,9 @@ static Tc plan(int T, int K, int Nout) {
   const int kblocks = (K + kCols - 1) / kCols;
   for (int share = 1; share <= kMaxShare && share <= kblocks; share *= 2) {
     Tc p{};
-    p.ntiles = (T + kMaxTN - 1) / kMaxTN;
-    p.TN = ((T + p.ntiles - 1) / p.ntiles + 15) / 16 * 16;
-    p.ntiles = (T + p.TN - 1) / p.TN;
+    p.ntiles = ceil_div(T, kMaxTN);  // in 64 bits: T may be nearly 2^31
+    p.TN = (ceil_div(T, p.ntiles) + 15) / 16 * 16;
+    p.ntiles = ceil_div(T, p.TN);
     p.DN = (p.TN + 31) / 32 * 32;
     p.NX = (int)((kRing - kSlotsW * kSlotW) / (p.TN * 256)) & ~1;
     if (p.NX > kMaxSlotsX) p.NX = kMaxSlotsX;
@@ -485,6 +485,11 @@ static Tc plan(int T, int K, int Nout) {
 }
 
 }  // namespace
+
+Division tc_division(int T, int K, int Nout) {
+  const Tc p = plan(T, K, Nout);
+  return {p.share, p.TN, p.halves * p.RH, p.mtiles * p.ntiles, p.grid};
+}
 
 medusa_status tc_launch(const Args& a, int withhold, cudaStream_t s) {
   if (!encode_fn()) return MEDUSA_ERR_CUDA;

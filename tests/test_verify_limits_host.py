@@ -43,3 +43,27 @@ def test_features_and_tokens_of_the_vocabulary(n):
 def test_sequences_whose_tokens_are_counted(B, S):
     """The kernel goes through sequences in steps of up to 65535: behind more than these an index would wrap below zero."""
     assert (mg.lib().medusa_count_tokens(at(0), B, S, 1, at(1), at(2), None, None) == INVALID) == (B >= LIMIT)
+
+
+def division(T, K, N):
+    """(kernel, CTAs that share a tile, tokens and features of a tile, tiles, CTAs)"""
+    d = (ctypes.c_int32 * 6)()
+    assert mg.lib().medusa_linear_w4_test_division(T, K, N, d) == 0
+    return list(d)
+
+
+@pytest.mark.parametrize("T", [65, 10 ** 6 + 1, 2113929153, 2113929217, 2130706433, 2139095041, LIMIT - 65, LIMIT - 1])
+@pytest.mark.parametrize("K,N", [(32, 1), (64, 20), (32, 130)])
+def test_tokens_of_a_linear_layer(T, K, N):
+    """Tiles of the tokens of the longest inputs: as high as the others', and covering all of them."""
+    kernel, share, tokens, features, tiles, ctas = division(T, K, N)
+    assert kernel in (1, 2) and share in (1, 2, 4, 8) and 1 <= ctas <= 152 * 8 and ctas % share == 0
+    assert 16 <= tokens <= (64 if kernel == 1 else 128) and tokens % 16 == 0 and 16 <= features <= (128 if kernel == 1 else 256)
+    across = -(-T // tokens)
+    assert tiles == across * -(-N // features) and 0 <= across * tokens - T < 16 * across + tokens
+
+
+def test_a_linear_layer_refuses_more_tokens():
+    L = mg.lib()
+    for T in SIZES:
+        assert (L.medusa_linear_w4(at(0), 32, at(1), at(2), None, T, 32, 1, 32, at(3), 1, None, None) == INVALID) == (T >= LIMIT)
