@@ -65,16 +65,18 @@ __device__ __forceinline__ int mask_row_of(const Args& a, size_t row) {
   return -1;
 }
 
-// The result of a token on a node's path, which occurs there c times.
+// The result of a token on a node's path, which occurs there c times.  Counts may lie below zero, so that it may be unsaid
+// all the same.  All that is asked for is on its way at once.
 __device__ __forceinline__ float on_path(const Args& a, int b, size_t row, int v, int c, float x) {
   const int m = a.r.mask ? mask_row_of(a, row) : -1;
+  const int before = a.r.counts ? a.r.counts[(size_t)b * a.V + v] : 0;
+  const uint32_t prompt = a.r.prompt_bits ? a.r.prompt_bits[(size_t)b * a.W + (v >> 5)] >> (v & 31) : 0;
+  const float rep = a.r.repetition ? a.r.repetition[b] : 1.f, fr = a.r.frequency ? a.r.frequency[b] : 0.f, pr = a.r.presence ? a.r.presence[b] : 0.f,
+              e = a.r.bias ? a.r.bias[(a.r.bias_rows > 1 ? (size_t)b * a.V : 0) + v] : 0.f;
   if (m >= 0 && !((a.r.mask[(size_t)m * a.W + (v >> 5)] >> (v & 31)) & 1u)) return -INFINITY;
-  if (a.r.counts) c += a.r.counts[(size_t)b * a.V + v];
-  if (a.r.repetition) x = x > 0.f ? x / a.r.repetition[b] : x * a.r.repetition[b];
-  if (a.r.frequency) x -= a.r.frequency[b] * (float)c;
-  if (a.r.presence) x -= a.r.presence[b];
-  if (a.r.bias) x += a.r.bias[(a.r.bias_rows > 1 ? (size_t)b * a.V : 0) + v];
-  return x;
+  c += before;
+  if (c > 0 || (prompt & 1u)) x = x > 0.f ? x / rep : x * rep;
+  return x - fr * (float)c - (c > 0 ? pr : 0.f) + e;
 }
 
 // All warps of a block, from places of their own.
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) process_kernel(const __grid
         const bool said = c[i] > 0 || ((prompt >> i) & 1u);
         pos[i] = said ? inv : 1.f;
         neg[i] = said ? rep : 1.f;
-        if (c[i] > 0) add[i] -= fr * (float)c[i] + pr;
+        if (c[i] != 0) add[i] -= fmaf(fr, (float)c[i], c[i] > 0 ? pr : 0.f);
       }
     }
     if (TREE && a.in_place) block_sync();
@@ -293,20 +295,30 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) rows_kernel(const __grid
 #pragma unroll
       for (int q = 0; q < COLS; ++q) allowed[q] = m >= 0 && here(q) ? mp[q * (STEP / 32)] >> shift : 0xffffffffu;
       const float inv = 1.f / rep;
+      int signs = 0;
 #pragma unroll
-      for (int q = 0; q < COLS; ++q) {
-        float y[VEC];
+      for (int q = 0; q < COLS; ++q)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float x = z[q].get(i), f = c[q][i] > 0 || (prompt[q] & (1u << i)) ? (x > 0.f ? inv : rep) : 1.f;
-          const float s = c[q][i] > 0 ? e[q][i] - (fr * (float)c[q][i] + pr) : e[q][i];
-          y[i] = allowed[q] & (1u << i) ? fmaf(x, f, s) : -INFINITY;
+        for (int i = 0; i < VEC; ++i) signs |= c[q][i];
+      auto write = [&](auto below) {  // whether counts below zero are among them: their part is a branch of its own
+#pragma unroll
+        for (int q = 0; q < COLS; ++q) {
+          float y[VEC];
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            const float x = z[q].get(i), f = c[q][i] > 0 || (prompt[q] & (1u << i)) ? (x > 0.f ? inv : rep) : 1.f;
+            float s = c[q][i] > 0 ? e[q][i] - (fr * (float)c[q][i] + pr) : e[q][i];
+            if (below() && c[q][i] < 0) s -= fr * (float)c[q][i];
+            y[i] = allowed[q] & (1u << i) ? fmaf(x, f, s) : -INFINITY;
+          }
+          if (here(q)) {
+            if constexpr (VEC == 4) *reinterpret_cast<float4*>(yp + q * STEP) = make_float4(y[0], y[1], y[2], y[3]);
+            else yp[q * STEP] = y[0];
+          }
         }
-        if (here(q)) {
-          if constexpr (VEC == 4) *reinterpret_cast<float4*>(yp + q * STEP) = make_float4(y[0], y[1], y[2], y[3]);
-          else yp[q * STEP] = y[0];
-        }
-      }
+      };
+      if (signs < 0) write(std::true_type());
+      else write(std::false_type());
     };
     if (whole) chunk([](int) { return true; });
     else chunk([&](int q) { return v0 + q * STEP < a.V; });
