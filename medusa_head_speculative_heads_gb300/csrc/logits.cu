@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) rows_kernel(const __grid
           for (int i = 0; i < VEC; ++i) {
             const float x = z[q].get(i), f = c[q][i] > 0 || (prompt[q] & (1u << i)) ? (x > 0.f ? inv : rep) : 1.f;
             float s = c[q][i] > 0 ? e[q][i] - (fr * (float)c[q][i] + pr) : e[q][i];
-            if (below() && c[q][i] < 0) s -= fr * (float)c[q][i];
+            if (below()) s -= fr * (float)min(c[q][i], 0);
             y[i] = allowed[q] & (1u << i) ? fmaf(x, f, s) : -INFINITY;
           }
           if (here(q)) {
@@ -317,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) rows_kernel(const __grid
           }
         }
       };
-      if (signs < 0) write(std::true_type());
-      else write(std::false_type());
+      if (signs >= 0) write(std::false_type());
+      else write(std::true_type());
     };
     if (whole) chunk([](int) { return true; });
     else chunk([&](int q) { return v0 + q * STEP < a.V; });
