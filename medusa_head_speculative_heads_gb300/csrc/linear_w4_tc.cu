@@ -14,9 +14,9 @@
 // cluster share a tile's columns: each sums up its blocks, sends the other CTAs their tokens' sums through
 // distributed shared memory, and adds what it receives in the CTAs' order.
 //
-// What bounds it: for prompts the tensor cores and the power they take (2311 tokens, 11008 features of 4096 columns: 134 us,
-// 1550 TFLOP/s, tensor pipe 80 %); for a few hundred tokens the unpacking, whose warps wait half of the time, and what a
-// shared tile's end costs (171 tokens, 4096 features of 11008 columns: 20.5 us, 750 TFLOP/s).  Tokens loaded once for
+// What bounds it: for prompts the tensor cores and the power they take (2311 tokens, 11008 features of 4096 columns: 134 to
+// 148 us by the machine, 1550 to 1410 TFLOP/s, tensor pipe 80 %); for a few hundred tokens the unpacking, which each tile of tokens repeats and whose warps
+// wait half of the time, and what a shared tile's end costs (171 tokens, two tiles, 4096 features of 11008 columns: 20.7 us, 740 TFLOP/s).  Tokens loaded once for
 // two neighbouring CTAs made it no faster (21.4 us, prompts 137).
 //
 // Every wait is bounded: a timeout sets MEDUSA_DEV_TIMEOUT, all roles stop, copies and products in

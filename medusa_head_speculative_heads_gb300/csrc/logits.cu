@@ -13,8 +13,8 @@
 // writes the last ones'; where there are few nodes and no tree, of several places in a row.  The rows of all chunks of
 // tokens, laid end to end, are divided evenly over the blocks that the SMs hold at once.  The paths are a warp's own
 // work, beside the others': what it finds out takes four trips to memory one after the other, which all waited for
-// when they shared it.  Measured: 16 trees of 57 nodes, 32000 tokens, bf16: 36.9 us, 4.8 TB/s (nothing asked for: 30.4
-// us); one tree of 64, fp32: 6.6 us; 64 rows of 50257: 10.1 us, 3.2 TB/s.
+// when they shared it.  Measured: 16 trees of 57 nodes, 32000 tokens, bf16: 37.3 us, 4.8 TB/s (nothing asked for: 30.4
+// us); one tree of 64, fp32: 6.7 us; 64 rows of bf16 logits, 50257 tokens: 10.4 us, 3.1 TB/s; 50258: 10.4; 32000: 5.4; 128256: 16.7.
 #include <math.h>
 
 #include <type_traits>
@@ -254,7 +254,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) process_kernel(const __grid
   }
 }
 
-// Few nodes and no tree: a thread has COLS times VEC tokens of a row, and nothing is worked out for other rows.
+// Few nodes and no tree: a thread has COLS times VEC tokens of a row, and nothing is worked out for other rows.  Seven places
+// of one token and kRowBlocks come from a sweep at 64 rows of 50257 tokens alone.
 template <typename T, int VEC, int COLS>
 __global__ void __launch_bounds__(kThreads, kRowBlocks) rows_kernel(const __grid_constant__ Args a) {
   constexpr int STEP = kThreads * VEC, WIDE = STEP * COLS;
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks) rows_kernel(const __grid
 // ------------------------------------------------------------------ counts
 
 // Grid (ceil(S / 256), B).  Sums of whole numbers, so that the order of the atomic additions changes nothing.  Bound by the
-// launch (7 prompts of up to 4099 tokens: 1.7 us).
+// launch (7 prompts of up to 4099 tokens: 1.7 us in a row, 2.8 as calls of their own).
 __global__ void __launch_bounds__(256)
 count_tokens_kernel(const int32_t* tokens, int B, int S, int V, int32_t* counts, uint32_t* bits, int32_t* d_status) {
   pdl_wait();
@@ -344,7 +345,8 @@ count_tokens_kernel(const int32_t* tokens, int B, int S, int V, int32_t* counts,
   }
 }
 
-// A warp a row: lane i has node i of the path.  Bound by the launch and three trips to memory (1.2 us).
+// A warp a row: lane i has node i of the path.  Bound by the launch and three trips to memory (1.2 us in a row, 2.7 as
+// calls of their own).
 __global__ void __launch_bounds__(128)
 count_accepted_kernel(const int32_t* tokens, const int32_t* path_nodes, const int32_t* accept_len, int B, int N, int D1, int V,
                       int32_t* counts, int32_t* d_status) {
