@@ -577,9 +577,9 @@ medusa_status medusa_w4_quantize(const void* w, int Nout, int K, int group, int 
 /* medusa_linear_w4: y = x W^T, W in 4 bits.
  *   x [T][K] bf16, ldx elements from one row to the next (>= K, a multiple of 8);
  *   y [T][Nout], bf16 or fp32 (y_dt), rounded once from fp32 sums.  Products are exact; the tensor
- *   cores that add them up 16 at a time cut a sum's last bits off, they do not round: an fp32 y is off
- *   by some 3e-7 of its size for one token of 4096 columns, 1.4e-6 for 64 and 4e-6 for more tokens
- *   (normal inputs), where sums that are rounded would be off by 1e-7.
+ *   cores that add them up 16 at a time cut a sum's last bits off, they do not round, so that what is
+ *   lost grows with K: an fp32 y is off by up to 1.2e-6 of its size for up to 64 tokens and 3.1e-6 for
+ *   more at K = 4096, by 2.5e-6 and 9.8e-6 at K = 11008 (normal inputs).
  * T >= 0 (nothing is launched for 0).  x and qweight 16-byte aligned.  y must
  * overlap no other buffer (ALIAS).  A row of x with NaN or infinities changes that
  * row of y alone.  Sums are made in a fixed order (deterministic on a given device).

@@ -19,6 +19,10 @@
 // wait half of the time, and what a shared tile's end costs (171 tokens, two tiles, 4096 features of 11008 columns: 20.7 us, 740 TFLOP/s).  Tokens loaded once for
 // two neighbouring CTAs made it no faster (21.4 us, prompts 137).
 //
+// A sum takes all of a CTA's columns: the tensor core cuts its last bits off at each of K / 16 additions, a loss of 3.1e-6 of the result at
+// 4096 columns and 9.8e-6 at 11008, which is what a product of bf16 matrices into fp32 loses in the library too.  Shorter sums
+// need tensor memory that is not there, or outputs read and written several times.
+//
 // Every wait is bounded: a timeout sets MEDUSA_DEV_TIMEOUT, all roles stop, copies and products in
 // flight are waited for and tensor memory is freed.
 #include "linear_w4_tc.cuh"
